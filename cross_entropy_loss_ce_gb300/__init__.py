@@ -62,9 +62,16 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.gbce_bsr_plan.restype = ctypes.c_char_p
         lib.gbce_timing_read.argtypes = [ctypes.POINTER(ctypes.c_double),
                                          ctypes.POINTER(ctypes.c_int64)]
+        lib.linear_ce_fwd.argtypes = [p, i64, p, i64, p, p, p, p, i64, i64, i64, i64, ci, ci, p]
+        lib.linear_ce_bwd.argtypes = [p, i64, p, i64, p, p, p, p, i64, p, i64, i64, i64, i64, i64,
+                                      ci, ci, p]
+        lib.linear_greedy.argtypes = [p, i64, p, i64, p, p, i64, i64, i64, ci, p]
+        lib.moe_balance.argtypes = [p, i64, p, i64, p, p, p, i64, p, i64, i64, i64, ctypes.c_float,
+                                    ctypes.c_float, ci, p]
         for f in ("ce_fwd_bwd", "softmax_fwd", "softmax_bwd", "gbce_last_error",
                   "gbce_timing_enable", "gbce_timing_read", "ce_fwd_bwd_ex", "scale_rows",
-                  "softmax_bwd_bsr"):
+                  "softmax_bwd_bsr", "linear_ce_fwd", "linear_ce_bwd", "linear_greedy",
+                  "moe_balance"):
             getattr(lib, f).restype = ci
         _lib = lib
     return _lib
@@ -498,3 +505,281 @@ def ce_fwd_bwd_noalloc(logits: torch.Tensor, targets: torch.Tensor, ignore_index
                 DTYPES[logits.dtype], _stream_handle(stream, dev))
     _check(rc, "ce_fwd_bwd_noalloc")
     return loss
+
+
+# ---------------------------------------------------------------------------
+# the output layer: losses and tokens from hidden states, the logits not stored
+
+
+def _rows(t: torch.Tensor, name: str):
+    """_matrix for operands whose rows must not share memory (no expanded rows)."""
+    if t.dim() == 2 and t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name} has overlapping rows (stride {t.stride(0)} for {t.shape[1]} columns)")
+    return _matrix(t, name)
+
+
+def _head(hidden, weight):
+    hp, hs, M, K = _rows(hidden, "hidden")
+    wp, ws, V, Kw = _rows(weight, "weight")
+    if Kw != K:
+        raise ValueError(f"hidden has {K} columns, weight {Kw}")
+    if hidden.dtype != weight.dtype:
+        raise TypeError(f"hidden is {hidden.dtype}, weight {weight.dtype}")
+    return hp, hs, wp, ws, M, K, V
+
+
+def _class_ids(targets, M):
+    if targets.dtype != torch.int64 or targets.dim() != 1 or targets.shape[0] != M:
+        raise ValueError("targets must be int64 of shape [M]")
+    if M and (not targets.is_cuda or not targets.is_contiguous()):
+        raise ValueError("targets must be a contiguous CUDA tensor")
+    return targets if M else None
+
+
+def _row_values(t, M, name):
+    if t.dtype != torch.float32 or t.shape != (M,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous float32 of shape [M]")
+    return t
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def linear_ce_fwd(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor,
+                  ignore_index: int = -100, reduction: str = "mean", loss: torch.Tensor = None,
+                  row_loss: torch.Tensor = None, lse: torch.Tensor = None, stream=None):
+    """Cross-entropy of ``hidden`` [M, K] through the output layer ``weight``
+    [V, K] (both bfloat16 or both float16) against int64 ``targets`` [M]; the
+    [M, V] logits are never stored.
+
+    Returns (loss, row_loss, lse): a 0-dim float32 CUDA tensor (None for the
+    reduction 'none'), the [M] row losses and the [M] log-sum-exps (0 for ignored
+    rows) that linear_ce_bwd takes.
+    """
+    hp, hs, wp, ws, M, K, V = _head(hidden, weight)
+    if reduction not in REDUCTIONS:
+        raise ValueError(f"reduction must be one of {sorted(REDUCTIONS)}")
+    ids = _class_ids(targets, M)
+    dev = hidden.device
+    if reduction == "none":
+        loss = None
+    elif loss is None:
+        loss = torch.empty((), dtype=torch.float32, device=dev)
+    elif loss.dtype != torch.float32 or loss.numel() != 1:
+        raise ValueError("loss must be a one-element float32 CUDA tensor")
+    row_loss = torch.empty((M,), dtype=torch.float32, device=dev) if row_loss is None else \
+        _row_values(row_loss, M, "row_loss")
+    lse = torch.empty((M,), dtype=torch.float32, device=dev) if lse is None else \
+        _row_values(lse, M, "lse")
+    dev = _call_device(("hidden", hidden), ("weight", weight), ("targets", ids), ("loss", loss),
+                       ("row_loss", row_loss), ("lse", lse))
+    with _OnDevice(dev):
+        rc = load_library().linear_ce_fwd(
+            hp, hs, wp, ws, targets.data_ptr(), _ptr(loss), row_loss.data_ptr(), lse.data_ptr(), M, K,
+            V, int(ignore_index), DTYPES[hidden.dtype], REDUCTIONS[reduction],
+            _stream_handle(stream, dev))
+    _check(rc, "linear_ce_fwd")
+    return loss, row_loss, lse
+
+
+def linear_ce_bwd(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor,
+                  lse: torch.Tensor, grad_scale=None, ignore_index: int = -100,
+                  reduction: str = "mean", want_hidden: bool = True, want_weight: bool = True,
+                  d_hidden: torch.Tensor = None, d_weight: torch.Tensor = None, stream=None):
+    """(d_hidden, d_weight) of linear_ce_fwd's loss, in the operands' type.
+
+    ``lse`` is what the forward returned; ``grad_scale`` the incoming gradient
+    (None, a number or a float32 CUDA tensor: one value, or one per row for
+    'none').  A gradient that is not wanted is None and costs nothing.
+    """
+    hp, hs, wp, ws, M, K, V = _head(hidden, weight)
+    if reduction not in REDUCTIONS:
+        raise ValueError(f"reduction must be one of {sorted(REDUCTIONS)}")
+    ids = _class_ids(targets, M)
+    lse = _row_values(lse, M, "lse")
+    dev, outs = hidden.device, []
+    for name, want, out, like in (("d_hidden", want_hidden, d_hidden, hidden),
+                                  ("d_weight", want_weight, d_weight, weight)):
+        if not want:
+            out = None
+        elif out is None:
+            out = torch.empty(like.shape, dtype=like.dtype, device=dev)
+        elif out.shape != like.shape or out.dtype != like.dtype:
+            raise ValueError(f"{name} must have the shape and dtype of {name[2:]}")
+        outs.append(out)
+    d_hidden, d_weight = outs
+    gs = None
+    if grad_scale is not None:
+        gs = _device_floats(grad_scale, M if reduction == "none" else 1, dev, "grad_scale")
+    dhp, dhs = _rows(d_hidden, "d_hidden")[:2] if d_hidden is not None else (None, 0)
+    dwp, dws = _rows(d_weight, "d_weight")[:2] if d_weight is not None else (None, 0)
+    dev = _call_device(("hidden", hidden), ("weight", weight), ("targets", ids), ("lse", lse),
+                       ("grad_scale", gs if M else None), ("d_hidden", d_hidden),
+                       ("d_weight", d_weight))
+    if d_hidden is None and d_weight is None:
+        return None, None
+    with _OnDevice(dev):
+        rc = load_library().linear_ce_bwd(
+            hp, hs, wp, ws, targets.data_ptr(), lse.data_ptr(), _ptr(gs), dhp, dhs, dwp, dws, M, K, V,
+            int(ignore_index), DTYPES[hidden.dtype], REDUCTIONS[reduction],
+            _stream_handle(stream, dev))
+    _check(rc, "linear_ce_bwd")
+    return d_hidden, d_weight
+
+
+def linear_greedy(hidden: torch.Tensor, weight: torch.Tensor, tokens: torch.Tensor = None,
+                  logprob: torch.Tensor = None, stream=None):
+    """The most probable class of each row of ``hidden`` [M, K] @ ``weight``
+    [V, K].T (the lowest index of equal ones) and its log-probability, the logits
+    never stored: (tokens [M] int64, logprob [M] float32)."""
+    hp, hs, wp, ws, M, K, V = _head(hidden, weight)
+    dev = hidden.device
+    if tokens is None:
+        tokens = torch.empty((M,), dtype=torch.int64, device=dev)
+    elif tokens.dtype != torch.int64 or tokens.shape != (M,) or not tokens.is_contiguous():
+        raise ValueError("tokens must be contiguous int64 of shape [M]")
+    logprob = torch.empty((M,), dtype=torch.float32, device=dev) if logprob is None else \
+        _row_values(logprob, M, "logprob")
+    dev = _call_device(("hidden", hidden), ("weight", weight), ("tokens", tokens), ("logprob", logprob))
+    with _OnDevice(dev):
+        rc = load_library().linear_greedy(hp, hs, wp, ws, tokens.data_ptr(), logprob.data_ptr(), M, K, V,
+                                          DTYPES[hidden.dtype], _stream_handle(stream, dev))
+    _check(rc, "linear_greedy")
+    return tokens, logprob
+
+
+def _unit_rows(t):
+    """t itself where the library can read its rows, else a contiguous copy."""
+    ok = (t.shape[1] == 1 or t.stride(1) == 1) and (t.shape[0] <= 1 or t.stride(0) >= t.shape[1])
+    return t if ok else t.contiguous()
+
+
+class FusedLinearCrossEntropy(torch.autograd.Function):
+    """Autograd form of linear_ce_fwd / linear_ce_bwd.  Saves the hidden states,
+    the weights and one number per row; nothing is overwritten, so backward may
+    run more than once."""
+
+    @staticmethod
+    def forward(ctx, hidden, weight, targets, ignore_index=-100, reduction="mean"):
+        h, w = _unit_rows(hidden.detach()), _unit_rows(weight.detach())
+        loss, row_loss, lse = linear_ce_fwd(h, w, targets, ignore_index, reduction)
+        ctx.save_for_backward(h, w, targets, lse)
+        ctx.ignore_index, ctx.reduction = ignore_index, reduction
+        return row_loss if reduction == "none" else loss
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_output):
+        h, w, targets, lse = ctx.saved_tensors
+        gs = grad_output.detach().to(torch.float32).contiguous().reshape(-1)
+        dh, dw = linear_ce_bwd(h, w, targets, lse, gs, ctx.ignore_index, ctx.reduction,
+                               want_hidden=ctx.needs_input_grad[0],
+                               want_weight=ctx.needs_input_grad[1])
+        return dh, dw, None, None, None
+
+
+def linear_cross_entropy(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor,
+                         ignore_index: int = -100, reduction: str = "mean") -> torch.Tensor:
+    """Hard-label cross-entropy of the logits hidden @ weight.T, differentiable in
+    both, without forming the logits.  ``hidden`` is [..., K] and ``targets`` [...]
+    (the same leading shape); 'none' returns row losses of the targets' shape."""
+    if hidden.shape[:-1] != targets.shape:
+        raise ValueError(f"hidden has rows {tuple(hidden.shape[:-1])}, targets {tuple(targets.shape)}")
+    out = FusedLinearCrossEntropy.apply(hidden.reshape(-1, hidden.shape[-1]), weight,
+                                        targets.reshape(-1).contiguous(), ignore_index, reduction)
+    return out.reshape(targets.shape) if reduction == "none" else out
+
+
+class LinearCrossEntropyLoss(torch.nn.Module):
+    """nn.Module form of linear_cross_entropy; the output layer's weights are an
+    argument, so they can be shared with an embedding."""
+
+    def __init__(self, ignore_index: int = -100, reduction: str = "mean"):
+        super().__init__()
+        if reduction not in REDUCTIONS:
+            raise ValueError(f"reduction must be one of {sorted(REDUCTIONS)}")
+        self.ignore_index, self.reduction = ignore_index, reduction
+
+    def forward(self, hidden, weight, targets):
+        return linear_cross_entropy(hidden, weight, targets, self.ignore_index, self.reduction)
+
+
+# ---------------------------------------------------------------------------
+# a router's balance loss
+
+
+def moe_balance(logits: torch.Tensor, experts: torch.Tensor, balance_coef: float,
+                z_coef: float = 0.0, grad_scale=None, want_loss: bool = True,
+                want_grad: bool = True, grad: torch.Tensor = None, stream=None):
+    """Balance loss and z-loss of router ``logits`` [T, E] whose tokens were sent to
+    ``experts`` [T, k] (int64, -1 for an empty slot), in one call:
+    (loss, counts, grad).
+
+    loss is balance_coef * E * sum_e (counts_e / (k n)) * mean_t softmax(logits_t)_e
+    + z_coef * mean_t logsumexp(logits_t)^2 over the n tokens with a slot in use;
+    counts is [E] int64; grad is d(loss)/d(logits) times grad_scale (a number or a
+    one-element float32 CUDA tensor), written to ``grad`` when given (which may be
+    ``logits``).  loss and grad are None when not wanted.
+    """
+    lp, ls, T, E = _rows(logits, "logits")
+    if experts.dtype != torch.int64 or experts.dim() != 2 or experts.shape[0] != T or \
+            experts.shape[1] < 1:
+        raise ValueError("experts must be int64 of shape [T, k]")
+    k = experts.shape[1]
+    if (k > 1 and experts.stride(1) != 1) or (T > 1 and experts.stride(0) < k):
+        raise ValueError("experts needs unit column stride and rows that do not overlap")
+    es = experts.stride(0) if T > 1 else k
+    dev = logits.device
+    if not want_grad:
+        grad = None
+    elif grad is None:
+        grad = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    elif grad.shape != logits.shape or grad.dtype != logits.dtype:
+        raise ValueError("grad must match the logits' shape and dtype")
+    gp, gstride = _rows(grad, "grad")[:2] if grad is not None else (None, 0)
+    gs = None if grad_scale is None else _device_floats(grad_scale, 1, dev, "grad_scale")
+    loss = torch.empty((), dtype=torch.float32, device=dev) if want_loss else None
+    counts = torch.empty((E,), dtype=torch.int64, device=dev)
+    dev = _call_device(("logits", logits), ("experts", experts if T else None), ("grad", grad),
+                       ("grad_scale", gs), ("counts", counts))
+    with _OnDevice(dev):
+        rc = load_library().moe_balance(lp, ls, experts.data_ptr(), max(es, k), counts.data_ptr(),
+                                        _ptr(loss), gp, gstride, _ptr(gs), T, E, k,
+                                        float(balance_coef), float(z_coef), DTYPES[logits.dtype],
+                                        _stream_handle(stream, dev))
+    _check(rc, "moe_balance")
+    return loss, counts, grad
+
+
+class MoeBalance(torch.autograd.Function):
+    """Autograd form of moe_balance: the forward computes the loss and the counts,
+    the backward the gradient with the incoming one folded in."""
+
+    @staticmethod
+    def forward(ctx, logits, experts, balance_coef, z_coef=0.0):
+        x = _unit_rows(logits.detach())
+        loss, counts, _ = moe_balance(x, experts, balance_coef, z_coef, want_grad=False)
+        ctx.save_for_backward(x, experts)
+        ctx.coefs = balance_coef, z_coef
+        ctx.mark_non_differentiable(counts)
+        return loss, counts
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_output, _):
+        x, experts = ctx.saved_tensors
+        gs = grad_output.detach().to(torch.float32).contiguous().reshape(-1)
+        grad = moe_balance(x, experts, *ctx.coefs, grad_scale=gs, want_loss=False)[2]
+        return grad, None, None, None
+
+
+def moe_balance_loss(logits: torch.Tensor, experts: torch.Tensor, balance_coef: float,
+                     z_coef: float = 0.0):
+    """(loss, counts) of moe_balance with the loss differentiable in the logits;
+    ``logits`` is [..., E], ``experts`` [..., k] with the same leading shape."""
+    if logits.shape[:-1] != experts.shape[:-1]:
+        raise ValueError(f"logits have tokens {tuple(logits.shape[:-1])}, experts "
+                         f"{tuple(experts.shape[:-1])}")
+    return MoeBalance.apply(logits.reshape(-1, logits.shape[-1]),
+                            experts.reshape(-1, experts.shape[-1]).contiguous(), balance_coef, z_coef)

@@ -1326,3 +1326,6 @@ extern "C" int ce_fwd_bwd_host(const void *logits_host, int64_t host_stride,
         e = ef;
     return map_error(e);
 }
+
+#include "linear_api.cuh"
+#include "moe_api.cuh"

@@ -1,0 +1,614 @@
+// Host side of the output-layer operators: argument checks, tensor maps, the
+// scratch layout and the launches of linear_kernels.cuh.  Part of gbce.cu.
+#pragma once
+
+#include "linear_kernels.cuh"
+
+namespace gbce {
+namespace {
+
+constexpr int64_t kSkinnyRows = 64;               // rows up to which W is streamed once
+constexpr int64_t kGradPieceBytes = 512ll << 20;  // 16-bit logit gradients held at a time
+
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                 const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                 const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+std::atomic<EncodeTiled> g_encode{nullptr};
+
+EncodeTiled encode_tiled()
+{
+    EncodeTiled fn = g_encode.load(std::memory_order_acquire);
+    if (!fn) {
+        RelaxedCapture relaxed;
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                             &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            return nullptr;
+        fn = reinterpret_cast<EncodeTiled>(p);
+        g_encode.store(fn, std::memory_order_release);
+    }
+    return fn;
+}
+
+// rows x cols 16-bit values, `stride` elements from row to row, read in boxes
+// of 64 columns x `box_rows` rows with 128-byte swizzle; zeros outside.
+cudaError_t make_map(CUtensorMap *map, const void *p, int dtype, int64_t rows, int64_t cols,
+                     int64_t stride, int box_rows)
+{
+    const EncodeTiled fn = encode_tiled();
+    if (!fn)
+        return cudaErrorNotSupported;
+    if (rows == 1)  // a single row may have any stride: give it a valid one
+        stride = (cols + 7) / 8 * 8;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride) * 2};
+    const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t step[2] = {1, 1};
+    const CUresult r = fn(map, dtype == GBCE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                          2, const_cast<void *>(p), dims, strides, box, step,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// May a tensor map read this matrix as it stands?
+bool mappable(const void *p, int64_t stride, int64_t rows)
+{
+    return aligned_to(p, 16) && (rows <= 1 || (stride % 8 == 0 && stride < (int64_t{1} << 38)));
+}
+
+int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+// Consecutive 256-byte-aligned parts of one allocation; with a NULL base it
+// only adds up their sizes.
+struct Carver {
+    char *base;
+    size_t used = 0;
+    explicit Carver(void *b) : base(static_cast<char *>(b)) {}
+    template <typename T>
+    T *take(int64_t count)
+    {
+        T *p = base ? reinterpret_cast<T *>(base + used) : nullptr;
+        used += (static_cast<size_t>(count) * sizeof(T) + 255) / 256 * 256;
+        return p;
+    }
+};
+
+struct HeadScratch {
+    int *n, *rows;      // divisor of the mean; listed rows
+    unsigned *fail;
+    float *alpha;
+    int *idx, *tgt;
+    float *l2, *rs, *xy;
+    unsigned short *h;  // packed hidden states
+    unsigned short *w;  // packed weights (rows a tensor map cannot read)
+    float2 *part;
+    int *part_idx;
+    float *part_max;
+    unsigned short *g;
+    float *acc;
+};
+
+struct HeadShape {
+    int64_t M, K, V;
+    int64_t kp;         // K rounded up to whole 16-byte vectors
+    int64_t mp;         // rows of the packed hidden states
+    bool skinny;
+    bool pack_h, pack_w;
+    int64_t parts;      // partial pairs of a row
+    int64_t vp;         // backward: vocabulary rows of a piece
+    int64_t pieces;
+};
+
+enum class HeadOp { Fwd, Bwd, Greedy };
+
+HeadScratch carve(Carver &c, const HeadShape &s, HeadOp op, bool want_hidden)
+{
+    HeadScratch r{};
+    int *words = c.take<int>(8);
+    r.n = words;
+    r.rows = words ? words + 1 : nullptr;
+    r.fail = reinterpret_cast<unsigned *>(words ? words + 2 : nullptr);
+    r.alpha = reinterpret_cast<float *>(words ? words + 3 : nullptr);
+    if (op != HeadOp::Greedy) {
+        r.idx = c.take<int>(s.M);
+        r.tgt = c.take<int>(s.M);
+    }
+    if (s.pack_h)
+        r.h = c.take<unsigned short>(s.mp * s.kp);
+    if (s.pack_w)
+        r.w = c.take<unsigned short>(s.V * s.kp);
+    if (op == HeadOp::Bwd) {
+        r.l2 = c.take<float>(s.M);
+        r.rs = c.take<float>(s.M);
+        r.g = c.take<unsigned short>(s.mp * s.vp);
+        if (want_hidden && s.pieces > 1)
+            r.acc = c.take<float>(s.mp * round_up(s.K, kPairN));
+    } else {
+        r.part = c.take<float2>(s.parts * s.mp);
+        if (op == HeadOp::Fwd)
+            r.xy = c.take<float>(s.mp);
+        else {
+            r.part_idx = c.take<int>(s.parts * s.mp);
+            r.part_max = c.take<float>(s.parts * s.mp);
+        }
+    }
+    return r;
+}
+
+// Per-kernel one-time attributes (the dynamic shared memory it is launched with).
+cudaError_t configure_smem(const void *fn, int device, int bytes)
+{
+    std::lock_guard<std::mutex> lk(g_cfg_mu);
+    for (const FnConfig &c : g_cfg)
+        if (c.fn == fn && c.device == device)
+            return cudaSuccess;
+    RelaxedCapture relaxed;
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess)
+        g_cfg.push_back({fn, device});
+    return e;
+}
+
+struct Call {
+    int device;
+    int64_t sms;
+    cudaStream_t stream;
+    int dtype;
+};
+
+template <Epi E>
+cudaError_t launch_pair(const Call &call, const PairArgs &a, int64_t max_tiles)
+{
+    using Fn = void (*)(const PairArgs);
+    const Fn fn = call.dtype == GBCE_BF16 ? static_cast<Fn>(pair_gemm_kernel<E, __nv_bfloat16>)
+                                          : static_cast<Fn>(pair_gemm_kernel<E, __half>);
+    const cudaError_t e = configure_smem(reinterpret_cast<const void *>(fn), call.device, kPairSmem);
+    if (e != cudaSuccess)
+        return e;
+    const int64_t pairs = max_tiles < call.sms / 2 ? max_tiles : call.sms / 2;
+    fn<<<static_cast<unsigned>(2 * pairs), kPairThreads, kPairSmem, call.stream>>>(a);
+    return cudaGetLastError();
+}
+
+template <int NG, bool GREEDY>
+cudaError_t launch_skinny_ng(const Call &call, const SkinnyArgs &a, int64_t ctas)
+{
+    const auto fn = skinny_kernel<NG, GREEDY>;
+    const cudaError_t e =
+        configure_smem(reinterpret_cast<const void *>(fn), call.device, skinny_smem<NG>());
+    if (e != cudaSuccess)
+        return e;
+    fn<<<static_cast<unsigned>(ctas), skinny_threads<NG>(), skinny_smem<NG>(), call.stream>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_gather(const Call &call, GatherArgs a, int64_t rows)
+{
+    a.vec = mappable(a.src, a.ss, 2) ? 1 : 0;
+    const int64_t most = call.sms * 8;
+    lin_gather_kernel<256><<<static_cast<unsigned>(rows < most ? rows : most), 256, 0, call.stream>>>(a);
+    return cudaGetLastError();
+}
+
+int check_head(const void *hidden, int64_t hs, const void *weight, int64_t ws, int64_t M, int64_t K,
+               int64_t V, int dtype)
+{
+    if (dtype != GBCE_BF16 && dtype != GBCE_F16)
+        return GBCE_ERR_DTYPE;
+    // tiles of 256 x 256 are counted in 31 bits
+    if (M < 0 || M > kMaxRows || K < 1 || K > (int64_t{1} << 24) || V < 1 || V > INT32_MAX - 1024 ||
+        (round_up(M, 256) / 256 + kBand) * (round_up(V, 256) / 256) > INT32_MAX)
+        return GBCE_ERR_SIZE;
+    const int st = check_matrix(hidden, hs, M, K, dtype);
+    return st ? st : check_matrix(weight, ws, V, K, dtype);
+}
+
+HeadShape head_shape(const Call &call, const void *hidden, int64_t hs, const void *weight, int64_t ws,
+                     int64_t M, int64_t K, int64_t V, HeadOp op)
+{
+    HeadShape s{};
+    s.M = M;
+    s.K = K;
+    s.V = V;
+    s.kp = round_up(K, 8);
+    s.skinny = op != HeadOp::Bwd && M <= kSkinnyRows;
+    s.mp = s.skinny ? (M <= 32 ? 32 : 64) : round_up(M, kPairM);
+    // packed when rows are left out (any target may be ignore_index) or cannot be mapped
+    s.pack_h = op != HeadOp::Greedy || !mappable(hidden, hs, M);
+    s.pack_w = !mappable(weight, ws, V);
+    if (s.skinny) {
+        const int64_t units = (V + kSkinnyUnit - 1) / kSkinnyUnit;
+        s.parts = units < call.sms ? units : call.sms;
+    } else {
+        s.parts = (V + kPairN - 1) / kPairN;
+    }
+    if (op == HeadOp::Bwd) {
+        int64_t vp = kGradPieceBytes / (s.mp * 2) / kPairN * kPairN;
+        vp = vp < kPairN ? kPairN : vp;
+        s.pieces = (V + vp - 1) / vp;
+        s.vp = round_up((V + s.pieces - 1) / s.pieces, kPairN);
+        s.pieces = (V + s.vp - 1) / s.vp;
+    }
+    return s;
+}
+
+// The weights as the products read them: in place, or packed.
+cudaError_t pack_weights(const Call &call, const HeadShape &s, const HeadScratch &r, const void *weight,
+                         int64_t ws, const void **w, int64_t *wstride)
+{
+    *w = weight;
+    *wstride = ws;
+    if (!s.pack_w)
+        return cudaSuccess;
+    GatherArgs g{};
+    g.src = weight;
+    g.ss = ws;
+    g.dst = r.w;
+    g.lds = s.kp;
+    g.n_host = s.V;
+    g.K = s.K;
+    g.pad = 1;
+    *w = r.w;
+    *wstride = s.kp;
+    return launch_gather(call, g, s.V);
+}
+
+cudaError_t pack_hidden(const Call &call, const HeadShape &s, const HeadScratch &r, const void *hidden,
+                        int64_t hs, const int *idx, const int *rows, GatherArgs g = GatherArgs{})
+{
+    g.src = hidden;
+    g.ss = hs;
+    g.dst = r.h;
+    g.lds = s.kp;
+    g.idx = idx;
+    g.n_ptr = rows;
+    g.n_host = s.M;
+    g.K = s.K;
+    g.pad = static_cast<int>(s.skinny ? s.mp : kPairM);
+    return launch_gather(call, g, s.mp);
+}
+
+// Forward of `op` from prepared rows: the products and the merge.
+template <bool GREEDY>
+cudaError_t launch_head(const Call &call, const HeadShape &s, const HeadScratch &r, const void *h,
+                        int64_t hstride, const void *w, int64_t wstride, int64_t hrows, MergeArgs m)
+{
+    cudaError_t e;
+    const int kblocks = static_cast<int>((s.K + 63) / 64);
+    m.part = r.part;
+    m.part_idx = r.part_idx;
+    m.part_max = r.part_max;
+    m.parts = static_cast<int>(s.parts);
+    m.ldp = s.mp;
+    m.n_ptr = GREEDY ? nullptr : r.rows;
+    m.n_host = static_cast<int>(s.M);
+    m.idx = r.idx;
+    m.xy = r.xy;
+    if (s.skinny) {
+        SkinnyArgs a{};
+        if ((e = make_map(&a.w, w, call.dtype, s.V, s.K, wstride, 128)) != cudaSuccess ||
+            (e = make_map(&a.wu, w, call.dtype, s.V, s.K, wstride, kSkinnyUnit)) != cudaSuccess ||
+            (e = make_map(&a.h, h, call.dtype, hrows, s.K, hstride, static_cast<int>(s.mp))) != cudaSuccess)
+            return e;
+        a.n_ptr = m.n_ptr;
+        a.n_host = m.n_host;
+        a.kblocks = kblocks;
+        a.V = s.V;
+        a.tgt = r.tgt;
+        a.part = r.part;
+        a.part_idx = r.part_idx;
+        a.part_max = r.part_max;
+        a.xy = r.xy;
+        a.ldp = s.mp;
+        a.fail = GREEDY ? nullptr : r.fail;
+        a.bf16 = call.dtype == GBCE_BF16;
+        e = s.mp == 32 ? launch_skinny_ng<1, GREEDY>(call, a, s.parts)
+                       : launch_skinny_ng<2, GREEDY>(call, a, s.parts);
+    } else {
+        PairArgs a{};
+        if ((e = make_map(&a.a, h, call.dtype, hrows, s.K, hstride, 128)) != cudaSuccess ||
+            (e = make_map(&a.b, w, call.dtype, s.V, s.K, wstride, 128)) != cudaSuccess)
+            return e;
+        a.n_ptr = m.n_ptr;
+        a.n_host = m.n_host;
+        a.tiles_n = static_cast<int>(s.parts);
+        a.kblocks = kblocks;
+        a.fail = GREEDY ? nullptr : r.fail;
+        a.part = r.part;
+        a.part_idx = r.part_idx;
+        a.xy = GREEDY ? r.part_max : r.xy;
+        a.ldp = s.mp;
+        a.tgt = r.tgt;
+        a.V = s.V;
+        e = launch_pair<GREEDY ? Epi::Greedy : Epi::Stats>(call, a, s.mp / kPairM * s.parts);
+    }
+    if (e != cudaSuccess)
+        return e;
+    lin_merge_kernel<GREEDY><<<static_cast<unsigned>((s.M + 31) / 32), 256, 0, call.stream>>>(m);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_linear_fwd(const Call &call, const HeadShape &s, const HeadScratch &r,
+                              const void *hidden, int64_t hs, const void *weight, int64_t ws,
+                              const PrepArgs &prep)
+{
+    cudaError_t e;
+    lin_prep_kernel<1024, false><<<1, 1024, 0, call.stream>>>(prep);
+    if ((e = cudaGetLastError()) != cudaSuccess || s.M == 0)
+        return e;
+    const void *w;
+    int64_t wstride;
+    if ((e = pack_hidden(call, s, r, hidden, hs, r.idx, r.rows)) != cudaSuccess ||
+        (e = pack_weights(call, s, r, weight, ws, &w, &wstride)) != cudaSuccess)
+        return e;
+    MergeArgs m{};
+    m.row_loss = prep.row_loss;
+    m.lse = prep.lse_out;
+    if ((e = launch_head<false>(call, s, r, r.h, s.kp, w, wstride, s.mp, m)) != cudaSuccess ||
+        prep.reduction == GBCE_NONE)
+        return e;
+    ce_mean_kernel<1024><<<1, 1024, 0, call.stream>>>(prep.row_loss, s.M, r.n, r.fail, prep.loss,
+                                                       prep.reduction);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_linear_bwd(const Call &call, const HeadShape &s, const HeadScratch &r,
+                              const void *hidden, int64_t hs, const void *weight, int64_t ws,
+                              void *d_hidden, int64_t dhs, void *d_weight, int64_t dws,
+                              const PrepArgs &prep)
+{
+    cudaError_t e;
+    lin_prep_kernel<1024, true><<<1, 1024, 0, call.stream>>>(prep);
+    if ((e = cudaGetLastError()) != cudaSuccess)
+        return e;
+    const void *w;
+    int64_t wstride;
+    GatherArgs zero{};
+    zero.zero = d_hidden;
+    zero.zs = dhs;
+    zero.M = s.M;
+    zero.V = s.V;
+    zero.ignore_index = prep.ignore_index;
+    zero.targets = prep.targets;
+    if ((e = pack_hidden(call, s, r, hidden, hs, r.idx, r.rows, zero)) != cudaSuccess ||
+        (e = pack_weights(call, s, r, weight, ws, &w, &wstride)) != cudaSuccess)
+        return e;
+    PairArgs grad{}, dw{}, dh{};
+    const int tiles_k = static_cast<int>((s.K + kPairN - 1) / kPairN);
+    if ((e = make_map(&grad.a, r.h, call.dtype, s.mp, s.K, s.kp, 128)) != cudaSuccess ||
+        (e = make_map(&grad.b, w, call.dtype, s.V, s.K, wstride, 128)) != cudaSuccess ||
+        (e = make_map(&dw.a, r.g, call.dtype, s.mp, s.vp, s.vp, 64)) != cudaSuccess ||
+        (e = make_map(&dw.b, r.h, call.dtype, s.mp, s.K, s.kp, 64)) != cudaSuccess ||
+        (e = make_map(&dh.a, r.g, call.dtype, s.mp, s.vp, s.vp, 128)) != cudaSuccess ||
+        (e = make_map(&dh.b, w, call.dtype, s.V, s.K, wstride, 64)) != cudaSuccess)
+        return e;
+    for (PairArgs *a : {&grad, &dw, &dh}) {
+        a->n_ptr = r.rows;
+        a->fail = r.fail;
+        a->alpha = r.alpha;
+        a->idx = r.idx;
+        a->tgt = r.tgt;
+        a->l2 = r.l2;
+        a->rs = r.rs;
+        a->g = r.g;
+        a->ldg = s.vp;
+        a->cols = s.K;
+        a->acc = r.acc;
+        a->lda = round_up(s.K, kPairN);
+    }
+    grad.kblocks = static_cast<int>((s.K + 63) / 64);
+    dw.tiles_n = dh.tiles_n = tiles_k;
+    dw.ldo = dws;
+    dw.vec = aligned_to(d_weight, 16) && dws % 8 == 0;
+    dh.out = d_hidden;
+    dh.ldo = dhs;
+    dh.vec = aligned_to(d_hidden, 16) && dhs % 8 == 0;
+    for (int64_t p = 0; p < s.pieces; ++p) {
+        const int64_t v0 = p * s.vp;
+        const int64_t vn = s.V - v0 < s.vp ? s.V - v0 : s.vp;
+        const int tiles_v = static_cast<int>((vn + kPairN - 1) / kPairN);
+        grad.b_row0 = dh.b_row0 = static_cast<int>(v0);
+        grad.V = vn;
+        grad.tiles_n = tiles_v;
+        if ((e = launch_pair<Epi::Grad>(call, grad, s.mp / kPairM * tiles_v)) != cudaSuccess)
+            return e;
+        if (d_weight) {
+            dw.out = static_cast<unsigned short *>(d_weight) + v0 * dws;
+            dw.rows = vn;
+            dw.tiles_m = tiles_v;
+            if ((e = launch_pair<Epi::Weight>(call, dw, int64_t{tiles_v} * tiles_k)) != cudaSuccess)
+                return e;
+        }
+        if (d_hidden) {
+            dh.kblocks = tiles_v * (kPairN / kPairK);  // G holds zeros up to whole tiles
+            dh.first = p == 0;
+            dh.last = p == s.pieces - 1;
+            if ((e = launch_pair<Epi::Hidden>(call, dh, s.mp / kPairM * tiles_k)) != cudaSuccess)
+                return e;
+        }
+    }
+    return cudaSuccess;
+}
+
+// The pool of the current device and one allocation from it, freed on the
+// stream when the call's launches are queued.
+struct PoolScratch {
+    void *p = nullptr;
+    cudaStream_t stream;
+    explicit PoolScratch(cudaStream_t s) : stream(s) {}
+    cudaError_t get(int device, size_t bytes)
+    {
+        cudaMemPool_t pool;
+        const cudaError_t e = pool_for(device, &pool);
+        return e != cudaSuccess ? e : cudaMallocFromPoolAsync(&p, bytes, pool, stream);
+    }
+    cudaError_t release(cudaError_t e)
+    {
+        const cudaError_t ef = p ? cudaFreeAsync(p, stream) : cudaSuccess;
+        p = nullptr;
+        return e != cudaSuccess ? e : ef;
+    }
+};
+
+cudaError_t begin_call(Call *call, int dtype, gbce_stream_t stream)
+{
+    call->dtype = dtype;
+    call->stream = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = cudaGetDevice(&call->device);
+    if (e != cudaSuccess)
+        return e;
+    call->sms = current_sm_count();
+    return call->sms < 2 ? cudaErrorInvalidDevice : cudaSuccess;
+}
+
+}  // namespace
+}  // namespace gbce
+
+extern "C" int linear_ce_fwd(const void *hidden, int64_t hidden_stride, const void *weight,
+                             int64_t weight_stride, const int64_t *targets, float *loss,
+                             float *row_loss, float *lse, int64_t M, int64_t K, int64_t V,
+                             int64_t ignore_index, int dtype, int reduction, gbce_stream_t stream)
+{
+    int st = check_head(hidden, hidden_stride, weight, weight_stride, M, K, V, dtype);
+    if (st)
+        return st;
+    if (reduction != GBCE_MEAN && reduction != GBCE_SUM && reduction != GBCE_NONE)
+        return GBCE_ERR_REDUCTION;
+    if ((reduction != GBCE_NONE && !loss) || (M > 0 && (!targets || !row_loss)))
+        return GBCE_ERR_NULL;
+    if (!aligned_to(targets, 8) || !aligned_to(loss, 4) || !aligned_to(row_loss, 16) || !aligned_to(lse, 4))
+        return GBCE_ERR_ALIGN;
+    Call call;
+    cudaError_t e = begin_call(&call, dtype, stream);
+    if (e != cudaSuccess)
+        return map_error(e);
+    const HeadShape s = head_shape(call, hidden, hidden_stride, weight, weight_stride, M, K, V, HeadOp::Fwd);
+    Carver size(nullptr);
+    carve(size, s, HeadOp::Fwd, false);
+    PoolScratch scratch(call.stream);
+    if ((e = scratch.get(call.device, size.used)) != cudaSuccess)
+        return map_error(e);
+    Carver place(scratch.p);
+    const HeadScratch r = carve(place, s, HeadOp::Fwd, false);
+    PrepArgs prep{};
+    prep.targets = targets;
+    prep.M = M;
+    prep.V = V;
+    prep.ignore_index = ignore_index;
+    prep.n_out = r.n;
+    prep.rows_out = r.rows;
+    prep.fail = r.fail;
+    prep.idx = r.idx;
+    prep.tgt = r.tgt;
+    prep.reduction = reduction;
+    prep.loss = loss;
+    prep.row_loss = row_loss;
+    prep.lse_out = lse;
+    return map_error(scratch.release(
+        launch_linear_fwd(call, s, r, hidden, hidden_stride, weight, weight_stride, prep)));
+}
+
+extern "C" int linear_ce_bwd(const void *hidden, int64_t hidden_stride, const void *weight,
+                             int64_t weight_stride, const int64_t *targets, const float *lse,
+                             const float *grad_scale, void *d_hidden, int64_t d_hidden_stride,
+                             void *d_weight, int64_t d_weight_stride, int64_t M, int64_t K, int64_t V,
+                             int64_t ignore_index, int dtype, int reduction, gbce_stream_t stream)
+{
+    int st = check_head(hidden, hidden_stride, weight, weight_stride, M, K, V, dtype);
+    if (st)
+        return st;
+    if (reduction != GBCE_MEAN && reduction != GBCE_SUM && reduction != GBCE_NONE)
+        return GBCE_ERR_REDUCTION;
+    if ((!d_hidden && !d_weight && M > 0) || (M > 0 && (!targets || !lse)))
+        return GBCE_ERR_NULL;
+    if (d_hidden && (st = check_matrix(d_hidden, d_hidden_stride, M, K, dtype)))
+        return st;
+    if (d_weight && (st = check_matrix(d_weight, d_weight_stride, V, K, dtype)))
+        return st;
+    if (!aligned_to(targets, 8) || !aligned_to(lse, 4) || !aligned_to(grad_scale, 4))
+        return GBCE_ERR_ALIGN;
+    if (M == 0 && !d_weight)
+        return GBCE_OK;
+    Call call;
+    cudaError_t e = begin_call(&call, dtype, stream);
+    if (e != cudaSuccess)
+        return map_error(e);
+    // M == 0 leaves the weights' gradient: zeros, by the same path with no row listed
+    const HeadShape s = head_shape(call, hidden, hidden_stride, weight, weight_stride, M > 0 ? M : 1, K, V, HeadOp::Bwd);
+    Carver size(nullptr);
+    carve(size, s, HeadOp::Bwd, d_hidden != nullptr);
+    PoolScratch scratch(call.stream);
+    if ((e = scratch.get(call.device, size.used)) != cudaSuccess)
+        return map_error(e);
+    Carver place(scratch.p);
+    const HeadScratch r = carve(place, s, HeadOp::Bwd, d_hidden != nullptr);
+    PrepArgs prep{};
+    prep.targets = targets;
+    prep.M = M;
+    prep.V = V;
+    prep.ignore_index = ignore_index;
+    prep.n_out = r.n;
+    prep.rows_out = r.rows;
+    prep.fail = r.fail;
+    prep.idx = r.idx;
+    prep.tgt = r.tgt;
+    prep.reduction = reduction;
+    prep.lse_in = lse;
+    prep.grad_scale = grad_scale;
+    prep.l2 = r.l2;
+    prep.rs = r.rs;
+    prep.alpha = r.alpha;
+    prep.head = dtype == GBCE_F16 ? 16384.f : 1.f;
+    return map_error(scratch.release(launch_linear_bwd(call, s, r, hidden, hidden_stride, weight,
+                                                       weight_stride, M > 0 ? d_hidden : nullptr,
+                                                       d_hidden_stride, d_weight, d_weight_stride, prep)));
+}
+
+extern "C" int linear_greedy(const void *hidden, int64_t hidden_stride, const void *weight,
+                             int64_t weight_stride, int64_t *tokens, float *logprob, int64_t M,
+                             int64_t K, int64_t V, int dtype, gbce_stream_t stream)
+{
+    int st = check_head(hidden, hidden_stride, weight, weight_stride, M, K, V, dtype);
+    if (st)
+        return st;
+    if (M > 0 && (!tokens || !logprob))
+        return GBCE_ERR_NULL;
+    if (!aligned_to(tokens, 8) || !aligned_to(logprob, 4))
+        return GBCE_ERR_ALIGN;
+    if (M == 0)
+        return GBCE_OK;
+    Call call;
+    cudaError_t e = begin_call(&call, dtype, stream);
+    if (e != cudaSuccess)
+        return map_error(e);
+    const HeadShape s = head_shape(call, hidden, hidden_stride, weight, weight_stride, M, K, V, HeadOp::Greedy);
+    Carver size(nullptr);
+    carve(size, s, HeadOp::Greedy, false);
+    PoolScratch scratch(call.stream);
+    if ((e = scratch.get(call.device, size.used)) != cudaSuccess)
+        return map_error(e);
+    Carver place(scratch.p);
+    const HeadScratch r = carve(place, s, HeadOp::Greedy, false);
+    const void *w = weight, *h = hidden;
+    int64_t wstride = weight_stride, hstride = hidden_stride, hrows = M;
+    if (s.pack_h) {
+        e = pack_hidden(call, s, r, hidden, hidden_stride, nullptr, nullptr);
+        h = r.h;
+        hstride = s.kp;
+        hrows = s.mp;
+    }
+    if (e == cudaSuccess)
+        e = pack_weights(call, s, r, weight, weight_stride, &w, &wstride);
+    if (e == cudaSuccess) {
+        MergeArgs m{};
+        m.token = tokens;
+        m.logprob = logprob;
+        e = launch_head<true>(call, s, r, h, hstride, w, wstride, hrows, m);
+    }
+    return map_error(scratch.release(e));
+}

@@ -1,0 +1,894 @@
+// The output layer's loss without its logits: hidden states H [n, K] times
+// weights W [V, K] in tiles on the tensor cores, each tile's logits consumed
+// where they are made (tensor memory) and never written out.
+//
+//   forward   x = H W^T; per row the online (s, d) pair of the softmax over each
+//             256-column tile, merged over the tiles: lse = m + ln d, and the row
+//             loss lse - x_y (linear_ce_fwd); or the arg max and its
+//             log-probability (linear_greedy).
+//   backward  in pieces of the vocabulary: G = (exp(x - lse) - onehot) r from a
+//             second product (16-bit, the one rounding between the products),
+//             then dW_piece = G^T H, complete, and dH += G W_piece in fp32.
+//
+// pair_gemm_kernel does every product: pairs of CTAs (cta_group::2) on 256 x 256
+// tiles, one CTA holding 128 rows of A, 128 of B's 256 rows, and 128 x 256
+// sums.  A producer thread per CTA keeps a ring of 64-wide operand tiles filled
+// by TMA, one thread of the pair issues the matrix instructions, and four warps
+// per CTA empty one accumulator while the other one fills (2 x 256 columns, all
+// of tensor memory).  The 256 x 256 pair tile reads 64 KB per 2 x 16.8 MFLOP
+// k-step, half of what two 128 x 256 tiles would take from L2.
+//
+// skinny_kernel is the forward for at most 64 rows, where reading W once is the
+// whole cost: W's rows take the M side of the instruction, so a tile is 128
+// vocabulary rows of any number of hidden states, and each CTA streams its own
+// contiguous share of W (in units of 16 rows, so that shares differ by 16 rows
+// at most) through a 200 KB ring.
+//
+// Rows whose target is ignore_index take part in nothing: lin_prep_kernel lists
+// the others in order and lin_gather_kernel packs their hidden states (zeros up
+// to the next multiple of 256 rows), so the products run over counted rows only.
+#pragma once
+
+#include "row_kernels.cuh"
+#include "tensor.cuh"
+
+namespace gbce {
+
+constexpr int kPairM = 256, kPairN = 256, kPairK = 64;  // tile of a CTA pair
+constexpr int kPairStages = 6;
+constexpr int kPairStageBytes = 2 * 128 * kPairK * 2;   // per CTA: 128 rows of A and of B
+constexpr int kPairThreads = 256;
+constexpr int kPairSmem = kPairStages * kPairStageBytes + 1024;
+constexpr int kBand = 8;                                // tiles of M that share a sweep over N
+
+enum class Epi { Stats, Greedy, Grad, Weight, Hidden };
+
+struct PairArgs {
+    CUtensorMap a, b;
+    const int *n_ptr;   // counted rows (device), NULL: n_host
+    int n_host;
+    int tiles_m;        // Weight: tiles of the piece; else from n
+    int tiles_n;
+    int kblocks;        // 64-wide steps along K; Weight: from n
+    int b_row0;         // first row of B along the axis of W's rows (piece offset)
+    unsigned *fail;
+    // Stats, Greedy
+    float2 *part;       // [tiles_n][ldp] (s, d) pairs
+    int *part_idx;      // Greedy: the arg max of each
+    float *xy;          // Stats: the target's logit
+    int64_t ldp;
+    const int *tgt;
+    int64_t V;          // columns of this launch's logits (vocabulary, or end of it) from row 0 of W
+    // Grad
+    const float *l2, *rs;
+    void *g;
+    int64_t ldg;
+    // Weight, Hidden
+    const float *alpha;
+    void *out;
+    int64_t ldo;
+    int64_t rows, cols; // valid rows (Weight) and columns of out
+    int vec;            // out allows 16-byte stores
+    const int *idx;     // Hidden: the row of out that a packed row belongs to
+    float *acc;         // Hidden: fp32 sums over pieces, [.., lda]
+    int64_t lda;
+    int first, last;    // Hidden: the first piece does not read acc, the last one writes out
+};
+
+__device__ __forceinline__ void tile_at(int t, int tiles_m, int tiles_n, int &m, int &n)
+{
+    const int band = t / (kBand * tiles_n);
+    const int r = t - band * kBand * tiles_n;
+    const int rows = min(kBand, tiles_m - band * kBand);
+    n = r / rows;
+    m = band * kBand + (r - n * rows);
+}
+
+// exp2 shift of a maximum, finite for an empty part.
+__device__ __forceinline__ float finite_shift(float m) { return m == -INFINITY ? 0.f : shift_of(m); }
+
+// A sum about the maximum `from`, about the larger maximum `to`.  An empty part
+// (-inf) holds 0, or a NaN that has to stay.
+__device__ __forceinline__ float rescaled(float d, float from, float to)
+{
+    return from == -INFINITY ? d : d * exp2f(shift_of(from) - shift_of(to));
+}
+
+// 32 logits of one row, columns c0 .. c0 + 31 of W's rows, into the running
+// maximum m and sum d = sum exp2(x log2e - fl(m log2e)).
+template <bool GREEDY>
+__device__ __forceinline__ void stats_chunk(const uint32_t (&r)[32], int c0, int limit, float &m,
+                                            float &d, int &best)
+{
+    float x[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        x[i] = c0 + i < limit ? __uint_as_float(r[i]) : -INFINITY;
+    float mc = x[0];
+#pragma unroll
+    for (int i = 1; i < 32; ++i)
+        mc = fmaxf(mc, x[i]);
+    if (mc > m) {
+        d = rescaled(d, m, mc);
+        m = mc;
+        if constexpr (GREEDY) {
+            int at = 31;
+#pragma unroll
+            for (int i = 31; i >= 0; --i)
+                at = x[i] == mc ? i : at;
+            best = c0 + at;
+        }
+    }
+    const float s = finite_shift(m);
+    float d0 = 0.f, d1 = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+        d0 += exp2_shift(x[i], s);
+        d1 += exp2_shift(x[i + 1], s);
+    }
+    d += d0 + d1;
+}
+
+// 32 values times alpha, rounded once, to out[row, c0 ..] below `cols`.
+template <typename T>
+__device__ __forceinline__ void store_chunk(T *row, int64_t c0, int64_t cols, const float (&f)[32],
+                                            int vec)
+{
+    if (vec && c0 + 32 <= cols) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float *p = f + 8 * q;
+            *reinterpret_cast<uint4 *>(row + c0 + 8 * q) =
+                make_uint4(Elem<T>::pack2(p[0], p[1]), Elem<T>::pack2(p[2], p[3]),
+                           Elem<T>::pack2(p[4], p[5]), Elem<T>::pack2(p[6], p[7]));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (c0 + i < cols)
+                Elem<T>::store(row + c0 + i, f[i]);
+    }
+}
+
+template <Epi E, typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    pair_gemm_kernel(const __grid_constant__ PairArgs a)
+{
+    constexpr bool A_MN = E == Epi::Weight;
+    constexpr bool B_MN = E == Epi::Weight || E == Epi::Hidden;
+    constexpr uint32_t kIdesc =
+        mma_idesc(std::is_same<T, __nv_bfloat16>::value, A_MN, B_MN, kPairM, kPairN);
+
+    extern __shared__ unsigned char dyn[];
+    __shared__ __align__(8) uint64_t bars[2 * kPairStages + 4];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int dead_word;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    volatile int *dead = &dead_word;
+    const uint32_t ring = (smem_addr(dyn) + 1023u) & ~1023u;
+    const uint32_t full = smem_addr(bars), empty = full + 8 * kPairStages;
+    const uint32_t tfull = empty + 8 * kPairStages, tempty = tfull + 16;
+
+    const int n = a.n_ptr ? *a.n_ptr : a.n_host;
+    const int tiles_m = E == Epi::Weight ? a.tiles_m : (n + kPairM - 1) / kPairM;
+    const int kblocks = E == Epi::Weight ? (n + kPairK - 1) / kPairK : a.kblocks;
+    const int tiles = tiles_m * a.tiles_n;
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        dead_word = 0;
+        for (int i = 0; i < kPairStages; ++i) {
+            mbar_init(full + 8 * i, 1);   // the leader's expect_tx; both CTAs' bytes count on it
+            mbar_init(empty + 8 * i, 1);  // the commit of the instructions that read the slot
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(tfull + 8 * i, 1);
+            mbar_init(tempty + 8 * i, 8);  // four warps of each CTA
+        }
+        fence_barrier_init();
+        prefetch_map(&a.a);
+        prefetch_map(&a.b);
+    }
+    if (warp == 2)
+        tmem_alloc<2>(smem_addr(&tmem_slot), 512);
+    tc_fence_before();
+    __syncthreads();
+    cluster_arrive();
+    cluster_wait();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+
+    if (warp == 0 && lane == 0) {
+        // producer: this CTA's halves of A and B
+        const uint32_t full0 = map_to_rank(full, 0);
+        int slot = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int t = pair; t < tiles && ok; t += pairs) {
+            int tm, tn;
+            tile_at(t, tiles_m, a.tiles_n, tm, tn);
+            const int am = tm * kPairM + static_cast<int>(rank) * 128;
+            const int bn = tn * kPairN + static_cast<int>(rank) * 128;
+            for (int kb = 0; kb < kblocks; ++kb) {
+                if (!(ok = bar_wait_cluster(empty + 8 * slot, phase ^ 1, dead)))
+                    break;
+                if (rank == 0)
+                    mbar_arrive_expect_tx(full + 8 * slot, 2 * kPairStageBytes);
+                const uint32_t sa = ring + slot * kPairStageBytes, sb = sa + kPairStageBytes / 2;
+                const uint32_t bar = full0 + 8 * slot;
+                const int k0 = kb * kPairK;
+                if constexpr (A_MN) {
+                    tma_load_pair(sa, &a.a, am, k0, bar);
+                    tma_load_pair(sa + 8192, &a.a, am + 64, k0, bar);
+                } else {
+                    tma_load_pair(sa, &a.a, k0, am, bar);
+                }
+                if constexpr (B_MN) {
+                    const int kr = E == Epi::Hidden ? a.b_row0 + k0 : k0;
+                    tma_load_pair(sb, &a.b, bn, kr, bar);
+                    tma_load_pair(sb + 8192, &a.b, bn + 64, kr, bar);
+                } else {
+                    tma_load_pair(sb, &a.b, k0, a.b_row0 + bn, bar);
+                }
+                if (++slot == kPairStages) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        // the pair's matrix instructions
+        int slot = 0, it = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int t = pair; t < tiles && ok; t += pairs, ++it) {
+            const int acc = it & 1;
+            if (!(ok = bar_wait_cluster(tempty + 8 * acc, ((it >> 1) & 1) ^ 1, dead)))
+                break;
+            tc_fence_after();
+            for (int kb = 0; kb < kblocks; ++kb) {
+                if (!(ok = bar_wait_cluster(full + 8 * slot, phase, dead)))
+                    break;
+                tc_fence_after();
+                const uint32_t sa = ring + slot * kPairStageBytes, sb = sa + kPairStageBytes / 2;
+                const uint64_t da = smem_desc(sa, A_MN ? 8192 : 16, 1024);
+                const uint64_t db = smem_desc(sb, B_MN ? 8192 : 16, 1024);
+#pragma unroll
+                for (int k = 0; k < kPairK / 16; ++k)  // 16 of K: 32 bytes, or 16 rows of 128 bytes
+                    mma_f16<2>(tmem + acc * kPairN, da + k * (A_MN ? 128 : 2),
+                               db + k * (B_MN ? 128 : 2), kIdesc, (kb | k) != 0);
+                mma_commit_pair(empty + 8 * slot);
+                if (++slot == kPairStages) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+            }
+            if (ok)
+                mma_commit_pair(tfull + 8 * acc);
+        }
+    } else if (warp >= 4) {
+        // epilogue: thread = one row of this CTA's 128, all 256 columns
+        const int ew = warp & 3;
+        const uint32_t tempty0 = map_to_rank(tempty, 0);
+        float alpha = 1.f;
+        if constexpr (E == Epi::Weight || E == Epi::Hidden)
+            alpha = __ldg(a.alpha);
+        int it = 0;
+        for (int t = pair; t < tiles; t += pairs, ++it) {
+            int tm, tn;
+            tile_at(t, tiles_m, a.tiles_n, tm, tn);
+            const int acc = it & 1;
+            const int row = tm * kPairM + static_cast<int>(rank) * 128 + ew * 32 + lane;
+            const int c0 = tn * kPairN;
+            if (!bar_wait_cluster(tfull + 8 * acc, (it >> 1) & 1, dead))
+                break;
+            tc_fence_after();
+            const uint32_t src = tmem + acc * kPairN + (static_cast<uint32_t>(ew * 32) << 16);
+            uint32_t buf[2][32];
+            tmem_ld32(src, buf[0]);
+            tmem_wait_ld(buf[0]);
+
+            [[maybe_unused]] float m = -INFINITY, d = 0.f;
+            [[maybe_unused]] int best = 0, y = -1;
+            [[maybe_unused]] float l2 = 0.f, rs = 0.f;
+            [[maybe_unused]] int64_t out_row = -1;
+            const bool live = row < n;
+            if constexpr (E == Epi::Stats || E == Epi::Grad)
+                y = live ? __ldg(a.tgt + row) - a.b_row0 : -1;
+            if constexpr (E == Epi::Grad)
+                if (live) {
+                    l2 = __ldg(a.l2 + row);
+                    rs = __ldg(a.rs + row);
+                }
+            if constexpr (E == Epi::Hidden)
+                if (live)
+                    out_row = a.last ? __ldg(a.idx + row) : row;
+            const int limit = static_cast<int>(min(a.V, static_cast<int64_t>(INT32_MAX)));
+#pragma unroll
+            for (int c = 0; c < kPairN / 32; ++c) {
+                uint32_t(&r)[32] = buf[c & 1];
+                if (c + 1 < kPairN / 32)
+                    tmem_ld32(src + 32 * (c + 1), buf[(c + 1) & 1]);
+                const int col = c0 + 32 * c;
+                if constexpr (E == Epi::Stats || E == Epi::Greedy) {
+                    stats_chunk<E == Epi::Greedy>(r, col, limit, m, d, best);
+                    if constexpr (E == Epi::Stats)
+                        if (y >= col && y < col + 32) {
+                            float v = 0.f;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                v = y == col + i ? __uint_as_float(r[i]) : v;
+                            a.xy[row] = v;
+                        }
+                } else if constexpr (E == Epi::Grad) {
+                    float f[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float p = exp2_shift(__uint_as_float(r[i]), l2);
+                        f[i] = (live && col + i < limit) ? fmaf(p, rs, y == col + i ? -rs : 0.f) : 0.f;
+                    }
+                    store_chunk<T>(static_cast<T *>(a.g) + row * a.ldg, col, a.ldg, f, 1);
+                } else if constexpr (E == Epi::Weight) {
+                    if (row < a.rows) {
+                        float f[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            f[i] = kblocks ? __uint_as_float(r[i]) * alpha : 0.f;
+                        store_chunk<T>(static_cast<T *>(a.out) + row * a.ldo, col, a.cols, f, a.vec);
+                    }
+                } else {
+                    if (live && col < a.cols) {
+                        float f[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            f[i] = __uint_as_float(r[i]);
+                        float4 *acc4 = reinterpret_cast<float4 *>(a.acc + row * a.lda + col);
+                        if (!a.first) {
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) {
+                                const float4 o = acc4[q];
+                                f[4 * q] += o.x;
+                                f[4 * q + 1] += o.y;
+                                f[4 * q + 2] += o.z;
+                                f[4 * q + 3] += o.w;
+                            }
+                        }
+                        if (a.last) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                f[i] *= alpha;
+                            store_chunk<T>(static_cast<T *>(a.out) + out_row * a.ldo, col, a.cols, f, a.vec);
+                        } else {
+#pragma unroll
+                            for (int q = 0; q < 8; ++q)
+                                acc4[q] = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
+                        }
+                    }
+                }
+                if (c + 1 < kPairN / 32)
+                    tmem_wait_ld(buf[(c + 1) & 1]);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                bar_arrive_cluster(tempty0 + 8 * acc);
+            if constexpr (E == Epi::Stats || E == Epi::Greedy)
+                if (live) {
+                    a.part[tn * a.ldp + row] = make_float2(m == -INFINITY ? m : shift_of(m), d);
+                    if constexpr (E == Epi::Greedy) {
+                        a.part_idx[tn * a.ldp + row] = best;
+                        // the maximum itself is needed beside its shift
+                        a.xy[tn * a.ldp + row] = m;
+                    }
+                }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (*dead) {
+        if (threadIdx.x == 0)
+            raise_timeout(a.fail);
+        settle_after_failure();
+    }
+    cluster_arrive();
+    cluster_wait();
+    if (warp == 2)
+        tmem_free<2>(tmem, 512);
+}
+
+// ---------------------------------------------------------------------------
+// at most 64 rows: W streamed once, its rows on the M side
+
+constexpr int kSkinnyStageW = 128 * 64 * 2;
+constexpr int kSkinnyUnit = 16;  // rows of W that the CTAs' shares are counted in
+
+template <int NG>
+__host__ __device__ constexpr int skinny_stage_bytes() { return kSkinnyStageW + NG * 32 * 128; }
+template <int NG>
+__host__ __device__ constexpr int skinny_stages() { return NG == 1 ? 10 : 8; }
+template <int NG>
+__host__ __device__ constexpr int skinny_smem() { return skinny_stages<NG>() * skinny_stage_bytes<NG>() + 1024; }
+template <int NG>
+__host__ __device__ constexpr int skinny_threads() { return 128 + NG * 128; }
+
+struct SkinnyArgs {
+    CUtensorMap w, wu;  // W in boxes of 128 and of 16 rows
+    CUtensorMap h;      // hidden states in boxes of 32 NG rows
+    const int *n_ptr;
+    int n_host;
+    int kblocks;
+    int64_t V;
+    const int *tgt;
+    float2 *part;       // [gridDim.x][ldp]
+    int *part_idx;
+    float *part_max;
+    float *xy;
+    int64_t ldp;
+    unsigned *fail;
+    uint32_t bf16;
+};
+
+// Merge of two (m, d, index) triples with shifts fl(m log2e): the larger
+// maximum, the lower index of equal ones.
+__device__ __forceinline__ void mdi_merge(float &m, float &d, int &i, float m2, float d2, int i2)
+{
+    if (m2 > m || (m2 == m && i2 < i))
+        i = i2;
+    const float mn = fmaxf(m, m2);
+    d = rescaled(d, m, mn) + rescaled(d2, m2, mn);
+    m = mn;
+}
+
+template <int NG, bool GREEDY>
+__global__ void __launch_bounds__(skinny_threads<NG>(), 1) skinny_kernel(const __grid_constant__ SkinnyArgs a)
+{
+    constexpr int kStages = skinny_stages<NG>();
+    constexpr int kStage = skinny_stage_bytes<NG>();
+    constexpr int kN = 32 * NG;
+    constexpr uint32_t kCols = 2 * kN;
+
+    extern __shared__ unsigned char dyn[];
+    __shared__ __align__(8) uint64_t bars[2 * kStages + 4];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int dead_word;
+    __shared__ int tgt[kN];
+    __shared__ float sm[NG * 4][32], sd[NG * 4][32];
+    __shared__ int si[NG * 4][32];
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile int *dead = &dead_word;
+    const uint32_t ring = (smem_addr(dyn) + 1023u) & ~1023u;
+    const uint32_t full = smem_addr(bars), empty = full + 8 * kStages;
+    const uint32_t tfull = empty + 8 * kStages, tempty = tfull + 16;
+    const uint32_t idesc = a.bf16 ? mma_idesc(true, false, false, 128, kN) : mma_idesc(false, false, false, 128, kN);
+
+    const int n = a.n_ptr ? *a.n_ptr : a.n_host;
+    const int64_t units = (a.V + kSkinnyUnit - 1) / kSkinnyUnit;
+    const int64_t v0 = units * blockIdx.x / gridDim.x * kSkinnyUnit;
+    const int64_t v1 = min(units * (blockIdx.x + 1) / gridDim.x * kSkinnyUnit, a.V);
+    const int tiles = n > 0 ? static_cast<int>((v1 - v0 + 127) / 128) : 0;
+
+    if (threadIdx.x == 0) {
+        dead_word = 0;
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(tfull + 8 * i, 1);
+            mbar_init(tempty + 8 * i, 4 * NG);
+        }
+        fence_barrier_init();
+        prefetch_map(&a.w);
+        prefetch_map(&a.wu);
+        prefetch_map(&a.h);
+    }
+    if (!GREEDY && threadIdx.x < kN)
+        tgt[threadIdx.x] = static_cast<int>(threadIdx.x) < n ? __ldg(a.tgt + threadIdx.x) : -1;
+    if (warp == 2)
+        tmem_alloc<1>(smem_addr(&tmem_slot), kCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+
+    if (warp == 0 && lane == 0) {
+        const uint64_t once = policy_evict_first(), again = policy_evict_last();
+        int slot = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int t = 0; t < tiles && ok; ++t) {
+            const int64_t row = v0 + 128 * t;
+            const int rows = static_cast<int>(min(v1 - row, int64_t{128}));
+            const int nunit = (rows + kSkinnyUnit - 1) / kSkinnyUnit;
+            for (int kb = 0; kb < a.kblocks; ++kb) {
+                if (!(ok = bar_wait(empty + 8 * slot, phase ^ 1, dead)))
+                    break;
+                const uint32_t sw = ring + slot * kStage, sh = sw + kSkinnyStageW;
+                const uint32_t bar = full + 8 * slot;
+                mbar_arrive_expect_tx(bar, nunit * kSkinnyUnit * 128 + kN * 128);
+                if (nunit == 8) {
+                    tma_load(sw, &a.w, kb * 64, static_cast<int>(row), bar, once);
+                } else {
+                    for (int u = 0; u < nunit; ++u)
+                        tma_load(sw + u * kSkinnyUnit * 128, &a.wu, kb * 64,
+                                 static_cast<int>(row) + u * kSkinnyUnit, bar, once);
+                }
+                tma_load(sh, &a.h, kb * 64, 0, bar, again);
+                if (++slot == kStages) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+    } else if (warp == 1 && lane == 0) {
+        int slot = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int t = 0; t < tiles && ok; ++t) {
+            const int acc = t & 1;
+            if (!(ok = bar_wait(tempty + 8 * acc, ((t >> 1) & 1) ^ 1, dead)))
+                break;
+            tc_fence_after();
+            for (int kb = 0; kb < a.kblocks; ++kb) {
+                if (!(ok = bar_wait(full + 8 * slot, phase, dead)))
+                    break;
+                tc_fence_after();
+                const uint32_t sw = ring + slot * kStage;
+                const uint64_t da = smem_desc(sw, 16, 1024), db = smem_desc(sw + kSkinnyStageW, 16, 1024);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_f16<1>(tmem + acc * kN, da + 2 * k, db + 2 * k, idesc, (kb | k) != 0);
+                mma_commit(empty + 8 * slot);
+                if (++slot == kStages) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+            }
+            if (ok)
+                mma_commit(tfull + 8 * acc);
+        }
+    } else if (warp >= 4) {
+        // lane = a vocabulary row, column = a hidden state; each thread keeps the
+        // running (m, d, index) of its vocabulary rows for 32 hidden states
+        const int ew = warp & 3, group = (warp - 4) >> 2;
+        float m[32], d[32];
+        int best[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            m[j] = -INFINITY;
+            d[j] = 0.f;
+            best[j] = INT32_MAX;
+        }
+        const int live = min(max(n - 32 * group, 0), 32);
+        for (int t = 0; t < tiles; ++t) {
+            const int acc = t & 1;
+            if (!bar_wait(tfull + 8 * acc, (t >> 1) & 1, dead))
+                break;
+            tc_fence_after();
+            uint32_t r[32];
+            tmem_ld32(tmem + acc * kN + 32 * group + (static_cast<uint32_t>(ew * 32) << 16), r);
+            tmem_wait_ld(r);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                bar_arrive(tempty + 8 * acc);
+            const int64_t v = v0 + 128 * t + ew * 32 + lane;
+            if (v < v1) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    if (j < live) {
+                        const float x = __uint_as_float(r[j]);
+                        if (x > m[j]) {
+                            d[j] = rescaled(d[j], m[j], x);
+                            m[j] = x;
+                            best[j] = static_cast<int>(v);
+                        }
+                        d[j] += exp2_shift(x, finite_shift(m[j]));
+                        if (!GREEDY && tgt[32 * group + j] == v)
+                            a.xy[32 * group + j] = x;
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            if (j < live) {
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) {
+                    const float m2 = __shfl_xor_sync(0xffffffffu, m[j], off);
+                    const float d2 = __shfl_xor_sync(0xffffffffu, d[j], off);
+                    const int i2 = __shfl_xor_sync(0xffffffffu, best[j], off);
+                    mdi_merge(m[j], d[j], best[j], m2, d2, i2);
+                }
+                if (lane == 0) {
+                    sm[warp - 4][j] = m[j];
+                    sd[warp - 4][j] = d[j];
+                    si[warp - 4][j] = best[j];
+                }
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (*dead) {
+        if (threadIdx.x == 0)
+            raise_timeout(a.fail);
+        settle_after_failure();
+    }
+    if (warp == 2)
+        tmem_free<1>(tmem, kCols);
+    if (static_cast<int>(threadIdx.x) < min(n, kN)) {
+        const int g = threadIdx.x >> 5, j = threadIdx.x & 31;
+        float m = sm[4 * g][j], d = sd[4 * g][j];
+        int best = si[4 * g][j];
+#pragma unroll
+        for (int q = 1; q < 4; ++q)
+            mdi_merge(m, d, best, sm[4 * g + q][j], sd[4 * g + q][j], si[4 * g + q][j]);
+        const int64_t at = blockIdx.x * a.ldp + threadIdx.x;
+        a.part[at] = make_float2(m == -INFINITY ? m : shift_of(m), d);
+        if (GREEDY) {
+            a.part_idx[at] = best;
+            a.part_max[at] = m;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// the rows that count, in order; their targets, shifts and factors
+
+struct PrepArgs {
+    const int64_t *targets;
+    int64_t M, V, ignore_index;
+    int *n_out;      // targets that are not ignore_index (the divisor of the mean)
+    int *rows_out;   // rows listed: those with a target in [0, V)
+    unsigned *fail;
+    int *idx, *tgt;
+    int reduction;
+    // forward: the values of the rows not listed, and of an empty batch
+    float *loss, *row_loss, *lse_out;
+    // backward
+    const float *lse_in, *grad_scale;
+    float *l2, *rs, *alpha;
+    float head;      // power of two that keeps 16-bit G in range (fp16: 2^14)
+};
+
+template <int NT, bool BWD>
+__global__ void __launch_bounds__(NT) lin_prep_kernel(const PrepArgs a)
+{
+    __shared__ int warp_rows[NT / 32], warp_n[NT / 32];
+    __shared__ float warp_max[NT / 32];
+    __shared__ int any_bad;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0)
+        any_bad = 0;
+    __syncthreads();
+    // each warp owns a contiguous range of rows: counts first, then the list
+    const int64_t per = ((a.M + NT - 1) / NT) * 32;
+    const int64_t lo = min(per * warp, a.M), hi = min(lo + per, a.M);
+    int rows = 0, n = 0;
+    float top = 0.f;
+    bool bad = false;
+#pragma unroll 4
+    for (int64_t i = lo + lane; i < hi; i += 32) {
+        const int64_t y = __ldg(a.targets + i);
+        if (y != a.ignore_index) {
+            ++n;
+            if (y >= 0 && y < a.V) {
+                ++rows;
+                if (BWD && a.grad_scale) {
+                    const float g = fabsf(__ldg(a.grad_scale + (a.reduction == kReduceNone ? i : 0)));
+                    top = g > top ? g : top;  // a NaN factor leaves the scale alone
+                }
+            } else {
+                bad = true;
+            }
+        }
+    }
+    if (bad)
+        any_bad = 1;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        rows += __shfl_xor_sync(0xffffffffu, rows, off);
+        n += __shfl_xor_sync(0xffffffffu, n, off);
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    }
+    if (lane == 0) {
+        warp_rows[warp] = rows;
+        warp_n[warp] = n;
+        warp_max[warp] = top;
+    }
+    __syncthreads();
+    int at = 0, total = 0, n_all = 0;
+    top = 0.f;
+    for (int w = 0; w < NT / 32; ++w) {
+        at += w < warp ? warp_rows[w] : 0;
+        total += warp_rows[w];
+        n_all += warp_n[w];
+        top = fmaxf(top, warp_max[w]);
+    }
+    // factors relative to a power of two at or above the largest, so that their
+    // 16-bit products with (p - onehot) stay in range whatever the loss scale
+    float inv = 1.f;
+    if (BWD) {
+        int e = 0;
+        if (a.grad_scale && top > 0.f && top < INFINITY)
+            frexpf(top, &e);
+        e = min(max(e, -100), 127);
+        inv = ldexpf(a.head, -e);
+        if (threadIdx.x == 0)
+            *a.alpha = (a.reduction == kReduceMean ? 1.f / static_cast<float>(n_all) : 1.f) *
+                       ldexpf(1.f / a.head, e);
+    }
+    if (threadIdx.x == 0) {
+        *a.n_out = n_all;
+        *a.rows_out = total;
+        *a.fail = 0u;
+        if (any_bad)
+            atomicOr(&g_flags, kFlagBadTarget);
+        if (!BWD && a.M == 0 && a.reduction != kReduceNone)
+            *a.loss = a.reduction == kReduceMean ? __int_as_float(0x7fc00000) : 0.f;
+    }
+    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
+        const int64_t i = i0 + lane;
+        const int64_t y = i < hi ? __ldg(a.targets + i) : a.ignore_index;
+        const bool skip = y == a.ignore_index;
+        const bool listed = !skip && y >= 0 && y < a.V;
+        const unsigned votes = __ballot_sync(0xffffffffu, listed);
+        if (listed) {
+            const int pos = at + __popc(votes & ((1u << lane) - 1));
+            a.idx[pos] = static_cast<int>(i);
+            a.tgt[pos] = static_cast<int>(y);
+            if (BWD) {
+                a.l2[pos] = __ldg(a.lse_in + i) * kLog2e;
+                a.rs[pos] = (a.grad_scale ? __ldg(a.grad_scale + (a.reduction == kReduceNone ? i : 0)) : 1.f) * inv;
+            }
+        } else if (!BWD && i < hi) {
+            const float v = skip ? 0.f : __int_as_float(0x7fc00000);
+            a.row_loss[i] = v;
+            if (a.lse_out)
+                a.lse_out[i] = v;
+        }
+        at += __popc(votes);
+    }
+}
+
+// Packed copy of the listed rows (dst [.., lds], zeros in columns K .. lds and in
+// the rows up to the next multiple of `pad`), and zeros in the rows of `zero`
+// that are not listed.  One CTA per row at a time.
+struct GatherArgs {
+    const void *src;
+    int64_t ss;
+    void *dst;
+    int64_t lds;
+    const int *idx;     // NULL: rows as they stand
+    const int *n_ptr;
+    int64_t n_host;
+    int64_t K;
+    int pad;
+    int vec;            // src allows 16-byte loads
+    // backward: unlisted rows of the hidden gradient
+    void *zero;
+    int64_t zs;
+    int64_t M, V, ignore_index;
+    const int64_t *targets;
+};
+
+template <int NT>
+__global__ void __launch_bounds__(NT) lin_gather_kernel(const GatherArgs a)
+{
+    const int64_t n = a.n_ptr ? *a.n_ptr : a.n_host;
+    const int64_t rows = (n + a.pad - 1) / a.pad * a.pad;
+    for (int64_t i = blockIdx.x; i < rows; i += gridDim.x) {
+        unsigned short *d = static_cast<unsigned short *>(a.dst) + i * a.lds;
+        if (i >= n) {
+            for (int64_t j = threadIdx.x; j < a.lds / 8; j += NT)
+                reinterpret_cast<uint4 *>(d)[j] = make_uint4(0, 0, 0, 0);
+            continue;
+        }
+        const unsigned short *s = static_cast<const unsigned short *>(a.src) +
+                                  (a.idx ? static_cast<int64_t>(a.idx[i]) : i) * a.ss;
+        if (a.vec) {  // K may end inside the last vector: the rest is zeroed one by one
+            const int64_t nv = a.K / 8;
+            for (int64_t j = threadIdx.x; j < nv; j += NT)
+                reinterpret_cast<uint4 *>(d)[j] = __ldg(reinterpret_cast<const uint4 *>(s) + j);
+            for (int64_t j = nv * 8 + threadIdx.x; j < a.lds; j += NT)
+                d[j] = j < a.K ? s[j] : 0;
+        } else {
+            for (int64_t j = threadIdx.x; j < a.lds; j += NT)
+                d[j] = j < a.K ? s[j] : 0;
+        }
+    }
+    if (a.zero)
+        for (int64_t i = blockIdx.x; i < a.M; i += gridDim.x) {
+            const int64_t y = a.targets[i];
+            if (y != a.ignore_index && y >= 0 && y < a.V)
+                continue;
+            unsigned short *z = static_cast<unsigned short *>(a.zero) + i * a.zs;
+            for (int64_t j = threadIdx.x; j < a.K; j += NT)
+                z[j] = 0;
+        }
+}
+
+// ---------------------------------------------------------------------------
+// the partial pairs of each row, merged in order
+
+struct MergeArgs {
+    const float2 *part;
+    const int *part_idx;
+    const float *part_max;
+    int parts;
+    int64_t ldp;
+    const int *n_ptr;
+    int n_host;
+    const int *idx;
+    const float *xy;
+    float *row_loss, *lse;
+    int64_t *token;
+    float *logprob;
+};
+
+// 32 rows x 8 shares of the partials per CTA.
+template <bool GREEDY>
+__global__ void __launch_bounds__(256) lin_merge_kernel(const MergeArgs a)
+{
+    __shared__ float ss[8][32], sd[8][32], sx[8][32];
+    __shared__ int si[8][32];
+    const int n = a.n_ptr ? *a.n_ptr : a.n_host;
+    const int lane = threadIdx.x & 31, share = threadIdx.x >> 5;
+    const int64_t row = blockIdx.x * int64_t{32} + lane;
+    if (blockIdx.x * int64_t{32} >= n)
+        return;
+    float s = -INFINITY, d = 0.f, top = -INFINITY;
+    int best = INT32_MAX;
+    if (row < n) {
+        const int lo = a.parts * share / 8, hi = a.parts * (share + 1) / 8;
+#pragma unroll 4
+        for (int p = lo; p < hi; ++p) {
+            const float2 q = a.part[p * a.ldp + row];
+            if (q.x == -INFINITY && q.y != 0.f)
+                d += q.y;  // a NaN among nothing but -inf
+            md_merge(s, d, q.x, q.y);
+            if (GREEDY) {
+                const float x = a.part_max[p * a.ldp + row];
+                if (x > top) {
+                    top = x;
+                    best = a.part_idx[p * a.ldp + row];
+                }
+            }
+        }
+    }
+    ss[share][lane] = s;
+    sd[share][lane] = d;
+    if (GREEDY) {
+        sx[share][lane] = top;
+        si[share][lane] = best;
+    }
+    __syncthreads();
+    if (share == 0 && row < n) {
+        for (int q = 1; q < 8; ++q) {
+            if (ss[q][lane] == -INFINITY && sd[q][lane] != 0.f)
+                d += sd[q][lane];
+            md_merge(s, d, ss[q][lane], sd[q][lane]);
+            if (GREEDY && sx[q][lane] > top) {
+                top = sx[q][lane];
+                best = si[q][lane];
+            }
+        }
+        if (GREEDY) {
+            a.token[row] = best == INT32_MAX ? 0 : best;
+            a.logprob[row] = -row_loss_from(s, d, top);
+        } else {
+            const int64_t out = a.idx[row];
+            a.row_loss[out] = row_loss_from(s, d, a.xy[row]);
+            if (a.lse)
+                a.lse[out] = fmaf(s, kLn2, logf(d));
+        }
+    }
+}
+
+}  // namespace gbce

@@ -1,0 +1,335 @@
+// A router's balance loss and z-loss with per-expert counts and the gradient
+// of its logits x [T, E], the experts each token was sent to given.
+//
+// With f_e the number of slots that chose expert e, n the counted tokens, k
+// slots a token, p_t = softmax(x_t) and lse_t its log-sum-exp:
+//   L       = a E / (k n^2) sum_t sum_e f_e p_te + b / n sum_t lse_t^2
+//   dL/dx_te = p_te (a E / (k n^2) (f_e - sum_j p_tj f_j) + 2 b / n lse_t)
+// (the first term is a E sum_e (f_e / (k n)) mean_t p_te, 1 a when tokens are
+// spread evenly).  sum_j p_tj = 1, so any constant may be taken from f: the
+// kernels use f_e less its mean, which keeps the small difference of two large
+// counts out of the rounding.
+//
+// The counts need every token before the first gradient can be formed, but not
+// the logits: moe_count_kernel reads the choices (integer atomics, so the
+// order is free) and moe_rows_kernel then reads each row of logits once, into
+// registers, and writes its gradient once.  A row belongs to 4, 16 or 32 lanes;
+// each lane keeps the counts of its experts in registers over all its rows.
+// Row losses are added in fp64 (one addition a row) in an order fixed by the
+// grid, and the last CTA to finish adds the CTAs' sums.
+#pragma once
+
+#include "row_kernels.cuh"
+
+namespace gbce {
+
+constexpr int kMoeThreads = 256;
+constexpr int kMoeMaxExperts = 1024;
+constexpr int kMoeMaxSlots = 64;
+constexpr int kMoeMaxCtas = 2048;
+
+// Zeroed before moe_count_kernel.
+struct MoeTotals {
+    unsigned long long counts[kMoeMaxExperts];
+    unsigned int n, bad, done, pad;
+};
+
+struct MoeArgs {
+    const void *logits;
+    int64_t ls;
+    const int64_t *experts;
+    int64_t es;
+    int64_t T;
+    int E, k;
+    MoeTotals *totals;
+    unsigned char *mask;   // [T]: the token counts
+    double *part;          // [gridDim.x] sums of row losses
+    int64_t *counts;       // out
+    float *loss;           // out, or NULL
+    void *grad;            // out, or NULL
+    int64_t gs;
+    const float *grad_scale;
+    float balance, z;
+};
+
+// Does token t count, i.e. has it a slot in [0, E) and none beyond?  -1: a bad slot.
+__device__ __forceinline__ int moe_token(const MoeArgs &a, int64_t t)
+{
+    const int64_t *ids = a.experts + t * a.es;
+    int any = 0;
+    for (int j = 0; j < a.k; ++j) {
+        const int64_t e = __ldg(ids + j);
+        if (e < -1 || e >= a.E)
+            return -1;
+        any |= e >= 0;
+    }
+    return any;
+}
+
+// Adds the choices of tokens first, first + step, ... to hist; returns how many count.
+__device__ __forceinline__ int moe_count_tokens(const MoeArgs &a, int64_t first, int64_t step,
+                                                unsigned *hist, bool &bad)
+{
+    int n = 0;
+    for (int64_t t = first; t < a.T; t += step) {
+        const int c = moe_token(a, t);
+        a.mask[t] = c > 0;
+        bad |= c < 0;
+        if (c > 0) {
+            ++n;
+            for (int j = 0; j < a.k; ++j) {
+                const int64_t e = __ldg(a.experts + t * a.es + j);
+                if (e >= 0)
+                    atomicAdd(hist + e, 1u);
+            }
+        }
+    }
+    return n;
+}
+
+template <int NT>
+__global__ void __launch_bounds__(NT) moe_count_kernel(const MoeArgs a)
+{
+    __shared__ unsigned hist[kMoeMaxExperts];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    for (int e = threadIdx.x; e < a.E; e += NT)
+        hist[e] = 0;
+    __syncthreads();
+    bool bad = false;
+    int n = moe_count_tokens(a, blockIdx.x * int64_t{NT} + threadIdx.x, int64_t{gridDim.x} * NT, hist, bad);
+    n = __reduce_add_sync(0xffffffffu, n);
+    if ((threadIdx.x & 31) == 0 && n)
+        atomicAdd(&a.totals->n, static_cast<unsigned>(n));
+    if (bad) {
+        atomicOr(&a.totals->bad, 1u);
+        atomicOr(&g_flags, kFlagBadTarget);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += NT)
+        if (hist[e])
+            atomicAdd(&a.totals->counts[e], static_cast<unsigned long long>(hist[e]));
+}
+
+template <int LPT>
+__device__ __forceinline__ float group_sum(float v)
+{
+#pragma unroll
+    for (int off = LPT / 2; off > 0; off >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+
+template <int LPT>
+__device__ __forceinline__ float group_max(float v)
+{
+#pragma unroll
+    for (int off = LPT / 2; off > 0; off >>= 1)
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+    return v;
+}
+
+// VEC values (16 bytes, or one) at p.
+template <typename T, int VEC>
+__device__ __forceinline__ void moe_load(const T *p, float *f)
+{
+    if constexpr (VEC == 1) {
+        f[0] = Elem<T>::load(p);
+    } else {
+        float v[VEC];
+        Elem<T>::unpack(__ldcs(reinterpret_cast<const uint4 *>(p)), v);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            f[i] = v[i];
+    }
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ void moe_store(T *p, const float *f)
+{
+    if constexpr (VEC == 1) {
+        Elem<T>::store(p, f[0]);
+    } else {
+        float v[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            v[i] = f[i];
+        __stcs(reinterpret_cast<uint4 *>(p), Elem<T>::pack(v));
+    }
+}
+
+// ALL: one CTA does everything, the counting too (small batches: one launch).
+template <typename T, int VEC, int LPT, int NJ, bool ALL, int NT>
+__global__ void __launch_bounds__(NT) moe_rows_kernel(const MoeArgs a)
+{
+    __shared__ unsigned hist[ALL ? kMoeMaxExperts : 1];
+    __shared__ double warp_part[NT / 32];
+    __shared__ int s_n, s_bad, s_last;
+    const int lane = threadIdx.x & 31, sub = lane % LPT;
+    const int64_t groups = int64_t{gridDim.x} * (NT / LPT);
+    const int64_t group = blockIdx.x * int64_t{NT / LPT} + threadIdx.x / LPT;
+
+    if constexpr (ALL) {
+        for (int e = threadIdx.x; e < a.E; e += NT)
+            hist[e] = 0;
+        if (threadIdx.x == 0)
+            s_n = s_bad = 0;
+        __syncthreads();
+        bool bad = false;
+        int n = moe_count_tokens(a, threadIdx.x, NT, hist, bad);
+        n = __reduce_add_sync(0xffffffffu, n);
+        if (lane == 0 && n)
+            atomicAdd(&s_n, n);
+        if (bad)
+            s_bad = 1;
+        __syncthreads();
+        if (threadIdx.x == 0 && s_bad)
+            atomicOr(&g_flags, kFlagBadTarget);
+    } else {
+        wait_prerequisite_grid();
+        if (threadIdx.x == 0) {
+            s_n = static_cast<int>(__ldcg(&a.totals->n));
+            s_bad = static_cast<int>(__ldcg(&a.totals->bad));
+        }
+        __syncthreads();
+    }
+    const auto count_of = [&](int e) -> unsigned long long {
+        if constexpr (ALL)
+            return hist[e];
+        else
+            return __ldcg(&a.totals->counts[e]);
+    };
+    const int n = s_n;
+    if (blockIdx.x == 0)
+        for (int e = threadIdx.x; e < a.E; e += NT)
+            a.counts[e] = static_cast<int64_t>(count_of(e));
+
+    // this lane's experts: e = (j LPT + sub) VEC + v; the mean over all of them
+    float f[NJ * VEC];
+    double sum = 0.0;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            const int e = (j * LPT + sub) * VEC + v;
+            if (e < a.E)
+                sum += static_cast<double>(count_of(e));
+        }
+#pragma unroll
+    for (int off = LPT / 2; off > 0; off >>= 1)
+        sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    const double mean = sum / a.E;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            const int e = (j * LPT + sub) * VEC + v;
+            f[j * VEC + v] = e < a.E ? static_cast<float>(static_cast<double>(count_of(e)) - mean) : 0.f;
+        }
+    const float fmean = static_cast<float>(mean);
+    const float per_n = 1.f / static_cast<float>(n);
+    const float ka = a.balance * static_cast<float>(a.E) / static_cast<float>(a.k) * per_n;  // a E / (k n)
+    const float gscale = a.grad ? (a.grad_scale ? __ldg(a.grad_scale) : 1.f) * per_n : 0.f;
+    const float ga = ka * gscale, gz = 2.f * a.z * gscale;
+
+    double part = 0.0;
+    for (int64_t t0 = group - (lane / LPT); t0 < a.T; t0 += groups) {  // one trip for the whole warp
+        const int64_t t = t0 + lane / LPT;
+        const bool in = t < a.T;
+        const bool counted = in && a.mask[t];
+        const T *row = static_cast<const T *>(a.logits) + t * a.ls;
+        float x[NJ * VEC];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            const int e = (j * LPT + sub) * VEC;
+            if (counted && e < a.E) {
+                moe_load<T, VEC>(row + e, x + j * VEC);
+            } else {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v)
+                    x[j * VEC + v] = -INFINITY;
+            }
+        }
+        float m = x[0];
+#pragma unroll
+        for (int i = 1; i < NJ * VEC; ++i)
+            m = fmaxf(m, x[i]);
+        m = group_max<LPT>(m);
+        const float s = m == -INFINITY ? 0.f : shift_of(m);
+        float d = 0.f, q = 0.f;
+#pragma unroll
+        for (int i = 0; i < NJ * VEC; ++i) {
+            x[i] = exp2_shift(x[i], s);
+            d += x[i];
+            q = fmaf(x[i], f[i], q);
+        }
+        d = group_sum<LPT>(d);
+        q = group_sum<LPT>(q);
+        const float inv = 1.f / d, dot = q * inv;
+        const float lse = fmaf(s, kLn2, logf(d));
+        if (counted && sub == 0)
+            part += static_cast<double>(fmaf(ka, fmean + dot, a.z * lse * lse));
+        if (a.grad && in) {
+            const float base = counted ? fmaf(-ga, dot, gz * lse) : 0.f;
+            T *out = static_cast<T *>(a.grad) + t * a.gs;
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                const int e = (j * LPT + sub) * VEC;
+                if (e < a.E) {
+                    float g[VEC];
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v)
+                        g[v] = counted ? x[j * VEC + v] * inv * fmaf(ga, f[j * VEC + v], base) : 0.f;
+                    moe_store<T, VEC>(out + e, g);
+                }
+            }
+        }
+    }
+
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+        part += __shfl_xor_sync(0xffffffffu, part, off);
+    if (lane == 0)
+        warp_part[threadIdx.x >> 5] = part;
+    __syncthreads();
+    if constexpr (ALL) {
+        if (threadIdx.x == 0 && a.loss) {
+            double total = 0.0;
+            for (int w = 0; w < NT / 32; ++w)
+                total += warp_part[w];
+            *a.loss = s_bad ? __int_as_float(0x7fc00000) : static_cast<float>(total / n);
+        }
+    } else {
+        if (!a.loss)
+            return;
+        if (threadIdx.x == 0) {
+            double total = 0.0;
+            for (int w = 0; w < NT / 32; ++w)
+                total += warp_part[w];
+            a.part[blockIdx.x] = total;
+            __threadfence();
+            s_last = atomicAdd(&a.totals->done, 1u) == gridDim.x - 1;
+        }
+        __syncthreads();
+        if (!s_last)
+            return;
+        __threadfence();
+        double total = 0.0;
+        for (int i = threadIdx.x; i < static_cast<int>(gridDim.x); i += NT)
+            total += __ldcg(a.part + i);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1)
+            total += __shfl_xor_sync(0xffffffffu, total, off);
+        __syncthreads();
+        if (lane == 0)
+            warp_part[threadIdx.x >> 5] = total;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            total = 0.0;
+            for (int w = 0; w < NT / 32; ++w)
+                total += warp_part[w];
+            *a.loss = s_bad ? __int_as_float(0x7fc00000) : static_cast<float>(total / n);
+        }
+    }
+}
+
+}  // namespace gbce

@@ -397,10 +397,119 @@ GBCE_API const char *gbce_status_string(int status);
  * gbce_pool_reserved -- device memory, in bytes, that the library's scratch
  * pool holds on `device` (reserved from the driver and kept for reuse), or 0
  * in *bytes when no call on that device has needed the pool yet.  The pool
- * serves ce_fwd_bwd, ce_fwd_bwd_ex and ce_fwd_bwd_host; ce_fwd_bwd_noalloc
+ * serves ce_fwd_bwd, ce_fwd_bwd_ex, ce_fwd_bwd_host, the linear_* calls and
+ * moe_balance; ce_fwd_bwd_noalloc
  * and the softmax calls never create it.  For diagnostics; no launch, no sync.
  */
 GBCE_API int gbce_pool_reserved(int device, uint64_t *bytes);
+
+/*
+ * linear_ce_fwd -- cross-entropy of hidden states through the output layer's
+ * weights, the logits x = H W^T never stored.
+ *
+ *   hidden        [M, hidden_stride], rows of K values (bf16 or fp16), read only.
+ *   weight        [V, weight_stride], rows of K values of the same type, read only.
+ *   targets       [M] int64 class indices or ignore_index, read only.
+ *   loss          one float (mean, sum; may be NULL for GBCE_NONE):
+ *                   L = sum_r l_r / n or sum_r l_r,  l_r = lse_r - x[r, t_r],
+ *                   lse_r = ln sum_v exp x[r, v],  n = rows not ignored.
+ *                 NaN when n == 0 and the reduction is the mean.
+ *   row_loss      [M] floats (16-byte aligned): l_r, 0 for ignored rows.
+ *   lse           [M] floats or NULL: lse_r, 0 for ignored rows; linear_ce_bwd
+ *                 takes it.
+ *   M, K, V       rows, hidden width and classes: 0 <= M <= 2^27 - 1,
+ *                 1 <= K <= 2^24, 1 <= V <= 2^31 - 1025.
+ *   dtype         GBCE_BF16 or GBCE_F16 (GBCE_F32 is refused: GBCE_ERR_DTYPE).
+ *   reduction     a gbce_reduction.
+ *
+ * Products of 16-bit values are summed in fp32 on the tensor cores; everything
+ * after them is fp32.  Ignored rows take no part in the products, so a batch
+ * costs what its counted rows cost.  A target outside [0, V) that is not
+ * ignore_index raises GBCE_ERR_BAD_TARGET: its row loss and lse are NaN.
+ * NaN or infinite logits make their row's loss NaN.
+ *
+ * Scratch comes from the library's pool on `stream` (gbce_pool_reserved): the
+ * counted rows' hidden states, 8 bytes per row and 256 classes, and a copy of
+ * the weights where their rows do not start on 16-byte boundaries.
+ */
+GBCE_API int linear_ce_fwd(const void *hidden, int64_t hidden_stride, const void *weight,
+                           int64_t weight_stride, const int64_t *targets, float *loss,
+                           float *row_loss, float *lse, int64_t M, int64_t K, int64_t V,
+                           int64_t ignore_index, int dtype, int reduction, gbce_stream_t stream);
+
+/*
+ * linear_ce_bwd -- gradients of linear_ce_fwd's loss.
+ *
+ *   hidden .. targets, M, K, V, ignore_index, dtype, reduction: as given to the forward.
+ *   lse           [M] floats that linear_ce_fwd wrote.
+ *   grad_scale    the incoming gradient: NULL (1), one float (mean, sum), or
+ *                 one per row (none).
+ *   d_hidden      [M, d_hidden_stride] of dtype or NULL: sum_v G[r, v] W[v, :], zeros
+ *                 for rows that are ignored or whose target is out of range.
+ *   d_weight      [V, d_weight_stride] of dtype or NULL: sum_r G[r, v] H[r, :].
+ *                 At least one of the two; neither may overlap an input.
+ *                   G[r, v] = (exp(x[r, v] - lse_r) - [v == t_r]) k_r,
+ *                   k_r = grad_scale / n (mean), grad_scale (sum), grad_scale[r] (none)
+ *
+ * G is formed a piece of the vocabulary at a time and rounded once to dtype (its
+ * factors relative to a power of two at or above the largest, so fp16 keeps
+ * small ones); both products are summed in fp32 and rounded once.  Both
+ * gradients are written, not added to.  Scratch: the counted rows' hidden states, up to
+ * 512 MB of G (more only when M exceeds 2^20 rows), and M x K floats when the
+ * vocabulary takes several pieces.
+ */
+GBCE_API int linear_ce_bwd(const void *hidden, int64_t hidden_stride, const void *weight,
+                           int64_t weight_stride, const int64_t *targets, const float *lse,
+                           const float *grad_scale, void *d_hidden, int64_t d_hidden_stride,
+                           void *d_weight, int64_t d_weight_stride, int64_t M, int64_t K, int64_t V,
+                           int64_t ignore_index, int dtype, int reduction, gbce_stream_t stream);
+
+/*
+ * linear_greedy -- the most probable class of each row of H W^T and its
+ * log-probability, the logits never stored (greedy decoding; M may be 1).
+ *
+ *   hidden, weight, M, K, V, dtype: as for linear_ce_fwd.
+ *   tokens        [M] int64: argmax_v x[r, v], the lowest index of equal ones.
+ *   logprob       [M] floats: x[r, tokens_r] - lse_r.
+ *
+ * NaN logits are passed over for the index (0 when a row holds nothing else)
+ * and make the row's logprob NaN.
+ */
+GBCE_API int linear_greedy(const void *hidden, int64_t hidden_stride, const void *weight,
+                           int64_t weight_stride, int64_t *tokens, float *logprob, int64_t M,
+                           int64_t K, int64_t V, int dtype, gbce_stream_t stream);
+
+/*
+ * moe_balance -- balance loss and z-loss of a mixture-of-experts router, with
+ * per-expert counts and the gradient of its logits.
+ *
+ *   logits        [T, logits_stride] of dtype, rows of E router logits, read only
+ *                 (unless grad is the same matrix).
+ *   experts       [T, experts_stride] int64, rows of k slots: the expert of each
+ *                 slot, or -1 for an empty one (padding, a dropped token).  A
+ *                 token counts when it has a slot in use.  The same expert may
+ *                 stand twice.
+ *   counts        [E] int64: f_e, the slots of counted tokens that hold e.
+ *   loss          one float or NULL:
+ *                   L = balance_coef E / (k n^2) sum_t sum_e f_e p_te
+ *                       + z_coef / n sum_t lse_t^2
+ *                 over the n counted tokens t, p_t = softmax of row t, lse_t its
+ *                 log-sum-exp (NaN when n == 0).
+ *   grad          [T, grad_stride] of dtype or NULL: dL/dlogits times *grad_scale
+ *                 (1 when that is NULL), zeros for tokens that do not count.  f is
+ *                 a constant.  May be logits itself (same stride).  At least one
+ *                 of loss and grad is given.
+ *   T, E, k       tokens, experts and slots: T <= 2^27 - 1, 1 <= E <= 1024,
+ *                 1 <= k <= 64.
+ *
+ * A slot outside [-1, E) raises GBCE_ERR_BAD_TARGET: its token does not count,
+ * and the loss is NaN.  Arithmetic is fp32 with fp64 sums over tokens; results
+ * do not depend on the order of execution.
+ */
+GBCE_API int moe_balance(const void *logits, int64_t logits_stride, const int64_t *experts,
+                         int64_t experts_stride, int64_t *counts, float *loss, void *grad,
+                         int64_t grad_stride, const float *grad_scale, int64_t T, int64_t E, int64_t k,
+                         float balance_coef, float z_coef, int dtype, gbce_stream_t stream);
 
 /*
  * gbce_test_failure_path -- a test of the bounded waits (no counterpart on the
