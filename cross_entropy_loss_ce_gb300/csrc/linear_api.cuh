@@ -83,7 +83,7 @@ struct HeadScratch {
     unsigned *fail;
     float *alpha;
     int *idx, *tgt;
-    float *l2, *rs, *xy;
+    float *l2, *rs, *gy, *xy;
     unsigned short *h;  // packed hidden states
     unsigned short *w;  // packed weights (rows a tensor map cannot read)
     float2 *part;
@@ -125,6 +125,7 @@ HeadScratch carve(Carver &c, const HeadShape &s, HeadOp op, bool want_hidden)
     if (op == HeadOp::Bwd) {
         r.l2 = c.take<float>(s.M);
         r.rs = c.take<float>(s.M);
+        r.gy = c.take<float>(s.M);
         r.g = c.take<unsigned short>(s.mp * s.vp);
         if (want_hidden && s.pieces > 1)
             r.acc = c.take<float>(s.mp * round_up(s.K, kPairN));
@@ -190,8 +191,14 @@ cudaError_t launch_skinny_ng(const Call &call, const SkinnyArgs &a, int64_t ctas
 cudaError_t launch_gather(const Call &call, GatherArgs a, int64_t rows)
 {
     a.vec = mappable(a.src, a.ss, 2) ? 1 : 0;
-    const int64_t most = call.sms * 8;
-    lin_gather_kernel<256><<<static_cast<unsigned>(rows < most ? rows : most), 256, 0, call.stream>>>(a);
+    a.wvec = a.vec && mappable(a.w, a.ws, 2);
+    a.zvec = mappable(a.zero, a.zs, 2);
+    const int64_t want = (rows + 7) / 8, most = call.sms * 8;
+    const unsigned grid = static_cast<unsigned>(want < most ? want : most);
+    if (call.dtype == GBCE_BF16)
+        lin_gather_kernel<__nv_bfloat16, 256><<<grid, 256, 0, call.stream>>>(a);
+    else
+        lin_gather_kernel<__half, 256><<<grid, 256, 0, call.stream>>>(a);
     return cudaGetLastError();
 }
 
@@ -225,7 +232,7 @@ HeadShape head_shape(const Call &call, const void *hidden, int64_t hs, const voi
         const int64_t units = (V + kSkinnyUnit - 1) / kSkinnyUnit;
         s.parts = units < call.sms ? units : call.sms;
     } else {
-        s.parts = (V + kPairN - 1) / kPairN;
+        s.parts = 2 * ((V + kPairN - 1) / kPairN);
     }
     if (op == HeadOp::Bwd) {
         int64_t vp = kGradPieceBytes / (s.mp * 2) / kPairN * kPairN;
@@ -303,7 +310,6 @@ cudaError_t launch_head(const Call &call, const HeadShape &s, const HeadScratch 
         a.part = r.part;
         a.part_idx = r.part_idx;
         a.part_max = r.part_max;
-        a.xy = r.xy;
         a.ldp = s.mp;
         a.fail = GREEDY ? nullptr : r.fail;
         a.bf16 = call.dtype == GBCE_BF16;
@@ -316,20 +322,30 @@ cudaError_t launch_head(const Call &call, const HeadShape &s, const HeadScratch 
             return e;
         a.n_ptr = m.n_ptr;
         a.n_host = m.n_host;
-        a.tiles_n = static_cast<int>(s.parts);
+        a.tiles_n = static_cast<int>(s.parts / 2);
         a.kblocks = kblocks;
         a.fail = GREEDY ? nullptr : r.fail;
         a.part = r.part;
         a.part_idx = r.part_idx;
-        a.xy = GREEDY ? r.part_max : r.xy;
+        a.part_max = r.part_max;
         a.ldp = s.mp;
         a.tgt = r.tgt;
         a.V = s.V;
-        e = launch_pair<GREEDY ? Epi::Greedy : Epi::Stats>(call, a, s.mp / kPairM * s.parts);
+        e = launch_pair<GREEDY ? Epi::Greedy : Epi::Stats>(call, a, s.mp / kPairM * a.tiles_n);
     }
     if (e != cudaSuccess)
         return e;
-    lin_merge_kernel<GREEDY><<<static_cast<unsigned>((s.M + 31) / 32), 256, 0, call.stream>>>(m);
+    m.h = h;
+    m.hs = hstride;
+    m.w = w;
+    m.ws = wstride;
+    m.K = s.K;
+    m.vec = mappable(h, hstride, hrows) && mappable(w, wstride, s.V);
+    const unsigned grid = static_cast<unsigned>((s.M + 31) / 32);
+    if (!GREEDY || call.dtype == GBCE_BF16)  // the loss reads no 16-bit operand
+        lin_merge_kernel<GREEDY, __nv_bfloat16><<<grid, 256, 0, call.stream>>>(m);
+    else
+        lin_merge_kernel<GREEDY, __half><<<grid, 256, 0, call.stream>>>(m);
     return cudaGetLastError();
 }
 
@@ -343,7 +359,12 @@ cudaError_t launch_linear_fwd(const Call &call, const HeadShape &s, const HeadSc
         return e;
     const void *w;
     int64_t wstride;
-    if ((e = pack_hidden(call, s, r, hidden, hs, r.idx, r.rows)) != cudaSuccess ||
+    GatherArgs target{};
+    target.w = weight;
+    target.ws = ws;
+    target.tgt = r.tgt;
+    target.xy = r.xy;
+    if ((e = pack_hidden(call, s, r, hidden, hs, r.idx, r.rows, target)) != cudaSuccess ||
         (e = pack_weights(call, s, r, weight, ws, &w, &wstride)) != cudaSuccess)
         return e;
     MergeArgs m{};
@@ -368,14 +389,20 @@ cudaError_t launch_linear_bwd(const Call &call, const HeadShape &s, const HeadSc
         return e;
     const void *w;
     int64_t wstride;
-    GatherArgs zero{};
-    zero.zero = d_hidden;
-    zero.zs = dhs;
-    zero.M = s.M;
-    zero.V = s.V;
-    zero.ignore_index = prep.ignore_index;
-    zero.targets = prep.targets;
-    if ((e = pack_hidden(call, s, r, hidden, hs, r.idx, r.rows, zero)) != cudaSuccess ||
+    GatherArgs rest{};
+    rest.w = weight;
+    rest.ws = ws;
+    rest.tgt = r.tgt;
+    rest.l2 = r.l2;
+    rest.rs = r.rs;
+    rest.gy = r.gy;
+    rest.zero = d_hidden;
+    rest.zs = dhs;
+    rest.M = s.M;
+    rest.V = s.V;
+    rest.ignore_index = prep.ignore_index;
+    rest.targets = prep.targets;
+    if ((e = pack_hidden(call, s, r, hidden, hs, r.idx, r.rows, rest)) != cudaSuccess ||
         (e = pack_weights(call, s, r, weight, ws, &w, &wstride)) != cudaSuccess)
         return e;
     PairArgs grad{}, dw{}, dh{};
@@ -395,6 +422,7 @@ cudaError_t launch_linear_bwd(const Call &call, const HeadShape &s, const HeadSc
         a->tgt = r.tgt;
         a->l2 = r.l2;
         a->rs = r.rs;
+        a->gy = r.gy;
         a->g = r.g;
         a->ldg = s.vp;
         a->cols = s.K;

@@ -13,10 +13,22 @@
 // pair_gemm_kernel does every product: pairs of CTAs (cta_group::2) on 256 x 256
 // tiles, one CTA holding 128 rows of A, 128 of B's 256 rows, and 128 x 256
 // sums.  A producer thread per CTA keeps a ring of 64-wide operand tiles filled
-// by TMA, one thread of the pair issues the matrix instructions, and four warps
+// by TMA, one thread of the pair issues the matrix instructions, and eight warps
 // per CTA empty one accumulator while the other one fills (2 x 256 columns, all
 // of tensor memory).  The 256 x 256 pair tile reads 64 KB per 2 x 16.8 MFLOP
 // k-step, half of what two 128 x 256 tiles would take from L2.
+//
+// The tensor cores cut each addition short instead of rounding it, toward zero,
+// which over a K of 4096 adds up to 40 steps of fp32 in a logit.  Two things
+// keep that out of the results.  The logit that a row's answer hangs on (the
+// target's, the arg max's) is formed again as an fp32 dot product of two rows
+// (0.5% of the time at 8192 rows), and the sums leave its term out, so that the
+// loss ln(1 + others / e^x_y) of a likely target and (p_y - 1) keep their
+// precision.  And logits are summed in tensor memory over kChunk k-steps (1024
+// of K) at a time, these sums in registers.  Emptying an accumulator takes
+// tensor-memory cycles from the running instructions: 8192 x 128256, K 4096
+// takes 4.90 ms unsplit, 5.04-5.22 in runs of 1024, 5.29 of 512, 5.86 of 256.
+// The gradient products and their logits, which end in 16 bits, are not split.
 //
 // skinny_kernel is the forward for at most 64 rows, where reading W once is the
 // whole cost: W's rows take the M side of the instruction, so a tile is 128
@@ -37,8 +49,9 @@ namespace gbce {
 constexpr int kPairM = 256, kPairN = 256, kPairK = 64;  // tile of a CTA pair
 constexpr int kPairStages = 6;
 constexpr int kPairStageBytes = 2 * 128 * kPairK * 2;   // per CTA: 128 rows of A and of B
-constexpr int kPairThreads = 256;
+constexpr int kPairThreads = 384;
 constexpr int kPairSmem = kPairStages * kPairStageBytes + 1024;
+constexpr int kChunk = 16;                              // k-steps of a logit summed in tensor memory
 constexpr int kBand = 8;                                // tiles of M that share a sweep over N
 
 enum class Epi { Stats, Greedy, Grad, Weight, Hidden };
@@ -53,14 +66,14 @@ struct PairArgs {
     int b_row0;         // first row of B along the axis of W's rows (piece offset)
     unsigned *fail;
     // Stats, Greedy
-    float2 *part;       // [tiles_n][ldp] (s, d) pairs
+    float2 *part;       // [2 tiles_n][ldp] (s, d) pairs, one for each 128 columns
     int *part_idx;      // Greedy: the arg max of each
-    float *xy;          // Stats: the target's logit
+    float *part_max;    // Greedy: the maximum of each
     int64_t ldp;
     const int *tgt;
     int64_t V;          // columns of this launch's logits (vocabulary, or end of it) from row 0 of W
     // Grad
-    const float *l2, *rs;
+    const float *l2, *rs, *gy;  // lse log2e, factor and target's entry of each row
     void *g;
     int64_t ldg;
     // Weight, Hidden
@@ -94,37 +107,66 @@ __device__ __forceinline__ float rescaled(float d, float from, float to)
     return from == -INFINITY ? d : d * exp2f(shift_of(from) - shift_of(to));
 }
 
-// 32 logits of one row, columns c0 .. c0 + 31 of W's rows, into the running
-// maximum m and sum d = sum exp2(x log2e - fl(m log2e)).
-template <bool GREEDY>
-__device__ __forceinline__ void stats_chunk(const uint32_t (&r)[32], int c0, int limit, float &m,
-                                            float &d, int &best)
+// exp2 of a maximum about its own shift: 1 up to the shift's rounding.
+__device__ __forceinline__ float self_term(float m) { return exp2_shift(m, shift_of(m)); }
+
+// The arg max keeps its sum without the maximum's own term: the log-probability
+// -ln(1 + d / self_term(m)) of a nearly certain token keeps its precision.  The
+// sum about a new maximum `to`, which the old one's term now joins:
+__device__ __forceinline__ float rescaled_others(float d, float from, float to)
 {
-    float x[32];
+    return from == -INFINITY ? d : (d + self_term(from)) * exp2f(shift_of(from) - shift_of(to));
+}
+
+// Merge of two (maximum, others, index) triples: the lower index of equal maxima.
+__device__ __forceinline__ void best_merge(float &m, float &d, int &i, float m2, float d2, int i2)
+{
+    if (m2 > m || (m2 == m && i2 < i)) {
+        d = d2 + rescaled_others(d, m, m2);
+        m = m2;
+        i = i2;
+    } else {
+        d += rescaled_others(d2, m2, m);
+    }
+}
+
+// 32 logits of one row, x[OFF ..], columns c0 .. c0 + 31 of W's rows, into the
+// running maximum m and sum d = sum exp2(x log2e - fl(m log2e)) (GREEDY: of all
+// but the maximum, whose column is `best`).
+template <bool GREEDY, int OFF, int N>
+__device__ __forceinline__ void stats_chunk(float (&x)[N], int c0, int limit, float &m, float &d, int &best)
+{
+    if (c0 + 32 > limit) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-        x[i] = c0 + i < limit ? __uint_as_float(r[i]) : -INFINITY;
-    float mc = x[0];
+        for (int i = 0; i < 32; ++i)
+            x[OFF + i] = c0 + i < limit ? x[OFF + i] : -INFINITY;
+    }
+    float mc = x[OFF];
 #pragma unroll
     for (int i = 1; i < 32; ++i)
-        mc = fmaxf(mc, x[i]);
+        mc = fmaxf(mc, x[OFF + i]);
     if (mc > m) {
-        d = rescaled(d, m, mc);
-        m = mc;
         if constexpr (GREEDY) {
             int at = 31;
 #pragma unroll
             for (int i = 31; i >= 0; --i)
-                at = x[i] == mc ? i : at;
+                at = x[OFF + i] == mc ? i : at;
             best = c0 + at;
+            d = rescaled_others(d, m, mc);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                x[OFF + i] = i == at ? -INFINITY : x[OFF + i];
+        } else {
+            d = rescaled(d, m, mc);
         }
+        m = mc;
     }
     const float s = finite_shift(m);
     float d0 = 0.f, d1 = 0.f;
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
-        d0 += exp2_shift(x[i], s);
-        d1 += exp2_shift(x[i + 1], s);
+        d0 += exp2_shift(x[OFF + i], s);
+        d1 += exp2_shift(x[OFF + i + 1], s);
     }
     d += d0 + d1;
 }
@@ -156,6 +198,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 {
     constexpr bool A_MN = E == Epi::Weight;
     constexpr bool B_MN = E == Epi::Weight || E == Epi::Hidden;
+    constexpr bool LOGITS = E == Epi::Stats || E == Epi::Greedy || E == Epi::Grad;
+    constexpr bool CHUNKED = E == Epi::Stats || E == Epi::Greedy;
     constexpr uint32_t kIdesc =
         mma_idesc(std::is_same<T, __nv_bfloat16>::value, A_MN, B_MN, kPairM, kPairN);
 
@@ -176,6 +220,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const int kblocks = E == Epi::Weight ? (n + kPairK - 1) / kPairK : a.kblocks;
     const int tiles = tiles_m * a.tiles_n;
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int run = CHUNKED ? kChunk : max(kblocks, 1);  // k-steps that stay in tensor memory
 
     if (threadIdx.x == 0) {
         dead_word = 0;
@@ -185,7 +230,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(tfull + 8 * i, 1);
-            mbar_init(tempty + 8 * i, 8);  // four warps of each CTA
+            mbar_init(tempty + 8 * i, 16);  // eight warps of each CTA
         }
         fence_barrier_init();
         prefetch_map(&a.a);
@@ -200,147 +245,196 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
 
-    if (warp == 0 && lane == 0) {
-        // producer: this CTA's halves of A and B
-        const uint32_t full0 = map_to_rank(full, 0);
-        int slot = 0;
-        uint32_t phase = 0;
+    // 128 sums a thread want more than the launch's 168 registers: the first
+    // four warps give some of theirs up (64 x 128 + 216 x 256 <= 168 x 384)
+    if (warp < 4) {
+        if constexpr (CHUNKED)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if (warp == 0 && lane == 0) {
+            // producer: this CTA's halves of A and B
+            const uint32_t full0 = map_to_rank(full, 0);
+            int slot = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int t = pair; t < tiles && ok; t += pairs) {
+                int tm, tn;
+                tile_at(t, tiles_m, a.tiles_n, tm, tn);
+                const int am = tm * kPairM + static_cast<int>(rank) * 128;
+                const int bn = tn * kPairN + static_cast<int>(rank) * 128;
+                for (int kb = 0; kb < kblocks; ++kb) {
+                    if (!(ok = bar_wait_cluster(empty + 8 * slot, phase ^ 1, dead)))
+                        break;
+                    if (rank == 0)
+                        mbar_arrive_expect_tx(full + 8 * slot, 2 * kPairStageBytes);
+                    const uint32_t sa = ring + slot * kPairStageBytes, sb = sa + kPairStageBytes / 2;
+                    const uint32_t bar = full0 + 8 * slot;
+                    const int k0 = kb * kPairK;
+                    if constexpr (A_MN) {
+                        tma_load_pair(sa, &a.a, am, k0, bar);
+                        tma_load_pair(sa + 8192, &a.a, am + 64, k0, bar);
+                    } else {
+                        tma_load_pair(sa, &a.a, k0, am, bar);
+                    }
+                    if constexpr (B_MN) {
+                        const int kr = E == Epi::Hidden ? a.b_row0 + k0 : k0;
+                        tma_load_pair(sb, &a.b, bn, kr, bar);
+                        tma_load_pair(sb + 8192, &a.b, bn + 64, kr, bar);
+                    } else {
+                        tma_load_pair(sb, &a.b, k0, a.b_row0 + bn, bar);
+                    }
+                    if (++slot == kPairStages) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+        } else if (warp == 1 && lane == 0 && rank == 0) {
+            // the pair's matrix instructions
+            int slot = 0, it = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int t = pair; t < tiles && ok; t += pairs) {
+                for (int kb0 = 0; ok && kb0 < max(kblocks, 1); kb0 += run, ++it) {
+                    const int acc = it & 1;
+                    if (!(ok = bar_wait_cluster(tempty + 8 * acc, ((it >> 1) & 1) ^ 1, dead)))
+                        break;
+                    tc_fence_after();
+                    const int kb1 = min(kb0 + run, kblocks);
+                    for (int kb = kb0; kb < kb1; ++kb) {
+                        if (!(ok = bar_wait_cluster(full + 8 * slot, phase, dead)))
+                            break;
+                        tc_fence_after();
+                        const uint32_t sa = ring + slot * kPairStageBytes, sb = sa + kPairStageBytes / 2;
+                        const uint64_t da = smem_desc(sa, A_MN ? 8192 : 16, 1024);
+                        const uint64_t db = smem_desc(sb, B_MN ? 8192 : 16, 1024);
+    #pragma unroll
+                        for (int k = 0; k < kPairK / 16; ++k)  // 16 of K: 32 bytes, or 16 rows of 128 bytes
+                            mma_f16<2>(tmem + acc * kPairN, da + k * (A_MN ? 128 : 2),
+                                       db + k * (B_MN ? 128 : 2), kIdesc, kb != kb0 || k != 0);
+                        mma_commit_pair(empty + 8 * slot);
+                        if (++slot == kPairStages) {
+                            slot = 0;
+                            phase ^= 1;
+                        }
+                    }
+                    if (ok)
+                        mma_commit_pair(tfull + 8 * acc);
+                }
+            }
+        }
+    } else {
+        if constexpr (CHUNKED)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        // epilogue: thread = one row of this CTA's 128, 128 of the 256 columns
+        const int ew = warp & 3, half = (warp - 4) >> 2;
+        const uint32_t tempty0 = map_to_rank(tempty, 0);
+        const int limit = static_cast<int>(min(a.V, static_cast<int64_t>(INT32_MAX)));
+        [[maybe_unused]] float alpha = 1.f;
+        if constexpr (!LOGITS)
+            alpha = __ldg(a.alpha);
+        int it = 0;
         bool ok = true;
         for (int t = pair; t < tiles && ok; t += pairs) {
             int tm, tn;
             tile_at(t, tiles_m, a.tiles_n, tm, tn);
-            const int am = tm * kPairM + static_cast<int>(rank) * 128;
-            const int bn = tn * kPairN + static_cast<int>(rank) * 128;
-            for (int kb = 0; kb < kblocks; ++kb) {
-                if (!(ok = bar_wait_cluster(empty + 8 * slot, phase ^ 1, dead)))
-                    break;
-                if (rank == 0)
-                    mbar_arrive_expect_tx(full + 8 * slot, 2 * kPairStageBytes);
-                const uint32_t sa = ring + slot * kPairStageBytes, sb = sa + kPairStageBytes / 2;
-                const uint32_t bar = full0 + 8 * slot;
-                const int k0 = kb * kPairK;
-                if constexpr (A_MN) {
-                    tma_load_pair(sa, &a.a, am, k0, bar);
-                    tma_load_pair(sa + 8192, &a.a, am + 64, k0, bar);
-                } else {
-                    tma_load_pair(sa, &a.a, k0, am, bar);
-                }
-                if constexpr (B_MN) {
-                    const int kr = E == Epi::Hidden ? a.b_row0 + k0 : k0;
-                    tma_load_pair(sb, &a.b, bn, kr, bar);
-                    tma_load_pair(sb + 8192, &a.b, bn + 64, kr, bar);
-                } else {
-                    tma_load_pair(sb, &a.b, k0, a.b_row0 + bn, bar);
-                }
-                if (++slot == kPairStages) {
-                    slot = 0;
-                    phase ^= 1;
-                }
-            }
-        }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
-        // the pair's matrix instructions
-        int slot = 0, it = 0;
-        uint32_t phase = 0;
-        bool ok = true;
-        for (int t = pair; t < tiles && ok; t += pairs, ++it) {
-            const int acc = it & 1;
-            if (!(ok = bar_wait_cluster(tempty + 8 * acc, ((it >> 1) & 1) ^ 1, dead)))
-                break;
-            tc_fence_after();
-            for (int kb = 0; kb < kblocks; ++kb) {
-                if (!(ok = bar_wait_cluster(full + 8 * slot, phase, dead)))
-                    break;
-                tc_fence_after();
-                const uint32_t sa = ring + slot * kPairStageBytes, sb = sa + kPairStageBytes / 2;
-                const uint64_t da = smem_desc(sa, A_MN ? 8192 : 16, 1024);
-                const uint64_t db = smem_desc(sb, B_MN ? 8192 : 16, 1024);
-#pragma unroll
-                for (int k = 0; k < kPairK / 16; ++k)  // 16 of K: 32 bytes, or 16 rows of 128 bytes
-                    mma_f16<2>(tmem + acc * kPairN, da + k * (A_MN ? 128 : 2),
-                               db + k * (B_MN ? 128 : 2), kIdesc, (kb | k) != 0);
-                mma_commit_pair(empty + 8 * slot);
-                if (++slot == kPairStages) {
-                    slot = 0;
-                    phase ^= 1;
-                }
-            }
-            if (ok)
-                mma_commit_pair(tfull + 8 * acc);
-        }
-    } else if (warp >= 4) {
-        // epilogue: thread = one row of this CTA's 128, all 256 columns
-        const int ew = warp & 3;
-        const uint32_t tempty0 = map_to_rank(tempty, 0);
-        float alpha = 1.f;
-        if constexpr (E == Epi::Weight || E == Epi::Hidden)
-            alpha = __ldg(a.alpha);
-        int it = 0;
-        for (int t = pair; t < tiles; t += pairs, ++it) {
-            int tm, tn;
-            tile_at(t, tiles_m, a.tiles_n, tm, tn);
-            const int acc = it & 1;
             const int row = tm * kPairM + static_cast<int>(rank) * 128 + ew * 32 + lane;
-            const int c0 = tn * kPairN;
-            if (!bar_wait_cluster(tfull + 8 * acc, (it >> 1) & 1, dead))
-                break;
-            tc_fence_after();
-            const uint32_t src = tmem + acc * kPairN + (static_cast<uint32_t>(ew * 32) << 16);
-            uint32_t buf[2][32];
-            tmem_ld32(src, buf[0]);
-            tmem_wait_ld(buf[0]);
-
-            [[maybe_unused]] float m = -INFINITY, d = 0.f;
-            [[maybe_unused]] int best = 0, y = -1;
-            [[maybe_unused]] float l2 = 0.f, rs = 0.f;
-            [[maybe_unused]] int64_t out_row = -1;
+            const int c0 = tn * kPairN + half * 128;
             const bool live = row < n;
-            if constexpr (E == Epi::Stats || E == Epi::Grad)
-                y = live ? __ldg(a.tgt + row) - a.b_row0 : -1;
-            if constexpr (E == Epi::Grad)
-                if (live) {
-                    l2 = __ldg(a.l2 + row);
-                    rs = __ldg(a.rs + row);
-                }
-            if constexpr (E == Epi::Hidden)
-                if (live)
-                    out_row = a.last ? __ldg(a.idx + row) : row;
-            const int limit = static_cast<int>(min(a.V, static_cast<int64_t>(INT32_MAX)));
+            const uint32_t lanes = tmem + half * 128 + (static_cast<uint32_t>(ew * 32) << 16);
+            if constexpr (CHUNKED) {
+                float x[128];
+                for (int kb0 = 0; kb0 < kblocks; kb0 += run, ++it) {
+                    const int acc = it & 1;
+                    if (!(ok = bar_wait_cluster(tfull + 8 * acc, (it >> 1) & 1, dead)))
+                        break;
+                    tc_fence_after();
+                    uint32_t buf[2][16];
+                    tmem_ld16(lanes + acc * kPairN, buf[0]);
 #pragma unroll
-            for (int c = 0; c < kPairN / 32; ++c) {
-                uint32_t(&r)[32] = buf[c & 1];
-                if (c + 1 < kPairN / 32)
-                    tmem_ld32(src + 32 * (c + 1), buf[(c + 1) & 1]);
-                const int col = c0 + 32 * c;
-                if constexpr (E == Epi::Stats || E == Epi::Greedy) {
-                    stats_chunk<E == Epi::Greedy>(r, col, limit, m, d, best);
-                    if constexpr (E == Epi::Stats)
-                        if (y >= col && y < col + 32) {
-                            float v = 0.f;
+                    for (int c = 0; c < 8; ++c) {
+                        tmem_wait_ld(buf[c & 1]);
+                        if (c + 1 < 8)
+                            tmem_ld16(lanes + acc * kPairN + 16 * (c + 1), buf[(c + 1) & 1]);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float v = __uint_as_float(buf[c & 1][i]);
+                            x[16 * c + i] = kb0 ? x[16 * c + i] + v : v;
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        bar_arrive_cluster(tempty0 + 8 * acc);
+                }
+                if (!ok)
+                    break;
+                if constexpr (E == Epi::Stats) {  // the target's term is left out
+                    const int y = live ? __ldg(a.tgt + row) - c0 : -1;
+                    if (y >= 0 && y < 128) {
+#pragma unroll
+                        for (int i = 0; i < 128; ++i)
+                            x[i] = y == i ? -INFINITY : x[i];
+                    }
+                }
+                float m = -INFINITY, d = 0.f;
+                int best = 0;
+                stats_chunk<E == Epi::Greedy, 0>(x, c0, limit, m, d, best);
+                stats_chunk<E == Epi::Greedy, 32>(x, c0 + 32, limit, m, d, best);
+                stats_chunk<E == Epi::Greedy, 64>(x, c0 + 64, limit, m, d, best);
+                stats_chunk<E == Epi::Greedy, 96>(x, c0 + 96, limit, m, d, best);
+                if (live) {
+                    const int64_t at = (2 * tn + half) * a.ldp + row;
+                    a.part[at] = make_float2(m == -INFINITY ? m : shift_of(m), d);
+                    if constexpr (E == Epi::Greedy) {
+                        a.part_idx[at] = best;
+                        a.part_max[at] = m;
+                    }
+                }
+            } else {
+                const int acc = it & 1;
+                if (!(ok = bar_wait_cluster(tfull + 8 * acc, (it >> 1) & 1, dead)))
+                    break;
+                ++it;
+                tc_fence_after();
+                [[maybe_unused]] int64_t out_row = row;
+                [[maybe_unused]] int y = -1, inside = 0;  // columns with a gradient: none of an unlisted row
+                [[maybe_unused]] float l2 = 0.f, rs = 0.f, gy = 0.f;
+                if constexpr (E == Epi::Grad)
+                    if (live) {
+                        y = __ldg(a.tgt + row) - a.b_row0;
+                        inside = limit;
+                        l2 = __ldg(a.l2 + row);
+                        rs = __ldg(a.rs + row);
+                        gy = __ldg(a.gy + row);
+                    }
+                if constexpr (E == Epi::Hidden)
+                    if (live && a.last)
+                        out_row = __ldg(a.idx + row);
+                uint32_t buf[2][32];
+                tmem_ld32(lanes + acc * kPairN, buf[0]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    tmem_wait_ld(buf[c & 1]);
+                    if (c + 1 < 4)
+                        tmem_ld32(lanes + acc * kPairN + 32 * (c + 1), buf[(c + 1) & 1]);
+                    uint32_t(&r)[32] = buf[c & 1];
+                    const int col = c0 + 32 * c;
+                    float f[32];
+                    if constexpr (E == Epi::Grad) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const float p = exp2_shift(__uint_as_float(r[i]), l2) * rs;
+                            f[i] = col + i < inside ? (y == col + i ? gy : p) : 0.f;
+                        }
+                        store_chunk<T>(static_cast<T *>(a.g) + row * a.ldg, col, a.ldg, f, 1);
+                    } else if constexpr (E == Epi::Weight) {
+                        if (row < a.rows && col < a.cols) {
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                v = y == col + i ? __uint_as_float(r[i]) : v;
-                            a.xy[row] = v;
+                                f[i] = kblocks ? __uint_as_float(r[i]) * alpha : 0.f;
+                            store_chunk<T>(static_cast<T *>(a.out) + row * a.ldo, col, a.cols, f, a.vec);
                         }
-                } else if constexpr (E == Epi::Grad) {
-                    float f[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float p = exp2_shift(__uint_as_float(r[i]), l2);
-                        f[i] = (live && col + i < limit) ? fmaf(p, rs, y == col + i ? -rs : 0.f) : 0.f;
-                    }
-                    store_chunk<T>(static_cast<T *>(a.g) + row * a.ldg, col, a.ldg, f, 1);
-                } else if constexpr (E == Epi::Weight) {
-                    if (row < a.rows) {
-                        float f[32];
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            f[i] = kblocks ? __uint_as_float(r[i]) * alpha : 0.f;
-                        store_chunk<T>(static_cast<T *>(a.out) + row * a.ldo, col, a.cols, f, a.vec);
-                    }
-                } else {
-                    if (live && col < a.cols) {
-                        float f[32];
+                    } else if (live && col < a.cols) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             f[i] = __uint_as_float(r[i]);
@@ -367,22 +461,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         }
                     }
                 }
-                if (c + 1 < kPairN / 32)
-                    tmem_wait_ld(buf[(c + 1) & 1]);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    bar_arrive_cluster(tempty0 + 8 * acc);
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                bar_arrive_cluster(tempty0 + 8 * acc);
-            if constexpr (E == Epi::Stats || E == Epi::Greedy)
-                if (live) {
-                    a.part[tn * a.ldp + row] = make_float2(m == -INFINITY ? m : shift_of(m), d);
-                    if constexpr (E == Epi::Greedy) {
-                        a.part_idx[tn * a.ldp + row] = best;
-                        // the maximum itself is needed beside its shift
-                        a.xy[tn * a.ldp + row] = m;
-                    }
-                }
         }
     }
     __syncwarp();
@@ -425,22 +508,10 @@ struct SkinnyArgs {
     float2 *part;       // [gridDim.x][ldp]
     int *part_idx;
     float *part_max;
-    float *xy;
     int64_t ldp;
     unsigned *fail;
     uint32_t bf16;
 };
-
-// Merge of two (m, d, index) triples with shifts fl(m log2e): the larger
-// maximum, the lower index of equal ones.
-__device__ __forceinline__ void mdi_merge(float &m, float &d, int &i, float m2, float d2, int i2)
-{
-    if (m2 > m || (m2 == m && i2 < i))
-        i = i2;
-    const float mn = fmaxf(m, m2);
-    d = rescaled(d, m, mn) + rescaled(d2, m2, mn);
-    m = mn;
-}
 
 template <int NG, bool GREEDY>
 __global__ void __launch_bounds__(skinny_threads<NG>(), 1) skinny_kernel(const __grid_constant__ SkinnyArgs a)
@@ -525,31 +596,34 @@ __global__ void __launch_bounds__(skinny_threads<NG>(), 1) skinny_kernel(const _
             }
         }
     } else if (warp == 1 && lane == 0) {
-        int slot = 0;
+        int slot = 0, it = 0;
         uint32_t phase = 0;
         bool ok = true;
         for (int t = 0; t < tiles && ok; ++t) {
-            const int acc = t & 1;
-            if (!(ok = bar_wait(tempty + 8 * acc, ((t >> 1) & 1) ^ 1, dead)))
-                break;
-            tc_fence_after();
-            for (int kb = 0; kb < a.kblocks; ++kb) {
-                if (!(ok = bar_wait(full + 8 * slot, phase, dead)))
+            for (int kb0 = 0; ok && kb0 < a.kblocks; kb0 += kChunk, ++it) {
+                const int acc = it & 1;
+                if (!(ok = bar_wait(tempty + 8 * acc, ((it >> 1) & 1) ^ 1, dead)))
                     break;
                 tc_fence_after();
-                const uint32_t sw = ring + slot * kStage;
-                const uint64_t da = smem_desc(sw, 16, 1024), db = smem_desc(sw + kSkinnyStageW, 16, 1024);
+                const int kb1 = min(kb0 + kChunk, a.kblocks);
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!(ok = bar_wait(full + 8 * slot, phase, dead)))
+                        break;
+                    tc_fence_after();
+                    const uint32_t sw = ring + slot * kStage;
+                    const uint64_t da = smem_desc(sw, 16, 1024), db = smem_desc(sw + kSkinnyStageW, 16, 1024);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_f16<1>(tmem + acc * kN, da + 2 * k, db + 2 * k, idesc, (kb | k) != 0);
-                mma_commit(empty + 8 * slot);
-                if (++slot == kStages) {
-                    slot = 0;
-                    phase ^= 1;
+                    for (int k = 0; k < 4; ++k)
+                        mma_f16<1>(tmem + acc * kN, da + 2 * k, db + 2 * k, idesc, kb != kb0 || k != 0);
+                    mma_commit(empty + 8 * slot);
+                    if (++slot == kStages) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
                 }
+                if (ok)
+                    mma_commit(tfull + 8 * acc);
             }
-            if (ok)
-                mma_commit(tfull + 8 * acc);
         }
     } else if (warp >= 4) {
         // lane = a vocabulary row, column = a hidden state; each thread keeps the
@@ -564,32 +638,55 @@ __global__ void __launch_bounds__(skinny_threads<NG>(), 1) skinny_kernel(const _
             best[j] = INT32_MAX;
         }
         const int live = min(max(n - 32 * group, 0), 32);
-        for (int t = 0; t < tiles; ++t) {
-            const int acc = t & 1;
-            if (!bar_wait(tfull + 8 * acc, (t >> 1) & 1, dead))
+        int it = 0;
+        bool ok = true;
+        for (int t = 0; t < tiles && ok; ++t) {
+            float sum[32];
+            for (int kb0 = 0; kb0 < a.kblocks; kb0 += kChunk, ++it) {
+                const int acc = it & 1;
+                if (!(ok = bar_wait(tfull + 8 * acc, (it >> 1) & 1, dead)))
+                    break;
+                tc_fence_after();
+                const uint32_t src = tmem + acc * kN + 32 * group + (static_cast<uint32_t>(ew * 32) << 16);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t r[16];
+                    tmem_ld16(src + 16 * c, r);
+                    tmem_wait_ld(r);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        sum[16 * c + j] = kb0 ? sum[16 * c + j] + __uint_as_float(r[j]) : __uint_as_float(r[j]);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    bar_arrive(tempty + 8 * acc);
+            }
+            if (!ok)
                 break;
-            tc_fence_after();
-            uint32_t r[32];
-            tmem_ld32(tmem + acc * kN + 32 * group + (static_cast<uint32_t>(ew * 32) << 16), r);
-            tmem_wait_ld(r);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                bar_arrive(tempty + 8 * acc);
             const int64_t v = v0 + 128 * t + ew * 32 + lane;
             if (v < v1) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
                     if (j < live) {
-                        const float x = __uint_as_float(r[j]);
-                        if (x > m[j]) {
-                            d[j] = rescaled(d[j], m[j], x);
-                            m[j] = x;
-                            best[j] = static_cast<int>(v);
+                        const float x = sum[j];
+                        if constexpr (GREEDY) {
+                            if (x > m[j]) {
+                                d[j] = rescaled_others(d[j], m[j], x);
+                                m[j] = x;
+                                best[j] = static_cast<int>(v);
+                            } else {
+                                d[j] += exp2_shift(x, finite_shift(m[j]));
+                            }
+                        } else {
+                            if (tgt[32 * group + j] == v)
+                                continue;  // the target's term is left out
+                            if (x > m[j]) {
+                                d[j] = rescaled(d[j], m[j], x);
+                                m[j] = x;
+                            }
+                            d[j] += exp2_shift(x, finite_shift(m[j]));
                         }
-                        d[j] += exp2_shift(x, finite_shift(m[j]));
-                        if (!GREEDY && tgt[32 * group + j] == v)
-                            a.xy[32 * group + j] = x;
                     }
                 }
             }
@@ -601,8 +698,14 @@ __global__ void __launch_bounds__(skinny_threads<NG>(), 1) skinny_kernel(const _
                 for (int off = 16; off > 0; off >>= 1) {
                     const float m2 = __shfl_xor_sync(0xffffffffu, m[j], off);
                     const float d2 = __shfl_xor_sync(0xffffffffu, d[j], off);
-                    const int i2 = __shfl_xor_sync(0xffffffffu, best[j], off);
-                    mdi_merge(m[j], d[j], best[j], m2, d2, i2);
+                    if constexpr (GREEDY) {
+                        const int i2 = __shfl_xor_sync(0xffffffffu, best[j], off);
+                        best_merge(m[j], d[j], best[j], m2, d2, i2);
+                    } else {
+                        const float mn = fmaxf(m[j], m2);
+                        d[j] = rescaled(d[j], m[j], mn) + rescaled(d2, m2, mn);
+                        m[j] = mn;
+                    }
                 }
                 if (lane == 0) {
                     sm[warp - 4][j] = m[j];
@@ -627,8 +730,16 @@ __global__ void __launch_bounds__(skinny_threads<NG>(), 1) skinny_kernel(const _
         float m = sm[4 * g][j], d = sd[4 * g][j];
         int best = si[4 * g][j];
 #pragma unroll
-        for (int q = 1; q < 4; ++q)
-            mdi_merge(m, d, best, sm[4 * g + q][j], sd[4 * g + q][j], si[4 * g + q][j]);
+        for (int q = 1; q < 4; ++q) {
+            const float m2 = sm[4 * g + q][j], d2 = sd[4 * g + q][j];
+            if constexpr (GREEDY) {
+                best_merge(m, d, best, m2, d2, si[4 * g + q][j]);
+            } else {
+                const float mn = fmaxf(m, m2);
+                d = rescaled(d, m, mn) + rescaled(d2, m2, mn);
+                m = mn;
+            }
+        }
         const int64_t at = blockIdx.x * a.ldp + threadIdx.x;
         a.part[at] = make_float2(m == -INFINITY ? m : shift_of(m), d);
         if (GREEDY) {
@@ -757,9 +868,35 @@ __global__ void __launch_bounds__(NT) lin_prep_kernel(const PrepArgs a)
     }
 }
 
+// sum_k a[k] b[k] of two rows in fp32, by a warp (every lane gets it).
+template <typename T>
+__device__ __forceinline__ float row_dot(const T *a, const T *b, int64_t K, bool vec)
+{
+    const int lane = threadIdx.x & 31;
+    float s0 = 0.f, s1 = 0.f;
+    int64_t k = 0;
+    if (vec) {
+#pragma unroll 4
+        for (int64_t j = lane; j < K / 8; j += 32) {
+            float x[8], y[8];
+            Elem<T>::unpack(__ldg(reinterpret_cast<const uint4 *>(a) + j), x);
+            Elem<T>::unpack(__ldg(reinterpret_cast<const uint4 *>(b) + j), y);
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                s0 = fmaf(x[i], y[i], s0);
+                s1 = fmaf(x[i + 1], y[i + 1], s1);
+            }
+        }
+        k = K / 8 * 8;
+    }
+    for (int64_t j = k + lane; j < K; j += 32)
+        s0 = fmaf(Elem<T>::load(a + j), Elem<T>::load(b + j), s0);
+    return warp_sum(s0 + s1);
+}
+
 // Packed copy of the listed rows (dst [.., lds], zeros in columns K .. lds and in
-// the rows up to the next multiple of `pad`), and zeros in the rows of `zero`
-// that are not listed.  One CTA per row at a time.
+// the rows up to the next multiple of `pad`), the logits of their targets, and
+// zeros in the rows of `zero` that are not listed.  One warp per row.
 struct GatherArgs {
     const void *src;
     int64_t ss;
@@ -771,46 +908,69 @@ struct GatherArgs {
     int64_t K;
     int pad;
     int vec;            // src allows 16-byte loads
+    // targets' logits
+    const void *w;      // NULL: none
+    int64_t ws;
+    int wvec;           // w and src allow 16-byte loads
+    const int *tgt;
+    float *xy;          // forward: x_y
+    const float *l2, *rs;
+    float *gy;          // backward: (p_y - 1) times the row's factor
     // backward: unlisted rows of the hidden gradient
     void *zero;
     int64_t zs;
+    int zvec;           // zero allows 16-byte stores
     int64_t M, V, ignore_index;
     const int64_t *targets;
 };
 
-template <int NT>
+template <typename T, int NT>
 __global__ void __launch_bounds__(NT) lin_gather_kernel(const GatherArgs a)
 {
+    const int lane = threadIdx.x & 31;
+    const int64_t first = blockIdx.x * int64_t{NT / 32} + (threadIdx.x >> 5);
+    const int64_t step = gridDim.x * int64_t{NT / 32};
     const int64_t n = a.n_ptr ? *a.n_ptr : a.n_host;
     const int64_t rows = (n + a.pad - 1) / a.pad * a.pad;
-    for (int64_t i = blockIdx.x; i < rows; i += gridDim.x) {
-        unsigned short *d = static_cast<unsigned short *>(a.dst) + i * a.lds;
+    const T zero_value = T(0.f);
+    for (int64_t i = first; i < rows; i += step) {
+        T *d = static_cast<T *>(a.dst) + i * a.lds;
         if (i >= n) {
-            for (int64_t j = threadIdx.x; j < a.lds / 8; j += NT)
+            for (int64_t j = lane; j < a.lds / 8; j += 32)
                 reinterpret_cast<uint4 *>(d)[j] = make_uint4(0, 0, 0, 0);
             continue;
         }
-        const unsigned short *s = static_cast<const unsigned short *>(a.src) +
-                                  (a.idx ? static_cast<int64_t>(a.idx[i]) : i) * a.ss;
+        const T *s = static_cast<const T *>(a.src) + (a.idx ? static_cast<int64_t>(a.idx[i]) : i) * a.ss;
+        int64_t done = 0;
         if (a.vec) {  // K may end inside the last vector: the rest is zeroed one by one
-            const int64_t nv = a.K / 8;
-            for (int64_t j = threadIdx.x; j < nv; j += NT)
+            done = a.K / 8 * 8;
+#pragma unroll 4
+            for (int64_t j = lane; j < a.K / 8; j += 32)
                 reinterpret_cast<uint4 *>(d)[j] = __ldg(reinterpret_cast<const uint4 *>(s) + j);
-            for (int64_t j = nv * 8 + threadIdx.x; j < a.lds; j += NT)
-                d[j] = j < a.K ? s[j] : 0;
-        } else {
-            for (int64_t j = threadIdx.x; j < a.lds; j += NT)
-                d[j] = j < a.K ? s[j] : 0;
+        }
+        for (int64_t j = done + lane; j < a.lds; j += 32)
+            d[j] = j < a.K ? s[j] : zero_value;
+        if (a.w) {
+            const float x = row_dot(s, static_cast<const T *>(a.w) + int64_t{a.tgt[i]} * a.ws, a.K, a.wvec);
+            if (lane == 0) {
+                if (a.xy)
+                    a.xy[i] = x;
+                else  // e^(x_y - lse) - 1, from the difference itself
+                    a.gy[i] = expm1f(fmaf(x, kLog2e, -a.l2[i]) * kLn2) * a.rs[i];
+            }
         }
     }
     if (a.zero)
-        for (int64_t i = blockIdx.x; i < a.M; i += gridDim.x) {
+        for (int64_t i = first; i < a.M; i += step) {
             const int64_t y = a.targets[i];
             if (y != a.ignore_index && y >= 0 && y < a.V)
                 continue;
-            unsigned short *z = static_cast<unsigned short *>(a.zero) + i * a.zs;
-            for (int64_t j = threadIdx.x; j < a.K; j += NT)
-                z[j] = 0;
+            T *z = static_cast<T *>(a.zero) + i * a.zs;
+            const int64_t whole = a.zvec ? a.K / 8 : 0;
+            for (int64_t j = lane; j < whole; j += 32)
+                reinterpret_cast<uint4 *>(z)[j] = make_uint4(0, 0, 0, 0);
+            for (int64_t j = whole * 8 + lane; j < a.K; j += 32)
+                z[j] = zero_value;
         }
 }
 
@@ -828,65 +988,103 @@ struct MergeArgs {
     const int *idx;
     const float *xy;
     float *row_loss, *lse;
+    // arg max: its logit is formed again from these rows
     int64_t *token;
     float *logprob;
+    const void *h, *w;
+    int64_t hs, ws, K;
+    int vec;
 };
 
+// ln(1 + others / e^x_y) for the others' sum d about the shift s (-inf: none),
+// and ln(others + e^x_y).
+__device__ __forceinline__ float loss_beside(float s, float d, float xy, float &lse)
+{
+    lse = __int_as_float(0x7fc00000);
+    if (!(xy < INFINITY))
+        return lse;
+    if (s == -INFINITY && d == 0.f) {  // the only class
+        lse = xy;
+        return xy - xy;
+    }
+    const float shift = s == -INFINITY ? 0.f : s;
+    const float t = fmaf(xy, kLog2e, -shift);  // log2 of e^x_y about the shift
+    if (t > -20.f) {
+        const float loss = log1pf(d * exp2f(-t));
+        lse = xy + loss;
+        return loss;
+    }
+    // an unlikely target: others / e^x_y might overflow
+    const float l = logf(d + exp2f(t));
+    lse = fmaf(shift, kLn2, l);
+    return l - t * kLn2;
+}
+
 // 32 rows x 8 shares of the partials per CTA.
-template <bool GREEDY>
+template <bool GREEDY, typename T>
 __global__ void __launch_bounds__(256) lin_merge_kernel(const MergeArgs a)
 {
-    __shared__ float ss[8][32], sd[8][32], sx[8][32];
+    __shared__ float ss[8][32], sd[8][32];
     __shared__ int si[8][32];
     const int n = a.n_ptr ? *a.n_ptr : a.n_host;
     const int lane = threadIdx.x & 31, share = threadIdx.x >> 5;
-    const int64_t row = blockIdx.x * int64_t{32} + lane;
-    if (blockIdx.x * int64_t{32} >= n)
+    const int64_t row0 = blockIdx.x * int64_t{32}, row = row0 + lane;
+    if (row0 >= n)
         return;
-    float s = -INFINITY, d = 0.f, top = -INFINITY;
+    // GREEDY: the maximum and the others' sum; else the shift and the sum
+    float s = -INFINITY, d = 0.f;
     int best = INT32_MAX;
+    const auto add = [&](float s2, float d2, int i2) {
+        if constexpr (GREEDY) {
+            best_merge(s, d, best, s2, d2, i2);
+        } else {
+            if (s2 == -INFINITY && d2 != 0.f)
+                d += d2;  // a NaN among nothing but -inf
+            md_merge(s, d, s2, d2);
+        }
+    };
     if (row < n) {
-        const int lo = a.parts * share / 8, hi = a.parts * (share + 1) / 8;
+        const int lo = static_cast<int>(int64_t{a.parts} * share / 8);
+        const int hi = static_cast<int>(int64_t{a.parts} * (share + 1) / 8);
 #pragma unroll 4
         for (int p = lo; p < hi; ++p) {
-            const float2 q = a.part[p * a.ldp + row];
-            if (q.x == -INFINITY && q.y != 0.f)
-                d += q.y;  // a NaN among nothing but -inf
-            md_merge(s, d, q.x, q.y);
-            if (GREEDY) {
-                const float x = a.part_max[p * a.ldp + row];
-                if (x > top) {
-                    top = x;
-                    best = a.part_idx[p * a.ldp + row];
-                }
-            }
+            const int64_t at = p * a.ldp + row;
+            const float2 q = a.part[at];
+            add(GREEDY ? a.part_max[at] : q.x, q.y, GREEDY ? a.part_idx[at] : 0);
         }
     }
     ss[share][lane] = s;
     sd[share][lane] = d;
-    if (GREEDY) {
-        sx[share][lane] = top;
-        si[share][lane] = best;
-    }
+    si[share][lane] = best;
     __syncthreads();
     if (share == 0 && row < n) {
-        for (int q = 1; q < 8; ++q) {
-            if (ss[q][lane] == -INFINITY && sd[q][lane] != 0.f)
-                d += sd[q][lane];
-            md_merge(s, d, ss[q][lane], sd[q][lane]);
-            if (GREEDY && sx[q][lane] > top) {
-                top = sx[q][lane];
-                best = si[q][lane];
-            }
-        }
-        if (GREEDY) {
+        for (int q = 1; q < 8; ++q)
+            add(ss[q][lane], sd[q][lane], si[q][lane]);
+        if constexpr (GREEDY) {
             a.token[row] = best == INT32_MAX ? 0 : best;
-            a.logprob[row] = -row_loss_from(s, d, top);
+            ss[0][lane] = s;
+            sd[0][lane] = d;
+            si[0][lane] = best;
         } else {
             const int64_t out = a.idx[row];
-            a.row_loss[out] = row_loss_from(s, d, a.xy[row]);
+            float lse;
+            a.row_loss[out] = loss_beside(s, d, a.xy[row], lse);
             if (a.lse)
-                a.lse[out] = fmaf(s, kLn2, logf(d));
+                a.lse[out] = lse;
+        }
+    }
+    if constexpr (GREEDY) {
+        __syncthreads();
+        for (int r = share; r < 32 && row0 + r < n; r += 8) {
+            const int token = si[0][r];
+            float lse, lp = __int_as_float(0x7fc00000);  // nothing but NaN or -inf
+            if (token != INT32_MAX) {
+                const float x = row_dot(static_cast<const T *>(a.h) + (row0 + r) * a.hs,
+                                        static_cast<const T *>(a.w) + token * a.ws, a.K, a.vec);
+                lp = -loss_beside(shift_of(ss[0][r]), sd[0][r], x, lse);
+            }
+            if (lane == 0)
+                a.logprob[row0 + r] = lp;
         }
     }
 }
