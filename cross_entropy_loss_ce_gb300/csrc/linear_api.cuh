@@ -87,10 +87,9 @@ struct HeadScratch {
     unsigned short *h;  // packed hidden states
     unsigned short *w;  // packed weights (rows a tensor map cannot read)
     float2 *part;
-    int *part_idx;
-    float *part_max;
+    float4 *best;
     unsigned short *g;
-    float *acc;
+    float *acc, *slices;
 };
 
 struct HeadShape {
@@ -102,6 +101,7 @@ struct HeadShape {
     int64_t parts;      // partial pairs of a row
     int64_t vp;         // backward: vocabulary rows of a piece
     int64_t pieces;
+    int64_t slices;     // split tiles' sums, at most
 };
 
 enum class HeadOp { Fwd, Bwd, Greedy };
@@ -129,13 +129,13 @@ HeadScratch carve(Carver &c, const HeadShape &s, HeadOp op, bool want_hidden)
         r.g = c.take<unsigned short>(s.mp * s.vp);
         if (want_hidden && s.pieces > 1)
             r.acc = c.take<float>(s.mp * round_up(s.K, kPairN));
+        r.slices = c.take<float>(s.slices * kPairM * kPairN);
     } else {
-        r.part = c.take<float2>(s.parts * s.mp);
-        if (op == HeadOp::Fwd)
+        if (op == HeadOp::Fwd) {
+            r.part = c.take<float2>(s.parts * s.mp);
             r.xy = c.take<float>(s.mp);
-        else {
-            r.part_idx = c.take<int>(s.parts * s.mp);
-            r.part_max = c.take<float>(s.parts * s.mp);
+        } else {
+            r.best = c.take<float4>(s.parts * s.mp);
         }
     }
     return r;
@@ -171,8 +171,17 @@ cudaError_t launch_pair(const Call &call, const PairArgs &a, int64_t max_tiles)
     const cudaError_t e = configure_smem(reinterpret_cast<const void *>(fn), call.device, kPairSmem);
     if (e != cudaSuccess)
         return e;
-    const int64_t pairs = max_tiles < call.sms / 2 ? max_tiles : call.sms / 2;
+    constexpr bool split = E == Epi::Weight || E == Epi::Hidden;
+    const int64_t most = call.sms / 2 < kSplitUnits / 4 ? call.sms / 2 : kSplitUnits / 4;
+    const int64_t pairs = split || max_tiles > most ? most : max_tiles;
     fn<<<static_cast<unsigned>(2 * pairs), kPairThreads, kPairSmem, call.stream>>>(a);
+    if constexpr (split) {
+        const unsigned grid = static_cast<unsigned>(4 * call.sms);
+        if (call.dtype == GBCE_BF16)
+            lin_slices_kernel<E, __nv_bfloat16><<<grid, 256, 0, call.stream>>>(a, static_cast<int>(pairs));
+        else
+            lin_slices_kernel<E, __half><<<grid, 256, 0, call.stream>>>(a, static_cast<int>(pairs));
+    }
     return cudaGetLastError();
 }
 
@@ -240,6 +249,9 @@ HeadShape head_shape(const Call &call, const void *hidden, int64_t hs, const voi
         s.pieces = (V + vp - 1) / vp;
         s.vp = round_up((V + s.pieces - 1) / s.pieces, kPairN);
         s.pieces = (V + s.vp - 1) / s.vp;
+        const int64_t rows = s.mp > s.vp ? s.mp : s.vp;
+        const int64_t units = rows / kPairM * ((K + kPairN - 1) / kPairN) * kSplitMax;
+        s.slices = units < kSplitUnits ? units : kSplitUnits;
     }
     return s;
 }
@@ -288,10 +300,8 @@ cudaError_t launch_head(const Call &call, const HeadShape &s, const HeadScratch 
     cudaError_t e;
     const int kblocks = static_cast<int>((s.K + 63) / 64);
     m.part = r.part;
-    m.part_idx = r.part_idx;
-    m.part_max = r.part_max;
+    m.best = r.best;
     m.parts = static_cast<int>(s.parts);
-    m.ldp = s.mp;
     m.n_ptr = GREEDY ? nullptr : r.rows;
     m.n_host = static_cast<int>(s.M);
     m.idx = r.idx;
@@ -308,9 +318,8 @@ cudaError_t launch_head(const Call &call, const HeadShape &s, const HeadScratch 
         a.V = s.V;
         a.tgt = r.tgt;
         a.part = r.part;
-        a.part_idx = r.part_idx;
-        a.part_max = r.part_max;
-        a.ldp = s.mp;
+        a.best = r.best;
+        a.ldp = s.parts;
         a.fail = GREEDY ? nullptr : r.fail;
         a.bf16 = call.dtype == GBCE_BF16;
         e = s.mp == 32 ? launch_skinny_ng<1, GREEDY>(call, a, s.parts)
@@ -326,9 +335,8 @@ cudaError_t launch_head(const Call &call, const HeadShape &s, const HeadScratch 
         a.kblocks = kblocks;
         a.fail = GREEDY ? nullptr : r.fail;
         a.part = r.part;
-        a.part_idx = r.part_idx;
-        a.part_max = r.part_max;
-        a.ldp = s.mp;
+        a.best = r.best;
+        a.ldp = s.parts;
         a.tgt = r.tgt;
         a.V = s.V;
         e = launch_pair<GREEDY ? Epi::Greedy : Epi::Stats>(call, a, s.mp / kPairM * a.tiles_n);
@@ -341,11 +349,12 @@ cudaError_t launch_head(const Call &call, const HeadShape &s, const HeadScratch 
     m.ws = wstride;
     m.K = s.K;
     m.vec = mappable(h, hstride, hrows) && mappable(w, wstride, s.V);
-    const unsigned grid = static_cast<unsigned>((s.M + 31) / 32);
-    if (!GREEDY || call.dtype == GBCE_BF16)  // the loss reads no 16-bit operand
-        lin_merge_kernel<GREEDY, __nv_bfloat16><<<grid, 256, 0, call.stream>>>(m);
+    if constexpr (!GREEDY)
+        lin_merge_kernel<256><<<static_cast<unsigned>((s.M + 7) / 8), 256, 0, call.stream>>>(m);
+    else if (call.dtype == GBCE_BF16)
+        lin_token_kernel<__nv_bfloat16, 128><<<static_cast<unsigned>(s.M), 128, 0, call.stream>>>(m);
     else
-        lin_merge_kernel<GREEDY, __half><<<grid, 256, 0, call.stream>>>(m);
+        lin_token_kernel<__half, 128><<<static_cast<unsigned>(s.M), 128, 0, call.stream>>>(m);
     return cudaGetLastError();
 }
 
@@ -427,6 +436,7 @@ cudaError_t launch_linear_bwd(const Call &call, const HeadShape &s, const HeadSc
         a->ldg = s.vp;
         a->cols = s.K;
         a->acc = r.acc;
+        a->slices = r.slices;
         a->lda = round_up(s.K, kPairN);
     }
     grad.kblocks = static_cast<int>((s.K + 63) / 64);

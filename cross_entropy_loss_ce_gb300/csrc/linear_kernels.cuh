@@ -66,9 +66,8 @@ struct PairArgs {
     int b_row0;         // first row of B along the axis of W's rows (piece offset)
     unsigned *fail;
     // Stats, Greedy
-    float2 *part;       // [2 tiles_n][ldp] (s, d) pairs, one for each 128 columns
-    int *part_idx;      // Greedy: the arg max of each
-    float *part_max;    // Greedy: the maximum of each
+    float2 *part;       // Stats: [row][ldp] (s, d) pairs, one for each 128 columns
+    float4 *best;       // Greedy: [row][ldp] (maximum, others' sum, arg max)
     int64_t ldp;
     const int *tgt;
     int64_t V;          // columns of this launch's logits (vocabulary, or end of it) from row 0 of W
@@ -86,7 +85,54 @@ struct PairArgs {
     float *acc;         // Hidden: fp32 sums over pieces, [.., lda]
     int64_t lda;
     int first, last;    // Hidden: the first piece does not read acc, the last one writes out
+    float *slices;      // Weight, Hidden: kSplitUnits sums of kPairM x kPairN, for split tiles
 };
+
+// The tiles of a product that fill no whole wave of the CTA pairs, cut along K:
+// 248 tiles on 76 pairs take 4 waves, of which the last is a quarter full; its
+// 20 tiles in 3 slices each make it a third of a wave.  The first `whole` tiles
+// are done as they are; then come `tail` tiles in `slices` slices, slice by
+// slice, whose sums go to memory and are added in order by lin_slices_kernel.
+struct Split {
+    int whole, tail, slices;
+};
+
+constexpr int kSplitUnits = 4 * 80;  // slices of a launch, at most
+constexpr int kSplitMax = 8;         // slices of a tile, at most
+
+// Costs in k-steps of one tile: a slice takes its steps and about 6 more to be
+// written, and the sums' addition about 30 (measured around 8 us).  The tail is
+// the last, partial wave, or that and a whole one.
+__host__ __device__ inline Split split_of(int tiles, int pairs, int kblocks)
+{
+    Split best{tiles, 0, 1};
+    int64_t least = static_cast<int64_t>((tiles + pairs - 1) / pairs) * kblocks;
+    const int rest = tiles % pairs;
+    for (int tail = rest; rest && tail <= tiles && tail <= rest + pairs; tail += pairs)
+        for (int s = 2; s <= kSplitMax && 4 * s <= kblocks && tail * s <= kSplitUnits; ++s) {
+            const int64_t cost = static_cast<int64_t>((tiles - tail) / pairs) * kblocks +
+                                 static_cast<int64_t>((tail * s + pairs - 1) / pairs) * ((kblocks + s - 1) / s + 6) + 30;
+            if (cost < least) {
+                least = cost;
+                best = Split{tiles - tail, tail, s};
+            }
+        }
+    return best;
+}
+
+// One CTA pair's share of a tile: k-steps k0 .. k1, and where a slice's sums go (-1: a whole tile).
+struct Unit {
+    int tile, k0, k1, slice;
+};
+
+__device__ __forceinline__ Unit unit_at(int u, const Split &sp, int kblocks)
+{
+    if (u < sp.whole)
+        return Unit{u, 0, kblocks, -1};
+    const int v = u - sp.whole, s = v / sp.tail, t = v - s * sp.tail;
+    return Unit{sp.whole + t, static_cast<int>(int64_t{kblocks} * s / sp.slices),
+                static_cast<int>(int64_t{kblocks} * (s + 1) / sp.slices), t * sp.slices + s};
+}
 
 __device__ __forceinline__ void tile_at(int t, int tiles_m, int tiles_n, int &m, int &n)
 {
@@ -130,6 +176,13 @@ __device__ __forceinline__ void best_merge(float &m, float &d, int &i, float m2,
     }
 }
 
+// A sum about the shift `from`, about the larger shift `to` (-inf: empty, or a
+// NaN that has to stay).
+__device__ __forceinline__ float shifted(float d, float from, float to)
+{
+    return from == -INFINITY ? d : d * exp2f(from - to);
+}
+
 // 32 logits of one row, x[OFF ..], columns c0 .. c0 + 31 of W's rows, into the
 // running maximum m and sum d = sum exp2(x log2e - fl(m log2e)) (GREEDY: of all
 // but the maximum, whose column is `best`).
@@ -171,14 +224,13 @@ __device__ __forceinline__ void stats_chunk(float (&x)[N], int c0, int limit, fl
     d += d0 + d1;
 }
 
-// 32 values times alpha, rounded once, to out[row, c0 ..] below `cols`.
-template <typename T>
-__device__ __forceinline__ void store_chunk(T *row, int64_t c0, int64_t cols, const float (&f)[32],
-                                            int vec)
+// N values, rounded once, to row[c0 ..] below `cols`.
+template <typename T, int N>
+__device__ __forceinline__ void store_chunk(T *row, int64_t c0, int64_t cols, const float (&f)[N], int vec)
 {
-    if (vec && c0 + 32 <= cols) {
+    if (vec && c0 + N <= cols) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < N / 8; ++q) {
             const float *p = f + 8 * q;
             *reinterpret_cast<uint4 *>(row + c0 + 8 * q) =
                 make_uint4(Elem<T>::pack2(p[0], p[1]), Elem<T>::pack2(p[2], p[3]),
@@ -186,7 +238,7 @@ __device__ __forceinline__ void store_chunk(T *row, int64_t c0, int64_t cols, co
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
+        for (int i = 0; i < N; ++i)
             if (c0 + i < cols)
                 Elem<T>::store(row + c0 + i, f[i]);
     }
@@ -220,6 +272,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const int kblocks = E == Epi::Weight ? (n + kPairK - 1) / kPairK : a.kblocks;
     const int tiles = tiles_m * a.tiles_n;
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const Split sp = LOGITS ? Split{tiles, 0, 1} : split_of(tiles, pairs, kblocks);
+    const int units = sp.whole + sp.tail * sp.slices;
     const int run = CHUNKED ? kChunk : max(kblocks, 1);  // k-steps that stay in tensor memory
 
     if (threadIdx.x == 0) {
@@ -256,12 +310,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             int slot = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (int t = pair; t < tiles && ok; t += pairs) {
+            for (int u = pair; u < units && ok; u += pairs) {
+                const Unit un = unit_at(u, sp, kblocks);
                 int tm, tn;
-                tile_at(t, tiles_m, a.tiles_n, tm, tn);
+                tile_at(un.tile, tiles_m, a.tiles_n, tm, tn);
                 const int am = tm * kPairM + static_cast<int>(rank) * 128;
                 const int bn = tn * kPairN + static_cast<int>(rank) * 128;
-                for (int kb = 0; kb < kblocks; ++kb) {
+                for (int kb = un.k0; kb < un.k1; ++kb) {
                     if (!(ok = bar_wait_cluster(empty + 8 * slot, phase ^ 1, dead)))
                         break;
                     if (rank == 0)
@@ -293,13 +348,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             int slot = 0, it = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (int t = pair; t < tiles && ok; t += pairs) {
-                for (int kb0 = 0; ok && kb0 < max(kblocks, 1); kb0 += run, ++it) {
+            for (int u = pair; u < units && ok; u += pairs) {
+                const Unit un = unit_at(u, sp, kblocks);
+                for (int kb0 = un.k0; ok && (kb0 < un.k1 || kb0 == 0); kb0 += run, ++it) {
                     const int acc = it & 1;
                     if (!(ok = bar_wait_cluster(tempty + 8 * acc, ((it >> 1) & 1) ^ 1, dead)))
                         break;
                     tc_fence_after();
-                    const int kb1 = min(kb0 + run, kblocks);
+                    const int kb1 = min(kb0 + run, un.k1);
                     for (int kb = kb0; kb < kb1; ++kb) {
                         if (!(ok = bar_wait_cluster(full + 8 * slot, phase, dead)))
                             break;
@@ -334,9 +390,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             alpha = __ldg(a.alpha);
         int it = 0;
         bool ok = true;
-        for (int t = pair; t < tiles && ok; t += pairs) {
+        for (int u = pair; u < units && ok; u += pairs) {
+            const Unit un = unit_at(u, sp, kblocks);
             int tm, tn;
-            tile_at(t, tiles_m, a.tiles_n, tm, tn);
+            tile_at(un.tile, tiles_m, a.tiles_n, tm, tn);
             const int row = tm * kPairM + static_cast<int>(rank) * 128 + ew * 32 + lane;
             const int c0 = tn * kPairN + half * 128;
             const bool live = row < n;
@@ -383,12 +440,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 stats_chunk<E == Epi::Greedy, 64>(x, c0 + 64, limit, m, d, best);
                 stats_chunk<E == Epi::Greedy, 96>(x, c0 + 96, limit, m, d, best);
                 if (live) {
-                    const int64_t at = (2 * tn + half) * a.ldp + row;
-                    a.part[at] = make_float2(m == -INFINITY ? m : shift_of(m), d);
-                    if constexpr (E == Epi::Greedy) {
-                        a.part_idx[at] = best;
-                        a.part_max[at] = m;
-                    }
+                    const int64_t at = row * a.ldp + 2 * tn + half;
+                    if constexpr (E == Epi::Greedy)
+                        a.best[at] = make_float4(m, d, __int_as_float(best), 0.f);
+                    else
+                        a.part[at] = make_float2(m == -INFINITY ? m : shift_of(m), d);
                 }
             } else {
                 const int acc = it & 1;
@@ -427,6 +483,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                             f[i] = col + i < inside ? (y == col + i ? gy : p) : 0.f;
                         }
                         store_chunk<T>(static_cast<T *>(a.g) + row * a.ldg, col, a.ldg, f, 1);
+                    } else if (un.slice >= 0) {
+                        float4 *to = reinterpret_cast<float4 *>(
+                            a.slices + (int64_t{un.slice} * kPairM + (row - tm * kPairM)) * kPairN + col - tn * kPairN);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            to[q] = make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
+                                                __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
                     } else if constexpr (E == Epi::Weight) {
                         if (row < a.rows && col < a.cols) {
 #pragma unroll
@@ -482,6 +545,64 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         tmem_free<2>(tmem, 512);
 }
 
+// Adds the slices of a launch's split tiles in order and finishes their sums as
+// pair_gemm_kernel does.  A CTA takes 16 rows of a tile, a thread 16 columns.
+template <Epi E, typename T>
+__global__ void __launch_bounds__(256) lin_slices_kernel(const __grid_constant__ PairArgs a, int pairs)
+{
+    const int n = *a.n_ptr;
+    const int tiles_m = E == Epi::Weight ? a.tiles_m : (n + kPairM - 1) / kPairM;
+    const int kblocks = E == Epi::Weight ? (n + kPairK - 1) / kPairK : a.kblocks;
+    const Split sp = split_of(tiles_m * a.tiles_n, pairs, kblocks);
+    const float alpha = __ldg(a.alpha);
+    for (int b = blockIdx.x; b < sp.tail * 16; b += gridDim.x) {
+        const int t = b >> 4, r = (b & 15) * 16 + (threadIdx.x >> 4), c = (threadIdx.x & 15) * 16;
+        int tm, tn;
+        tile_at(sp.whole + t, tiles_m, a.tiles_n, tm, tn);
+        const int row = tm * kPairM + r, col = tn * kPairN + c;
+        if (row >= (E == Epi::Weight ? a.rows : n) || col >= a.cols)
+            continue;
+        float f[16] = {};
+        for (int s = 0; s < sp.slices; ++s) {
+            const float4 *from = reinterpret_cast<const float4 *>(
+                a.slices + (int64_t{t * sp.slices + s} * kPairM + r) * kPairN + c);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float4 v = __ldcs(from + q);
+                f[4 * q] += v.x;
+                f[4 * q + 1] += v.y;
+                f[4 * q + 2] += v.z;
+                f[4 * q + 3] += v.w;
+            }
+        }
+        int64_t out_row = row;
+        if constexpr (E == Epi::Hidden) {
+            float4 *acc4 = reinterpret_cast<float4 *>(a.acc + row * a.lda + col);
+            if (!a.first) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float4 v = acc4[q];
+                    f[4 * q] += v.x;
+                    f[4 * q + 1] += v.y;
+                    f[4 * q + 2] += v.z;
+                    f[4 * q + 3] += v.w;
+                }
+            }
+            if (!a.last) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    acc4[q] = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
+                continue;
+            }
+            out_row = __ldg(a.idx + row);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            f[i] *= alpha;
+        store_chunk<T>(static_cast<T *>(a.out) + out_row * a.ldo, col, a.cols, f, a.vec);
+    }
+}
+
 // ---------------------------------------------------------------------------
 // at most 64 rows: W streamed once, its rows on the M side
 
@@ -505,9 +626,8 @@ struct SkinnyArgs {
     int kblocks;
     int64_t V;
     const int *tgt;
-    float2 *part;       // [gridDim.x][ldp]
-    int *part_idx;
-    float *part_max;
+    float2 *part;       // [row][ldp], one for each CTA
+    float4 *best;
     int64_t ldp;
     unsigned *fail;
     uint32_t bf16;
@@ -691,28 +811,36 @@ __global__ void __launch_bounds__(skinny_threads<NG>(), 1) skinny_kernel(const _
                 }
             }
         }
+        // each warp turns its 32 x 32 states around in the ring, which is idle once
+        // the last accumulator is full: lane j merges the 32 lanes' states of hidden
+        // state j
+        if (ok && tiles > 0) {
+            float *tm = reinterpret_cast<float *>(dyn + (ring - smem_addr(dyn))) + (warp - 4) * 3 * 32 * 33;
+            float *td = tm + 32 * 33;
+            int *ti = reinterpret_cast<int *>(td + 32 * 33);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            if (j < live) {
-#pragma unroll
-                for (int off = 16; off > 0; off >>= 1) {
-                    const float m2 = __shfl_xor_sync(0xffffffffu, m[j], off);
-                    const float d2 = __shfl_xor_sync(0xffffffffu, d[j], off);
-                    if constexpr (GREEDY) {
-                        const int i2 = __shfl_xor_sync(0xffffffffu, best[j], off);
-                        best_merge(m[j], d[j], best[j], m2, d2, i2);
-                    } else {
-                        const float mn = fmaxf(m[j], m2);
-                        d[j] = rescaled(d[j], m[j], mn) + rescaled(d2, m2, mn);
-                        m[j] = mn;
-                    }
-                }
-                if (lane == 0) {
-                    sm[warp - 4][j] = m[j];
-                    sd[warp - 4][j] = d[j];
-                    si[warp - 4][j] = best[j];
+            for (int j = 0; j < 32; ++j) {
+                tm[lane * 33 + j] = m[j];
+                td[lane * 33 + j] = d[j];
+                if (GREEDY)
+                    ti[lane * 33 + j] = best[j];
+            }
+            __syncwarp();
+            float mt = tm[lane], dt = td[lane];
+            int it = GREEDY ? ti[lane] : 0;
+            for (int l = 1; l < 32; ++l) {
+                const float m2 = tm[l * 33 + lane], d2 = td[l * 33 + lane];
+                if constexpr (GREEDY) {
+                    best_merge(mt, dt, it, m2, d2, ti[l * 33 + lane]);
+                } else {
+                    const float mn = fmaxf(mt, m2);
+                    dt = rescaled(dt, mt, mn) + rescaled(d2, m2, mn);
+                    mt = mn;
                 }
             }
+            sm[warp - 4][lane] = mt;
+            sd[warp - 4][lane] = dt;
+            si[warp - 4][lane] = it;
         }
     }
     __syncwarp();
@@ -740,12 +868,11 @@ __global__ void __launch_bounds__(skinny_threads<NG>(), 1) skinny_kernel(const _
                 m = mn;
             }
         }
-        const int64_t at = blockIdx.x * a.ldp + threadIdx.x;
-        a.part[at] = make_float2(m == -INFINITY ? m : shift_of(m), d);
-        if (GREEDY) {
-            a.part_idx[at] = best;
-            a.part_max[at] = m;
-        }
+        const int64_t at = threadIdx.x * a.ldp + blockIdx.x;
+        if constexpr (GREEDY)
+            a.best[at] = make_float4(m, d, __int_as_float(best), 0.f);
+        else
+            a.part[at] = make_float2(m == -INFINITY ? m : shift_of(m), d);
     }
 }
 
@@ -781,10 +908,11 @@ __global__ void __launch_bounds__(NT) lin_prep_kernel(const PrepArgs a)
     // each warp owns a contiguous range of rows: counts first, then the list
     const int64_t per = ((a.M + NT - 1) / NT) * 32;
     const int64_t lo = min(per * warp, a.M), hi = min(lo + per, a.M);
+    const float one = BWD && a.grad_scale && a.reduction != kReduceNone ? __ldg(a.grad_scale) : 1.f;
     int rows = 0, n = 0;
     float top = 0.f;
     bool bad = false;
-#pragma unroll 4
+#pragma unroll 8
     for (int64_t i = lo + lane; i < hi; i += 32) {
         const int64_t y = __ldg(a.targets + i);
         if (y != a.ignore_index) {
@@ -792,7 +920,7 @@ __global__ void __launch_bounds__(NT) lin_prep_kernel(const PrepArgs a)
             if (y >= 0 && y < a.V) {
                 ++rows;
                 if (BWD && a.grad_scale) {
-                    const float g = fabsf(__ldg(a.grad_scale + (a.reduction == kReduceNone ? i : 0)));
+                    const float g = fabsf(a.reduction == kReduceNone ? __ldg(a.grad_scale + i) : one);
                     top = g > top ? g : top;  // a NaN factor leaves the scale alone
                 }
             } else {
@@ -844,6 +972,7 @@ __global__ void __launch_bounds__(NT) lin_prep_kernel(const PrepArgs a)
         if (!BWD && a.M == 0 && a.reduction != kReduceNone)
             *a.loss = a.reduction == kReduceMean ? __int_as_float(0x7fc00000) : 0.f;
     }
+#pragma unroll 4
     for (int64_t i0 = lo; i0 < hi; i0 += 32) {
         const int64_t i = i0 + lane;
         const int64_t y = i < hi ? __ldg(a.targets + i) : a.ignore_index;
@@ -856,7 +985,7 @@ __global__ void __launch_bounds__(NT) lin_prep_kernel(const PrepArgs a)
             a.tgt[pos] = static_cast<int>(y);
             if (BWD) {
                 a.l2[pos] = __ldg(a.lse_in + i) * kLog2e;
-                a.rs[pos] = (a.grad_scale ? __ldg(a.grad_scale + (a.reduction == kReduceNone ? i : 0)) : 1.f) * inv;
+                a.rs[pos] = (a.grad_scale && a.reduction == kReduceNone ? __ldg(a.grad_scale + i) : one) * inv;
             }
         } else if (!BWD && i < hi) {
             const float v = skip ? 0.f : __int_as_float(0x7fc00000);
@@ -868,16 +997,16 @@ __global__ void __launch_bounds__(NT) lin_prep_kernel(const PrepArgs a)
     }
 }
 
-// sum_k a[k] b[k] of two rows in fp32, by a warp (every lane gets it).
-template <typename T>
+// sum_k a[k] b[k] of two rows in fp32, by NT threads (a warp's share in each of its lanes).
+template <typename T, int NT>
 __device__ __forceinline__ float row_dot(const T *a, const T *b, int64_t K, bool vec)
 {
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & (NT - 1);
     float s0 = 0.f, s1 = 0.f;
     int64_t k = 0;
     if (vec) {
 #pragma unroll 4
-        for (int64_t j = lane; j < K / 8; j += 32) {
+        for (int64_t j = lane; j < K / 8; j += NT) {
             float x[8], y[8];
             Elem<T>::unpack(__ldg(reinterpret_cast<const uint4 *>(a) + j), x);
             Elem<T>::unpack(__ldg(reinterpret_cast<const uint4 *>(b) + j), y);
@@ -889,7 +1018,7 @@ __device__ __forceinline__ float row_dot(const T *a, const T *b, int64_t K, bool
         }
         k = K / 8 * 8;
     }
-    for (int64_t j = k + lane; j < K; j += 32)
+    for (int64_t j = k + lane; j < K; j += NT)
         s0 = fmaf(Elem<T>::load(a + j), Elem<T>::load(b + j), s0);
     return warp_sum(s0 + s1);
 }
@@ -951,7 +1080,7 @@ __global__ void __launch_bounds__(NT) lin_gather_kernel(const GatherArgs a)
         for (int64_t j = done + lane; j < a.lds; j += 32)
             d[j] = j < a.K ? s[j] : zero_value;
         if (a.w) {
-            const float x = row_dot(s, static_cast<const T *>(a.w) + int64_t{a.tgt[i]} * a.ws, a.K, a.wvec);
+            const float x = row_dot<T, 32>(s, static_cast<const T *>(a.w) + int64_t{a.tgt[i]} * a.ws, a.K, a.wvec);
             if (lane == 0) {
                 if (a.xy)
                     a.xy[i] = x;
@@ -979,10 +1108,8 @@ __global__ void __launch_bounds__(NT) lin_gather_kernel(const GatherArgs a)
 
 struct MergeArgs {
     const float2 *part;
-    const int *part_idx;
-    const float *part_max;
+    const float4 *best;
     int parts;
-    int64_t ldp;
     const int *n_ptr;
     int n_host;
     const int *idx;
@@ -1020,72 +1147,94 @@ __device__ __forceinline__ float loss_beside(float s, float d, float xy, float &
     return l - t * kLn2;
 }
 
-// 32 rows x 8 shares of the partials per CTA.
-template <bool GREEDY, typename T>
-__global__ void __launch_bounds__(256) lin_merge_kernel(const MergeArgs a)
+// One warp per listed row.
+template <int NT>
+__global__ void __launch_bounds__(NT) lin_merge_kernel(const MergeArgs a)
 {
-    __shared__ float ss[8][32], sd[8][32];
-    __shared__ int si[8][32];
-    const int n = a.n_ptr ? *a.n_ptr : a.n_host;
-    const int lane = threadIdx.x & 31, share = threadIdx.x >> 5;
-    const int64_t row0 = blockIdx.x * int64_t{32}, row = row0 + lane;
-    if (row0 >= n)
+    const int lane = threadIdx.x & 31;
+    const int64_t row = blockIdx.x * int64_t{NT / 32} + (threadIdx.x >> 5);
+    if (row >= *a.n_ptr)
         return;
-    // GREEDY: the maximum and the others' sum; else the shift and the sum
+    const float2 *part = a.part + row * a.parts;
     float s = -INFINITY, d = 0.f;
-    int best = INT32_MAX;
-    const auto add = [&](float s2, float d2, int i2) {
-        if constexpr (GREEDY) {
-            best_merge(s, d, best, s2, d2, i2);
-        } else {
-            if (s2 == -INFINITY && d2 != 0.f)
-                d += d2;  // a NaN among nothing but -inf
-            md_merge(s, d, s2, d2);
-        }
-    };
-    if (row < n) {
-        const int lo = static_cast<int>(int64_t{a.parts} * share / 8);
-        const int hi = static_cast<int>(int64_t{a.parts} * (share + 1) / 8);
 #pragma unroll 4
-        for (int p = lo; p < hi; ++p) {
-            const int64_t at = p * a.ldp + row;
-            const float2 q = a.part[at];
-            add(GREEDY ? a.part_max[at] : q.x, q.y, GREEDY ? a.part_idx[at] : 0);
+    for (int p = lane; p < a.parts; p += 32) {
+        const float2 q = part[p];
+        const float sn = fmaxf(s, q.x);
+        d = shifted(d, s, sn) + shifted(q.y, q.x, sn);
+        s = sn;
+    }
+    float top = s;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    d = warp_sum(shifted(d, s, top));
+    if (lane == 0) {
+        const int64_t out = a.idx[row];
+        float lse;
+        a.row_loss[out] = loss_beside(top, d, a.xy[row], lse);
+        if (a.lse)
+            a.lse[out] = lse;
+    }
+}
+
+// One CTA per row: its partials, then the dot product of its token.
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT) lin_token_kernel(const MergeArgs a)
+{
+    __shared__ float sm[NT / 32], sd[NT / 32];
+    __shared__ int si[NT / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t row = blockIdx.x;
+    const float4 *part = a.best + row * a.parts;
+    float m = -INFINITY, d = 0.f;
+    int best = INT32_MAX;
+#pragma unroll 2
+    for (int p = threadIdx.x; p < a.parts; p += NT) {
+        const float4 q = part[p];
+        best_merge(m, d, best, q.x, q.y, __float_as_int(q.z));
+    }
+    float mt = m;
+    int it = best;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, mt, off);
+        const int i2 = __shfl_xor_sync(0xffffffffu, it, off);
+        if (m2 > mt || (m2 == mt && i2 < it)) {
+            mt = m2;
+            it = i2;
         }
     }
-    ss[share][lane] = s;
-    sd[share][lane] = d;
-    si[share][lane] = best;
+    d = warp_sum(best == it ? d : rescaled_others(d, m, mt));
+    if (lane == 0) {
+        sm[warp] = mt;
+        sd[warp] = d;
+        si[warp] = it;
+    }
     __syncthreads();
-    if (share == 0 && row < n) {
-        for (int q = 1; q < 8; ++q)
-            add(ss[q][lane], sd[q][lane], si[q][lane]);
-        if constexpr (GREEDY) {
-            a.token[row] = best == INT32_MAX ? 0 : best;
-            ss[0][lane] = s;
-            sd[0][lane] = d;
-            si[0][lane] = best;
-        } else {
-            const int64_t out = a.idx[row];
-            float lse;
-            a.row_loss[out] = loss_beside(s, d, a.xy[row], lse);
-            if (a.lse)
-                a.lse[out] = lse;
-        }
-    }
-    if constexpr (GREEDY) {
+    m = sm[0];
+    d = sd[0];
+    best = si[0];
+#pragma unroll
+    for (int w = 1; w < NT / 32; ++w)
+        best_merge(m, d, best, sm[w], sd[w], si[w]);
+    float lse, lp = __int_as_float(0x7fc00000);  // nothing but NaN or -inf
+    if (best != INT32_MAX) {
+        const float x = row_dot<T, NT>(static_cast<const T *>(a.h) + row * a.hs,
+                                       static_cast<const T *>(a.w) + best * a.ws, a.K, a.vec);
         __syncthreads();
-        for (int r = share; r < 32 && row0 + r < n; r += 8) {
-            const int token = si[0][r];
-            float lse, lp = __int_as_float(0x7fc00000);  // nothing but NaN or -inf
-            if (token != INT32_MAX) {
-                const float x = row_dot(static_cast<const T *>(a.h) + (row0 + r) * a.hs,
-                                        static_cast<const T *>(a.w) + token * a.ws, a.K, a.vec);
-                lp = -loss_beside(shift_of(ss[0][r]), sd[0][r], x, lse);
-            }
-            if (lane == 0)
-                a.logprob[row0 + r] = lp;
-        }
+        if (lane == 0)
+            sm[warp] = x;
+        __syncthreads();
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < NT / 32; ++w)
+            sum += sm[w];
+        lp = -loss_beside(shift_of(m), d, sum, lse);
+    }
+    if (threadIdx.x == 0) {
+        a.token[row] = best == INT32_MAX ? 0 : best;
+        a.logprob[row] = lp;
     }
 }
 

@@ -7,8 +7,8 @@
 namespace gbce {
 namespace {
 
-constexpr int64_t kMoeSmallTokens = 256;  // tokens up to which one CTA does everything
 constexpr int kMoeSmallThreads = 512;
+constexpr int64_t kMoeRowsPerGroup = 2;   // rows that share a group's set-up, at least
 
 using MoeFn = void (*)(const MoeArgs);
 
@@ -26,7 +26,7 @@ MoeFn pick_moe_units(int P)
         return moe_rows_kernel<T, VEC, 32, 2, ALL, NT>;
     if (P <= 128)
         return moe_rows_kernel<T, VEC, 32, 4, ALL, NT>;
-    if constexpr (VEC <= 4) {
+    if constexpr (VEC <= 4) {  // E <= 1024: at most 128 units of 8 values
         if (P <= 256)
             return moe_rows_kernel<T, VEC, 32, 8, ALL, NT>;
     }
@@ -38,25 +38,44 @@ MoeFn pick_moe_units(int P)
     return nullptr;  // not reached: P <= kMoeMaxExperts / VEC
 }
 
-template <bool ALL, int NT>
-MoeFn pick_moe(int dtype, bool vec, int E)
+template <typename T, bool ALL, int NT>
+MoeFn pick_moe_vec(int vec, int E)
 {
-    if (dtype == GBCE_F32)
-        return vec ? pick_moe_units<float, 4, ALL, NT>(E / 4) : pick_moe_units<float, 1, ALL, NT>(E);
-    if (dtype == GBCE_F16)
-        return vec ? pick_moe_units<__half, 8, ALL, NT>(E / 8) : pick_moe_units<__half, 1, ALL, NT>(E);
-    return vec ? pick_moe_units<__nv_bfloat16, 8, ALL, NT>(E / 8)
-               : pick_moe_units<__nv_bfloat16, 1, ALL, NT>(E);
+    if (vec == 1)
+        return pick_moe_units<T, 1, ALL, NT>(E);
+    if (vec == 4)
+        return pick_moe_units<T, 4, ALL, NT>(E / 4);
+    if constexpr (sizeof(T) == 2)
+        return pick_moe_units<T, 8, ALL, NT>(E / 8);
+    return nullptr;  // not reached: 4 fp32 values are 16 bytes
 }
 
-cudaError_t launch_moe(MoeArgs a, int dtype, bool vec, void *scratch, int device, int64_t sms,
-                       cudaStream_t stream)
+template <bool ALL, int NT>
+MoeFn pick_moe(int dtype, int vec, int E)
 {
-    if (a.T <= kMoeSmallTokens) {
-        a.mask = static_cast<unsigned char *>(scratch);
-        pick_moe<true, kMoeSmallThreads>(dtype, vec, a.E)<<<1, kMoeSmallThreads, 0, stream>>>(a);
-        return cudaGetLastError();
+    switch (dtype) {
+    case GBCE_F32: return pick_moe_vec<float, ALL, NT>(vec, E);
+    case GBCE_F16: return pick_moe_vec<__half, ALL, NT>(vec, E);
+    default: return pick_moe_vec<__nv_bfloat16, ALL, NT>(vec, E);
     }
+}
+
+// Values a lane moves at a time: 16 bytes, 4 values, or one, whatever divides E
+// and suits both matrices' rows.
+int moe_vec(const MoeArgs &a, int dtype)
+{
+    const int64_t es = static_cast<int64_t>(elem_size(dtype));
+    for (int64_t v = 16 / es; v >= 4; v /= 2) {
+        const size_t bytes = static_cast<size_t>(v * es);
+        if (a.E % v == 0 && aligned_to(a.logits, bytes) && (a.T <= 1 || a.ls % v == 0) &&
+            (!a.grad || (aligned_to(a.grad, bytes) && (a.T <= 1 || a.gs % v == 0))))
+            return static_cast<int>(v);
+    }
+    return 1;
+}
+
+cudaError_t launch_moe(MoeArgs a, int dtype, int vec, void *scratch, int64_t sms, cudaStream_t stream)
+{
     Carver place(scratch);
     a.totals = place.take<MoeTotals>(1);
     a.part = place.take<double>(kMoeMaxCtas);
@@ -70,9 +89,10 @@ cudaError_t launch_moe(MoeArgs a, int dtype, bool vec, void *scratch, int device
     if ((e = cudaGetLastError()) != cudaSuccess)
         return e;
     const MoeFn fn = pick_moe<false, kMoeThreads>(dtype, vec, a.E);
-    const int units = vec ? a.E / static_cast<int>(16 / elem_size(dtype)) : a.E;
+    const int units = a.E / vec;
     const int lanes = units <= 4 ? 4 : (units <= 16 ? 16 : 32);
-    const int64_t ctas = (a.T * lanes + kMoeThreads - 1) / kMoeThreads;
+    const int64_t rows = kMoeThreads / lanes * kMoeRowsPerGroup;  // of a CTA, at least
+    const int64_t ctas = (a.T + rows - 1) / rows;
     const int64_t most = sms * 8 < kMoeMaxCtas ? sms * 8 : kMoeMaxCtas;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas < most ? ctas : most), 1, 1);
@@ -126,12 +146,17 @@ extern "C" int moe_balance(const void *logits, int64_t logits_stride, const int6
     a.grad_scale = grad_scale;
     a.balance = balance_coef;
     a.z = z_coef;
-    const int64_t per = 16 / static_cast<int64_t>(elem_size(dtype));
-    const bool vec = E % per == 0 && aligned_to(logits, 16) && (T <= 1 || logits_stride % per == 0) &&
-                     (!grad || (aligned_to(grad, 16) && (T <= 1 || grad_stride % per == 0)));
+    const int vec = moe_vec(a, dtype);
+    if (T <= kMoeSmallTokens) {
+        pick_moe<true, kMoeSmallThreads>(dtype, vec, a.E)<<<1, kMoeSmallThreads, 0, call.stream>>>(a);
+        return map_error(cudaGetLastError());
+    }
     PoolScratch scratch(call.stream);
-    const size_t bytes = sizeof(MoeTotals) + kMoeMaxCtas * sizeof(double) + static_cast<size_t>(T) + 1024;
-    if ((e = scratch.get(call.device, bytes)) != cudaSuccess)
+    Carver size(nullptr);
+    size.take<MoeTotals>(1);
+    size.take<double>(kMoeMaxCtas);
+    size.take<unsigned char>(T);
+    if ((e = scratch.get(call.device, size.used)) != cudaSuccess)
         return map_error(e);
-    return map_error(scratch.release(launch_moe(a, dtype, vec, scratch.p, call.device, call.sms, call.stream)));
+    return map_error(scratch.release(launch_moe(a, dtype, vec, scratch.p, call.sms, call.stream)));
 }

@@ -14,9 +14,10 @@
 // the logits: moe_count_kernel reads the choices (integer atomics, so the
 // order is free) and moe_rows_kernel then reads each row of logits once, into
 // registers, and writes its gradient once.  A row belongs to 4, 16 or 32 lanes;
-// each lane keeps the counts of its experts in registers over all its rows.
-// Row losses are added in fp64 (one addition a row) in an order fixed by the
-// grid, and the last CTA to finish adds the CTAs' sums.
+// each lane keeps the counts of its experts in registers over all its rows and
+// has the next row's loads in flight while it works on one.  Row losses are
+// added in fp32 with their rounding errors carried (Neumaier) in an order fixed
+// by the grid; the last CTA to finish adds the CTAs' sums in fp64.
 #pragma once
 
 #include "row_kernels.cuh"
@@ -42,7 +43,7 @@ struct MoeArgs {
     int64_t T;
     int E, k;
     MoeTotals *totals;
-    unsigned char *mask;   // [T]: the token counts
+    unsigned char *mask;   // [T]: the token counts (one CTA: in its shared memory)
     double *part;          // [gridDim.x] sums of row losses
     int64_t *counts;       // out
     float *loss;           // out, or NULL
@@ -68,12 +69,12 @@ __device__ __forceinline__ int moe_token(const MoeArgs &a, int64_t t)
 
 // Adds the choices of tokens first, first + step, ... to hist; returns how many count.
 __device__ __forceinline__ int moe_count_tokens(const MoeArgs &a, int64_t first, int64_t step,
-                                                unsigned *hist, bool &bad)
+                                                unsigned *hist, unsigned char *mask, bool &bad)
 {
     int n = 0;
     for (int64_t t = first; t < a.T; t += step) {
         const int c = moe_token(a, t);
-        a.mask[t] = c > 0;
+        mask[t] = c > 0;
         bad |= c < 0;
         if (c > 0) {
             ++n;
@@ -96,7 +97,7 @@ __global__ void __launch_bounds__(NT) moe_count_kernel(const MoeArgs a)
         hist[e] = 0;
     __syncthreads();
     bool bad = false;
-    int n = moe_count_tokens(a, blockIdx.x * int64_t{NT} + threadIdx.x, int64_t{gridDim.x} * NT, hist, bad);
+    int n = moe_count_tokens(a, blockIdx.x * int64_t{NT} + threadIdx.x, int64_t{gridDim.x} * NT, hist, a.mask, bad);
     n = __reduce_add_sync(0xffffffffu, n);
     if ((threadIdx.x & 31) == 0 && n)
         atomicAdd(&a.totals->n, static_cast<unsigned>(n));
@@ -128,45 +129,78 @@ __device__ __forceinline__ float group_max(float v)
     return v;
 }
 
-// VEC values (16 bytes, or one) at p.
+// VEC values of a row as they lie in memory: 16 or 8 bytes, or one value.
 template <typename T, int VEC>
-__device__ __forceinline__ void moe_load(const T *p, float *f)
-{
-    if constexpr (VEC == 1) {
-        f[0] = Elem<T>::load(p);
-    } else {
-        float v[VEC];
-        Elem<T>::unpack(__ldcs(reinterpret_cast<const uint4 *>(p)), v);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i)
-            f[i] = v[i];
+struct MoeUnit {
+    using Raw = std::conditional_t<VEC == 1, T, std::conditional_t<VEC * sizeof(T) == 16, uint4, uint2>>;
+    __device__ static __forceinline__ Raw load(const T *p)
+    {
+        if constexpr (VEC == 1)
+            return *p;
+        else
+            return __ldcs(reinterpret_cast<const Raw *>(p));
     }
-}
+    __device__ static __forceinline__ void unpack(const Raw &r, float *f)
+    {
+        if constexpr (VEC == 1) {
+            f[0] = Elem<T>::load(&r);
+        } else {
+            float v[Elem<T>::kPerVec];
+            if constexpr (sizeof(Raw) == 16)
+                Elem<T>::unpack(r, v);
+            else
+                Elem<T>::unpack(make_uint4(r.x, r.y, 0, 0), v);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                f[i] = v[i];
+        }
+    }
+    __device__ static __forceinline__ void store(T *p, const float *f)
+    {
+        if constexpr (VEC == 1) {
+            Elem<T>::store(p, f[0]);
+        } else {
+            float v[Elem<T>::kPerVec] = {};
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                v[i] = f[i];
+            const uint4 r = Elem<T>::pack(v);
+            if constexpr (sizeof(Raw) == 16)
+                __stcs(reinterpret_cast<uint4 *>(p), r);
+            else
+                __stcs(reinterpret_cast<uint2 *>(p), make_uint2(r.x, r.y));
+        }
+    }
+};
 
-template <typename T, int VEC>
-__device__ __forceinline__ void moe_store(T *p, const float *f)
-{
-    if constexpr (VEC == 1) {
-        Elem<T>::store(p, f[0]);
-    } else {
-        float v[VEC];
-#pragma unroll
-        for (int i = 0; i < VEC; ++i)
-            v[i] = f[i];
-        __stcs(reinterpret_cast<uint4 *>(p), Elem<T>::pack(v));
-    }
-}
+constexpr int kMoeSmallTokens = 256;  // tokens up to which one CTA does everything
 
 // ALL: one CTA does everything, the counting too (small batches: one launch).
 template <typename T, int VEC, int LPT, int NJ, bool ALL, int NT>
 __global__ void __launch_bounds__(NT) moe_rows_kernel(const MoeArgs a)
 {
+    using Unit = MoeUnit<T, VEC>;
     __shared__ unsigned hist[ALL ? kMoeMaxExperts : 1];
+    __shared__ unsigned char small_mask[ALL ? kMoeSmallTokens : 1];
     __shared__ double warp_part[NT / 32];
     __shared__ int s_n, s_bad, s_last;
     const int lane = threadIdx.x & 31, sub = lane % LPT;
     const int64_t groups = int64_t{gridDim.x} * (NT / LPT);
-    const int64_t group = blockIdx.x * int64_t{NT / LPT} + threadIdx.x / LPT;
+    int64_t t = blockIdx.x * int64_t{NT / LPT} + threadIdx.x / LPT;
+    const T *logits = static_cast<const T *>(a.logits);
+    const unsigned char *mask = ALL ? small_mask : a.mask;
+
+    // the row's values as loaded; the first ones before the counts are needed
+    typename Unit::Raw raw[NJ];
+    const auto load_row = [&](int64_t row) {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            const int e = (j * LPT + sub) * VEC;
+            if (row < a.T && e < a.E)
+                raw[j] = Unit::load(logits + row * a.ls + e);
+        }
+    };
+    load_row(t);
 
     if constexpr (ALL) {
         for (int e = threadIdx.x; e < a.E; e += NT)
@@ -175,7 +209,7 @@ __global__ void __launch_bounds__(NT) moe_rows_kernel(const MoeArgs a)
             s_n = s_bad = 0;
         __syncthreads();
         bool bad = false;
-        int n = moe_count_tokens(a, threadIdx.x, NT, hist, bad);
+        int n = moe_count_tokens(a, threadIdx.x, NT, hist, small_mask, bad);
         n = __reduce_add_sync(0xffffffffu, n);
         if (lane == 0 && n)
             atomicAdd(&s_n, n);
@@ -186,69 +220,62 @@ __global__ void __launch_bounds__(NT) moe_rows_kernel(const MoeArgs a)
             atomicOr(&g_flags, kFlagBadTarget);
     } else {
         wait_prerequisite_grid();
-        if (threadIdx.x == 0) {
-            s_n = static_cast<int>(__ldcg(&a.totals->n));
-            s_bad = static_cast<int>(__ldcg(&a.totals->bad));
-        }
-        __syncthreads();
     }
-    const auto count_of = [&](int e) -> unsigned long long {
+    const auto count_of = [&](int e) -> long long {
         if constexpr (ALL)
             return hist[e];
         else
-            return __ldcg(&a.totals->counts[e]);
+            return static_cast<long long>(__ldcg(&a.totals->counts[e]));
     };
-    const int n = s_n;
+    const int n = ALL ? s_n : static_cast<int>(__ldcg(&a.totals->n));
+    const int bad = ALL ? s_bad : static_cast<int>(__ldcg(&a.totals->bad));
     if (blockIdx.x == 0)
         for (int e = threadIdx.x; e < a.E; e += NT)
-            a.counts[e] = static_cast<int64_t>(count_of(e));
+            a.counts[e] = count_of(e);
 
-    // this lane's experts: e = (j LPT + sub) VEC + v; the mean over all of them
-    float f[NJ * VEC];
-    double sum = 0.0;
+    // this lane's experts e = (j LPT + sub) VEC + v: their counts less the mean
+    // over all of them, (E f_e - sum) / E with the difference formed in integers
+    long long c[NJ * VEC], sum = 0;
 #pragma unroll
-    for (int j = 0; j < NJ; ++j)
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            const int e = (j * LPT + sub) * VEC + v;
-            if (e < a.E)
-                sum += static_cast<double>(count_of(e));
-        }
+    for (int i = 0; i < NJ * VEC; ++i) {
+        const int e = (i / VEC * LPT + sub) * VEC + i % VEC;
+        c[i] = e < a.E ? count_of(e) : 0;
+        sum += c[i];
+    }
 #pragma unroll
     for (int off = LPT / 2; off > 0; off >>= 1)
         sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    const double mean = sum / a.E;
+    const float per_e = 1.f / static_cast<float>(a.E);
+    const float fmean = static_cast<float>(sum) * per_e;
+    float f[NJ * VEC];
 #pragma unroll
-    for (int j = 0; j < NJ; ++j)
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            const int e = (j * LPT + sub) * VEC + v;
-            f[j * VEC + v] = e < a.E ? static_cast<float>(static_cast<double>(count_of(e)) - mean) : 0.f;
-        }
-    const float fmean = static_cast<float>(mean);
+    for (int i = 0; i < NJ * VEC; ++i)
+        f[i] = static_cast<float>(c[i] * a.E - sum) * per_e;
     const float per_n = 1.f / static_cast<float>(n);
     const float ka = a.balance * static_cast<float>(a.E) / static_cast<float>(a.k) * per_n;  // a E / (k n)
     const float gscale = a.grad ? (a.grad_scale ? __ldg(a.grad_scale) : 1.f) * per_n : 0.f;
     const float ga = ka * gscale, gz = 2.f * a.z * gscale;
 
-    double part = 0.0;
-    for (int64_t t0 = group - (lane / LPT); t0 < a.T; t0 += groups) {  // one trip for the whole warp
-        const int64_t t = t0 + lane / LPT;
-        const bool in = t < a.T;
-        const bool counted = in && a.mask[t];
-        const T *row = static_cast<const T *>(a.logits) + t * a.ls;
+    float part = 0.f, carry = 0.f;
+    bool counted = t < a.T && mask[t];
+    for (int64_t t0 = t - lane / LPT; t0 < a.T; t0 += groups) {  // one trip for the whole warp
         float x[NJ * VEC];
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
-            const int e = (j * LPT + sub) * VEC;
-            if (counted && e < a.E) {
-                moe_load<T, VEC>(row + e, x + j * VEC);
+            if (counted && (j * LPT + sub) * VEC < a.E) {
+                Unit::unpack(raw[j], x + j * VEC);
             } else {
 #pragma unroll
                 for (int v = 0; v < VEC; ++v)
                     x[j * VEC + v] = -INFINITY;
             }
         }
+        const int64_t row = t;
+        const bool in = row < a.T, live = counted;
+        t += groups;
+        load_row(t);
+        counted = t < a.T && mask[t];
+
         float m = x[0];
 #pragma unroll
         for (int i = 1; i < NJ * VEC; ++i)
@@ -266,11 +293,15 @@ __global__ void __launch_bounds__(NT) moe_rows_kernel(const MoeArgs a)
         q = group_sum<LPT>(q);
         const float inv = 1.f / d, dot = q * inv;
         const float lse = fmaf(s, kLn2, logf(d));
-        if (counted && sub == 0)
-            part += static_cast<double>(fmaf(ka, fmean + dot, a.z * lse * lse));
+        if (live && sub == 0) {
+            const float v = fmaf(ka, fmean + dot, a.z * lse * lse);
+            const float sum = part + v;
+            carry += fabsf(part) >= fabsf(v) ? (part - sum) + v : (v - sum) + part;
+            part = sum;
+        }
         if (a.grad && in) {
-            const float base = counted ? fmaf(-ga, dot, gz * lse) : 0.f;
-            T *out = static_cast<T *>(a.grad) + t * a.gs;
+            const float base = fmaf(-ga, dot, gz * lse);
+            T *out = static_cast<T *>(a.grad) + row * a.gs;
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
                 const int e = (j * LPT + sub) * VEC;
@@ -278,44 +309,17 @@ __global__ void __launch_bounds__(NT) moe_rows_kernel(const MoeArgs a)
                     float g[VEC];
 #pragma unroll
                     for (int v = 0; v < VEC; ++v)
-                        g[v] = counted ? x[j * VEC + v] * inv * fmaf(ga, f[j * VEC + v], base) : 0.f;
-                    moe_store<T, VEC>(out + e, g);
+                        g[v] = live ? x[j * VEC + v] * inv * fmaf(ga, f[j * VEC + v], base) : 0.f;
+                    Unit::store(out + e, g);
                 }
             }
         }
     }
+    if (!a.loss)
+        return;
 
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-        part += __shfl_xor_sync(0xffffffffu, part, off);
-    if (lane == 0)
-        warp_part[threadIdx.x >> 5] = part;
-    __syncthreads();
-    if constexpr (ALL) {
-        if (threadIdx.x == 0 && a.loss) {
-            double total = 0.0;
-            for (int w = 0; w < NT / 32; ++w)
-                total += warp_part[w];
-            *a.loss = s_bad ? __int_as_float(0x7fc00000) : static_cast<float>(total / n);
-        }
-    } else {
-        if (!a.loss)
-            return;
-        if (threadIdx.x == 0) {
-            double total = 0.0;
-            for (int w = 0; w < NT / 32; ++w)
-                total += warp_part[w];
-            a.part[blockIdx.x] = total;
-            __threadfence();
-            s_last = atomicAdd(&a.totals->done, 1u) == gridDim.x - 1;
-        }
-        __syncthreads();
-        if (!s_last)
-            return;
-        __threadfence();
-        double total = 0.0;
-        for (int i = threadIdx.x; i < static_cast<int>(gridDim.x); i += NT)
-            total += __ldcg(a.part + i);
+    double total = static_cast<double>(part) + static_cast<double>(carry);
+    const auto add_up = [&]() {  // over the CTA, in thread 0
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1)
             total += __shfl_xor_sync(0xffffffffu, total, off);
@@ -327,9 +331,26 @@ __global__ void __launch_bounds__(NT) moe_rows_kernel(const MoeArgs a)
             total = 0.0;
             for (int w = 0; w < NT / 32; ++w)
                 total += warp_part[w];
-            *a.loss = s_bad ? __int_as_float(0x7fc00000) : static_cast<float>(total / n);
         }
+    };
+    add_up();
+    if constexpr (!ALL) {
+        if (threadIdx.x == 0) {
+            a.part[blockIdx.x] = total;
+            __threadfence();
+            s_last = atomicAdd(&a.totals->done, 1u) == gridDim.x - 1;
+        }
+        __syncthreads();
+        if (!s_last)
+            return;
+        __threadfence();
+        total = 0.0;
+        for (int i = threadIdx.x; i < static_cast<int>(gridDim.x); i += NT)
+            total += __ldcg(a.part + i);
+        add_up();
     }
+    if (threadIdx.x == 0)
+        *a.loss = bad ? __int_as_float(0x7fc00000) : static_cast<float>(total / n);
 }
 
 }  // namespace gbce
