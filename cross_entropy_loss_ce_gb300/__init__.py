@@ -127,9 +127,9 @@ class _OnDevice:
 def _stream_handle(stream, device) -> ctypes.c_void_p:
     """The stream of a call on ``device``: the given one (which must belong to
     that device) or the device's current torch stream."""
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
+    if stream is None:  # the handle itself: no Stream object for it
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(device.index))
+    if stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
     return ctypes.c_void_p(stream.cuda_stream)
 
@@ -513,8 +513,12 @@ def ce_fwd_bwd_noalloc(logits: torch.Tensor, targets: torch.Tensor, ignore_index
 
 def _rows(t: torch.Tensor, name: str):
     """_matrix for operands whose rows must not share memory (no expanded rows)."""
-    if t.dim() == 2 and t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-        raise ValueError(f"{name} has overlapping rows (stride {t.stride(0)} for {t.shape[1]} columns)")
+    if t.dim() == 2 and t.is_cuda and t.dtype in DTYPES:
+        (rows, cols), (step, unit) = t.shape, t.stride()
+        if unit == 1 and step >= cols:
+            return t.data_ptr(), step, rows, cols
+        if rows > 1 and step < cols:
+            raise ValueError(f"{name} has overlapping rows (stride {step} for {cols} columns)")
     return _matrix(t, name)
 
 
@@ -727,27 +731,29 @@ def moe_balance(logits: torch.Tensor, experts: torch.Tensor, balance_coef: float
             experts.shape[1] < 1:
         raise ValueError("experts must be int64 of shape [T, k]")
     k = experts.shape[1]
-    if (k > 1 and experts.stride(1) != 1) or (T > 1 and experts.stride(0) < k):
+    es, unit = experts.stride()
+    if (k > 1 and unit != 1) or (T > 1 and es < k):
         raise ValueError("experts needs unit column stride and rows that do not overlap")
-    es = experts.stride(0) if T > 1 else k
     dev = logits.device
+    gp, gstride = None, 0
     if not want_grad:
         grad = None
     elif grad is None:
         grad = torch.empty((T, E), dtype=logits.dtype, device=dev)
+        gp, gstride = grad.data_ptr(), E
     elif grad.shape != logits.shape or grad.dtype != logits.dtype:
         raise ValueError("grad must match the logits' shape and dtype")
-    gp, gstride = _rows(grad, "grad")[:2] if grad is not None else (None, 0)
+    else:
+        gp, gstride = _rows(grad, "grad")[:2]
     gs = None if grad_scale is None else _device_floats(grad_scale, 1, dev, "grad_scale")
     loss = torch.empty((), dtype=torch.float32, device=dev) if want_loss else None
     counts = torch.empty((E,), dtype=torch.int64, device=dev)
     dev = _call_device(("logits", logits), ("experts", experts if T else None), ("grad", grad),
-                       ("grad_scale", gs), ("counts", counts))
+                       ("grad_scale", gs))
     with _OnDevice(dev):
         rc = load_library().moe_balance(lp, ls, experts.data_ptr(), max(es, k), counts.data_ptr(),
-                                        _ptr(loss), gp, gstride, _ptr(gs), T, E, k,
-                                        float(balance_coef), float(z_coef), DTYPES[logits.dtype],
-                                        _stream_handle(stream, dev))
+                                        _ptr(loss), gp, gstride, _ptr(gs), T, E, k, balance_coef,
+                                        z_coef, DTYPES[logits.dtype], _stream_handle(stream, dev))
     _check(rc, "moe_balance")
     return loss, counts, grad
 

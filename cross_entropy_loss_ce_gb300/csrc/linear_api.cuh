@@ -80,8 +80,9 @@ struct Carver {
 
 struct HeadScratch {
     int *n, *rows;      // divisor of the mean; listed rows
-    unsigned *fail;
+    unsigned *fail, *done;
     float *alpha;
+    unsigned *arrived;
     int *idx, *tgt;
     float *l2, *rs, *gy, *xy;
     unsigned short *h;  // packed hidden states
@@ -114,6 +115,7 @@ HeadScratch carve(Carver &c, const HeadShape &s, HeadOp op, bool want_hidden)
     r.rows = words ? words + 1 : nullptr;
     r.fail = reinterpret_cast<unsigned *>(words ? words + 2 : nullptr);
     r.alpha = reinterpret_cast<float *>(words ? words + 3 : nullptr);
+    r.done = reinterpret_cast<unsigned *>(words ? words + 4 : nullptr);
     if (op != HeadOp::Greedy) {
         r.idx = c.take<int>(s.M);
         r.tgt = c.take<int>(s.M);
@@ -129,6 +131,7 @@ HeadScratch carve(Carver &c, const HeadShape &s, HeadOp op, bool want_hidden)
         r.g = c.take<unsigned short>(s.mp * s.vp);
         if (want_hidden && s.pieces > 1)
             r.acc = c.take<float>(s.mp * round_up(s.K, kPairN));
+        r.arrived = c.take<unsigned>(kSplitUnits / 2 * 16);
         r.slices = c.take<float>(s.slices * kPairM * kPairN);
     } else {
         if (op == HeadOp::Fwd) {
@@ -162,8 +165,28 @@ struct Call {
     int dtype;
 };
 
+// A kernel of a call.  All but the first may be set up while their predecessor
+// on the stream still runs (`early`); they wait on the device before they touch
+// anything.
+template <typename... Args, typename... Given>
+cudaError_t launch_kernel(const Call &call, bool early, void (*fn)(Args...), int64_t grid, int threads,
+                          int smem, const Given &...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = call.stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = early ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, fn, static_cast<Args>(args)...);
+}
+
 template <Epi E>
-cudaError_t launch_pair(const Call &call, const PairArgs &a, int64_t max_tiles)
+cudaError_t launch_pair(const Call &call, const PairArgs &a, int64_t max_tiles, bool early = true)
 {
     using Fn = void (*)(const PairArgs);
     const Fn fn = call.dtype == GBCE_BF16 ? static_cast<Fn>(pair_gemm_kernel<E, __nv_bfloat16>)
@@ -171,44 +194,65 @@ cudaError_t launch_pair(const Call &call, const PairArgs &a, int64_t max_tiles)
     const cudaError_t e = configure_smem(reinterpret_cast<const void *>(fn), call.device, kPairSmem);
     if (e != cudaSuccess)
         return e;
-    constexpr bool split = E == Epi::Weight || E == Epi::Hidden;
+    constexpr bool split = E == Epi::Weight || E == Epi::Hidden;  // uses every pair it can
     const int64_t most = call.sms / 2 < kSplitUnits / 4 ? call.sms / 2 : kSplitUnits / 4;
     const int64_t pairs = split || max_tiles > most ? most : max_tiles;
-    fn<<<static_cast<unsigned>(2 * pairs), kPairThreads, kPairSmem, call.stream>>>(a);
-    if constexpr (split) {
-        const unsigned grid = static_cast<unsigned>(4 * call.sms);
-        if (call.dtype == GBCE_BF16)
-            lin_slices_kernel<E, __nv_bfloat16><<<grid, 256, 0, call.stream>>>(a, static_cast<int>(pairs));
-        else
-            lin_slices_kernel<E, __half><<<grid, 256, 0, call.stream>>>(a, static_cast<int>(pairs));
-    }
-    return cudaGetLastError();
+    return launch_kernel(call, early, fn, 2 * pairs, kPairThreads, kPairSmem, a);
 }
 
 template <int NG, bool GREEDY>
-cudaError_t launch_skinny_ng(const Call &call, const SkinnyArgs &a, int64_t ctas)
+cudaError_t launch_skinny_ng(const Call &call, const SkinnyArgs &a, int64_t ctas, bool early)
 {
     const auto fn = skinny_kernel<NG, GREEDY>;
     const cudaError_t e =
         configure_smem(reinterpret_cast<const void *>(fn), call.device, skinny_smem<NG>());
     if (e != cudaSuccess)
         return e;
-    fn<<<static_cast<unsigned>(ctas), skinny_threads<NG>(), skinny_smem<NG>(), call.stream>>>(a);
-    return cudaGetLastError();
+    return launch_kernel(call, early, fn, ctas, skinny_threads<NG>(), skinny_smem<NG>(), a);
 }
 
-cudaError_t launch_gather(const Call &call, GatherArgs a, int64_t rows)
+int64_t gather_grid(const Call &call, int64_t rows)
 {
-    a.vec = mappable(a.src, a.ss, 2) ? 1 : 0;
-    a.wvec = a.vec && mappable(a.w, a.ws, 2);
-    a.zvec = mappable(a.zero, a.zs, 2);
     const int64_t want = (rows + 7) / 8, most = call.sms * 8;
-    const unsigned grid = static_cast<unsigned>(want < most ? want : most);
-    if (call.dtype == GBCE_BF16)
-        lin_gather_kernel<__nv_bfloat16, 256><<<grid, 256, 0, call.stream>>>(a);
-    else
-        lin_gather_kernel<__half, 256><<<grid, 256, 0, call.stream>>>(a);
-    return cudaGetLastError();
+    return want < most ? want : most;
+}
+
+// Lists the rows that count and packs them into g.dst (rows as far as s.mp).
+template <bool BWD>
+cudaError_t launch_start(const Call &call, const HeadShape &s, GatherArgs g, const PrepArgs &p)
+{
+    g.lds = s.kp;
+    g.K = s.K;
+    g.pad = static_cast<int>(s.skinny ? s.mp : kPairM);
+    g.vec = mappable(g.src, g.ss, 2);
+    g.wvec = g.vec && mappable(g.w, g.ws, 2);
+    g.zvec = mappable(g.zero, g.zs, 2);
+    const bool bf16 = call.dtype == GBCE_BF16;
+    const int64_t grid = gather_grid(call, s.mp);
+    if (p.M <= kStartRows)
+        return launch_kernel(call, false, bf16 ? lin_start_kernel<__nv_bfloat16, BWD, 256> : lin_start_kernel<__half, BWD, 256>,
+                             grid, 256, 0, g, p);
+    const cudaError_t e = launch_kernel(call, false, lin_prep_kernel<1024, BWD>, 1, 1024, 0, p);
+    if (e != cudaSuccess)
+        return e;
+    return launch_kernel(call, true, bf16 ? lin_gather_kernel<__nv_bfloat16, 256> : lin_gather_kernel<__half, 256>,
+                         grid, 256, 0, g, p);
+}
+
+// Packed copy of n rows, and zeros up to a multiple of `pad`.  `first`: the first kernel of its call.
+cudaError_t launch_pack(const Call &call, const HeadShape &s, const void *src, int64_t ss, void *dst,
+                        int64_t n, int pad, bool first)
+{
+    GatherArgs g{};
+    g.src = src;
+    g.ss = ss;
+    g.dst = dst;
+    g.lds = s.kp;
+    g.K = s.K;
+    g.pad = pad;
+    g.vec = mappable(src, ss, 2);
+    return launch_kernel(call, !first, call.dtype == GBCE_BF16 ? lin_pack_kernel<__nv_bfloat16, 256> : lin_pack_kernel<__half, 256>,
+                         gather_grid(call, round_up(n, pad)), 256, 0, g, n);
 }
 
 int check_head(const void *hidden, int64_t hs, const void *weight, int64_t ws, int64_t M, int64_t K,
@@ -258,38 +302,15 @@ HeadShape head_shape(const Call &call, const void *hidden, int64_t hs, const voi
 
 // The weights as the products read them: in place, or packed.
 cudaError_t pack_weights(const Call &call, const HeadShape &s, const HeadScratch &r, const void *weight,
-                         int64_t ws, const void **w, int64_t *wstride)
+                         int64_t ws, const void **w, int64_t *wstride, bool first)
 {
     *w = weight;
     *wstride = ws;
     if (!s.pack_w)
         return cudaSuccess;
-    GatherArgs g{};
-    g.src = weight;
-    g.ss = ws;
-    g.dst = r.w;
-    g.lds = s.kp;
-    g.n_host = s.V;
-    g.K = s.K;
-    g.pad = 1;
     *w = r.w;
     *wstride = s.kp;
-    return launch_gather(call, g, s.V);
-}
-
-cudaError_t pack_hidden(const Call &call, const HeadShape &s, const HeadScratch &r, const void *hidden,
-                        int64_t hs, const int *idx, const int *rows, GatherArgs g = GatherArgs{})
-{
-    g.src = hidden;
-    g.ss = hs;
-    g.dst = r.h;
-    g.lds = s.kp;
-    g.idx = idx;
-    g.n_ptr = rows;
-    g.n_host = s.M;
-    g.K = s.K;
-    g.pad = static_cast<int>(s.skinny ? s.mp : kPairM);
-    return launch_gather(call, g, s.mp);
+    return launch_pack(call, s, weight, ws, r.w, s.V, 1, first);
 }
 
 // Forward of `op` from prepared rows: the products and the merge.
@@ -297,6 +318,7 @@ template <bool GREEDY>
 cudaError_t launch_head(const Call &call, const HeadShape &s, const HeadScratch &r, const void *h,
                         int64_t hstride, const void *w, int64_t wstride, int64_t hrows, MergeArgs m)
 {
+    const bool early = !GREEDY || s.pack_h || s.pack_w;  // not the call's first kernel
     cudaError_t e;
     const int kblocks = static_cast<int>((s.K + 63) / 64);
     m.part = r.part;
@@ -322,8 +344,8 @@ cudaError_t launch_head(const Call &call, const HeadShape &s, const HeadScratch 
         a.ldp = s.parts;
         a.fail = GREEDY ? nullptr : r.fail;
         a.bf16 = call.dtype == GBCE_BF16;
-        e = s.mp == 32 ? launch_skinny_ng<1, GREEDY>(call, a, s.parts)
-                       : launch_skinny_ng<2, GREEDY>(call, a, s.parts);
+        e = s.mp == 32 ? launch_skinny_ng<1, GREEDY>(call, a, s.parts, early)
+                       : launch_skinny_ng<2, GREEDY>(call, a, s.parts, early);
     } else {
         PairArgs a{};
         if ((e = make_map(&a.a, h, call.dtype, hrows, s.K, hstride, 128)) != cudaSuccess ||
@@ -339,7 +361,7 @@ cudaError_t launch_head(const Call &call, const HeadShape &s, const HeadScratch 
         a.ldp = s.parts;
         a.tgt = r.tgt;
         a.V = s.V;
-        e = launch_pair<GREEDY ? Epi::Greedy : Epi::Stats>(call, a, s.mp / kPairM * a.tiles_n);
+        e = launch_pair<GREEDY ? Epi::Greedy : Epi::Stats>(call, a, s.mp / kPairM * a.tiles_n, early);
     }
     if (e != cudaSuccess)
         return e;
@@ -350,41 +372,41 @@ cudaError_t launch_head(const Call &call, const HeadShape &s, const HeadScratch 
     m.K = s.K;
     m.vec = mappable(h, hstride, hrows) && mappable(w, wstride, s.V);
     if constexpr (!GREEDY)
-        lin_merge_kernel<256><<<static_cast<unsigned>((s.M + 7) / 8), 256, 0, call.stream>>>(m);
-    else if (call.dtype == GBCE_BF16)
-        lin_token_kernel<__nv_bfloat16, 128><<<static_cast<unsigned>(s.M), 128, 0, call.stream>>>(m);
+        return launch_kernel(call, true, lin_merge_kernel<256>, (s.M + 7) / 8, 256, 0, m);
     else
-        lin_token_kernel<__half, 128><<<static_cast<unsigned>(s.M), 128, 0, call.stream>>>(m);
-    return cudaGetLastError();
+        return launch_kernel(call, true, call.dtype == GBCE_BF16 ? lin_token_kernel<__nv_bfloat16, 128>
+                                                         : lin_token_kernel<__half, 128>,
+                           s.M, 128, 0, m);
 }
 
 cudaError_t launch_linear_fwd(const Call &call, const HeadShape &s, const HeadScratch &r,
                               const void *hidden, int64_t hs, const void *weight, int64_t ws,
                               const PrepArgs &prep)
 {
-    cudaError_t e;
-    lin_prep_kernel<1024, false><<<1, 1024, 0, call.stream>>>(prep);
-    if ((e = cudaGetLastError()) != cudaSuccess || s.M == 0)
+    GatherArgs g{};
+    g.src = hidden;
+    g.ss = hs;
+    g.dst = r.h;
+    g.w = weight;
+    g.ws = ws;
+    g.xy = r.xy;
+    cudaError_t e = launch_start<false>(call, s, g, prep);
+    if (e != cudaSuccess || s.M == 0)
         return e;
     const void *w;
     int64_t wstride;
-    GatherArgs target{};
-    target.w = weight;
-    target.ws = ws;
-    target.tgt = r.tgt;
-    target.xy = r.xy;
-    if ((e = pack_hidden(call, s, r, hidden, hs, r.idx, r.rows, target)) != cudaSuccess ||
-        (e = pack_weights(call, s, r, weight, ws, &w, &wstride)) != cudaSuccess)
+    if ((e = pack_weights(call, s, r, weight, ws, &w, &wstride, false)) != cudaSuccess)
         return e;
     MergeArgs m{};
     m.row_loss = prep.row_loss;
     m.lse = prep.lse_out;
-    if ((e = launch_head<false>(call, s, r, r.h, s.kp, w, wstride, s.mp, m)) != cudaSuccess ||
-        prep.reduction == GBCE_NONE)
-        return e;
-    ce_mean_kernel<1024><<<1, 1024, 0, call.stream>>>(prep.row_loss, s.M, r.n, r.fail, prep.loss,
-                                                       prep.reduction);
-    return cudaGetLastError();
+    m.loss = prep.reduction == GBCE_NONE ? nullptr : prep.loss;
+    m.n_mean = r.n;
+    m.fail = r.fail;
+    m.done = r.done;
+    m.M = s.M;
+    m.reduction = prep.reduction;
+    return launch_head<false>(call, s, r, r.h, s.kp, w, wstride, s.mp, m);
 }
 
 cudaError_t launch_linear_bwd(const Call &call, const HeadShape &s, const HeadScratch &r,
@@ -392,27 +414,25 @@ cudaError_t launch_linear_bwd(const Call &call, const HeadShape &s, const HeadSc
                               void *d_hidden, int64_t dhs, void *d_weight, int64_t dws,
                               const PrepArgs &prep)
 {
-    cudaError_t e;
-    lin_prep_kernel<1024, true><<<1, 1024, 0, call.stream>>>(prep);
-    if ((e = cudaGetLastError()) != cudaSuccess)
+    GatherArgs g{};
+    g.src = hidden;
+    g.ss = hs;
+    g.dst = r.h;
+    g.w = weight;
+    g.ws = ws;
+    g.gy = r.gy;
+    g.zero = d_hidden;
+    g.zs = dhs;
+    g.M = s.M;
+    g.V = s.V;
+    g.ignore_index = prep.ignore_index;
+    g.targets = prep.targets;
+    cudaError_t e = launch_start<true>(call, s, g, prep);
+    if (e != cudaSuccess)
         return e;
     const void *w;
     int64_t wstride;
-    GatherArgs rest{};
-    rest.w = weight;
-    rest.ws = ws;
-    rest.tgt = r.tgt;
-    rest.l2 = r.l2;
-    rest.rs = r.rs;
-    rest.gy = r.gy;
-    rest.zero = d_hidden;
-    rest.zs = dhs;
-    rest.M = s.M;
-    rest.V = s.V;
-    rest.ignore_index = prep.ignore_index;
-    rest.targets = prep.targets;
-    if ((e = pack_hidden(call, s, r, hidden, hs, r.idx, r.rows, rest)) != cudaSuccess ||
-        (e = pack_weights(call, s, r, weight, ws, &w, &wstride)) != cudaSuccess)
+    if ((e = pack_weights(call, s, r, weight, ws, &w, &wstride, false)) != cudaSuccess)
         return e;
     PairArgs grad{}, dw{}, dh{};
     const int tiles_k = static_cast<int>((s.K + kPairN - 1) / kPairN);
@@ -437,6 +457,7 @@ cudaError_t launch_linear_bwd(const Call &call, const HeadShape &s, const HeadSc
         a->cols = s.K;
         a->acc = r.acc;
         a->slices = r.slices;
+        a->arrived = r.arrived;
         a->lda = round_up(s.K, kPairN);
     }
     grad.kblocks = static_cast<int>((s.K + 63) / 64);
@@ -541,6 +562,7 @@ extern "C" int linear_ce_fwd(const void *hidden, int64_t hidden_stride, const vo
     prep.n_out = r.n;
     prep.rows_out = r.rows;
     prep.fail = r.fail;
+    prep.done = r.done;
     prep.idx = r.idx;
     prep.tgt = r.tgt;
     prep.reduction = reduction;
@@ -593,6 +615,7 @@ extern "C" int linear_ce_bwd(const void *hidden, int64_t hidden_stride, const vo
     prep.n_out = r.n;
     prep.rows_out = r.rows;
     prep.fail = r.fail;
+    prep.done = r.done;
     prep.idx = r.idx;
     prep.tgt = r.tgt;
     prep.reduction = reduction;
@@ -601,6 +624,7 @@ extern "C" int linear_ce_bwd(const void *hidden, int64_t hidden_stride, const vo
     prep.l2 = r.l2;
     prep.rs = r.rs;
     prep.alpha = r.alpha;
+    prep.arrived = r.arrived;
     prep.head = dtype == GBCE_F16 ? 16384.f : 1.f;
     return map_error(scratch.release(launch_linear_bwd(call, s, r, hidden, hidden_stride, weight,
                                                        weight_stride, M > 0 ? d_hidden : nullptr,
@@ -635,13 +659,13 @@ extern "C" int linear_greedy(const void *hidden, int64_t hidden_stride, const vo
     const void *w = weight, *h = hidden;
     int64_t wstride = weight_stride, hstride = hidden_stride, hrows = M;
     if (s.pack_h) {
-        e = pack_hidden(call, s, r, hidden, hidden_stride, nullptr, nullptr);
+        e = launch_pack(call, s, hidden, hidden_stride, r.h, M, static_cast<int>(s.skinny ? s.mp : kPairM), true);
         h = r.h;
         hstride = s.kp;
         hrows = s.mp;
     }
     if (e == cudaSuccess)
-        e = pack_weights(call, s, r, weight, weight_stride, &w, &wstride);
+        e = pack_weights(call, s, r, weight, weight_stride, &w, &wstride, !s.pack_h);
     if (e == cudaSuccess) {
         MergeArgs m{};
         m.token = tokens;

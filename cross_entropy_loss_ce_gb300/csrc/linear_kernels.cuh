@@ -86,13 +86,15 @@ struct PairArgs {
     int64_t lda;
     int first, last;    // Hidden: the first piece does not read acc, the last one writes out
     float *slices;      // Weight, Hidden: kSplitUnits sums of kPairM x kPairN, for split tiles
+    unsigned *arrived;  // ... and 16 counters a split tile, zero before and after
 };
 
 // The tiles of a product that fill no whole wave of the CTA pairs, cut along K:
 // 248 tiles on 76 pairs take 4 waves, of which the last is a quarter full; its
 // 20 tiles in 3 slices each make it a third of a wave.  The first `whole` tiles
 // are done as they are; then come `tail` tiles in `slices` slices, slice by
-// slice, whose sums go to memory and are added in order by lin_slices_kernel.
+// slice, whose sums go to memory; whichever warp is the last to write its 32 x 128
+// part of a tile adds the slices of that part, in order, and finishes it.
 struct Split {
     int whole, tail, slices;
 };
@@ -101,8 +103,8 @@ constexpr int kSplitUnits = 4 * 80;  // slices of a launch, at most
 constexpr int kSplitMax = 8;         // slices of a tile, at most
 
 // Costs in k-steps of one tile: a slice takes its steps and about 6 more to be
-// written, and the sums' addition about 30 (measured around 8 us).  The tail is
-// the last, partial wave, or that and a whole one.
+// written, and 3 to be read again.  The tail is the last, partial wave, or that and
+// a whole one.
 __host__ __device__ inline Split split_of(int tiles, int pairs, int kblocks)
 {
     Split best{tiles, 0, 1};
@@ -111,7 +113,7 @@ __host__ __device__ inline Split split_of(int tiles, int pairs, int kblocks)
     for (int tail = rest; rest && tail <= tiles && tail <= rest + pairs; tail += pairs)
         for (int s = 2; s <= kSplitMax && 4 * s <= kblocks && tail * s <= kSplitUnits; ++s) {
             const int64_t cost = static_cast<int64_t>((tiles - tail) / pairs) * kblocks +
-                                 static_cast<int64_t>((tail * s + pairs - 1) / pairs) * ((kblocks + s - 1) / s + 6) + 30;
+                                 static_cast<int64_t>((tail * s + pairs - 1) / pairs) * ((kblocks + s - 1) / s + 6) + 3 * s;
             if (cost < least) {
                 least = cost;
                 best = Split{tiles - tail, tail, s};
@@ -132,6 +134,14 @@ __device__ __forceinline__ Unit unit_at(int u, const Split &sp, int kblocks)
     const int v = u - sp.whole, s = v / sp.tail, t = v - s * sp.tail;
     return Unit{sp.whole + t, static_cast<int>(int64_t{kblocks} * s / sp.slices),
                 static_cast<int>(int64_t{kblocks} * (s + 1) / sp.slices), t * sp.slices + s};
+}
+
+// Lets the next kernel of the stream be set up while this one runs.  Every
+// kernel of a call then waits for its predecessor before it reads or ends, so
+// that a kernel's end means the end of all before it.
+__device__ __forceinline__ void next_kernel_may_start()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 __device__ __forceinline__ void tile_at(int t, int tiles_m, int tiles_n, int &m, int &n)
@@ -244,6 +254,104 @@ __device__ __forceinline__ void store_chunk(T *row, int64_t c0, int64_t cols, co
     }
 }
 
+// 32 finished sums of a gradient product: dW times alpha to its rows; dH added
+// to what earlier pieces left and kept for the next one, or times alpha to the
+// row it belongs to.
+template <Epi E, typename T>
+__device__ __forceinline__ void finish_chunk(const PairArgs &a, float (&f)[32], int64_t row, int64_t out_row,
+                                             int64_t col, bool live, float alpha)
+{
+    if (col >= a.cols || (E == Epi::Weight ? row >= a.rows : !live))
+        return;
+    if constexpr (E == Epi::Hidden) {
+        float4 *acc4 = reinterpret_cast<float4 *>(a.acc + row * a.lda + col);
+        if (!a.first) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const float4 o = acc4[q];
+                f[4 * q] += o.x;
+                f[4 * q + 1] += o.y;
+                f[4 * q + 2] += o.z;
+                f[4 * q + 3] += o.w;
+            }
+        }
+        if (!a.last) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                acc4[q] = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        f[i] *= alpha;
+    store_chunk<T>(static_cast<T *>(a.out) + out_row * a.ldo, col, a.cols, f, a.vec);
+}
+
+// The same for a split tile's part of 32 rows (from row0) and 128 columns (from
+// col0): its slices lie kPairM x kPairN apart.  A lane takes 4 columns of each
+// row, so that a warp reads and writes whole rows.
+template <Epi E, typename T>
+__device__ __forceinline__ void finish_slices(const PairArgs &a, const float *part, int slices, int row0, int col0,
+                                              int64_t rows, float alpha)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t col = col0 + 4 * lane;
+    if (col >= a.cols)
+        return;
+    constexpr int R = 8;  // rows whose loads are in flight together, ahead of any store
+#pragma unroll 1
+    for (int r0 = 0; r0 < 32 && row0 + r0 < rows; r0 += R) {
+        float4 f[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            f[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float *from = part + r0 * kPairN + 4 * lane;  // written to the tile's end, whatever `rows`
+#pragma unroll 2
+        for (int s = 0; s < slices; ++s, from += kPairM * kPairN)
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(from + r * kPairN));
+                f[r].x += v.x;
+                f[r].y += v.y;
+                f[r].z += v.z;
+                f[r].w += v.w;
+            }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t row = row0 + r0 + r;
+            if (row >= rows)
+                break;
+            int64_t out_row = row;
+            if constexpr (E == Epi::Hidden) {
+                float4 *acc4 = reinterpret_cast<float4 *>(a.acc + row * a.lda + col);
+                if (!a.first) {
+                    const float4 o = *acc4;
+                    f[r].x += o.x;
+                    f[r].y += o.y;
+                    f[r].z += o.z;
+                    f[r].w += o.w;
+                }
+                if (!a.last) {
+                    *acc4 = f[r];
+                    continue;
+                }
+                out_row = a.idx[row];
+            }
+            T *out = static_cast<T *>(a.out) + out_row * a.ldo + col;
+            const float v[4] = {f[r].x * alpha, f[r].y * alpha, f[r].z * alpha, f[r].w * alpha};
+            if (a.vec && col + 4 <= a.cols) {
+                *reinterpret_cast<uint2 *>(out) = make_uint2(Elem<T>::pack2(v[0], v[1]), Elem<T>::pack2(v[2], v[3]));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (col + i < a.cols)
+                        Elem<T>::store(out + i, v[i]);
+            }
+        }
+    }
+}
+
 template <Epi E, typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     pair_gemm_kernel(const __grid_constant__ PairArgs a)
@@ -267,15 +375,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const uint32_t full = smem_addr(bars), empty = full + 8 * kPairStages;
     const uint32_t tfull = empty + 8 * kPairStages, tempty = tfull + 16;
 
-    const int n = a.n_ptr ? *a.n_ptr : a.n_host;
-    const int tiles_m = E == Epi::Weight ? a.tiles_m : (n + kPairM - 1) / kPairM;
-    const int kblocks = E == Epi::Weight ? (n + kPairK - 1) / kPairK : a.kblocks;
-    const int tiles = tiles_m * a.tiles_n;
-    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-    const Split sp = LOGITS ? Split{tiles, 0, 1} : split_of(tiles, pairs, kblocks);
-    const int units = sp.whole + sp.tail * sp.slices;
-    const int run = CHUNKED ? kChunk : max(kblocks, 1);  // k-steps that stay in tensor memory
-
     if (threadIdx.x == 0) {
         dead_word = 0;
         for (int i = 0; i < kPairStages; ++i) {
@@ -298,6 +397,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     cluster_wait();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
+    next_kernel_may_start();
+    wait_prerequisite_grid();
+
+    const int n = a.n_ptr ? *a.n_ptr : a.n_host;
+    const int tiles_m = E == Epi::Weight ? a.tiles_m : (n + kPairM - 1) / kPairM;
+    const int kblocks = E == Epi::Weight ? (n + kPairK - 1) / kPairK : a.kblocks;
+    const int tiles = tiles_m * a.tiles_n;
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const Split sp = LOGITS ? Split{tiles, 0, 1} : split_of(tiles, pairs, kblocks);
+    const int units = sp.whole + sp.tail * sp.slices;
+    const int run = CHUNKED ? kChunk : max(kblocks, 1);  // k-steps that stay in tensor memory
 
     // 128 sums a thread want more than the launch's 168 registers: the first
     // four warps give some of theirs up (64 x 128 + 216 x 256 <= 168 x 384)
@@ -387,7 +497,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const int limit = static_cast<int>(min(a.V, static_cast<int64_t>(INT32_MAX)));
         [[maybe_unused]] float alpha = 1.f;
         if constexpr (!LOGITS)
-            alpha = __ldg(a.alpha);
+            alpha = *a.alpha;
         int it = 0;
         bool ok = true;
         for (int u = pair; u < units && ok; u += pairs) {
@@ -426,7 +536,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 if (!ok)
                     break;
                 if constexpr (E == Epi::Stats) {  // the target's term is left out
-                    const int y = live ? __ldg(a.tgt + row) - c0 : -1;
+                    const int y = live ? a.tgt[row] - c0 : -1;
                     if (y >= 0 && y < 128) {
 #pragma unroll
                         for (int i = 0; i < 128; ++i)
@@ -457,15 +567,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 [[maybe_unused]] float l2 = 0.f, rs = 0.f, gy = 0.f;
                 if constexpr (E == Epi::Grad)
                     if (live) {
-                        y = __ldg(a.tgt + row) - a.b_row0;
+                        y = a.tgt[row] - a.b_row0;
                         inside = limit;
-                        l2 = __ldg(a.l2 + row);
-                        rs = __ldg(a.rs + row);
-                        gy = __ldg(a.gy + row);
+                        l2 = a.l2[row];
+                        rs = a.rs[row];
+                        gy = a.gy[row];
                     }
                 if constexpr (E == Epi::Hidden)
                     if (live && a.last)
-                        out_row = __ldg(a.idx + row);
+                        out_row = a.idx[row];
                 uint32_t buf[2][32];
                 tmem_ld32(lanes + acc * kPairN, buf[0]);
 #pragma unroll
@@ -490,44 +600,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         for (int q = 0; q < 8; ++q)
                             to[q] = make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
                                                 __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
-                    } else if constexpr (E == Epi::Weight) {
-                        if (row < a.rows && col < a.cols) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                f[i] = kblocks ? __uint_as_float(r[i]) * alpha : 0.f;
-                            store_chunk<T>(static_cast<T *>(a.out) + row * a.ldo, col, a.cols, f, a.vec);
-                        }
-                    } else if (live && col < a.cols) {
+                    } else {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            f[i] = __uint_as_float(r[i]);
-                        float4 *acc4 = reinterpret_cast<float4 *>(a.acc + row * a.lda + col);
-                        if (!a.first) {
-#pragma unroll
-                            for (int q = 0; q < 8; ++q) {
-                                const float4 o = acc4[q];
-                                f[4 * q] += o.x;
-                                f[4 * q + 1] += o.y;
-                                f[4 * q + 2] += o.z;
-                                f[4 * q + 3] += o.w;
-                            }
-                        }
-                        if (a.last) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                f[i] *= alpha;
-                            store_chunk<T>(static_cast<T *>(a.out) + out_row * a.ldo, col, a.cols, f, a.vec);
-                        } else {
-#pragma unroll
-                            for (int q = 0; q < 8; ++q)
-                                acc4[q] = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
-                        }
+                            f[i] = kblocks ? __uint_as_float(r[i]) : 0.f;
+                        finish_chunk<E, T>(a, f, row, out_row, col, live, alpha);
                     }
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
                     bar_arrive_cluster(tempty0 + 8 * acc);
+                if constexpr (!LOGITS)
+                    if (un.slice >= 0) {
+                        // the last of this part's slices to arrive adds them all up
+                        const int t = un.tile - sp.whole;
+                        unsigned *count = a.arrived + t * 16 + rank * 8 + (warp - 4);
+                        unsigned before = 0;
+                        __threadfence();
+                        __syncwarp();
+                        if (lane == 0)
+                            before = atomicAdd(count, 1u);
+                        before = __shfl_sync(0xffffffffu, before, 0);
+                        if (before == static_cast<unsigned>(sp.slices - 1)) {
+                            __threadfence();
+                            if (lane == 0)
+                                *count = 0u;  // for the next launch
+                            const int r0 = tm * kPairM + static_cast<int>(rank) * 128 + ew * 32;
+                            finish_slices<E, T>(a, a.slices + int64_t{t} * sp.slices * kPairM * kPairN +
+                                                       (r0 - tm * kPairM) * kPairN + half * 128,
+                                                sp.slices, r0, c0, E == Epi::Weight ? a.rows : n, alpha);
+                        }
+                    }
             }
         }
     }
@@ -543,64 +647,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     cluster_wait();
     if (warp == 2)
         tmem_free<2>(tmem, 512);
-}
-
-// Adds the slices of a launch's split tiles in order and finishes their sums as
-// pair_gemm_kernel does.  A CTA takes 16 rows of a tile, a thread 16 columns.
-template <Epi E, typename T>
-__global__ void __launch_bounds__(256) lin_slices_kernel(const __grid_constant__ PairArgs a, int pairs)
-{
-    const int n = *a.n_ptr;
-    const int tiles_m = E == Epi::Weight ? a.tiles_m : (n + kPairM - 1) / kPairM;
-    const int kblocks = E == Epi::Weight ? (n + kPairK - 1) / kPairK : a.kblocks;
-    const Split sp = split_of(tiles_m * a.tiles_n, pairs, kblocks);
-    const float alpha = __ldg(a.alpha);
-    for (int b = blockIdx.x; b < sp.tail * 16; b += gridDim.x) {
-        const int t = b >> 4, r = (b & 15) * 16 + (threadIdx.x >> 4), c = (threadIdx.x & 15) * 16;
-        int tm, tn;
-        tile_at(sp.whole + t, tiles_m, a.tiles_n, tm, tn);
-        const int row = tm * kPairM + r, col = tn * kPairN + c;
-        if (row >= (E == Epi::Weight ? a.rows : n) || col >= a.cols)
-            continue;
-        float f[16] = {};
-        for (int s = 0; s < sp.slices; ++s) {
-            const float4 *from = reinterpret_cast<const float4 *>(
-                a.slices + (int64_t{t * sp.slices + s} * kPairM + r) * kPairN + c);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float4 v = __ldcs(from + q);
-                f[4 * q] += v.x;
-                f[4 * q + 1] += v.y;
-                f[4 * q + 2] += v.z;
-                f[4 * q + 3] += v.w;
-            }
-        }
-        int64_t out_row = row;
-        if constexpr (E == Epi::Hidden) {
-            float4 *acc4 = reinterpret_cast<float4 *>(a.acc + row * a.lda + col);
-            if (!a.first) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float4 v = acc4[q];
-                    f[4 * q] += v.x;
-                    f[4 * q + 1] += v.y;
-                    f[4 * q + 2] += v.z;
-                    f[4 * q + 3] += v.w;
-                }
-            }
-            if (!a.last) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    acc4[q] = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
-                continue;
-            }
-            out_row = __ldg(a.idx + row);
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            f[i] *= alpha;
-        store_chunk<T>(static_cast<T *>(a.out) + out_row * a.ldo, col, a.cols, f, a.vec);
-    }
 }
 
 // ---------------------------------------------------------------------------
@@ -656,12 +702,6 @@ __global__ void __launch_bounds__(skinny_threads<NG>(), 1) skinny_kernel(const _
     const uint32_t tfull = empty + 8 * kStages, tempty = tfull + 16;
     const uint32_t idesc = a.bf16 ? mma_idesc(true, false, false, 128, kN) : mma_idesc(false, false, false, 128, kN);
 
-    const int n = a.n_ptr ? *a.n_ptr : a.n_host;
-    const int64_t units = (a.V + kSkinnyUnit - 1) / kSkinnyUnit;
-    const int64_t v0 = units * blockIdx.x / gridDim.x * kSkinnyUnit;
-    const int64_t v1 = min(units * (blockIdx.x + 1) / gridDim.x * kSkinnyUnit, a.V);
-    const int tiles = n > 0 ? static_cast<int>((v1 - v0 + 127) / 128) : 0;
-
     if (threadIdx.x == 0) {
         dead_word = 0;
         for (int i = 0; i < kStages; ++i) {
@@ -677,14 +717,22 @@ __global__ void __launch_bounds__(skinny_threads<NG>(), 1) skinny_kernel(const _
         prefetch_map(&a.wu);
         prefetch_map(&a.h);
     }
-    if (!GREEDY && threadIdx.x < kN)
-        tgt[threadIdx.x] = static_cast<int>(threadIdx.x) < n ? __ldg(a.tgt + threadIdx.x) : -1;
     if (warp == 2)
         tmem_alloc<1>(smem_addr(&tmem_slot), kCols);
+    next_kernel_may_start();
+    wait_prerequisite_grid();
+    const int n = a.n_ptr ? *a.n_ptr : a.n_host;
+    if (!GREEDY && threadIdx.x < kN)
+        tgt[threadIdx.x] = static_cast<int>(threadIdx.x) < n ? a.tgt[threadIdx.x] : -1;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
+
+    const int64_t units = (a.V + kSkinnyUnit - 1) / kSkinnyUnit;
+    const int64_t v0 = units * blockIdx.x / gridDim.x * kSkinnyUnit;
+    const int64_t v1 = min(units * (blockIdx.x + 1) / gridDim.x * kSkinnyUnit, a.V);
+    const int tiles = n > 0 ? static_cast<int>((v1 - v0 + 127) / 128) : 0;
 
     if (warp == 0 && lane == 0) {
         const uint64_t once = policy_evict_first(), again = policy_evict_last();
@@ -826,17 +874,24 @@ __global__ void __launch_bounds__(skinny_threads<NG>(), 1) skinny_kernel(const _
                     ti[lane * 33 + j] = best[j];
             }
             __syncwarp();
-            float mt = tm[lane], dt = td[lane];
+            float mt = tm[lane], dt = 0.f;
             int it = GREEDY ? ti[lane] : 0;
+#pragma unroll 8
             for (int l = 1; l < 32; ++l) {
-                const float m2 = tm[l * 33 + lane], d2 = td[l * 33 + lane];
+                const float m2 = tm[l * 33 + lane];
                 if constexpr (GREEDY) {
-                    best_merge(mt, dt, it, m2, d2, ti[l * 33 + lane]);
-                } else {
-                    const float mn = fmaxf(mt, m2);
-                    dt = rescaled(dt, mt, mn) + rescaled(d2, m2, mn);
-                    mt = mn;
+                    const int i2 = ti[l * 33 + lane];
+                    it = m2 > mt || (m2 == mt && i2 < it) ? i2 : it;
                 }
+                mt = fmaxf(mt, m2);
+            }
+#pragma unroll 8
+            for (int l = 0; l < 32; ++l) {
+                const float m2 = tm[l * 33 + lane], d2 = td[l * 33 + lane];
+                if constexpr (GREEDY)
+                    dt += ti[l * 33 + lane] == it ? d2 : rescaled_others(d2, m2, mt);
+                else
+                    dt += rescaled(d2, m2, mt);
             }
             sm[warp - 4][lane] = mt;
             sd[warp - 4][lane] = dt;
@@ -885,6 +940,7 @@ struct PrepArgs {
     int *n_out;      // targets that are not ignore_index (the divisor of the mean)
     int *rows_out;   // rows listed: those with a target in [0, V)
     unsigned *fail;
+    unsigned *done;  // forward: CTAs of the merge that have finished
     int *idx, *tgt;
     int reduction;
     // forward: the values of the rows not listed, and of an empty batch
@@ -892,11 +948,20 @@ struct PrepArgs {
     // backward
     const float *lse_in, *grad_scale;
     float *l2, *rs, *alpha;
+    unsigned *arrived;  // counters of split tiles
     float head;      // power of two that keeps 16-bit G in range (fp16: 2^14)
 };
 
+// What a CTA knows of the listed rows after prep_rows.
+struct Listed {
+    int rows;
+    float one, inv;  // the factor that all rows share, and the power of two it is relative to
+};
+
+// By all NT threads of a CTA.  `write`: this CTA writes the call's lists and
+// values to memory; s_idx, s_tgt (NULL: not kept) get the list for this CTA.
 template <int NT, bool BWD>
-__global__ void __launch_bounds__(NT) lin_prep_kernel(const PrepArgs a)
+__device__ __forceinline__ Listed prep_rows(const PrepArgs &a, bool write, int *s_idx, int *s_tgt)
 {
     __shared__ int warp_rows[NT / 32], warp_n[NT / 32];
     __shared__ float warp_max[NT / 32];
@@ -912,7 +977,7 @@ __global__ void __launch_bounds__(NT) lin_prep_kernel(const PrepArgs a)
     int rows = 0, n = 0;
     float top = 0.f;
     bool bad = false;
-#pragma unroll 8
+#pragma unroll 4
     for (int64_t i = lo + lane; i < hi; i += 32) {
         const int64_t y = __ldg(a.targets + i);
         if (y != a.ignore_index) {
@@ -930,43 +995,48 @@ __global__ void __launch_bounds__(NT) lin_prep_kernel(const PrepArgs a)
     }
     if (bad)
         any_bad = 1;
+    rows = __reduce_add_sync(0xffffffffu, rows);
+    n = __reduce_add_sync(0xffffffffu, n);
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        rows += __shfl_xor_sync(0xffffffffu, rows, off);
-        n += __shfl_xor_sync(0xffffffffu, n, off);
+    for (int off = 16; off > 0; off >>= 1)
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    }
     if (lane == 0) {
         warp_rows[warp] = rows;
         warp_n[warp] = n;
         warp_max[warp] = top;
     }
     __syncthreads();
-    int at = 0, total = 0, n_all = 0;
+    int at = 0;
+    Listed list{0, one, 1.f};
+    int n_all = 0;
     top = 0.f;
+#pragma unroll 8
     for (int w = 0; w < NT / 32; ++w) {
         at += w < warp ? warp_rows[w] : 0;
-        total += warp_rows[w];
+        list.rows += warp_rows[w];
         n_all += warp_n[w];
         top = fmaxf(top, warp_max[w]);
     }
     // factors relative to a power of two at or above the largest, so that their
     // 16-bit products with (p - onehot) stay in range whatever the loss scale
-    float inv = 1.f;
     if (BWD) {
         int e = 0;
         if (a.grad_scale && top > 0.f && top < INFINITY)
             frexpf(top, &e);
         e = min(max(e, -100), 127);
-        inv = ldexpf(a.head, -e);
-        if (threadIdx.x == 0)
-            *a.alpha = (a.reduction == kReduceMean ? 1.f / static_cast<float>(n_all) : 1.f) *
+        list.inv = ldexpf(a.head, -e);
+        if (write && threadIdx.x == 0)
+            *a.alpha = (a.reduction == kReduceMean ? 1.f / static_cast<float>(max(n_all, 1)) : 1.f) *
                        ldexpf(1.f / a.head, e);
+        if (write)
+            for (int i = threadIdx.x; i < kSplitUnits / 2 * 16; i += NT)
+                a.arrived[i] = 0u;
     }
-    if (threadIdx.x == 0) {
+    if (write && threadIdx.x == 0) {
         *a.n_out = n_all;
-        *a.rows_out = total;
+        *a.rows_out = list.rows;
         *a.fail = 0u;
+        *a.done = 0u;
         if (any_bad)
             atomicOr(&g_flags, kFlagBadTarget);
         if (!BWD && a.M == 0 && a.reduction != kReduceNone)
@@ -981,13 +1051,19 @@ __global__ void __launch_bounds__(NT) lin_prep_kernel(const PrepArgs a)
         const unsigned votes = __ballot_sync(0xffffffffu, listed);
         if (listed) {
             const int pos = at + __popc(votes & ((1u << lane) - 1));
-            a.idx[pos] = static_cast<int>(i);
-            a.tgt[pos] = static_cast<int>(y);
-            if (BWD) {
-                a.l2[pos] = __ldg(a.lse_in + i) * kLog2e;
-                a.rs[pos] = (a.grad_scale && a.reduction == kReduceNone ? __ldg(a.grad_scale + i) : one) * inv;
+            if (s_idx) {
+                s_idx[pos] = static_cast<int>(i);
+                s_tgt[pos] = static_cast<int>(y);
             }
-        } else if (!BWD && i < hi) {
+            if (write) {
+                a.idx[pos] = static_cast<int>(i);
+                a.tgt[pos] = static_cast<int>(y);
+                if (BWD) {
+                    a.l2[pos] = __ldg(a.lse_in + i) * kLog2e;
+                    a.rs[pos] = (a.grad_scale && a.reduction == kReduceNone ? __ldg(a.grad_scale + i) : one) * list.inv;
+                }
+            }
+        } else if (!BWD && write && i < hi) {
             const float v = skip ? 0.f : __int_as_float(0x7fc00000);
             a.row_loss[i] = v;
             if (a.lse_out)
@@ -995,6 +1071,7 @@ __global__ void __launch_bounds__(NT) lin_prep_kernel(const PrepArgs a)
         }
         at += __popc(votes);
     }
+    return list;
 }
 
 // sum_k a[k] b[k] of two rows in fp32, by NT threads (a warp's share in each of its lanes).
@@ -1008,8 +1085,8 @@ __device__ __forceinline__ float row_dot(const T *a, const T *b, int64_t K, bool
 #pragma unroll 4
         for (int64_t j = lane; j < K / 8; j += NT) {
             float x[8], y[8];
-            Elem<T>::unpack(__ldg(reinterpret_cast<const uint4 *>(a) + j), x);
-            Elem<T>::unpack(__ldg(reinterpret_cast<const uint4 *>(b) + j), y);
+            Elem<T>::unpack(reinterpret_cast<const uint4 *>(a)[j], x);
+            Elem<T>::unpack(reinterpret_cast<const uint4 *>(b)[j], y);
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
                 s0 = fmaf(x[i], y[i], s0);
@@ -1031,9 +1108,6 @@ struct GatherArgs {
     int64_t ss;
     void *dst;
     int64_t lds;
-    const int *idx;     // NULL: rows as they stand
-    const int *n_ptr;
-    int64_t n_host;
     int64_t K;
     int pad;
     int vec;            // src allows 16-byte loads
@@ -1041,9 +1115,7 @@ struct GatherArgs {
     const void *w;      // NULL: none
     int64_t ws;
     int wvec;           // w and src allow 16-byte loads
-    const int *tgt;
     float *xy;          // forward: x_y
-    const float *l2, *rs;
     float *gy;          // backward: (p_y - 1) times the row's factor
     // backward: unlisted rows of the hidden gradient
     void *zero;
@@ -1053,13 +1125,13 @@ struct GatherArgs {
     const int64_t *targets;
 };
 
-template <typename T, int NT>
-__global__ void __launch_bounds__(NT) lin_gather_kernel(const GatherArgs a)
+// By one warp of `step`; row_of(i) and target_of(i) of the n listed rows,
+// entry_of(i, x_y) the backward's entry of its target.
+template <typename T, typename RowOf, typename TargetOf, typename EntryOf>
+__device__ __forceinline__ void gather_rows(const GatherArgs &a, int64_t n, int64_t first, int64_t step,
+                                            RowOf row_of, TargetOf target_of, EntryOf entry_of)
 {
     const int lane = threadIdx.x & 31;
-    const int64_t first = blockIdx.x * int64_t{NT / 32} + (threadIdx.x >> 5);
-    const int64_t step = gridDim.x * int64_t{NT / 32};
-    const int64_t n = a.n_ptr ? *a.n_ptr : a.n_host;
     const int64_t rows = (n + a.pad - 1) / a.pad * a.pad;
     const T zero_value = T(0.f);
     for (int64_t i = first; i < rows; i += step) {
@@ -1069,7 +1141,7 @@ __global__ void __launch_bounds__(NT) lin_gather_kernel(const GatherArgs a)
                 reinterpret_cast<uint4 *>(d)[j] = make_uint4(0, 0, 0, 0);
             continue;
         }
-        const T *s = static_cast<const T *>(a.src) + (a.idx ? static_cast<int64_t>(a.idx[i]) : i) * a.ss;
+        const T *s = static_cast<const T *>(a.src) + row_of(i) * a.ss;
         int64_t done = 0;
         if (a.vec) {  // K may end inside the last vector: the rest is zeroed one by one
             done = a.K / 8 * 8;
@@ -1080,12 +1152,12 @@ __global__ void __launch_bounds__(NT) lin_gather_kernel(const GatherArgs a)
         for (int64_t j = done + lane; j < a.lds; j += 32)
             d[j] = j < a.K ? s[j] : zero_value;
         if (a.w) {
-            const float x = row_dot<T, 32>(s, static_cast<const T *>(a.w) + int64_t{a.tgt[i]} * a.ws, a.K, a.wvec);
+            const float x = row_dot<T, 32>(s, static_cast<const T *>(a.w) + target_of(i) * a.ws, a.K, a.wvec);
             if (lane == 0) {
                 if (a.xy)
                     a.xy[i] = x;
-                else  // e^(x_y - lse) - 1, from the difference itself
-                    a.gy[i] = expm1f(fmaf(x, kLog2e, -a.l2[i]) * kLn2) * a.rs[i];
+                else
+                    a.gy[i] = entry_of(i, x);
             }
         }
     }
@@ -1103,6 +1175,62 @@ __global__ void __launch_bounds__(NT) lin_gather_kernel(const GatherArgs a)
         }
 }
 
+// (e^(x_y - lse) - 1) times the row's factor, from the difference itself.
+__device__ __forceinline__ float target_entry(float x, float l2, float rs)
+{
+    return expm1f(fmaf(x, kLog2e, -l2) * kLn2) * rs;
+}
+
+// Many rows: one CTA lists them, then many pack them.
+template <int NT, bool BWD>
+__global__ void __launch_bounds__(NT) lin_prep_kernel(const PrepArgs a)
+{
+    next_kernel_may_start();
+    prep_rows<NT, BWD>(a, true, nullptr, nullptr);
+}
+
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT) lin_gather_kernel(const GatherArgs a, const PrepArgs p)
+{
+    next_kernel_may_start();
+    wait_prerequisite_grid();
+    gather_rows<T>(
+        a, *p.rows_out, blockIdx.x * int64_t{NT / 32} + (threadIdx.x >> 5), gridDim.x * int64_t{NT / 32},
+        [&](int64_t i) { return int64_t{p.idx[i]}; }, [&](int64_t i) { return int64_t{p.tgt[i]}; },
+        [&](int64_t i, float x) { return target_entry(x, p.l2[i], p.rs[i]); });
+}
+
+// Up to kStartRows rows: every CTA lists them for itself (8 KB of targets from
+// L2) and packs its own, one launch in place of two.
+constexpr int kStartRows = 1024;
+
+template <typename T, bool BWD, int NT>
+__global__ void __launch_bounds__(NT) lin_start_kernel(const GatherArgs a, const PrepArgs p)
+{
+    __shared__ int idx[kStartRows], tgt[kStartRows];
+    next_kernel_may_start();
+    const Listed list = prep_rows<NT, BWD>(p, blockIdx.x == 0, idx, tgt);
+    __syncthreads();
+    gather_rows<T>(
+        a, list.rows, blockIdx.x * int64_t{NT / 32} + (threadIdx.x >> 5), gridDim.x * int64_t{NT / 32},
+        [&](int64_t i) { return int64_t{idx[i]}; }, [&](int64_t i) { return int64_t{tgt[i]}; },
+        [&](int64_t i, float x) {
+            const float g = p.grad_scale && p.reduction == kReduceNone ? p.grad_scale[idx[i]] : list.one;
+            return target_entry(x, p.lse_in[idx[i]] * kLog2e, g * list.inv);
+        });
+}
+
+// Rows as they stand (weights, or hidden states of the arg max, that a tensor map cannot read).
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT) lin_pack_kernel(const GatherArgs a, int64_t n)
+{
+    next_kernel_may_start();
+    wait_prerequisite_grid();
+    gather_rows<T>(
+        a, n, blockIdx.x * int64_t{NT / 32} + (threadIdx.x >> 5), gridDim.x * int64_t{NT / 32},
+        [](int64_t i) { return i; }, [](int64_t) { return int64_t{0}; }, [](int64_t, float) { return 0.f; });
+}
+
 // ---------------------------------------------------------------------------
 // the partial pairs of each row, merged in order
 
@@ -1115,6 +1243,12 @@ struct MergeArgs {
     const int *idx;
     const float *xy;
     float *row_loss, *lse;
+    float *loss;        // NULL: no reduction
+    const int *n_mean;  // targets that are not ignored
+    const unsigned *fail;
+    unsigned *done;
+    int64_t M;
+    int reduction;
     // arg max: its logit is formed again from these rows
     int64_t *token;
     float *logprob;
@@ -1147,35 +1281,55 @@ __device__ __forceinline__ float loss_beside(float s, float d, float xy, float &
     return l - t * kLn2;
 }
 
-// One warp per listed row.
+// One warp per listed row; the last CTA to finish adds the row losses in an
+// order fixed by M.
 template <int NT>
 __global__ void __launch_bounds__(NT) lin_merge_kernel(const MergeArgs a)
 {
+    __shared__ int last;
     const int lane = threadIdx.x & 31;
     const int64_t row = blockIdx.x * int64_t{NT / 32} + (threadIdx.x >> 5);
-    if (row >= *a.n_ptr)
-        return;
-    const float2 *part = a.part + row * a.parts;
-    float s = -INFINITY, d = 0.f;
+    next_kernel_may_start();
+    wait_prerequisite_grid();
+    if (row < *a.n_ptr) {
+        const float2 *part = a.part + row * a.parts;
+        float s = -INFINITY, d = 0.f;
 #pragma unroll 4
-    for (int p = lane; p < a.parts; p += 32) {
-        const float2 q = part[p];
-        const float sn = fmaxf(s, q.x);
-        d = shifted(d, s, sn) + shifted(q.y, q.x, sn);
-        s = sn;
-    }
-    float top = s;
+        for (int p = lane; p < a.parts; p += 32) {
+            const float2 q = part[p];
+            const float sn = fmaxf(s, q.x);
+            d = shifted(d, s, sn) + shifted(q.y, q.x, sn);
+            s = sn;
+        }
+        float top = s;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    d = warp_sum(shifted(d, s, top));
-    if (lane == 0) {
-        const int64_t out = a.idx[row];
-        float lse;
-        a.row_loss[out] = loss_beside(top, d, a.xy[row], lse);
-        if (a.lse)
-            a.lse[out] = lse;
+        for (int off = 16; off > 0; off >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        d = warp_sum(shifted(d, s, top));
+        if (lane == 0) {
+            const int64_t out = a.idx[row];
+            float lse;
+            a.row_loss[out] = loss_beside(top, d, a.xy[row], lse);
+            if (a.lse)
+                a.lse[out] = lse;
+        }
     }
+    if (!a.loss)
+        return;
+    __threadfence();
+    __syncthreads();
+    if (gridDim.x > 1) {
+        if (threadIdx.x == 0)
+            last = atomicAdd(a.done, 1u) == gridDim.x - 1;
+        __syncthreads();
+        if (!last)
+            return;
+        __threadfence();
+    }
+    const float s = sum_row_losses<NT>(a.row_loss, a.M, threadIdx.x, 1);
+    if (threadIdx.x == 0)
+        *a.loss = __ldcg(a.fail) ? __int_as_float(0x7fc00000)
+                                 : a.reduction == kReduceMean ? s / static_cast<float>(*a.n_mean) : s;
 }
 
 // One CTA per row: its partials, then the dot product of its token.
@@ -1186,6 +1340,8 @@ __global__ void __launch_bounds__(NT) lin_token_kernel(const MergeArgs a)
     __shared__ int si[NT / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t row = blockIdx.x;
+    next_kernel_may_start();
+    wait_prerequisite_grid();
     const float4 *part = a.best + row * a.parts;
     float m = -INFINITY, d = 0.f;
     int best = INT32_MAX;
