@@ -427,7 +427,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 const int am = tm * kPairM + static_cast<int>(rank) * 128;
                 const int bn = tn * kPairN + static_cast<int>(rank) * 128;
                 for (int kb = un.k0; kb < un.k1; ++kb) {
-                    if (!(ok = bar_wait_cluster(empty + 8 * slot, phase ^ 1, dead)))
+                    if (!(ok = bar_wait<true>(empty + 8 * slot, phase ^ 1, dead)))
                         break;
                     if (rank == 0)
                         mbar_arrive_expect_tx(full + 8 * slot, 2 * kPairStageBytes);
@@ -462,12 +462,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 const Unit un = unit_at(u, sp, kblocks);
                 for (int kb0 = un.k0; ok && (kb0 < un.k1 || kb0 == 0); kb0 += run, ++it) {
                     const int acc = it & 1;
-                    if (!(ok = bar_wait_cluster(tempty + 8 * acc, ((it >> 1) & 1) ^ 1, dead)))
+                    if (!(ok = bar_wait<true>(tempty + 8 * acc, ((it >> 1) & 1) ^ 1, dead)))
                         break;
                     tc_fence_after();
                     const int kb1 = min(kb0 + run, un.k1);
                     for (int kb = kb0; kb < kb1; ++kb) {
-                        if (!(ok = bar_wait_cluster(full + 8 * slot, phase, dead)))
+                        if (!(ok = bar_wait<true>(full + 8 * slot, phase, dead)))
                             break;
                         tc_fence_after();
                         const uint32_t sa = ring + slot * kPairStageBytes, sb = sa + kPairStageBytes / 2;
@@ -512,7 +512,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 float x[128];
                 for (int kb0 = 0; kb0 < kblocks; kb0 += run, ++it) {
                     const int acc = it & 1;
-                    if (!(ok = bar_wait_cluster(tfull + 8 * acc, (it >> 1) & 1, dead)))
+                    if (!(ok = bar_wait<true>(tfull + 8 * acc, (it >> 1) & 1, dead)))
                         break;
                     tc_fence_after();
                     uint32_t buf[2][16];
@@ -558,7 +558,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 }
             } else {
                 const int acc = it & 1;
-                if (!(ok = bar_wait_cluster(tfull + 8 * acc, (it >> 1) & 1, dead)))
+                if (!(ok = bar_wait<true>(tfull + 8 * acc, (it >> 1) & 1, dead)))
                     break;
                 ++it;
                 tc_fence_after();
@@ -744,7 +744,7 @@ __global__ void __launch_bounds__(skinny_threads<NG>(), 1) skinny_kernel(const _
             const int rows = static_cast<int>(min(v1 - row, int64_t{128}));
             const int nunit = (rows + kSkinnyUnit - 1) / kSkinnyUnit;
             for (int kb = 0; kb < a.kblocks; ++kb) {
-                if (!(ok = bar_wait(empty + 8 * slot, phase ^ 1, dead)))
+                if (!(ok = bar_wait<false>(empty + 8 * slot, phase ^ 1, dead)))
                     break;
                 const uint32_t sw = ring + slot * kStage, sh = sw + kSkinnyStageW;
                 const uint32_t bar = full + 8 * slot;
@@ -770,12 +770,12 @@ __global__ void __launch_bounds__(skinny_threads<NG>(), 1) skinny_kernel(const _
         for (int t = 0; t < tiles && ok; ++t) {
             for (int kb0 = 0; ok && kb0 < a.kblocks; kb0 += kChunk, ++it) {
                 const int acc = it & 1;
-                if (!(ok = bar_wait(tempty + 8 * acc, ((it >> 1) & 1) ^ 1, dead)))
+                if (!(ok = bar_wait<false>(tempty + 8 * acc, ((it >> 1) & 1) ^ 1, dead)))
                     break;
                 tc_fence_after();
                 const int kb1 = min(kb0 + kChunk, a.kblocks);
                 for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!(ok = bar_wait(full + 8 * slot, phase, dead)))
+                    if (!(ok = bar_wait<false>(full + 8 * slot, phase, dead)))
                         break;
                     tc_fence_after();
                     const uint32_t sw = ring + slot * kStage;
@@ -812,7 +812,7 @@ __global__ void __launch_bounds__(skinny_threads<NG>(), 1) skinny_kernel(const _
             float sum[32];
             for (int kb0 = 0; kb0 < a.kblocks; kb0 += kChunk, ++it) {
                 const int acc = it & 1;
-                if (!(ok = bar_wait(tfull + 8 * acc, (it >> 1) & 1, dead)))
+                if (!(ok = bar_wait<false>(tfull + 8 * acc, (it >> 1) & 1, dead)))
                     break;
                 tc_fence_after();
                 const uint32_t src = tmem + acc * kN + 32 * group + (static_cast<uint32_t>(ew * 32) << 16);

@@ -9,44 +9,43 @@
 
 namespace gbce {
 
-// A wait that runs out sets *dead (shared memory); every later wait of the CTA
-// then returns at once, so a failed copy ends the kernel instead of hanging it.
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *dead)
-{
-    if (mbar_try_wait(bar, parity))
-        return true;
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait(bar, parity)) {
-        if (*dead)
-            return false;
-        if (globaltimer_ns() - t0 > kWaitLimitNs) {
-            *dead = 1;
-            return false;
-        }
-    }
-    return true;
-}
-
-// The same for a barrier that the other CTA of a pair arrives on.
-__device__ __forceinline__ bool bar_try_wait_cluster(uint32_t bar, uint32_t parity)
+// One look at phase `parity` of an mbarrier that sleeps in hardware until the
+// phase ends, 10 ms at most: waits that look again and again take issue slots
+// and power from the matrix instructions (8192 x 128256, K 4096 forward: 5.06 ms
+// so, 5.18 with the default sleep, 5.5 with tight loops).  CLUSTER: the other CTA
+// of a pair arrives on it too.
+template <bool CLUSTER>
+__device__ __forceinline__ bool bar_try_wait(uint32_t bar, uint32_t parity)
 {
     uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
+    if constexpr (CLUSTER)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(bar), "r"(parity), "r"(10000000u)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(bar), "r"(parity), "r"(10000000u)
+            : "memory");
     return done != 0;
 }
 
-__device__ __forceinline__ bool bar_wait_cluster(uint32_t bar, uint32_t parity, volatile int *dead)
+// A wait that runs out sets *dead (shared memory); every later wait of the CTA
+// then returns soon, so a failed copy ends the kernel instead of hanging it.
+template <bool CLUSTER>
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *dead)
 {
-    if (bar_try_wait_cluster(bar, parity))
+    if (bar_try_wait<CLUSTER>(bar, parity))
         return true;
     const uint64_t t0 = globaltimer_ns();
-    while (!bar_try_wait_cluster(bar, parity)) {
+    while (!bar_try_wait<CLUSTER>(bar, parity)) {
         if (*dead)
             return false;
         if (globaltimer_ns() - t0 > kWaitLimitNs) {
