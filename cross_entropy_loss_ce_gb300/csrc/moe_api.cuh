@@ -12,30 +12,46 @@ constexpr int64_t kMoeRowsPerGroup = 2;   // rows that share a group's set-up, a
 
 using MoeFn = void (*)(const MoeArgs);
 
-// The rows kernel for P = ceil(E / VEC) units of VEC values a row.
+// Lanes that share a row of P = E / VEC units: about 16 values a lane, so that
+// the reductions' shuffles are few and a warp holds several rows.
+int moe_lanes(int P, int vec)
+{
+    if (vec == 1)
+        return P <= 64 ? 16 : 32;
+    return P <= 8 ? 4 : (P <= 32 ? 8 : (P <= 64 ? 16 : 32));
+}
+
+// The rows kernel for P units of VEC values a row.
 template <typename T, int VEC, bool ALL, int NT>
 MoeFn pick_moe_units(int P)
 {
-    if (P <= 4)
-        return moe_rows_kernel<T, VEC, 4, 1, ALL, NT>;
-    if (P <= 16)
-        return moe_rows_kernel<T, VEC, 16, 1, ALL, NT>;
-    if (P <= 32)
-        return moe_rows_kernel<T, VEC, 32, 1, ALL, NT>;
-    if (P <= 64)
-        return moe_rows_kernel<T, VEC, 32, 2, ALL, NT>;
-    if (P <= 128)
-        return moe_rows_kernel<T, VEC, 32, 4, ALL, NT>;
-    if constexpr (VEC <= 4) {  // E <= 1024: at most 128 units of 8 values
-        if (P <= 256)
+    if constexpr (VEC == 1) {
+        if (P <= 16)
+            return moe_rows_kernel<T, 1, 16, 1, ALL, NT>;
+        if (P <= 64)
+            return moe_rows_kernel<T, 1, 16, 4, ALL, NT>;
+        if (P <= 128)
+            return moe_rows_kernel<T, 1, 32, 4, ALL, NT>;
+        if (P <= 512)
+            return moe_rows_kernel<T, 1, 32, 16, ALL, NT>;
+        return moe_rows_kernel<T, 1, 32, 32, ALL, NT>;
+    } else {
+        if (P <= 4)
+            return moe_rows_kernel<T, VEC, 4, 1, ALL, NT>;
+        if (P <= 8)
+            return moe_rows_kernel<T, VEC, 4, 2, ALL, NT>;
+        if (P <= 16)
+            return moe_rows_kernel<T, VEC, 8, 2, ALL, NT>;
+        if (P <= 32)
+            return moe_rows_kernel<T, VEC, 8, 4, ALL, NT>;
+        if (P <= 64)
+            return moe_rows_kernel<T, VEC, 16, 4, ALL, NT>;
+        if (VEC == 8 || P <= 128)
+            return moe_rows_kernel<T, VEC, 32, 4, ALL, NT>;
+        if constexpr (VEC == 4)
             return moe_rows_kernel<T, VEC, 32, 8, ALL, NT>;
     }
-    if constexpr (VEC == 1) {
-        if (P <= 512)
-            return moe_rows_kernel<T, VEC, 32, 16, ALL, NT>;
-        return moe_rows_kernel<T, VEC, 32, 32, ALL, NT>;
-    }
-    return nullptr;  // not reached: P <= kMoeMaxExperts / VEC
+    return nullptr;  // not reached
 }
 
 template <typename T, bool ALL, int NT>
@@ -74,7 +90,36 @@ int moe_vec(const MoeArgs &a, int dtype)
     return 1;
 }
 
-cudaError_t launch_moe(MoeArgs a, int dtype, int vec, void *scratch, int64_t sms, cudaStream_t stream)
+struct MoeGrid {
+    MoeFn fn;
+    int device;
+    int64_t ctas;
+};
+std::vector<MoeGrid> g_moe_grid;
+
+// CTAs of a rows kernel that fit on the device at once (cached).
+cudaError_t moe_resident(MoeFn fn, int device, int64_t sms, int64_t *out)
+{
+    std::lock_guard<std::mutex> lk(g_cfg_mu);
+    for (const MoeGrid &g : g_moe_grid)
+        if (g.fn == fn && g.device == device) {
+            *out = g.ctas;
+            return cudaSuccess;
+        }
+    RelaxedCapture relaxed;
+    int n = 0;
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, kMoeThreads, 0);
+    if (e != cudaSuccess)
+        return e;
+    *out = (n < 1 ? 1 : n) * sms;
+    if (*out > kMoeMaxCtas)
+        *out = kMoeMaxCtas;
+    g_moe_grid.push_back({fn, device, *out});
+    return cudaSuccess;
+}
+
+cudaError_t launch_moe(MoeArgs a, int dtype, int vec, void *scratch, int device, int64_t sms,
+                       cudaStream_t stream)
 {
     Carver place(scratch);
     a.totals = place.take<MoeTotals>(1);
@@ -89,11 +134,12 @@ cudaError_t launch_moe(MoeArgs a, int dtype, int vec, void *scratch, int64_t sms
     if ((e = cudaGetLastError()) != cudaSuccess)
         return e;
     const MoeFn fn = pick_moe<false, kMoeThreads>(dtype, vec, a.E);
-    const int units = a.E / vec;
-    const int lanes = units <= 4 ? 4 : (units <= 16 ? 16 : 32);
+    const int lanes = moe_lanes(a.E / vec, vec);
     const int64_t rows = kMoeThreads / lanes * kMoeRowsPerGroup;  // of a CTA, at least
     const int64_t ctas = (a.T + rows - 1) / rows;
-    const int64_t most = sms * 8 < kMoeMaxCtas ? sms * 8 : kMoeMaxCtas;
+    int64_t most = 0;
+    if ((e = moe_resident(fn, device, sms, &most)) != cudaSuccess)
+        return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas < most ? ctas : most), 1, 1);
     cfg.blockDim = dim3(kMoeThreads, 1, 1);
@@ -158,5 +204,5 @@ extern "C" int moe_balance(const void *logits, int64_t logits_stride, const int6
     size.take<unsigned char>(T);
     if ((e = scratch.get(call.device, size.used)) != cudaSuccess)
         return map_error(e);
-    return map_error(scratch.release(launch_moe(a, dtype, vec, scratch.p, call.sms, call.stream)));
+    return map_error(scratch.release(launch_moe(a, dtype, vec, scratch.p, call.device, call.sms, call.stream)));
 }

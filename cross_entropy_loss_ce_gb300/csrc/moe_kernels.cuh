@@ -13,7 +13,7 @@
 // The counts need every token before the first gradient can be formed, but not
 // the logits: moe_count_kernel reads the choices (integer atomics, so the
 // order is free) and moe_rows_kernel then reads each row of logits once, into
-// registers, and writes its gradient once.  A row belongs to 4, 16 or 32 lanes;
+// registers, and writes its gradient once.  A row belongs to 4 to 32 lanes;
 // each lane keeps the counts of its experts in registers over all its rows and
 // has the next row's loads in flight while it works on one.  Row losses are
 // added in fp32 with their rounding errors carried (Neumaier) in an order fixed
@@ -182,6 +182,8 @@ __global__ void __launch_bounds__(NT) moe_rows_kernel(const MoeArgs a)
     using Unit = MoeUnit<T, VEC>;
     __shared__ unsigned hist[ALL ? kMoeMaxExperts : 1];
     __shared__ unsigned char small_mask[ALL ? kMoeSmallTokens : 1];
+    __shared__ float centred[kMoeMaxExperts];
+    __shared__ long long warp_sum64[NT / 32];
     __shared__ double warp_part[NT / 32];
     __shared__ int s_n, s_bad, s_last;
     const int lane = threadIdx.x & 31, sub = lane % LPT;
@@ -233,24 +235,32 @@ __global__ void __launch_bounds__(NT) moe_rows_kernel(const MoeArgs a)
         for (int e = threadIdx.x; e < a.E; e += NT)
             a.counts[e] = count_of(e);
 
-    // this lane's experts e = (j LPT + sub) VEC + v: their counts less the mean
-    // over all of them, (E f_e - sum) / E with the difference formed in integers
-    long long c[NJ * VEC], sum = 0;
+    // the counts less their mean, (E f_e - sum) / E with the difference formed in
+    // integers; then those of this lane's experts e = (j LPT + sub) VEC + v
+    long long sum = 0;
+    for (int e = threadIdx.x; e < a.E; e += NT)
+        sum += count_of(e);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+        sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    if (lane == 0)
+        warp_sum64[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    sum = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w)
+        sum += warp_sum64[w];
+    const float per_e = 1.f / static_cast<float>(a.E);
+    const float fmean = static_cast<float>(sum) * per_e;
+    for (int e = threadIdx.x; e < a.E; e += NT)
+        centred[e] = static_cast<float>(count_of(e) * a.E - sum) * per_e;
+    __syncthreads();
+    float f[NJ * VEC];
 #pragma unroll
     for (int i = 0; i < NJ * VEC; ++i) {
         const int e = (i / VEC * LPT + sub) * VEC + i % VEC;
-        c[i] = e < a.E ? count_of(e) : 0;
-        sum += c[i];
+        f[i] = e < a.E ? centred[e] : 0.f;
     }
-#pragma unroll
-    for (int off = LPT / 2; off > 0; off >>= 1)
-        sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    const float per_e = 1.f / static_cast<float>(a.E);
-    const float fmean = static_cast<float>(sum) * per_e;
-    float f[NJ * VEC];
-#pragma unroll
-    for (int i = 0; i < NJ * VEC; ++i)
-        f[i] = static_cast<float>(c[i] * a.E - sum) * per_e;
     const float per_n = 1.f / static_cast<float>(n);
     const float ka = a.balance * static_cast<float>(a.E) / static_cast<float>(a.k) * per_n;  // a E / (k n)
     const float gscale = a.grad ? (a.grad_scale ? __ldg(a.grad_scale) : 1.f) * per_n : 0.f;
