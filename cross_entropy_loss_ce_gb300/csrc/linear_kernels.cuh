@@ -32,9 +32,9 @@
 //
 // skinny_kernel is the forward for at most 64 rows, where reading W once is the
 // whole cost: W's rows take the M side of the instruction, so a tile is 128
-// vocabulary rows of any number of hidden states, and each CTA streams its own
-// contiguous share of W (in units of 16 rows, so that shares differ by 16 rows
-// at most) through a 200 KB ring.
+// vocabulary rows of any number of hidden states, and each CTA streams every
+// gridDim-th tile through a 200 KB ring.  The last, partial round of tiles runs
+// at the same bandwidth: the CTAs that have one hold enough loads in flight.
 //
 // Rows whose target is ignore_index take part in nothing: lin_prep_kernel lists
 // the others in order and lin_gather_kernel packs their hidden states (zeros up
@@ -653,7 +653,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 // at most 64 rows: W streamed once, its rows on the M side
 
 constexpr int kSkinnyStageW = 128 * 64 * 2;
-constexpr int kSkinnyUnit = 16;  // rows of W that the CTAs' shares are counted in
 
 template <int NG>
 __host__ __device__ constexpr int skinny_stage_bytes() { return kSkinnyStageW + NG * 32 * 128; }
@@ -665,7 +664,7 @@ template <int NG>
 __host__ __device__ constexpr int skinny_threads() { return 128 + NG * 128; }
 
 struct SkinnyArgs {
-    CUtensorMap w, wu;  // W in boxes of 128 and of 16 rows
+    CUtensorMap w;      // W in boxes of 128 rows
     CUtensorMap h;      // hidden states in boxes of 32 NG rows
     const int *n_ptr;
     int n_host;
@@ -714,7 +713,6 @@ __global__ void __launch_bounds__(skinny_threads<NG>(), 1) skinny_kernel(const _
         }
         fence_barrier_init();
         prefetch_map(&a.w);
-        prefetch_map(&a.wu);
         prefetch_map(&a.h);
     }
     if (warp == 2)
@@ -729,33 +727,22 @@ __global__ void __launch_bounds__(skinny_threads<NG>(), 1) skinny_kernel(const _
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
 
-    const int64_t units = (a.V + kSkinnyUnit - 1) / kSkinnyUnit;
-    const int64_t v0 = units * blockIdx.x / gridDim.x * kSkinnyUnit;
-    const int64_t v1 = min(units * (blockIdx.x + 1) / gridDim.x * kSkinnyUnit, a.V);
-    const int tiles = n > 0 ? static_cast<int>((v1 - v0 + 127) / 128) : 0;
+    const int all = n > 0 ? static_cast<int>((a.V + 127) / 128) : 0;
+    const int first = blockIdx.x, step = gridDim.x;
 
     if (warp == 0 && lane == 0) {
         const uint64_t once = policy_evict_first(), again = policy_evict_last();
         int slot = 0;
         uint32_t phase = 0;
         bool ok = true;
-        for (int t = 0; t < tiles && ok; ++t) {
-            const int64_t row = v0 + 128 * t;
-            const int rows = static_cast<int>(min(v1 - row, int64_t{128}));
-            const int nunit = (rows + kSkinnyUnit - 1) / kSkinnyUnit;
+        for (int t = first; t < all && ok; t += step) {
             for (int kb = 0; kb < a.kblocks; ++kb) {
                 if (!(ok = bar_wait<false>(empty + 8 * slot, phase ^ 1, dead)))
                     break;
                 const uint32_t sw = ring + slot * kStage, sh = sw + kSkinnyStageW;
                 const uint32_t bar = full + 8 * slot;
-                mbar_arrive_expect_tx(bar, nunit * kSkinnyUnit * 128 + kN * 128);
-                if (nunit == 8) {
-                    tma_load(sw, &a.w, kb * 64, static_cast<int>(row), bar, once);
-                } else {
-                    for (int u = 0; u < nunit; ++u)
-                        tma_load(sw + u * kSkinnyUnit * 128, &a.wu, kb * 64,
-                                 static_cast<int>(row) + u * kSkinnyUnit, bar, once);
-                }
+                mbar_arrive_expect_tx(bar, kStage);
+                tma_load(sw, &a.w, kb * 64, t * 128, bar, once);
                 tma_load(sh, &a.h, kb * 64, 0, bar, again);
                 if (++slot == kStages) {
                     slot = 0;
@@ -767,7 +754,7 @@ __global__ void __launch_bounds__(skinny_threads<NG>(), 1) skinny_kernel(const _
         int slot = 0, it = 0;
         uint32_t phase = 0;
         bool ok = true;
-        for (int t = 0; t < tiles && ok; ++t) {
+        for (int t = first; t < all && ok; t += step) {
             for (int kb0 = 0; ok && kb0 < a.kblocks; kb0 += kChunk, ++it) {
                 const int acc = it & 1;
                 if (!(ok = bar_wait<false>(tempty + 8 * acc, ((it >> 1) & 1) ^ 1, dead)))
@@ -808,7 +795,7 @@ __global__ void __launch_bounds__(skinny_threads<NG>(), 1) skinny_kernel(const _
         const int live = min(max(n - 32 * group, 0), 32);
         int it = 0;
         bool ok = true;
-        for (int t = 0; t < tiles && ok; ++t) {
+        for (int t = first; t < all && ok; t += step) {
             float sum[32];
             for (int kb0 = 0; kb0 < a.kblocks; kb0 += kChunk, ++it) {
                 const int acc = it & 1;
@@ -832,8 +819,8 @@ __global__ void __launch_bounds__(skinny_threads<NG>(), 1) skinny_kernel(const _
             }
             if (!ok)
                 break;
-            const int64_t v = v0 + 128 * t + ew * 32 + lane;
-            if (v < v1) {
+            const int64_t v = 128 * int64_t{t} + ew * 32 + lane;
+            if (v < a.V) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
                     if (j < live) {
@@ -862,7 +849,7 @@ __global__ void __launch_bounds__(skinny_threads<NG>(), 1) skinny_kernel(const _
         // each warp turns its 32 x 32 states around in the ring, which is idle once
         // the last accumulator is full: lane j merges the 32 lanes' states of hidden
         // state j
-        if (ok && tiles > 0) {
+        if (ok && first < all) {
             float *tm = reinterpret_cast<float *>(dyn + (ring - smem_addr(dyn))) + (warp - 4) * 3 * 32 * 33;
             float *td = tm + 32 * 33;
             int *ti = reinterpret_cast<int *>(td + 32 * 33);
