@@ -102,7 +102,7 @@ struct HeadShape {
     int64_t parts;      // partial pairs of a row
     int64_t vp;         // backward: vocabulary rows of a piece
     int64_t pieces;
-    int64_t slices;     // split tiles' sums, at most
+    int64_t slices;     // slices of split tiles, at most, of either gradient
 };
 
 enum class HeadOp { Fwd, Bwd, Greedy };
@@ -131,8 +131,8 @@ HeadScratch carve(Carver &c, const HeadShape &s, HeadOp op, bool want_hidden)
         r.g = c.take<unsigned short>(s.mp * s.vp);
         if (want_hidden && s.pieces > 1)
             r.acc = c.take<float>(s.mp * round_up(s.K, kPairN));
-        r.arrived = c.take<unsigned>(kSplitUnits / 2 * 16);
-        r.slices = c.take<float>(s.slices * kPairM * kPairN);
+        r.arrived = c.take<unsigned>(kSplitCounters);
+        r.slices = c.take<float>(2 * s.slices * kPairM * kPairN);
     } else {
         if (op == HeadOp::Fwd) {
             r.part = c.take<float2>(s.parts * s.mp);
@@ -186,18 +186,19 @@ cudaError_t launch_kernel(const Call &call, bool early, void (*fn)(Args...), int
 }
 
 template <Epi E>
-cudaError_t launch_pair(const Call &call, const PairArgs &a, int64_t max_tiles, bool early = true)
+cudaError_t launch_pair(const Call &call, const PairArgs &a, const PairArgs &w, int64_t max_tiles,
+                        bool early = true)
 {
-    using Fn = void (*)(const PairArgs);
+    using Fn = void (*)(const PairArgs, const PairArgs);
     const Fn fn = call.dtype == GBCE_BF16 ? static_cast<Fn>(pair_gemm_kernel<E, __nv_bfloat16>)
                                           : static_cast<Fn>(pair_gemm_kernel<E, __half>);
     const cudaError_t e = configure_smem(reinterpret_cast<const void *>(fn), call.device, kPairSmem);
     if (e != cudaSuccess)
         return e;
-    constexpr bool split = E == Epi::Weight || E == Epi::Hidden;  // uses every pair it can
     const int64_t most = call.sms / 2 < kSplitUnits / 4 ? call.sms / 2 : kSplitUnits / 4;
-    const int64_t pairs = split || max_tiles > most ? most : max_tiles;
-    return launch_kernel(call, early, fn, 2 * pairs, kPairThreads, kPairSmem, a);
+    // split tiles use every pair they can
+    const int64_t pairs = E == Epi::Both || max_tiles > most ? most : max_tiles;
+    return launch_kernel(call, early, fn, 2 * pairs, kPairThreads, kPairSmem, a, w);
 }
 
 template <int NG, bool GREEDY>
@@ -363,7 +364,7 @@ cudaError_t launch_head(const Call &call, const HeadShape &s, const HeadScratch 
         a.ldp = s.parts;
         a.tgt = r.tgt;
         a.V = s.V;
-        e = launch_pair<GREEDY ? Epi::Greedy : Epi::Stats>(call, a, s.mp / kPairM * a.tiles_n, early);
+        e = launch_pair<GREEDY ? Epi::Greedy : Epi::Stats>(call, a, a, s.mp / kPairM * a.tiles_n, early);
     }
     if (e != cudaSuccess)
         return e;
@@ -463,7 +464,10 @@ cudaError_t launch_linear_bwd(const Call &call, const HeadShape &s, const HeadSc
         a->lda = round_up(s.K, kPairN);
     }
     grad.kblocks = static_cast<int>((s.K + 63) / 64);
-    dw.tiles_n = dh.tiles_n = tiles_k;
+    dw.tiles_n = d_weight ? tiles_k : 0;  // none: no tiles
+    dh.tiles_n = d_hidden ? tiles_k : 0;
+    dw.slices = r.slices + s.slices * kPairM * kPairN;
+    dw.arrived = r.arrived + kSplitUnits / 2 * 16;
     dw.ldo = dws;
     dw.vec = aligned_to(d_weight, 16) && dws % 8 == 0;
     dh.out = d_hidden;
@@ -476,22 +480,18 @@ cudaError_t launch_linear_bwd(const Call &call, const HeadShape &s, const HeadSc
         grad.b_row0 = dh.b_row0 = static_cast<int>(v0);
         grad.V = vn;
         grad.tiles_n = tiles_v;
-        if ((e = launch_pair<Epi::Grad>(call, grad, s.mp / kPairM * tiles_v)) != cudaSuccess)
+        if ((e = launch_pair<Epi::Grad>(call, grad, grad, s.mp / kPairM * tiles_v)) != cudaSuccess)
             return e;
         if (d_weight) {
             dw.out = static_cast<unsigned short *>(d_weight) + v0 * dws;
             dw.rows = vn;
             dw.tiles_m = tiles_v;
-            if ((e = launch_pair<Epi::Weight>(call, dw, int64_t{tiles_v} * tiles_k)) != cudaSuccess)
-                return e;
         }
-        if (d_hidden) {
-            dh.kblocks = tiles_v * (kPairN / kPairK);  // G holds zeros up to whole tiles
-            dh.first = p == 0;
-            dh.last = p == s.pieces - 1;
-            if ((e = launch_pair<Epi::Hidden>(call, dh, s.mp / kPairM * tiles_k)) != cudaSuccess)
-                return e;
-        }
+        dh.kblocks = tiles_v * (kPairN / kPairK);  // G holds zeros up to whole tiles
+        dh.first = p == 0;
+        dh.last = p == s.pieces - 1;
+        if ((e = launch_pair<Epi::Both>(call, dh, dw, 0)) != cudaSuccess)
+            return e;
     }
     return cudaSuccess;
 }

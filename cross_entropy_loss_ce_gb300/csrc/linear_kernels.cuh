@@ -54,16 +54,16 @@ constexpr int kPairSmem = kPairStages * kPairStageBytes + 1024;
 constexpr int kChunk = 16;                              // k-steps of a logit summed in tensor memory
 constexpr int kBand = 8;                                // tiles of M that share a sweep over N
 
-enum class Epi { Stats, Greedy, Grad, Weight, Hidden };
+enum class Epi { Stats, Greedy, Grad, Both };  // Both: the two gradient products
 
 struct PairArgs {
     CUtensorMap a, b;
     const int *n_ptr;   // counted rows (device), NULL: n_host
     int n_host;
-    int tiles_m;        // Weight: tiles of the piece; else from n
+    int tiles_m;        // dW: tiles of the piece's classes; else from n
     int tiles_n;
-    int kblocks;        // 64-wide steps along K; Weight: from n
-    int b_row0;         // first row of B along the axis of W's rows (piece offset)
+    int kblocks;        // 64-wide steps along K; dW: from n
+    int b_row0;         // Grad, dH: the piece's first row of W
     unsigned *fail;
     // Stats, Greedy
     float2 *part;       // Stats: [row][ldp] (s, d) pairs, one for each 128 columns
@@ -75,17 +75,17 @@ struct PairArgs {
     const float *l2, *rs, *gy;  // lse log2e, factor and target's entry of each row
     void *g;
     int64_t ldg;
-    // Weight, Hidden
+    // dH and dW
     const float *alpha;
     void *out;
     int64_t ldo;
-    int64_t rows, cols; // valid rows (Weight) and columns of out
+    int64_t rows, cols; // valid rows (dW) and columns of out
     int vec;            // out allows 16-byte stores
-    const int *idx;     // Hidden: the row of out that a packed row belongs to
-    float *acc;         // Hidden: fp32 sums over pieces, [.., lda]
+    const int *idx;     // dH: the row of out that a packed row belongs to
+    float *acc;         // dH: fp32 sums over pieces, [.., lda]
     int64_t lda;
-    int first, last;    // Hidden: the first piece does not read acc, the last one writes out
-    float *slices;      // Weight, Hidden: kSplitUnits sums of kPairM x kPairN, for split tiles
+    int first, last;    // dH: the first piece does not read acc, the last one writes out
+    float *slices;      // kSplitUnits sums of kPairM x kPairN, for split tiles
     unsigned *arrived;  // ... and 16 counters a split tile, zero before and after
 };
 
@@ -101,6 +101,7 @@ struct Split {
 
 constexpr int kSplitUnits = 4 * 80;  // slices of a launch, at most
 constexpr int kSplitMax = 8;         // slices of a tile, at most
+constexpr int kSplitCounters = 2 * (kSplitUnits / 2) * 16;  // 16 for each split tile of dH and of dW
 
 // Costs in k-steps of one tile: a slice takes its steps and about 6 more to be
 // written, and 3 to be read again.  The tail is the last, partial wave, or that and
@@ -257,13 +258,13 @@ __device__ __forceinline__ void store_chunk(T *row, int64_t c0, int64_t cols, co
 // 32 finished sums of a gradient product: dW times alpha to its rows; dH added
 // to what earlier pieces left and kept for the next one, or times alpha to the
 // row it belongs to.
-template <Epi E, typename T>
+template <bool WEIGHT, typename T>
 __device__ __forceinline__ void finish_chunk(const PairArgs &a, float (&f)[32], int64_t row, int64_t out_row,
                                              int64_t col, bool live, float alpha)
 {
-    if (col >= a.cols || (E == Epi::Weight ? row >= a.rows : !live))
+    if (col >= a.cols || (WEIGHT ? row >= a.rows : !live))
         return;
-    if constexpr (E == Epi::Hidden) {
+    if constexpr (!WEIGHT) {
         float4 *acc4 = reinterpret_cast<float4 *>(a.acc + row * a.lda + col);
         if (!a.first) {
 #pragma unroll
@@ -291,7 +292,7 @@ __device__ __forceinline__ void finish_chunk(const PairArgs &a, float (&f)[32], 
 // The same for a split tile's part of 32 rows (from row0) and 128 columns (from
 // col0): its slices lie kPairM x kPairN apart.  A lane takes 4 columns of each
 // row, so that a warp reads and writes whole rows.
-template <Epi E, typename T>
+template <bool WEIGHT, typename T>
 __device__ __forceinline__ void finish_slices(const PairArgs &a, const float *part, int slices, int row0, int col0,
                                               int64_t rows, float alpha)
 {
@@ -323,7 +324,7 @@ __device__ __forceinline__ void finish_slices(const PairArgs &a, const float *pa
             if (row >= rows)
                 break;
             int64_t out_row = row;
-            if constexpr (E == Epi::Hidden) {
+            if constexpr (!WEIGHT) {
                 float4 *acc4 = reinterpret_cast<float4 *>(a.acc + row * a.lda + col);
                 if (!a.first) {
                     const float4 o = *acc4;
@@ -354,14 +355,15 @@ __device__ __forceinline__ void finish_slices(const PairArgs &a, const float *pa
 
 template <Epi E, typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
-    pair_gemm_kernel(const __grid_constant__ PairArgs a)
+    pair_gemm_kernel(const __grid_constant__ PairArgs a, const __grid_constant__ PairArgs w)
 {
-    constexpr bool A_MN = E == Epi::Weight;
-    constexpr bool B_MN = E == Epi::Weight || E == Epi::Hidden;
-    constexpr bool LOGITS = E == Epi::Stats || E == Epi::Greedy || E == Epi::Grad;
+    // Both: `a` is dH = G W (G K-major, W MN-major), then `w` is dW = G^T H (both
+    // MN-major); either may have no tiles.  Else `a` alone, both operands K-major.
+    constexpr bool BOTH = E == Epi::Both;
     constexpr bool CHUNKED = E == Epi::Stats || E == Epi::Greedy;
-    constexpr uint32_t kIdesc =
-        mma_idesc(std::is_same<T, __nv_bfloat16>::value, A_MN, B_MN, kPairM, kPairN);
+    constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    constexpr uint32_t kIdesc = mma_idesc(kBf16, false, BOTH, kPairM, kPairN);
+    constexpr uint32_t kIdescW = mma_idesc(kBf16, true, true, kPairM, kPairN);
 
     extern __shared__ unsigned char dyn[];
     __shared__ __align__(8) uint64_t bars[2 * kPairStages + 4];
@@ -388,6 +390,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         fence_barrier_init();
         prefetch_map(&a.a);
         prefetch_map(&a.b);
+        if (BOTH) {
+            prefetch_map(&w.a);
+            prefetch_map(&w.b);
+        }
     }
     if (warp == 2)
         tmem_alloc<2>(smem_addr(&tmem_slot), 512);
@@ -401,13 +407,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     wait_prerequisite_grid();
 
     const int n = a.n_ptr ? *a.n_ptr : a.n_host;
-    const int tiles_m = E == Epi::Weight ? a.tiles_m : (n + kPairM - 1) / kPairM;
-    const int kblocks = E == Epi::Weight ? (n + kPairK - 1) / kPairK : a.kblocks;
-    const int tiles = tiles_m * a.tiles_n;
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-    const Split sp = LOGITS ? Split{tiles, 0, 1} : split_of(tiles, pairs, kblocks);
-    const int units = sp.whole + sp.tail * sp.slices;
-    const int run = CHUNKED ? kChunk : max(kblocks, 1);  // k-steps that stay in tensor memory
+    const int tiles_m = (n + kPairM - 1) / kPairM;
+    const int steps_w = (n + kPairK - 1) / kPairK;  // dW's k-steps run over the rows
+    const Split sp = BOTH ? split_of(tiles_m * a.tiles_n, pairs, a.kblocks) : Split{tiles_m * a.tiles_n, 0, 1};
+    const Split spw = BOTH ? split_of(w.tiles_m * w.tiles_n, pairs, steps_w) : Split{0, 0, 1};
+    const int units = sp.whole + sp.tail * sp.slices, units_w = spw.whole + spw.tail * spw.slices;
+    // body(part of a tile, its row and column of tiles, is it dW's) until it is false;
+    // dW's parts go first to the pairs that the last round of dH's left out
+    const auto each_unit = [&](auto &&body) {
+        int tm, tn;
+        for (int u = pair; u < units; u += pairs) {
+            const Unit un = unit_at(u, sp, a.kblocks);
+            tile_at(un.tile, tiles_m, a.tiles_n, tm, tn);
+            if (!body(un, tm, tn, false))
+                return;
+        }
+        for (int u = (pair + pairs - units % pairs) % pairs; BOTH && u < units_w; u += pairs) {
+            const Unit un = unit_at(u, spw, steps_w);
+            tile_at(un.tile, w.tiles_m, w.tiles_n, tm, tn);
+            if (!body(un, tm, tn, true))
+                return;
+        }
+    };
 
     // 128 sums a thread want more than the launch's 168 registers: the first
     // four warps give some of theirs up (64 x 128 + 216 x 256 <= 168 x 384)
@@ -419,74 +441,72 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             const uint32_t full0 = map_to_rank(full, 0);
             int slot = 0;
             uint32_t phase = 0;
-            bool ok = true;
-            for (int u = pair; u < units && ok; u += pairs) {
-                const Unit un = unit_at(u, sp, kblocks);
-                int tm, tn;
-                tile_at(un.tile, tiles_m, a.tiles_n, tm, tn);
+            each_unit([&](const Unit &un, int tm, int tn, bool dw) {
+                const PairArgs &p = BOTH && dw ? w : a;
                 const int am = tm * kPairM + static_cast<int>(rank) * 128;
                 const int bn = tn * kPairN + static_cast<int>(rank) * 128;
                 for (int kb = un.k0; kb < un.k1; ++kb) {
-                    if (!(ok = bar_wait<true>(empty + 8 * slot, phase ^ 1, dead)))
-                        break;
+                    if (!bar_wait<true>(empty + 8 * slot, phase ^ 1, dead))
+                        return false;
                     if (rank == 0)
                         mbar_arrive_expect_tx(full + 8 * slot, 2 * kPairStageBytes);
                     const uint32_t sa = ring + slot * kPairStageBytes, sb = sa + kPairStageBytes / 2;
                     const uint32_t bar = full0 + 8 * slot;
                     const int k0 = kb * kPairK;
-                    if constexpr (A_MN) {
-                        tma_load_pair(sa, &a.a, am, k0, bar);
-                        tma_load_pair(sa + 8192, &a.a, am + 64, k0, bar);
+                    if (BOTH && dw) {
+                        tma_load_pair(sa, &p.a, am, k0, bar);
+                        tma_load_pair(sa + 8192, &p.a, am + 64, k0, bar);
                     } else {
-                        tma_load_pair(sa, &a.a, k0, am, bar);
+                        tma_load_pair(sa, &p.a, k0, am, bar);
                     }
-                    if constexpr (B_MN) {
-                        const int kr = E == Epi::Hidden ? a.b_row0 + k0 : k0;
-                        tma_load_pair(sb, &a.b, bn, kr, bar);
-                        tma_load_pair(sb + 8192, &a.b, bn + 64, kr, bar);
+                    if constexpr (BOTH) {
+                        tma_load_pair(sb, &p.b, bn, p.b_row0 + k0, bar);
+                        tma_load_pair(sb + 8192, &p.b, bn + 64, p.b_row0 + k0, bar);
                     } else {
-                        tma_load_pair(sb, &a.b, k0, a.b_row0 + bn, bar);
+                        tma_load_pair(sb, &p.b, k0, p.b_row0 + bn, bar);
                     }
                     if (++slot == kPairStages) {
                         slot = 0;
                         phase ^= 1;
                     }
                 }
-            }
+                return true;
+            });
         } else if (warp == 1 && lane == 0 && rank == 0) {
             // the pair's matrix instructions
             int slot = 0, it = 0;
             uint32_t phase = 0;
-            bool ok = true;
-            for (int u = pair; u < units && ok; u += pairs) {
-                const Unit un = unit_at(u, sp, kblocks);
-                for (int kb0 = un.k0; ok && (kb0 < un.k1 || kb0 == 0); kb0 += run, ++it) {
+            each_unit([&](const Unit &un, int, int, bool dw) {
+                const uint32_t idesc = BOTH && dw ? kIdescW : kIdesc;
+                const uint32_t lbo_a = BOTH && dw ? 8192 : 16, step_a = BOTH && dw ? 128 : 2;
+                const int run = CHUNKED ? kChunk : max(un.k1 - un.k0, 1);  // k-steps that stay in tensor memory
+                for (int kb0 = un.k0; kb0 < un.k1 || kb0 == 0; kb0 += run, ++it) {
                     const int acc = it & 1;
-                    if (!(ok = bar_wait<true>(tempty + 8 * acc, ((it >> 1) & 1) ^ 1, dead)))
-                        break;
+                    if (!bar_wait<true>(tempty + 8 * acc, ((it >> 1) & 1) ^ 1, dead))
+                        return false;
                     tc_fence_after();
                     const int kb1 = min(kb0 + run, un.k1);
                     for (int kb = kb0; kb < kb1; ++kb) {
-                        if (!(ok = bar_wait<true>(full + 8 * slot, phase, dead)))
-                            break;
+                        if (!bar_wait<true>(full + 8 * slot, phase, dead))
+                            return false;
                         tc_fence_after();
                         const uint32_t sa = ring + slot * kPairStageBytes, sb = sa + kPairStageBytes / 2;
-                        const uint64_t da = smem_desc(sa, A_MN ? 8192 : 16, 1024);
-                        const uint64_t db = smem_desc(sb, B_MN ? 8192 : 16, 1024);
-    #pragma unroll
+                        const uint64_t da = smem_desc(sa, lbo_a, 1024);
+                        const uint64_t db = smem_desc(sb, BOTH ? 8192 : 16, 1024);
+#pragma unroll
                         for (int k = 0; k < kPairK / 16; ++k)  // 16 of K: 32 bytes, or 16 rows of 128 bytes
-                            mma_f16<2>(tmem + acc * kPairN, da + k * (A_MN ? 128 : 2),
-                                       db + k * (B_MN ? 128 : 2), kIdesc, kb != kb0 || k != 0);
+                            mma_f16<2>(tmem + acc * kPairN, da + k * step_a, db + k * (BOTH ? 128 : 2), idesc,
+                                       kb != kb0 || k != 0);
                         mma_commit_pair(empty + 8 * slot);
                         if (++slot == kPairStages) {
                             slot = 0;
                             phase ^= 1;
                         }
                     }
-                    if (ok)
-                        mma_commit_pair(tfull + 8 * acc);
+                    mma_commit_pair(tfull + 8 * acc);
                 }
-            }
+                return true;
+            });
         }
     } else {
         if constexpr (CHUNKED)
@@ -495,25 +515,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const int ew = warp & 3, half = (warp - 4) >> 2;
         const uint32_t tempty0 = map_to_rank(tempty, 0);
         const int limit = static_cast<int>(min(a.V, static_cast<int64_t>(INT32_MAX)));
-        [[maybe_unused]] float alpha = 1.f;
-        if constexpr (!LOGITS)
-            alpha = *a.alpha;
+        [[maybe_unused]] const float alpha = BOTH ? *a.alpha : 1.f;
         int it = 0;
-        bool ok = true;
-        for (int u = pair; u < units && ok; u += pairs) {
-            const Unit un = unit_at(u, sp, kblocks);
-            int tm, tn;
-            tile_at(un.tile, tiles_m, a.tiles_n, tm, tn);
+        each_unit([&](const Unit &un, int tm, int tn, bool dw) {
+            const PairArgs &p = BOTH && dw ? w : a;
             const int row = tm * kPairM + static_cast<int>(rank) * 128 + ew * 32 + lane;
             const int c0 = tn * kPairN + half * 128;
             const bool live = row < n;
             const uint32_t lanes = tmem + half * 128 + (static_cast<uint32_t>(ew * 32) << 16);
             if constexpr (CHUNKED) {
                 float x[128];
-                for (int kb0 = 0; kb0 < kblocks; kb0 += run, ++it) {
+                for (int kb0 = 0; kb0 < un.k1; kb0 += kChunk, ++it) {
                     const int acc = it & 1;
-                    if (!(ok = bar_wait<true>(tfull + 8 * acc, (it >> 1) & 1, dead)))
-                        break;
+                    if (!bar_wait<true>(tfull + 8 * acc, (it >> 1) & 1, dead))
+                        return false;
                     tc_fence_after();
                     uint32_t buf[2][16];
                     tmem_ld16(lanes + acc * kPairN, buf[0]);
@@ -533,8 +548,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     if (lane == 0)
                         bar_arrive_cluster(tempty0 + 8 * acc);
                 }
-                if (!ok)
-                    break;
                 if constexpr (E == Epi::Stats) {  // the target's term is left out
                     const int y = live ? a.tgt[row] - c0 : -1;
                     if (y >= 0 && y < 128) {
@@ -558,8 +571,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 }
             } else {
                 const int acc = it & 1;
-                if (!(ok = bar_wait<true>(tfull + 8 * acc, (it >> 1) & 1, dead)))
-                    break;
+                if (!bar_wait<true>(tfull + 8 * acc, (it >> 1) & 1, dead))
+                    return false;
                 ++it;
                 tc_fence_after();
                 [[maybe_unused]] int64_t out_row = row;
@@ -573,9 +586,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         rs = a.rs[row];
                         gy = a.gy[row];
                     }
-                if constexpr (E == Epi::Hidden)
-                    if (live && a.last)
-                        out_row = a.idx[row];
+                if constexpr (BOTH)
+                    if (!dw && live && p.last)
+                        out_row = p.idx[row];
                 uint32_t buf[2][32];
                 tmem_ld32(lanes + acc * kPairN, buf[0]);
 #pragma unroll
@@ -595,7 +608,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         store_chunk<T>(static_cast<T *>(a.g) + row * a.ldg, col, a.ldg, f, 1);
                     } else if (un.slice >= 0) {
                         float4 *to = reinterpret_cast<float4 *>(
-                            a.slices + (int64_t{un.slice} * kPairM + (row - tm * kPairM)) * kPairN + col - tn * kPairN);
+                            p.slices + (int64_t{un.slice} * kPairM + (row - tm * kPairM)) * kPairN + col - tn * kPairN);
 #pragma unroll
                         for (int q = 0; q < 8; ++q)
                             to[q] = make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
@@ -603,37 +616,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     } else {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            f[i] = kblocks ? __uint_as_float(r[i]) : 0.f;
-                        finish_chunk<E, T>(a, f, row, out_row, col, live, alpha);
+                            f[i] = un.k1 ? __uint_as_float(r[i]) : 0.f;
+                        if (dw)
+                            finish_chunk<true, T>(p, f, row, row, col, live, alpha);
+                        else
+                            finish_chunk<false, T>(p, f, row, out_row, col, live, alpha);
                     }
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
                     bar_arrive_cluster(tempty0 + 8 * acc);
-                if constexpr (!LOGITS)
+                if constexpr (BOTH)
                     if (un.slice >= 0) {
                         // the last of this part's slices to arrive adds them all up
-                        const int t = un.tile - sp.whole;
-                        unsigned *count = a.arrived + t * 16 + rank * 8 + (warp - 4);
+                        const Split &split = dw ? spw : sp;
+                        const int t = un.tile - split.whole;
+                        unsigned *count = p.arrived + t * 16 + rank * 8 + (warp - 4);
                         unsigned before = 0;
                         __threadfence();
                         __syncwarp();
                         if (lane == 0)
                             before = atomicAdd(count, 1u);
                         before = __shfl_sync(0xffffffffu, before, 0);
-                        if (before == static_cast<unsigned>(sp.slices - 1)) {
+                        if (before == static_cast<unsigned>(split.slices - 1)) {
                             __threadfence();
                             if (lane == 0)
                                 *count = 0u;  // for the next launch
-                            const int r0 = tm * kPairM + static_cast<int>(rank) * 128 + ew * 32;
-                            finish_slices<E, T>(a, a.slices + int64_t{t} * sp.slices * kPairM * kPairN +
-                                                       (r0 - tm * kPairM) * kPairN + half * 128,
-                                                sp.slices, r0, c0, E == Epi::Weight ? a.rows : n, alpha);
+                            const int r0 = static_cast<int>(rank) * 128 + ew * 32;
+                            const float *part = p.slices + int64_t{t} * split.slices * kPairM * kPairN +
+                                                r0 * kPairN + half * 128;
+                            if (dw)
+                                finish_slices<true, T>(p, part, split.slices, tm * kPairM + r0, c0, p.rows, alpha);
+                            else
+                                finish_slices<false, T>(p, part, split.slices, tm * kPairM + r0, c0, n, alpha);
                         }
                     }
             }
-        }
+            return true;
+        });
     }
     __syncwarp();
     tc_fence_before();
@@ -1016,7 +1037,7 @@ __device__ __forceinline__ Listed prep_rows(const PrepArgs &a, bool write, int *
             *a.alpha = (a.reduction == kReduceMean ? 1.f / static_cast<float>(max(n_all, 1)) : 1.f) *
                        ldexpf(1.f / a.head, e);
         if (write)
-            for (int i = threadIdx.x; i < kSplitUnits / 2 * 16; i += NT)
+            for (int i = threadIdx.x; i < kSplitCounters; i += NT)
                 a.arrived[i] = 0u;
     }
     if (write && threadIdx.x == 0) {
