@@ -517,7 +517,7 @@ def _rows(t: torch.Tensor, name: str):
         (rows, cols), (step, unit) = t.shape, t.stride()
         if unit == 1 and step >= cols:
             return t.data_ptr(), step, rows, cols
-        if rows > 1 and step < cols:
+        if rows > 1 and step < cols and (unit == 1 or cols == 1):
             raise ValueError(f"{name} has overlapping rows (stride {step} for {cols} columns)")
     return _matrix(t, name)
 
@@ -544,6 +544,18 @@ def _row_values(t, M, name):
     if t.dtype != torch.float32 or t.shape != (M,) or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous float32 of shape [M]")
     return t
+
+
+def _apart(name, out, *inputs):
+    """Raises ValueError when the matrix ``out`` shares memory with an input."""
+    def span(t):
+        last = sum((n - 1) * s for n, s in zip(t.shape, t.stride())) if t.numel() else -1
+        return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+    lo, hi = span(out)
+    for other, t in inputs:
+        a, b = span(t)
+        if lo < b and a < hi:
+            raise ValueError(f"{name} shares memory with {other}")
 
 
 def _ptr(t):
@@ -611,8 +623,12 @@ def linear_ce_bwd(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Ten
             out = torch.empty(like.shape, dtype=like.dtype, device=dev)
         elif out.shape != like.shape or out.dtype != like.dtype:
             raise ValueError(f"{name} must have the shape and dtype of {name[2:]}")
+        else:
+            _apart(name, out, ("hidden", hidden), ("weight", weight))
         outs.append(out)
     d_hidden, d_weight = outs
+    if d_hidden is not None and d_weight is not None:
+        _apart("d_hidden", d_hidden, ("d_weight", d_weight))
     gs = None
     if grad_scale is not None:
         gs = _device_floats(grad_scale, M if reduction == "none" else 1, dev, "grad_scale")
@@ -686,7 +702,9 @@ class FusedLinearCrossEntropy(torch.autograd.Function):
 def linear_cross_entropy(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor,
                          ignore_index: int = -100, reduction: str = "mean") -> torch.Tensor:
     """Hard-label cross-entropy of the logits hidden @ weight.T, differentiable in
-    both, without forming the logits.  ``hidden`` is [..., K] and ``targets`` [...]
+    both, without forming the logits.  (Captured into a CUDA graph with its
+    backward: torch refuses while an eager graph of the same leaves, built on
+    another stream, is alive; linear_ce_fwd and linear_ce_bwd know no leaves.)  ``hidden`` is [..., K] and ``targets`` [...]
     (the same leading shape); 'none' returns row losses of the targets' shape."""
     if hidden.shape[:-1] != targets.shape:
         raise ValueError(f"hidden has rows {tuple(hidden.shape[:-1])}, targets {tuple(targets.shape)}")

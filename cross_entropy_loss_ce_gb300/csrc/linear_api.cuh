@@ -186,9 +186,10 @@ cudaError_t launch_kernel(const Call &call, bool early, void (*fn)(Args...), int
 }
 
 template <Epi E>
-cudaError_t launch_pair(const Call &call, const PairArgs &a, const PairArgs &w, int64_t max_tiles,
+cudaError_t launch_pair(const Call &call, PairArgs a, const PairArgs &w, int64_t max_tiles,
                         bool early = true)
 {
+    a.drop_copy = g_drop_copy.load(std::memory_order_relaxed);
     using Fn = void (*)(const PairArgs, const PairArgs);
     const Fn fn = call.dtype == GBCE_BF16 ? static_cast<Fn>(pair_gemm_kernel<E, __nv_bfloat16>)
                                           : static_cast<Fn>(pair_gemm_kernel<E, __half>);
@@ -202,8 +203,9 @@ cudaError_t launch_pair(const Call &call, const PairArgs &a, const PairArgs &w, 
 }
 
 template <int NG, bool GREEDY>
-cudaError_t launch_skinny_ng(const Call &call, const SkinnyArgs &a, int64_t ctas, bool early)
+cudaError_t launch_skinny_ng(const Call &call, SkinnyArgs a, int64_t ctas, bool early)
 {
+    a.drop_copy = g_drop_copy.load(std::memory_order_relaxed);
     const auto fn = skinny_kernel<NG, GREEDY>;
     const cudaError_t e =
         configure_smem(reinterpret_cast<const void *>(fn), call.device, skinny_smem<NG>());
@@ -373,6 +375,7 @@ cudaError_t launch_head(const Call &call, const HeadShape &s, const HeadScratch 
     m.w = w;
     m.ws = wstride;
     m.K = s.K;
+    m.V = s.V;
     m.vec = mappable(h, hstride, hrows) && mappable(w, wstride, s.V);
     if constexpr (!GREEDY)
         return launch_kernel(call, true, lin_merge_kernel<256>, (s.M + 7) / 8, 256, 0, m);
@@ -505,8 +508,12 @@ struct PoolScratch {
     cudaError_t get(int device, size_t bytes)
     {
         cudaMemPool_t pool;
-        const cudaError_t e = pool_for(device, &pool);
-        return e != cudaSuccess ? e : cudaMallocFromPoolAsync(&p, bytes, pool, stream);
+        cudaError_t e = pool_for(device, &pool);
+        if (e == cudaSuccess && (e = cudaMallocFromPoolAsync(&p, bytes, pool, stream)) != cudaSuccess) {
+            p = nullptr;
+            cudaGetLastError();  // reported here: a later launch must not find it
+        }
+        return e;
     }
     cudaError_t release(cudaError_t e)
     {

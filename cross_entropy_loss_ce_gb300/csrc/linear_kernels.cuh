@@ -65,6 +65,7 @@ struct PairArgs {
     int kblocks;        // 64-wide steps along K; dW: from n
     int b_row0;         // Grad, dH: the piece's first row of W
     unsigned *fail;
+    int drop_copy;      // failure-path tests: the k-step whose A block CTA 0 leaves out, else -1
     // Stats, Greedy
     float2 *part;       // Stats: [row][ldp] (s, d) pairs, one for each 128 columns
     float4 *best;       // Greedy: [row][ldp] (maximum, others' sum, arg max)
@@ -308,7 +309,7 @@ __device__ __forceinline__ void finish_slices(const PairArgs &a, const float *pa
         for (int r = 0; r < R; ++r)
             f[r] = make_float4(0.f, 0.f, 0.f, 0.f);
         const float *from = part + r0 * kPairN + 4 * lane;  // written to the tile's end, whatever `rows`
-#pragma unroll 2
+#pragma unroll 4
         for (int s = 0; s < slices; ++s, from += kPairM * kPairN)
 #pragma unroll
             for (int r = 0; r < R; ++r) {
@@ -439,7 +440,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         if (warp == 0 && lane == 0) {
             // producer: this CTA's halves of A and B
             const uint32_t full0 = map_to_rank(full, 0);
-            int slot = 0;
+            int slot = 0, steps = 0;
             uint32_t phase = 0;
             each_unit([&](const Unit &un, int tm, int tn, bool dw) {
                 const PairArgs &p = BOTH && dw ? w : a;
@@ -453,7 +454,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     const uint32_t sa = ring + slot * kPairStageBytes, sb = sa + kPairStageBytes / 2;
                     const uint32_t bar = full0 + 8 * slot;
                     const int k0 = kb * kPairK;
-                    if (BOTH && dw) {
+                    if (blockIdx.x == 0 && steps++ == a.drop_copy) {
+                        // nothing arrives for A: the waits for this slot run out
+                    } else if (BOTH && dw) {
                         tma_load_pair(sa, &p.a, am, k0, bar);
                         tma_load_pair(sa + 8192, &p.a, am + 64, k0, bar);
                     } else {
@@ -696,6 +699,7 @@ struct SkinnyArgs {
     float4 *best;
     int64_t ldp;
     unsigned *fail;
+    int drop_copy;      // as in PairArgs, of W
     uint32_t bf16;
 };
 
@@ -753,7 +757,7 @@ __global__ void __launch_bounds__(skinny_threads<NG>(), 1) skinny_kernel(const _
 
     if (warp == 0 && lane == 0) {
         const uint64_t once = policy_evict_first(), again = policy_evict_last();
-        int slot = 0;
+        int slot = 0, steps = 0;
         uint32_t phase = 0;
         bool ok = true;
         for (int t = first; t < all && ok; t += step) {
@@ -763,7 +767,8 @@ __global__ void __launch_bounds__(skinny_threads<NG>(), 1) skinny_kernel(const _
                 const uint32_t sw = ring + slot * kStage, sh = sw + kSkinnyStageW;
                 const uint32_t bar = full + 8 * slot;
                 mbar_arrive_expect_tx(bar, kStage);
-                tma_load(sw, &a.w, kb * 64, t * 128, bar, once);
+                if (blockIdx.x != 0 || steps++ != a.drop_copy)
+                    tma_load(sw, &a.w, kb * 64, t * 128, bar, once);
                 tma_load(sh, &a.h, kb * 64, 0, bar, again);
                 if (++slot == kStages) {
                     slot = 0;
@@ -1261,7 +1266,7 @@ struct MergeArgs {
     int64_t *token;
     float *logprob;
     const void *h, *w;
-    int64_t hs, ws, K;
+    int64_t hs, ws, K, V;
     int vec;
 };
 
@@ -1382,8 +1387,11 @@ __global__ void __launch_bounds__(NT) lin_token_kernel(const MergeArgs a)
 #pragma unroll
     for (int w = 1; w < NT / 32; ++w)
         best_merge(m, d, best, sm[w], sd[w], si[w]);
-    float lse, lp = __int_as_float(0x7fc00000);  // nothing but NaN or -inf
-    if (best != INT32_MAX) {
+    // no index: nothing but NaN or -inf, or partials that a kernel which gave up
+    // on a copy left unwritten (any bits: the index is checked before it is used)
+    float lse, lp = __int_as_float(0x7fc00000);
+    const bool found = best >= 0 && best < a.V;
+    if (found) {
         const float x = row_dot<T, NT>(static_cast<const T *>(a.h) + row * a.hs,
                                        static_cast<const T *>(a.w) + best * a.ws, a.K, a.vec);
         __syncthreads();
@@ -1397,7 +1405,7 @@ __global__ void __launch_bounds__(NT) lin_token_kernel(const MergeArgs a)
         lp = -loss_beside(shift_of(m), d, sum, lse);
     }
     if (threadIdx.x == 0) {
-        a.token[row] = best == INT32_MAX ? 0 : best;
+        a.token[row] = found ? best : 0;
         a.logprob[row] = lp;
     }
 }

@@ -428,9 +428,9 @@ GBCE_API int gbce_pool_reserved(int device, uint64_t *bytes);
  * ignore_index raises GBCE_ERR_BAD_TARGET: its row loss and lse are NaN.
  * NaN or infinite logits make their row's loss NaN.
  *
- * Scratch comes from the library's pool on `stream` (gbce_pool_reserved): the
- * counted rows' hidden states, 8 bytes per row and 256 classes, and a copy of
- * the weights where their rows do not start on 16-byte boundaries.
+ * Scratch comes from the library's pool on `stream` (gbce_pool_reserved) and stays in
+ * the pool: the counted rows' hidden states, 8 bytes per row and 128 classes,
+ * and a copy of the weights where their rows do not start on 16-byte boundaries.
  */
 GBCE_API int linear_ce_fwd(const void *hidden, int64_t hidden_stride, const void *weight,
                            int64_t weight_stride, const int64_t *targets, float *loss,
@@ -455,8 +455,9 @@ GBCE_API int linear_ce_fwd(const void *hidden, int64_t hidden_stride, const void
  * factors relative to a power of two at or above the largest, so fp16 keeps
  * small ones); both products are summed in fp32 and rounded once.  Both
  * gradients are written, not added to.  Scratch: the counted rows' hidden states, up to
- * 512 MB of G (more only when M exceeds 2^20 rows), and M x K floats when the
- * vocabulary takes several pieces.
+ * 512 MB of G (more only when M exceeds 2^20 rows), M x K floats when the
+ * vocabulary takes several pieces, up to 168 MB of partial sums, and the
+ * weights' copy as in the forward.
  */
 GBCE_API int linear_ce_bwd(const void *hidden, int64_t hidden_stride, const void *weight,
                            int64_t weight_stride, const int64_t *targets, const float *lse,
@@ -473,7 +474,8 @@ GBCE_API int linear_ce_bwd(const void *hidden, int64_t hidden_stride, const void
  *   logprob       [M] floats: x[r, tokens_r] - lse_r.
  *
  * NaN logits are passed over for the index (0 when a row holds nothing else)
- * and make the row's logprob NaN.
+ * and make the row's logprob NaN.  Scratch: 16 bytes per row and 128 classes,
+ * and copies of operands whose rows do not start on 16-byte boundaries.
  */
 GBCE_API int linear_greedy(const void *hidden, int64_t hidden_stride, const void *weight,
                            int64_t weight_stride, int64_t *tokens, float *logprob, int64_t M,
