@@ -53,36 +53,41 @@ struct MoeArgs {
     float balance, z;
 };
 
-// Does token t count, i.e. has it a slot in [0, E) and none beyond?  -1: a bad slot.
-__device__ __forceinline__ int moe_token(const MoeArgs &a, int64_t t)
-{
-    const int64_t *ids = a.experts + t * a.es;
-    int any = 0;
-    for (int j = 0; j < a.k; ++j) {
-        const int64_t e = __ldg(ids + j);
-        if (e < -1 || e >= a.E)
-            return -1;
-        any |= e >= 0;
-    }
-    return any;
-}
-
-// Adds the choices of tokens first, first + step, ... to hist; returns how many count.
+// Adds the choices of tokens first, first + step, ... to hist; returns how many
+// count, i.e. have a slot in [0, E) and none beyond.  Up to 8 slots are loaded at
+// once and kept; further ones are read again to be counted.
 __device__ __forceinline__ int moe_count_tokens(const MoeArgs &a, int64_t first, int64_t step,
                                                 unsigned *hist, unsigned char *mask, bool &bad)
 {
     int n = 0;
     for (int64_t t = first; t < a.T; t += step) {
-        const int c = moe_token(a, t);
-        mask[t] = c > 0;
-        bad |= c < 0;
-        if (c > 0) {
-            ++n;
-            for (int j = 0; j < a.k; ++j) {
-                const int64_t e = __ldg(a.experts + t * a.es + j);
-                if (e >= 0)
-                    atomicAdd(hist + e, 1u);
+        const int64_t *ids = a.experts + t * a.es;
+        int64_t e[8];
+        bool any = false, wrong = false;
+        const auto look = [&](int j0) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                e[j] = j0 + j < a.k ? __ldg(ids + j0 + j) : -1;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                any |= e[j] >= 0;
+                wrong |= e[j] < -1 || e[j] >= a.E;
             }
+        };
+        for (int j0 = 8; j0 < a.k; j0 += 8)
+            look(j0);
+        look(0);
+        const bool counted = any && !wrong;
+        mask[t] = counted;
+        bad |= wrong;
+        n += counted;
+        for (int j0 = 0; counted && j0 < a.k; j0 += 8) {
+            if (j0)
+                look(j0);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (e[j] >= 0)
+                    atomicAdd(hist + e[j], 1u);
         }
     }
     return n;
