@@ -256,18 +256,25 @@ __device__ __forceinline__ void store_chunk(T *row, int64_t c0, int64_t cols, co
     }
 }
 
-// 32 finished sums of a gradient product: dW times alpha to its rows; dH added
-// to what earlier pieces left and kept for the next one, or times alpha to the
-// row it belongs to.
+// 32 columns (from col) of a warp's 32 finished rows (from row0, a thread each) of
+// a gradient product: dW times alpha to its rows; dH added to what earlier pieces
+// left and kept for the next one, or times alpha to the rows they belong to.  Rows
+// that allow no 16-byte stores are turned around in `turn`, the warp's own, so that
+// its lanes write neighbouring columns of one row.
+constexpr int kTurnStride = 34;
+
 template <bool WEIGHT, typename T>
-__device__ __forceinline__ void finish_chunk(const PairArgs &a, float (&f)[32], int64_t row, int64_t out_row,
-                                             int64_t col, bool live, float alpha)
+__device__ __forceinline__ void finish_chunk(const PairArgs &a, float (&f)[32], int64_t row0, int64_t col,
+                                             int64_t rows, float alpha, T *turn)
 {
-    if (col >= a.cols || (WEIGHT ? row >= a.rows : !live))
+    const int lane = threadIdx.x & 31;
+    const int64_t row = row0 + lane;
+    if (col >= a.cols || row0 >= rows)
         return;
+    const bool live = row < rows;
     if constexpr (!WEIGHT) {
         float4 *acc4 = reinterpret_cast<float4 *>(a.acc + row * a.lda + col);
-        if (!a.first) {
+        if (!a.first && live) {
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
                 const float4 o = acc4[q];
@@ -278,16 +285,35 @@ __device__ __forceinline__ void finish_chunk(const PairArgs &a, float (&f)[32], 
             }
         }
         if (!a.last) {
+            if (live) {
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-                acc4[q] = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
+                for (int q = 0; q < 8; ++q)
+                    acc4[q] = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
+            }
             return;
         }
     }
 #pragma unroll
     for (int i = 0; i < 32; ++i)
         f[i] *= alpha;
-    store_chunk<T>(static_cast<T *>(a.out) + out_row * a.ldo, col, a.cols, f, a.vec);
+    T *out = static_cast<T *>(a.out);
+    if (a.vec) {
+        if (live)
+            store_chunk<T>(out + (WEIGHT ? row : int64_t{a.idx[row]}) * a.ldo, col, a.cols, f, 1);
+        return;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 32; i += 2)
+        *reinterpret_cast<uint32_t *>(turn + lane * kTurnStride + i) = Elem<T>::pack2(f[i], f[i + 1]);
+    __syncwarp();
+    const int64_t c = col + lane;
+    if (c < a.cols) {
+#pragma unroll 8
+        for (int r = 0; r < 32; ++r)
+            if (row0 + r < rows)
+                out[(WEIGHT ? row0 + r : int64_t{a.idx[row0 + r]}) * a.ldo + c] = turn[r * kTurnStride + lane];
+    }
 }
 
 // The same for a split tile's part of 32 rows (from row0) and 128 columns (from
@@ -370,6 +396,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     __shared__ __align__(8) uint64_t bars[2 * kPairStages + 4];
     __shared__ uint32_t tmem_slot;
     __shared__ int dead_word;
+    __shared__ T turn[BOTH ? 8 : 1][BOTH ? 32 * kTurnStride : 1];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
@@ -578,7 +605,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     return false;
                 ++it;
                 tc_fence_after();
-                [[maybe_unused]] int64_t out_row = row;
                 [[maybe_unused]] int y = -1, inside = 0;  // columns with a gradient: none of an unlisted row
                 [[maybe_unused]] float l2 = 0.f, rs = 0.f, gy = 0.f;
                 if constexpr (E == Epi::Grad)
@@ -589,9 +615,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         rs = a.rs[row];
                         gy = a.gy[row];
                     }
-                if constexpr (BOTH)
-                    if (!dw && live && p.last)
-                        out_row = p.idx[row];
                 uint32_t buf[2][32];
                 tmem_ld32(lanes + acc * kPairN, buf[0]);
 #pragma unroll
@@ -621,9 +644,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         for (int i = 0; i < 32; ++i)
                             f[i] = un.k1 ? __uint_as_float(r[i]) : 0.f;
                         if (dw)
-                            finish_chunk<true, T>(p, f, row, row, col, live, alpha);
+                            finish_chunk<true, T>(p, f, row - lane, col, p.rows, alpha, turn[warp - 4]);
                         else
-                            finish_chunk<false, T>(p, f, row, out_row, col, live, alpha);
+                            finish_chunk<false, T>(p, f, row - lane, col, n, alpha, turn[warp - 4]);
                     }
                 }
                 tc_fence_before();
@@ -1162,8 +1185,14 @@ __device__ __forceinline__ void gather_rows(const GatherArgs &a, int64_t n, int6
             for (int64_t j = lane; j < a.K / 8; j += 32)
                 reinterpret_cast<uint4 *>(d)[j] = __ldg(reinterpret_cast<const uint4 *>(s) + j);
         }
-        for (int64_t j = done + lane; j < a.lds; j += 32)
-            d[j] = j < a.K ? s[j] : zero_value;
+#pragma unroll 2
+        for (int64_t j = done / 8 + lane; j < a.lds / 8; j += 32) {
+            alignas(16) T v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = 8 * j + i < a.K ? s[8 * j + i] : zero_value;
+            reinterpret_cast<uint4 *>(d)[j] = *reinterpret_cast<const uint4 *>(v);
+        }
         if (a.w) {
             const float x = row_dot<T, 32>(s, static_cast<const T *>(a.w) + target_of(i) * a.ws, a.K, a.wvec);
             if (lane == 0) {
