@@ -464,7 +464,6 @@ cudaError_t launch_linear_bwd(const Call &call, const HeadShape &s, const HeadSc
         a->acc = r.acc;
         a->slices = r.slices;
         a->arrived = r.arrived;
-        a->lda = round_up(s.K, kPairN);
     }
     grad.kblocks = static_cast<int>((s.K + 63) / 64);
     dw.tiles_n = d_weight ? tiles_k : 0;  // none: no tiles

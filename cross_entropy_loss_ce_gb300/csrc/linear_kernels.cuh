@@ -83,8 +83,7 @@ struct PairArgs {
     int64_t rows, cols; // valid rows (dW) and columns of out
     int vec;            // out allows 16-byte stores
     const int *idx;     // dH: the row of out that a packed row belongs to
-    float *acc;         // dH: fp32 sums over pieces, [.., lda]
-    int64_t lda;
+    float *acc;         // dH: fp32 sums over pieces
     int first, last;    // dH: the first piece does not read acc, the last one writes out
     float *slices;      // kSplitUnits sums of kPairM x kPairN, for split tiles
     unsigned *arrived;  // ... and 16 counters a split tile, zero before and after
@@ -236,148 +235,102 @@ __device__ __forceinline__ void stats_chunk(float (&x)[N], int c0, int limit, fl
     d += d0 + d1;
 }
 
-// N values, rounded once, to row[c0 ..] below `cols`.
-template <typename T, int N>
-__device__ __forceinline__ void store_chunk(T *row, int64_t c0, int64_t cols, const float (&f)[N], int vec)
+// A warp's 32 x 32 block of finished values, a thread one row, rounded once and
+// written to rows of `out` (row_of(r): where row r of the block goes, for r <
+// rows; columns col .. below cols).  A thread's own row would make each store of
+// a warp touch 32 lines (one row of 128256 x 2048, whose gradient is all stores:
+// 250 us for the weights' gradient, 14 GB/s from each SM); turned around in
+// `turn`, the warp's own, 4 lanes write 64 bytes of a row, or 32 lanes one row
+// where it allows no 16-byte stores.
+constexpr int kTurnStride = 40;  // 80 bytes: 16-byte accesses of 8 rows meet in no bank
+
+template <typename T, typename RowOf>
+__device__ __forceinline__ void store_block(T *out, int64_t ldo, int64_t col, int64_t cols, int rows,
+                                            const float (&f)[32], bool vec, T *turn, RowOf row_of)
 {
-    if (vec && c0 + N <= cols) {
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
 #pragma unroll
-        for (int q = 0; q < N / 8; ++q) {
-            const float *p = f + 8 * q;
-            *reinterpret_cast<uint4 *>(row + c0 + 8 * q) =
-                make_uint4(Elem<T>::pack2(p[0], p[1]), Elem<T>::pack2(p[2], p[3]),
-                           Elem<T>::pack2(p[4], p[5]), Elem<T>::pack2(p[6], p[7]));
+    for (int q = 0; q < 4; ++q) {
+        const float *p = f + 8 * q;
+        *reinterpret_cast<uint4 *>(turn + lane * kTurnStride + 8 * q) =
+            make_uint4(Elem<T>::pack2(p[0], p[1]), Elem<T>::pack2(p[2], p[3]),
+                       Elem<T>::pack2(p[4], p[5]), Elem<T>::pack2(p[6], p[7]));
+    }
+    __syncwarp();
+    if (vec) {
+        const int64_t c = col + 8 * (lane & 3);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 8 * i + (lane >> 2);
+            if (r >= rows || c >= cols)
+                continue;
+            const T *from = turn + r * kTurnStride + 8 * (lane & 3);
+            T *to = out + row_of(r) * ldo + c;
+            if (c + 8 <= cols) {
+                *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(from);
+            } else {
+                for (int e = 0; c + e < cols; ++e)
+                    to[e] = from[e];
+            }
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (c0 + i < cols)
-                Elem<T>::store(row + c0 + i, f[i]);
+    } else if (col + lane < cols) {
+#pragma unroll 8
+        for (int r = 0; r < 32; ++r)
+            if (r < rows)
+                out[row_of(r) * ldo + col + lane] = turn[r * kTurnStride + lane];
     }
 }
 
-// 32 columns (from col) of a warp's 32 finished rows (from row0, a thread each) of
-// a gradient product: dW times alpha to its rows; dH added to what earlier pieces
-// left and kept for the next one, or times alpha to the rows they belong to.  Rows
-// that allow no 16-byte stores are turned around in `turn`, the warp's own, so that
-// its lanes write neighbouring columns of one row.
-constexpr int kTurnStride = 34;
-
-template <bool WEIGHT, typename T>
-__device__ __forceinline__ void finish_chunk(const PairArgs &a, float (&f)[32], int64_t row0, int64_t col,
-                                             int64_t rows, float alpha, T *turn)
+// Sums that a kernel keeps for itself lie as the threads hold them: 16 parts of a
+// tile (a warp of a CTA each), 4 blocks of 32 x 32 a part, 16 bytes of each of
+// the 32 lanes together.
+__device__ __forceinline__ float4 *block_at(float *base, int64_t tile, int part, int c)
 {
-    const int lane = threadIdx.x & 31;
-    const int64_t row = row0 + lane;
+    return reinterpret_cast<float4 *>(base + ((tile * 16 + part) * 4 + c) * 1024) + (threadIdx.x & 31);
+}
+
+__device__ __forceinline__ void add_block(float (&f)[32], const float4 *from)
+{
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        const float4 v = __ldcg(from + 32 * q);
+        f[4 * q] += v.x;
+        f[4 * q + 1] += v.y;
+        f[4 * q + 2] += v.z;
+        f[4 * q + 3] += v.w;
+    }
+}
+
+__device__ __forceinline__ void put_block(float4 *to, const float (&f)[32])
+{
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+        to[32 * q] = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
+}
+
+// A block of a gradient product whose sums over K are complete: dW times alpha to
+// its rows; dH added to what earlier pieces left and kept for the next one, or
+// times alpha to the rows they belong to.
+template <bool WEIGHT, typename T>
+__device__ __forceinline__ void finish_block(const PairArgs &a, float (&f)[32], int tile, int part, int c,
+                                             int64_t row0, int64_t col, int64_t rows, float alpha, T *turn)
+{
     if (col >= a.cols || row0 >= rows)
         return;
-    const bool live = row < rows;
     if constexpr (!WEIGHT) {
-        float4 *acc4 = reinterpret_cast<float4 *>(a.acc + row * a.lda + col);
-        if (!a.first && live) {
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const float4 o = acc4[q];
-                f[4 * q] += o.x;
-                f[4 * q + 1] += o.y;
-                f[4 * q + 2] += o.z;
-                f[4 * q + 3] += o.w;
-            }
-        }
+        if (!a.first)
+            add_block(f, block_at(a.acc, tile, part, c));
         if (!a.last) {
-            if (live) {
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    acc4[q] = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
-            }
+            put_block(block_at(a.acc, tile, part, c), f);
             return;
         }
     }
 #pragma unroll
     for (int i = 0; i < 32; ++i)
         f[i] *= alpha;
-    T *out = static_cast<T *>(a.out);
-    if (a.vec) {
-        if (live)
-            store_chunk<T>(out + (WEIGHT ? row : int64_t{a.idx[row]}) * a.ldo, col, a.cols, f, 1);
-        return;
-    }
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 32; i += 2)
-        *reinterpret_cast<uint32_t *>(turn + lane * kTurnStride + i) = Elem<T>::pack2(f[i], f[i + 1]);
-    __syncwarp();
-    const int64_t c = col + lane;
-    if (c < a.cols) {
-#pragma unroll 8
-        for (int r = 0; r < 32; ++r)
-            if (row0 + r < rows)
-                out[(WEIGHT ? row0 + r : int64_t{a.idx[row0 + r]}) * a.ldo + c] = turn[r * kTurnStride + lane];
-    }
-}
-
-// The same for a split tile's part of 32 rows (from row0) and 128 columns (from
-// col0): its slices lie kPairM x kPairN apart.  A lane takes 4 columns of each
-// row, so that a warp reads and writes whole rows.
-template <bool WEIGHT, typename T>
-__device__ __forceinline__ void finish_slices(const PairArgs &a, const float *part, int slices, int row0, int col0,
-                                              int64_t rows, float alpha)
-{
-    const int lane = threadIdx.x & 31;
-    const int64_t col = col0 + 4 * lane;
-    if (col >= a.cols)
-        return;
-    constexpr int R = 8;  // rows whose loads are in flight together, ahead of any store
-#pragma unroll 1
-    for (int r0 = 0; r0 < 32 && row0 + r0 < rows; r0 += R) {
-        float4 f[R];
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-            f[r] = make_float4(0.f, 0.f, 0.f, 0.f);
-        const float *from = part + r0 * kPairN + 4 * lane;  // written to the tile's end, whatever `rows`
-#pragma unroll 4
-        for (int s = 0; s < slices; ++s, from += kPairM * kPairN)
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const float4 v = __ldcg(reinterpret_cast<const float4 *>(from + r * kPairN));
-                f[r].x += v.x;
-                f[r].y += v.y;
-                f[r].z += v.z;
-                f[r].w += v.w;
-            }
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int64_t row = row0 + r0 + r;
-            if (row >= rows)
-                break;
-            int64_t out_row = row;
-            if constexpr (!WEIGHT) {
-                float4 *acc4 = reinterpret_cast<float4 *>(a.acc + row * a.lda + col);
-                if (!a.first) {
-                    const float4 o = *acc4;
-                    f[r].x += o.x;
-                    f[r].y += o.y;
-                    f[r].z += o.z;
-                    f[r].w += o.w;
-                }
-                if (!a.last) {
-                    *acc4 = f[r];
-                    continue;
-                }
-                out_row = a.idx[row];
-            }
-            T *out = static_cast<T *>(a.out) + out_row * a.ldo + col;
-            const float v[4] = {f[r].x * alpha, f[r].y * alpha, f[r].z * alpha, f[r].w * alpha};
-            if (a.vec && col + 4 <= a.cols) {
-                *reinterpret_cast<uint2 *>(out) = make_uint2(Elem<T>::pack2(v[0], v[1]), Elem<T>::pack2(v[2], v[3]));
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (col + i < a.cols)
-                        Elem<T>::store(out + i, v[i]);
-            }
-        }
-    }
+    store_block(static_cast<T *>(a.out), a.ldo, col, a.cols, static_cast<int>(min(rows - row0, int64_t{32})), f, a.vec,
+                turn, [&](int r) { return WEIGHT ? row0 + r : int64_t{a.idx[row0 + r]}; });
 }
 
 template <Epi E, typename T>
@@ -396,7 +349,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     __shared__ __align__(8) uint64_t bars[2 * kPairStages + 4];
     __shared__ uint32_t tmem_slot;
     __shared__ int dead_word;
-    __shared__ T turn[BOTH ? 8 : 1][BOTH ? 32 * kTurnStride : 1];
+    __shared__ __align__(16) T turn[CHUNKED ? 1 : 8][CHUNKED ? 1 : 32 * kTurnStride];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
@@ -615,6 +568,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         rs = a.rs[row];
                         gy = a.gy[row];
                     }
+                [[maybe_unused]] const int part = static_cast<int>(rank) * 8 + warp - 4;
                 uint32_t buf[2][32];
                 tmem_ld32(lanes + acc * kPairN, buf[0]);
 #pragma unroll
@@ -631,22 +585,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                             const float p = exp2_shift(__uint_as_float(r[i]), l2) * rs;
                             f[i] = col + i < inside ? (y == col + i ? gy : p) : 0.f;
                         }
-                        store_chunk<T>(static_cast<T *>(a.g) + row * a.ldg, col, a.ldg, f, 1);
-                    } else if (un.slice >= 0) {
-                        float4 *to = reinterpret_cast<float4 *>(
-                            p.slices + (int64_t{un.slice} * kPairM + (row - tm * kPairM)) * kPairN + col - tn * kPairN);
-#pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            to[q] = make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
-                                                __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
+                        store_block(static_cast<T *>(a.g), a.ldg, col, a.ldg, 32, f, true, turn[warp - 4],
+                                    [&](int k) { return int64_t{row - lane + k}; });
                     } else {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             f[i] = un.k1 ? __uint_as_float(r[i]) : 0.f;
-                        if (dw)
-                            finish_chunk<true, T>(p, f, row - lane, col, p.rows, alpha, turn[warp - 4]);
+                        if (un.slice >= 0)
+                            put_block(block_at(p.slices, un.slice, part, c), f);
+                        else if (dw)
+                            finish_block<true, T>(p, f, un.tile, part, c, row - lane, col, p.rows, alpha, turn[warp - 4]);
                         else
-                            finish_chunk<false, T>(p, f, row - lane, col, n, alpha, turn[warp - 4]);
+                            finish_block<false, T>(p, f, un.tile, part, c, row - lane, col, n, alpha, turn[warp - 4]);
                     }
                 }
                 tc_fence_before();
@@ -658,7 +608,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         // the last of this part's slices to arrive adds them all up
                         const Split &split = dw ? spw : sp;
                         const int t = un.tile - split.whole;
-                        unsigned *count = p.arrived + t * 16 + rank * 8 + (warp - 4);
+                        unsigned *count = p.arrived + t * 16 + part;
                         unsigned before = 0;
                         __threadfence();
                         __syncwarp();
@@ -669,13 +619,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                             __threadfence();
                             if (lane == 0)
                                 *count = 0u;  // for the next launch
-                            const int r0 = static_cast<int>(rank) * 128 + ew * 32;
-                            const float *part = p.slices + int64_t{t} * split.slices * kPairM * kPairN +
-                                                r0 * kPairN + half * 128;
-                            if (dw)
-                                finish_slices<true, T>(p, part, split.slices, tm * kPairM + r0, c0, p.rows, alpha);
-                            else
-                                finish_slices<false, T>(p, part, split.slices, tm * kPairM + r0, c0, n, alpha);
+#pragma unroll 1
+                            for (int c = 0; c < 4; ++c) {
+                                float f[32] = {};
+#pragma unroll 2
+                                for (int k = 0; k < split.slices; ++k)
+                                    add_block(f, block_at(p.slices, t * split.slices + k, part, c));
+                                if (dw)
+                                    finish_block<true, T>(p, f, un.tile, part, c, row - lane, c0 + 32 * c, p.rows,
+                                                          alpha, turn[warp - 4]);
+                                else
+                                    finish_block<false, T>(p, f, un.tile, part, c, row - lane, c0 + 32 * c, n, alpha,
+                                                           turn[warp - 4]);
+                            }
                         }
                     }
             }
