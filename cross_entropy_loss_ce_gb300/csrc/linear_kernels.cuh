@@ -1117,6 +1117,26 @@ struct GatherArgs {
     const int64_t *targets;
 };
 
+// The 16 bytes that begin `off` (even, < 16) bytes into the aligned v[0], v[1].
+__device__ __forceinline__ uint4 shifted_vector(const uint4 *v, int off)
+{
+    const uint4 a = __ldg(v), b = __ldg(v + 1);
+    uint32_t x[5] = {a.x, a.y, a.z, a.w, b.x};
+    if (off & 8) {
+        x[0] = a.z, x[1] = a.w, x[2] = b.x, x[3] = b.y, x[4] = b.z;
+        if (off & 4)
+            x[0] = a.w, x[1] = b.x, x[2] = b.y, x[3] = b.z, x[4] = b.w;
+    } else if (off & 4) {
+        x[0] = a.y, x[1] = a.z, x[2] = a.w, x[3] = b.x, x[4] = b.y;
+    }
+    if (off & 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            x[i] = __funnelshift_r(x[i], x[i + 1], 16);
+    }
+    return make_uint4(x[0], x[1], x[2], x[3]);
+}
+
 // By one warp of `step`; row_of(i) and target_of(i) of the n listed rows,
 // entry_of(i, x_y) the backward's entry of its target.
 template <typename T, typename RowOf, typename TargetOf, typename EntryOf>
@@ -1134,6 +1154,8 @@ __device__ __forceinline__ void gather_rows(const GatherArgs &a, int64_t n, int6
             continue;
         }
         const T *s = static_cast<const T *>(a.src) + row_of(i) * a.ss;
+        const int off = static_cast<int>(reinterpret_cast<uintptr_t>(s) & 15);
+        const uint4 *s0 = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(s) - off);
         int64_t done = 0;
         if (a.vec) {  // K may end inside the last vector: the rest is zeroed one by one
             done = a.K / 8 * 8;
@@ -1143,6 +1165,10 @@ __device__ __forceinline__ void gather_rows(const GatherArgs &a, int64_t n, int6
         }
 #pragma unroll 2
         for (int64_t j = done / 8 + lane; j < a.lds / 8; j += 32) {
+            if (16 * (j + 2) <= off + 2 * a.K && (j > 0 || off == 0)) {
+                reinterpret_cast<uint4 *>(d)[j] = shifted_vector(s0 + j, off);
+                continue;
+            }
             alignas(16) T v[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)

@@ -310,3 +310,55 @@ def test_greedy_rows_of_longer_sequences():
     w = (torch.randn(900, 64, device="cuda") / 8).to(BF)
     last = full[:, -1]
     assert torch.equal(gbce.linear_greedy(last, w)[0], gbce.linear_greedy(last.contiguous(), w)[0])
+
+
+@pytest.mark.parametrize("K", [9, 17, 129, 203, 1001])
+@pytest.mark.parametrize("M,V", [(20, 333), (300, 515)])
+def test_odd_widths_at_every_offset(M, V, K):
+    # rows that start at every even offset of 16 bytes, packed and written unaligned
+    h, w, t = make_head(M, K, V, BF, shift=1, pad=2, ignored=0.2)
+    dh = torch.full((M, K + 2), 3.0, device="cuda", dtype=BF)
+    dw = torch.full((V, K + 4), 5.0, device="cuda", dtype=BF)
+    _, _, lse = gbce.linear_ce_fwd(h, w, t)
+    gbce.linear_ce_bwd(h, w, t, lse, d_hidden=dh[:, 1:K + 1], d_weight=dw[:, 3:K + 3])
+    ref = HeadRef(h, w, t)
+    near(dh[:, 1:K + 1], ref.d_hidden, ref.dh_tol, "d_hidden")
+    near(dw[:, 3:K + 3], ref.d_weight, ref.dw_tol, "d_weight")
+    assert bool((dh[:, 0] == 3).all() and (dh[:, K + 1] == 3).all())
+    assert bool((dw[:, :3] == 5).all() and (dw[:, K + 3:] == 5).all())
+
+
+@pytest.mark.parametrize("n", [1, 255, 256, 257])
+def test_counted_rows_at_the_borders_of_a_tile(n):
+    # a padded batch of 600 rows of which n count
+    h, w, t = make_head(600, 72, 700, BF)
+    keep = torch.randperm(600, generator=torch.Generator().manual_seed(n))[:n].cuda()
+    targets = torch.full_like(t, -100)
+    targets[keep] = t[keep]
+    run_all(h, w, targets)
+
+
+@pytest.mark.parametrize("M", [1024, 1025, 2000])
+def test_the_two_ways_of_listing_rows(M):
+    # up to 1024 rows every CTA lists them, above one CTA does
+    h, w, t = make_head(M, 64, 300, BF, ignored=0.5)
+    run_all(h, w, t, "none", torch.rand(M, device="cuda"))
+
+
+def test_split_tiles_of_both_gradients():
+    # few output tiles and a long axis: both products are cut along K and added up
+    h, w, t = make_head(2100, 264, 9000, BF, ignored=0.1)
+    run_all(h, w, t)
+    h, w, t = make_head(300, 520, 20000, F16, ignored=0.1)
+    run_all(h, w, t, "sum")
+
+
+def test_matches_the_loss_from_stored_logits():
+    # the library's ce_fwd_bwd on fp32 logits formed in 64 bits: the same losses
+    h, w, t = make_head(200, 136, 1500, BF, ignored=0.2)
+    logits = (h.double() @ w.double().T).float()
+    loss, rows = gbce.ce_fwd_bwd_ex(logits, t, want_row_loss=True)
+    ref = HeadRef(h, w, t)
+    got, row, _ = gbce.linear_ce_fwd(h, w, t)
+    near(row, rows, ref.row_tol + 1e-5 * rows.abs(), "row loss")
+    near(got, loss, ref.loss_tol + 1e-5 * loss.abs(), "loss")
