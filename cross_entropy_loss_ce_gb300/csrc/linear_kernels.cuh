@@ -969,7 +969,7 @@ __device__ __forceinline__ Listed prep_rows(const PrepArgs &a, bool write, int *
     int rows = 0, n = 0;
     float top = 0.f;
     bool bad = false;
-#pragma unroll 4
+#pragma unroll 8
     for (int64_t i = lo + lane; i < hi; i += 32) {
         const int64_t y = __ldg(a.targets + i);
         if (y != a.ignore_index) {
@@ -1034,34 +1034,47 @@ __device__ __forceinline__ Listed prep_rows(const PrepArgs &a, bool write, int *
         if (!BWD && a.M == 0 && a.reduction != kReduceNone)
             *a.loss = a.reduction == kReduceMean ? __int_as_float(0x7fc00000) : 0.f;
     }
-#pragma unroll 4
-    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
-        const int64_t i = i0 + lane;
-        const int64_t y = i < hi ? __ldg(a.targets + i) : a.ignore_index;
-        const bool skip = y == a.ignore_index;
-        const bool listed = !skip && y >= 0 && y < a.V;
-        const unsigned votes = __ballot_sync(0xffffffffu, listed);
-        if (listed) {
-            const int pos = at + __popc(votes & ((1u << lane) - 1));
-            if (s_idx) {
-                s_idx[pos] = static_cast<int>(i);
-                s_tgt[pos] = static_cast<int>(y);
-            }
-            if (write) {
-                a.idx[pos] = static_cast<int>(i);
-                a.tgt[pos] = static_cast<int>(y);
-                if (BWD) {
-                    a.l2[pos] = __ldg(a.lse_in + i) * kLog2e;
-                    a.rs[pos] = (a.grad_scale && a.reduction == kReduceNone ? __ldg(a.grad_scale + i) : one) * list.inv;
-                }
-            }
-        } else if (!BWD && write && i < hi) {
-            const float v = skip ? 0.f : __int_as_float(0x7fc00000);
-            a.row_loss[i] = v;
-            if (a.lse_out)
-                a.lse_out[i] = v;
+    // four rounds' loads ahead of any of their stores
+    constexpr int R = 4;
+#pragma unroll 1
+    for (int64_t i0 = lo; i0 < hi; i0 += 32 * R) {
+        int64_t y[R];
+        float lse[R], g[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t i = i0 + 32 * r + lane;
+            y[r] = i < hi ? __ldg(a.targets + i) : a.ignore_index;
+            lse[r] = BWD && write && i < hi ? __ldg(a.lse_in + i) : 0.f;
+            g[r] = BWD && write && i < hi && a.grad_scale && a.reduction == kReduceNone ? __ldg(a.grad_scale + i) : one;
         }
-        at += __popc(votes);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t i = i0 + 32 * r + lane;
+            const bool skip = y[r] == a.ignore_index;
+            const bool listed = !skip && y[r] >= 0 && y[r] < a.V;
+            const unsigned votes = __ballot_sync(0xffffffffu, listed);
+            if (listed) {
+                const int pos = at + __popc(votes & ((1u << lane) - 1));
+                if (s_idx) {
+                    s_idx[pos] = static_cast<int>(i);
+                    s_tgt[pos] = static_cast<int>(y[r]);
+                }
+                if (write) {
+                    a.idx[pos] = static_cast<int>(i);
+                    a.tgt[pos] = static_cast<int>(y[r]);
+                    if (BWD) {
+                        a.l2[pos] = lse[r] * kLog2e;
+                        a.rs[pos] = g[r] * list.inv;
+                    }
+                }
+            } else if (!BWD && write && i < hi) {
+                const float v = skip ? 0.f : __int_as_float(0x7fc00000);
+                a.row_loss[i] = v;
+                if (a.lse_out)
+                    a.lse_out[i] = v;
+            }
+            at += __popc(votes);
+        }
     }
     return list;
 }
