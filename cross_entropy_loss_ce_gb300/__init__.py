@@ -1,4 +1,5 @@
-"""Fused hard-label cross-entropy and row softmax on GB300 (sm_103a).
+"""Fused hard-label cross-entropy and row softmax on GB300 (sm_103a), the
+cross-entropy of hidden states through an output layer, and a router's balance loss.
 
 Thin ctypes binding of ``_lib/libgbce.so`` (C ABI in ``include/gbce.h``): it
 checks tensor shapes, takes raw device pointers, row strides and the current

@@ -1,5 +1,6 @@
 /*
- * gbce: fused hard-label cross-entropy and row softmax for NVIDIA GB300 (sm_103a).
+ * gbce: fused hard-label cross-entropy and row softmax for NVIDIA GB300 (sm_103a),
+ * the cross-entropy of hidden states through an output layer, and a router's balance loss.
  *
  * Plain C ABI.  Every pointer argument of the compute calls is DEVICE memory
  * owned by the caller; the library keeps no reference after a call returns.
