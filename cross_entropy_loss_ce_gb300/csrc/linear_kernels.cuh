@@ -104,23 +104,34 @@ constexpr int kSplitMax = 8;         // slices of a tile, at most
 constexpr int kSplitCounters = 2 * (kSplitUnits / 2) * 16;  // 16 for each split tile of dH and of dW
 
 // Costs in k-steps of one tile: a slice takes its steps and about 6 more to be
-// written, and 3 to be read again.  The tail is the last, partial wave, or that and
-// a whole one.
-__host__ __device__ inline Split split_of(int tiles, int pairs, int kblocks)
+// written, and 8 to be read again (3 cut too finely: 1500 x 3000, K 2048 took 78 us
+// backward, 66 with 8).  The tail is the last, partial wave, or that and
+// a whole one.  A warp weighs up all choices at once, one in each lane.
+__device__ __forceinline__ Split split_of(int tiles, int pairs, int kblocks)
 {
-    Split best{tiles, 0, 1};
-    int64_t least = static_cast<int64_t>((tiles + pairs - 1) / pairs) * kblocks;
-    const int rest = tiles % pairs;
-    for (int tail = rest; rest && tail <= tiles && tail <= rest + pairs; tail += pairs)
-        for (int s = 2; s <= kSplitMax && 4 * s <= kblocks && tail * s <= kSplitUnits; ++s) {
-            const int64_t cost = static_cast<int64_t>((tiles - tail) / pairs) * kblocks +
-                                 static_cast<int64_t>((tail * s + pairs - 1) / pairs) * ((kblocks + s - 1) / s + 6) + 3 * s;
-            if (cost < least) {
-                least = cost;
-                best = Split{tiles - tail, tail, s};
-            }
+    const int lane = threadIdx.x & 31;
+    const int s = 2 + (lane & 7), rest = tiles % pairs, tail = rest + (lane & 8 ? pairs : 0);
+    int64_t cost = static_cast<int64_t>((tiles + pairs - 1) / pairs) * kblocks;  // no slices
+    if (lane < 16) {
+        const bool fits = rest && tail <= tiles && s <= kSplitMax && 4 * s <= kblocks && tail * s <= kSplitUnits;
+        const int64_t sliced = static_cast<int64_t>((tiles - tail) / pairs) * kblocks +
+                               static_cast<int64_t>((tail * s + pairs - 1) / pairs) * ((kblocks + s - 1) / s + 6) + 8 * s;
+        cost = fits ? sliced : INT64_MAX;
+    }
+    int best = lane;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        const int64_t c = __shfl_xor_sync(0xffffffffu, cost, off);
+        const int b = __shfl_xor_sync(0xffffffffu, best, off);
+        if (c < cost || (c == cost && b > best)) {  // of equal ones the last: lanes 16 .. 31 cut nothing
+            cost = c;
+            best = b;
         }
-    return best;
+    }
+    if (best >= 16)
+        return Split{tiles, 0, 1};
+    const int slices = 2 + (best & 7), cut = rest + (best & 8 ? pairs : 0);
+    return Split{tiles - cut, cut, slices};
 }
 
 // One CTA pair's share of a tile: k-steps k0 .. k1, and where a slice's sums go (-1: a whole tile).
@@ -797,7 +808,8 @@ __global__ void __launch_bounds__(skinny_threads<NG>(), 1) skinny_kernel(const _
             d[j] = 0.f;
             best[j] = INT32_MAX;
         }
-        const int live = min(max(n - 32 * group, 0), 32);
+        const int per = (n + NG - 1) / NG, col0 = group * per;  // of a group's warps
+        const int live = min(max(n - col0, 0), per);
         int it = 0;
         bool ok = true;
         for (int t = first; t < all && ok; t += step) {
@@ -807,7 +819,7 @@ __global__ void __launch_bounds__(skinny_threads<NG>(), 1) skinny_kernel(const _
                 if (!(ok = bar_wait<false>(tfull + 8 * acc, (it >> 1) & 1, dead)))
                     break;
                 tc_fence_after();
-                const uint32_t src = tmem + acc * kN + 32 * group + (static_cast<uint32_t>(ew * 32) << 16);
+                const uint32_t src = tmem + acc * kN + col0 + (static_cast<uint32_t>(ew * 32) << 16);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     uint32_t r[16];
@@ -839,7 +851,7 @@ __global__ void __launch_bounds__(skinny_threads<NG>(), 1) skinny_kernel(const _
                                 d[j] += exp2_shift(x, finite_shift(m[j]));
                             }
                         } else {
-                            if (tgt[32 * group + j] == v)
+                            if (tgt[col0 + j] == v)
                                 continue;  // the target's term is left out
                             if (x > m[j]) {
                                 d[j] = rescaled(d[j], m[j], x);
@@ -901,7 +913,8 @@ __global__ void __launch_bounds__(skinny_threads<NG>(), 1) skinny_kernel(const _
     if (warp == 2)
         tmem_free<1>(tmem, kCols);
     if (static_cast<int>(threadIdx.x) < min(n, kN)) {
-        const int g = threadIdx.x >> 5, j = threadIdx.x & 31;
+        const int per = (n + NG - 1) / NG;
+        const int g = static_cast<int>(threadIdx.x) / per, j = static_cast<int>(threadIdx.x) % per;
         float m = sm[4 * g][j], d = sd[4 * g][j];
         int best = si[4 * g][j];
 #pragma unroll

@@ -7,6 +7,7 @@
 namespace gbce {
 namespace {
 
+constexpr int64_t kMoeOneCtaSlots = 8192;   // slots up to which one CTA counts (no zeroing first)
 constexpr int kMoeSmallThreads = 512;
 constexpr int64_t kMoeRowsPerGroup = 2;   // rows that share a group's set-up, at least
 
@@ -125,12 +126,16 @@ cudaError_t launch_moe(MoeArgs a, int dtype, int vec, void *scratch, int device,
     a.totals = place.take<MoeTotals>(1);
     a.part = place.take<double>(kMoeMaxCtas);
     a.mask = place.take<unsigned char>(a.T);
-    cudaError_t e = cudaMemsetAsync(a.totals, 0, sizeof(MoeTotals), stream);
-    if (e != cudaSuccess)
-        return e;
-    const int64_t want = (a.T + kMoeThreads - 1) / kMoeThreads;
-    moe_count_kernel<kMoeThreads><<<static_cast<unsigned>(want < 2 * sms ? want : 2 * sms), kMoeThreads,
-                                    0, stream>>>(a);
+    cudaError_t e;
+    if (a.T * a.k <= kMoeOneCtaSlots) {
+        moe_count_kernel<1024><<<1, 1024, 0, stream>>>(a);
+    } else {
+        if ((e = cudaMemsetAsync(a.totals, 0, sizeof(MoeTotals), stream)) != cudaSuccess)
+            return e;
+        const int64_t want = (a.T + kMoeThreads - 1) / kMoeThreads;
+        moe_count_kernel<kMoeThreads><<<static_cast<unsigned>(want < 2 * sms ? want : 2 * sms), kMoeThreads,
+                                        0, stream>>>(a);
+    }
     if ((e = cudaGetLastError()) != cudaSuccess)
         return e;
     const MoeFn fn = pick_moe<false, kMoeThreads>(dtype, vec, a.E);

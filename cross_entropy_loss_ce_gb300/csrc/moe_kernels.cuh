@@ -29,7 +29,7 @@ constexpr int kMoeMaxExperts = 1024;
 constexpr int kMoeMaxSlots = 64;
 constexpr int kMoeMaxCtas = 2048;
 
-// Zeroed before moe_count_kernel.
+// Zeroed before a moe_count_kernel of several CTAs.
 struct MoeTotals {
     unsigned long long counts[kMoeMaxExperts];
     unsigned int n, bad, done, pad;
@@ -97,19 +97,37 @@ template <int NT>
 __global__ void __launch_bounds__(NT) moe_count_kernel(const MoeArgs a)
 {
     __shared__ unsigned hist[kMoeMaxExperts];
+    __shared__ int all, wrong;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (threadIdx.x == 0)
+        all = wrong = 0;
     for (int e = threadIdx.x; e < a.E; e += NT)
         hist[e] = 0;
     __syncthreads();
     bool bad = false;
     int n = moe_count_tokens(a, blockIdx.x * int64_t{NT} + threadIdx.x, int64_t{gridDim.x} * NT, hist, a.mask, bad);
     n = __reduce_add_sync(0xffffffffu, n);
+    if (bad)
+        atomicOr(&g_flags, kFlagBadTarget);
+    if (gridDim.x == 1) {  // nothing to add to: no zeroing before
+        if ((threadIdx.x & 31) == 0 && n)
+            atomicAdd(&all, n);
+        if (bad)
+            wrong = 1;
+        __syncthreads();
+        for (int e = threadIdx.x; e < a.E; e += NT)
+            a.totals->counts[e] = hist[e];
+        if (threadIdx.x == 0) {
+            a.totals->n = static_cast<unsigned>(all);
+            a.totals->bad = static_cast<unsigned>(wrong);
+            a.totals->done = 0u;
+        }
+        return;
+    }
     if ((threadIdx.x & 31) == 0 && n)
         atomicAdd(&a.totals->n, static_cast<unsigned>(n));
-    if (bad) {
+    if (bad)
         atomicOr(&a.totals->bad, 1u);
-        atomicOr(&g_flags, kFlagBadTarget);
-    }
     __syncthreads();
     for (int e = threadIdx.x; e < a.E; e += NT)
         if (hist[e])

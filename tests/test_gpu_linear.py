@@ -362,3 +362,22 @@ def test_matches_the_loss_from_stored_logits():
     got, row, _ = gbce.linear_ce_fwd(h, w, t)
     near(row, rows, ref.row_tol + 1e-5 * rows.abs(), "row loss")
     near(got, loss, ref.loss_tol + 1e-5 * loss.abs(), "loss")
+
+
+@pytest.mark.parametrize("M", [20, 64, 300, 1100])
+def test_rows_that_do_not_count_may_hold_anything(M):
+    h, w, t = make_head(M, 64, 500, BF, ignored=0.4)
+    clean = h.clone()
+    h[t == -100] = float("nan")
+    h[(t == -100) & (torch.arange(M, device="cuda") % 2 == 0)] = float("inf")
+    run_all(h, w, t, ref=HeadRef(torch.where((t == -100)[:, None], torch.zeros_like(clean), clean), w, t))
+
+
+@pytest.mark.parametrize("n", list(range(29, 65, 5)) + [64])
+def test_few_rows_shared_out_among_the_groups(n):
+    h, w, t = make_head(n, 72, 1111, F16, ignored=0.1)
+    run_all(h, w, t)
+    tok, lp = gbce.linear_greedy(h, w)
+    ref = HeadRef(h, w)
+    near(lp, ref.logprob, 2 * ref.D + 2.0 ** -19 * (1 + ref.lse.abs()), "logprob")
+    near(ref.x.gather(1, tok[:, None]).squeeze(1), ref.x.amax(1), 2 * ref.D, "the token's logit")

@@ -174,3 +174,10 @@ def test_same_bits_on_two_streams_and_captured():
         ref = MoeRef(x, ex, A, B)
         near(out[0], ref.loss, ref.loss_tol, "loss")
         near(out[2], ref.grad, ref.grad_tol, "grad")
+
+
+@pytest.mark.parametrize("T,k", [(2048, 4), (2049, 4), (8192, 1), (8193, 1), (1025, 8)])
+def test_the_ways_of_counting(T, k):
+    # up to 8192 slots one CTA counts, above several do
+    x, ex = make(T, 48, k, torch.bfloat16, padded=0.2)
+    check(x, ex)
