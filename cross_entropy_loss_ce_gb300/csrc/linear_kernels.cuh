@@ -255,9 +255,8 @@ __device__ __forceinline__ void stats_chunk(float (&x)[N], int c0, int limit, fl
 // where it allows no 16-byte stores.
 constexpr int kTurnStride = 40;  // 80 bytes: 16-byte accesses of 8 rows meet in no bank
 
-template <typename T, typename RowOf>
-__device__ __forceinline__ void store_block(T *out, int64_t ldo, int64_t col, int64_t cols, int rows,
-                                            const float (&f)[32], bool vec, T *turn, RowOf row_of)
+template <typename T>
+__device__ __forceinline__ void turn_block(const float (&f)[32], T *turn)
 {
     const int lane = threadIdx.x & 31;
     __syncwarp();
@@ -269,6 +268,29 @@ __device__ __forceinline__ void store_block(T *out, int64_t ldo, int64_t col, in
                        Elem<T>::pack2(p[4], p[5]), Elem<T>::pack2(p[6], p[7]));
     }
     __syncwarp();
+}
+
+// A whole block to rows that allow 16-byte stores: `to[i]` is where this lane's
+// 8 columns of row 8 i + lane / 4 go.  (With bounds checks and addresses formed
+// for each block, the gradient of one row of 128256 x 2048 spends a third of
+// its issue slots there and the stores come at 3 TB/s.)
+template <typename T>
+__device__ __forceinline__ void store_whole_block(T *const (&to)[4], int offset, const float (&f)[32], T *turn)
+{
+    const int lane = threadIdx.x & 31;
+    turn_block(f, turn);
+    const T *from = turn + (lane >> 2) * kTurnStride + 8 * (lane & 3);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4 *>(to[i] + offset) = *reinterpret_cast<const uint4 *>(from + 8 * i * kTurnStride);
+}
+
+template <typename T, typename RowOf>
+__device__ __forceinline__ void store_block(T *out, int64_t ldo, int64_t col, int64_t cols, int rows,
+                                            const float (&f)[32], bool vec, T *turn, RowOf row_of)
+{
+    const int lane = threadIdx.x & 31;
+    turn_block(f, turn);
     if (vec) {
         const int64_t c = col + 8 * (lane & 3);
 #pragma unroll
@@ -580,24 +602,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         gy = a.gy[row];
                     }
                 [[maybe_unused]] const int part = static_cast<int>(rank) * 8 + warp - 4;
-                uint32_t buf[2][32];
-                tmem_ld32(lanes + acc * kPairN, buf[0]);
+                // where this lane's share of each block goes, for blocks that are whole
+                const int row0 = row - lane;
+                T *to[4];
+                bool whole = true;
+                if constexpr (BOTH)
+                    whole = un.slice < 0 && un.k1 && p.vec && (dw || p.last) && row0 + 32 <= (dw ? p.rows : n) &&
+                            c0 + 128 <= p.cols;
 #pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    int64_t r = row0 + 8 * i + (lane >> 2);
+                    if constexpr (BOTH)
+                        if (!dw && whole)
+                            r = p.idx[r];
+                    to[i] = static_cast<T *>(BOTH ? p.out : a.g) + r * (BOTH ? p.ldo : a.ldg) + c0 + 8 * (lane & 3);
+                }
+                // one body for all four blocks: unrolled, its code leaves the instruction cache
+#pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
-                    tmem_wait_ld(buf[c & 1]);
-                    if (c + 1 < 4)
-                        tmem_ld32(lanes + acc * kPairN + 32 * (c + 1), buf[(c + 1) & 1]);
-                    uint32_t(&r)[32] = buf[c & 1];
+                    uint32_t r[32];
+                    tmem_ld32(lanes + acc * kPairN + 32 * c, r);
+                    tmem_wait_ld(r);
                     const int col = c0 + 32 * c;
                     float f[32];
                     if constexpr (E == Epi::Grad) {
+                        if (col + 32 <= inside) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const float p = exp2_shift(__uint_as_float(r[i]), l2) * rs;
-                            f[i] = col + i < inside ? (y == col + i ? gy : p) : 0.f;
+                            for (int i = 0; i < 32; ++i)
+                                f[i] = exp2_shift(__uint_as_float(r[i]), l2) * rs;
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                f[i] = col + i < inside ? exp2_shift(__uint_as_float(r[i]), l2) * rs : 0.f;
                         }
-                        store_block(static_cast<T *>(a.g), a.ldg, col, a.ldg, 32, f, true, turn[warp - 4],
-                                    [&](int k) { return int64_t{row - lane + k}; });
+                        if (y >= col && y < col + 32) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                f[i] = y == col + i ? gy : f[i];
+                        }
+                        store_whole_block(to, 32 * c, f, turn[warp - 4]);
+                    } else if (whole) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            f[i] = __uint_as_float(r[i]);
+                        if (!dw && !p.first)
+                            add_block(f, block_at(p.acc, un.tile, part, c));
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            f[i] *= alpha;
+                        store_whole_block(to, 32 * c, f, turn[warp - 4]);
                     } else {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
@@ -605,9 +658,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         if (un.slice >= 0)
                             put_block(block_at(p.slices, un.slice, part, c), f);
                         else if (dw)
-                            finish_block<true, T>(p, f, un.tile, part, c, row - lane, col, p.rows, alpha, turn[warp - 4]);
+                            finish_block<true, T>(p, f, un.tile, part, c, row0, col, p.rows, alpha, turn[warp - 4]);
                         else
-                            finish_block<false, T>(p, f, un.tile, part, c, row - lane, col, n, alpha, turn[warp - 4]);
+                            finish_block<false, T>(p, f, un.tile, part, c, row0, col, n, alpha, turn[warp - 4]);
                     }
                 }
                 tc_fence_before();
@@ -637,10 +690,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                                 for (int k = 0; k < split.slices; ++k)
                                     add_block(f, block_at(p.slices, t * split.slices + k, part, c));
                                 if (dw)
-                                    finish_block<true, T>(p, f, un.tile, part, c, row - lane, c0 + 32 * c, p.rows,
+                                    finish_block<true, T>(p, f, un.tile, part, c, row0, c0 + 32 * c, p.rows,
                                                           alpha, turn[warp - 4]);
                                 else
-                                    finish_block<false, T>(p, f, un.tile, part, c, row - lane, c0 + 32 * c, n, alpha,
+                                    finish_block<false, T>(p, f, un.tile, part, c, row0, c0 + 32 * c, n, alpha,
                                                            turn[warp - 4]);
                             }
                         }
