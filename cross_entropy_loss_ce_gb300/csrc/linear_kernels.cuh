@@ -249,10 +249,9 @@ __device__ __forceinline__ void stats_chunk(float (&x)[N], int c0, int limit, fl
 // A warp's 32 x 32 block of finished values, a thread one row, rounded once and
 // written to rows of `out` (row_of(r): where row r of the block goes, for r <
 // rows; columns col .. below cols).  A thread's own row would make each store of
-// a warp touch 32 lines (one row of 128256 x 2048, whose gradient is all stores:
-// 250 us for the weights' gradient, 14 GB/s from each SM); turned around in
-// `turn`, the warp's own, 4 lanes write 64 bytes of a row, or 32 lanes one row
-// where it allows no 16-byte stores.
+// a warp touch 32 lines (the weights' gradient of one row of 128256 x 2048, which
+// is all stores: 250 us, 171 so); turned around in `turn`, the warp's own, 4 lanes
+// write 64 bytes of a row, or 32 lanes one row where it allows no 16-byte stores.
 constexpr int kTurnStride = 40;  // 80 bytes: 16-byte accesses of 8 rows meet in no bank
 
 template <typename T>
@@ -271,9 +270,10 @@ __device__ __forceinline__ void turn_block(const float (&f)[32], T *turn)
 }
 
 // A whole block to rows that allow 16-byte stores: `to[i]` is where this lane's
-// 8 columns of row 8 i + lane / 4 go.  (With bounds checks and addresses formed
-// for each block, the gradient of one row of 128256 x 2048 spends a third of
-// its issue slots there and the stores come at 3 TB/s.)
+// 8 columns of row 8 i + lane / 4 go.  Without bounds checks and addresses formed
+// anew for each block the weights' gradient of one row of 128256 x 2048 takes
+// 137 us instead of 171 (its 525 MB are 78 us at the copy bandwidth; what is left
+// is the latency from one accumulator to the next).
 template <typename T>
 __device__ __forceinline__ void store_whole_block(T *const (&to)[4], int offset, const float (&f)[32], T *turn)
 {
