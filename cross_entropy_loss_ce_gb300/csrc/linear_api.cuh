@@ -7,7 +7,6 @@
 namespace gbce {
 namespace {
 
-constexpr int64_t kSkinnyRows = 64;               // rows up to which W is streamed once
 constexpr int64_t kGradPieceBytes = 512ll << 20;  // 16-bit logit gradients held at a time
 
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
@@ -98,7 +97,8 @@ struct HeadShape {
     int64_t kp;         // row stride of packed matrices: K rounded up to 128 bytes
     int64_t mp;         // rows of the packed hidden states
     bool skinny;
-    bool pack_h, pack_w;
+    bool pack_h, pack_w; // copies of the operands in scratch; a skinny forward without
+                         // pack_h reads the hidden states as they stand
     int64_t parts;      // partial pairs of a row
     int64_t vp;         // backward: vocabulary rows of a piece
     int64_t pieces;
@@ -279,10 +279,10 @@ HeadShape head_shape(const Call &call, const void *hidden, int64_t hs, const voi
     s.K = K;
     s.V = V;
     s.kp = round_up(K, 64);
-    s.skinny = op != HeadOp::Bwd && M <= kSkinnyRows;
+    s.skinny = op != HeadOp::Bwd && M <= kFewRows;
     s.mp = s.skinny ? (M <= 32 ? 32 : 64) : round_up(M, kPairM);
     // packed when rows are left out (any target may be ignore_index) or cannot be mapped
-    s.pack_h = op != HeadOp::Greedy || !mappable(hidden, hs, M);
+    s.pack_h = (op != HeadOp::Greedy && !s.skinny) || !mappable(hidden, hs, M);
     // weights whose rows start on 16 but not on 128 bytes are read as they are: a
     // copy to whole lines was measured (32000 classes, K 1000) and pays from about
     // 6000 rows on in the forward and 3000 in the backward, by at most 4% and 10%
@@ -322,15 +322,16 @@ cudaError_t pack_weights(const Call &call, const HeadShape &s, const HeadScratch
 // Forward of `op` from prepared rows: the products and the merge.
 template <bool GREEDY>
 cudaError_t launch_head(const Call &call, const HeadShape &s, const HeadScratch &r, const void *h,
-                        int64_t hstride, const void *w, int64_t wstride, int64_t hrows, MergeArgs m)
+                        int64_t hstride, const void *w, int64_t wstride, int64_t hrows, MergeArgs m,
+                        const PrepArgs *as_they_stand = nullptr)
 {
-    const bool early = !GREEDY || s.pack_h || s.pack_w;  // not the call's first kernel
+    const bool early = s.pack_h || s.pack_w;  // not the call's first kernel
     cudaError_t e;
     const int kblocks = static_cast<int>((s.K + 63) / 64);
     m.part = r.part;
     m.best = r.best;
     m.parts = static_cast<int>(s.parts);
-    m.n_ptr = GREEDY ? nullptr : r.rows;
+    m.n_ptr = GREEDY || as_they_stand ? nullptr : r.rows;
     m.n_host = static_cast<int>(s.M);
     m.idx = r.idx;
     m.xy = r.xy;
@@ -344,6 +345,7 @@ cudaError_t launch_head(const Call &call, const HeadShape &s, const HeadScratch 
         a.kblocks = kblocks;
         a.V = s.V;
         a.tgt = r.tgt;
+        a.targets = as_they_stand ? as_they_stand->targets : nullptr;
         a.part = r.part;
         a.best = r.best;
         a.ldp = s.parts;
@@ -372,11 +374,17 @@ cudaError_t launch_head(const Call &call, const HeadShape &s, const HeadScratch 
         return e;
     m.h = h;
     m.hs = hstride;
-    m.w = w;
-    m.ws = wstride;
+    if (!m.w) {
+        m.w = w;
+        m.ws = wstride;
+    }
     m.K = s.K;
     m.V = s.V;
-    m.vec = mappable(h, hstride, hrows) && mappable(w, wstride, s.V);
+    m.vec = mappable(h, hstride, hrows) && mappable(m.w, m.ws, s.V);
+    if (!GREEDY && as_they_stand)
+        return launch_kernel(call, true, call.dtype == GBCE_BF16 ? lin_few_kernel<__nv_bfloat16, 1024>
+                                                                 : lin_few_kernel<__half, 1024>,
+                             1, 1024, 0, m, *as_they_stand);
     if constexpr (!GREEDY)
         return launch_kernel(call, true, lin_merge_kernel<256>, (s.M + 7) / 8, 256, 0, m);
     else
@@ -389,19 +397,23 @@ cudaError_t launch_linear_fwd(const Call &call, const HeadShape &s, const HeadSc
                               const void *hidden, int64_t hs, const void *weight, int64_t ws,
                               const PrepArgs &prep)
 {
-    GatherArgs g{};
-    g.src = hidden;
-    g.ss = hs;
-    g.dst = r.h;
-    g.w = weight;
-    g.ws = ws;
-    g.xy = r.xy;
-    cudaError_t e = launch_start<false>(call, s, g, prep);
-    if (e != cudaSuccess || s.M == 0)
-        return e;
+    const bool few = s.skinny && !s.pack_h && s.M > 0;
+    cudaError_t e = cudaSuccess;
+    if (!few) {
+        GatherArgs g{};
+        g.src = hidden;
+        g.ss = hs;
+        g.dst = r.h;
+        g.w = weight;
+        g.ws = ws;
+        g.xy = r.xy;
+        e = launch_start<false>(call, s, g, prep);
+        if (e != cudaSuccess || s.M == 0)
+            return e;
+    }
     const void *w;
     int64_t wstride;
-    if ((e = pack_weights(call, s, r, weight, ws, &w, &wstride, false)) != cudaSuccess)
+    if ((e = pack_weights(call, s, r, weight, ws, &w, &wstride, few)) != cudaSuccess)
         return e;
     MergeArgs m{};
     m.row_loss = prep.row_loss;
@@ -412,7 +424,12 @@ cudaError_t launch_linear_fwd(const Call &call, const HeadShape &s, const HeadSc
     m.done = r.done;
     m.M = s.M;
     m.reduction = prep.reduction;
-    return launch_head<false>(call, s, r, r.h, s.kp, w, wstride, s.mp, m);
+    if (few) {  // lin_few_kernel reads the weights before it waits for their copy
+        m.w = weight;
+        m.ws = ws;
+    }
+    return few ? launch_head<false>(call, s, r, hidden, hs, w, wstride, s.M, m, &prep)
+               : launch_head<false>(call, s, r, r.h, s.kp, w, wstride, s.mp, m);
 }
 
 cudaError_t launch_linear_bwd(const Call &call, const HeadShape &s, const HeadScratch &r,

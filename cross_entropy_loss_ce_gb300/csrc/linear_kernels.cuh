@@ -36,8 +36,8 @@
 // gridDim-th tile through a 200 KB ring.  The last, partial round of tiles runs
 // at the same bandwidth: the CTAs that have one hold enough loads in flight.
 //
-// Rows whose target is ignore_index take part in nothing: lin_prep_kernel lists
-// the others in order and lin_gather_kernel packs their hidden states (zeros up
+// Rows whose target is ignore_index take part in nothing (but where skinny_kernel
+// reads the hidden states as they stand): lin_prep_kernel lists the others in order and lin_gather_kernel packs their hidden states (zeros up
 // to the next multiple of 256 rows), so the products run over counted rows only.
 #pragma once
 
@@ -737,7 +737,8 @@ struct SkinnyArgs {
     int n_host;
     int kblocks;
     int64_t V;
-    const int *tgt;
+    const int *tgt;     // targets of the listed rows, or
+    const int64_t *targets;  // ... of all rows as they stand (then CTA 0 clears *fail)
     float2 *part;       // [row][ldp], one for each CTA
     float4 *best;
     int64_t ldp;
@@ -788,8 +789,14 @@ __global__ void __launch_bounds__(skinny_threads<NG>(), 1) skinny_kernel(const _
     next_kernel_may_start();
     wait_prerequisite_grid();
     const int n = a.n_ptr ? *a.n_ptr : a.n_host;
-    if (!GREEDY && threadIdx.x < kN)
-        tgt[threadIdx.x] = static_cast<int>(threadIdx.x) < n ? a.tgt[threadIdx.x] : -1;
+    if (!GREEDY && threadIdx.x < kN) {
+        int64_t y = -1;
+        if (static_cast<int>(threadIdx.x) < n)
+            y = a.targets ? a.targets[threadIdx.x] : a.tgt[threadIdx.x];
+        tgt[threadIdx.x] = y >= 0 && y < a.V ? static_cast<int>(y) : -1;
+        if (a.targets && blockIdx.x == 0 && threadIdx.x == 0)
+            *a.fail = 0u;  // no wait has given up yet: each takes 2 s to
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -1284,6 +1291,8 @@ __device__ __forceinline__ float target_entry(float x, float l2, float rs)
     return expm1f(fmaf(x, kLog2e, -l2) * kLn2) * rs;
 }
 
+constexpr int kFewRows = 64;  // rows that skinny_kernel takes
+
 // Many rows: one CTA lists them, then many pack them.
 template <int NT, bool BWD>
 __global__ void __launch_bounds__(NT) lin_prep_kernel(const PrepArgs a)
@@ -1433,6 +1442,81 @@ __global__ void __launch_bounds__(NT) lin_merge_kernel(const MergeArgs a)
     if (threadIdx.x == 0)
         *a.loss = __ldcg(a.fail) ? __int_as_float(0x7fc00000)
                                  : a.reduction == kReduceMean ? s / static_cast<float>(*a.n_mean) : s;
+}
+
+// Up to 64 rows as they stand, none listed or packed before: one CTA merges their
+// partials, forms their targets' logits and the mean.
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT) lin_few_kernel(const MergeArgs a, const PrepArgs p)
+{
+    __shared__ int n_all, any_bad;
+    const int lane = threadIdx.x & 31;
+    next_kernel_may_start();
+    if (threadIdx.x == 0)
+        n_all = any_bad = 0;
+    __syncthreads();
+    // the dot products read nothing that the kernel before wrote
+    constexpr int kMost = (kFewRows + NT / 32 - 1) / (NT / 32);
+    float xy[kMost];
+#pragma unroll
+    for (int k = 0; k < kMost; ++k) {
+        const int64_t row = (threadIdx.x >> 5) + k * (NT / 32);
+        xy[k] = 0.f;
+        if (row >= a.M)
+            continue;
+        const int64_t y = p.targets[row];
+        if (y == p.ignore_index)
+            continue;
+        const bool good = y >= 0 && y < p.V;
+        if (good)
+            xy[k] = row_dot<T, 32>(static_cast<const T *>(a.h) + row * a.hs, static_cast<const T *>(a.w) + y * a.ws,
+                                   a.K, a.vec);
+        if (lane == 0) {
+            atomicAdd(&n_all, 1);
+            if (!good)
+                any_bad = 1;
+        }
+    }
+    wait_prerequisite_grid();
+#pragma unroll
+    for (int k = 0; k < kMost; ++k) {
+        const int64_t row = (threadIdx.x >> 5) + k * (NT / 32);
+        if (row >= a.M)
+            continue;
+        const int64_t y = p.targets[row];
+        const float2 *part = a.part + row * a.parts;
+        float s = -INFINITY, d = 0.f;
+#pragma unroll 4
+        for (int q = lane; q < a.parts; q += 32) {
+            const float2 v = part[q];
+            const float sn = fmaxf(s, v.x);
+            d = shifted(d, s, sn) + shifted(v.y, v.x, sn);
+            s = sn;
+        }
+        float top = s;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        d = warp_sum(shifted(d, s, top));
+        if (lane == 0) {
+            float lse = y == p.ignore_index ? 0.f : __int_as_float(0x7fc00000), loss = lse;
+            if (y != p.ignore_index && y >= 0 && y < p.V)
+                loss = loss_beside(top, d, xy[k], lse);
+            a.row_loss[row] = loss;
+            if (a.lse)
+                a.lse[row] = lse;
+        }
+    }
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0 && any_bad)
+        atomicOr(&g_flags, kFlagBadTarget);
+    if (!a.loss)
+        return;
+    const float s = sum_row_losses<NT>(a.row_loss, a.M, threadIdx.x, 1);
+    if (threadIdx.x == 0)
+        *a.loss = __ldcg(a.fail) ? __int_as_float(0x7fc00000)
+                                 : a.reduction == kReduceMean ? s / static_cast<float>(n_all) : s;
 }
 
 // One CTA per row: its partials, then the dot product of its token.

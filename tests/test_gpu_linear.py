@@ -381,3 +381,22 @@ def test_few_rows_shared_out_among_the_groups(n):
     ref = HeadRef(h, w)
     near(lp, ref.logprob, 2 * ref.D + 2.0 ** -19 * (1 + ref.lse.abs()), "logprob")
     near(ref.x.gather(1, tok[:, None]).squeeze(1), ref.x.amax(1), 2 * ref.D, "the token's logit")
+
+
+@pytest.mark.parametrize("reduction", ["mean", "sum", "none"])
+@pytest.mark.parametrize("M,K,V,pad,shift", [(1, 64, 700, 0, 0), (31, 72, 1000, 8, 0), (64, 200, 3001, 0, 0),
+                                             (40, 201, 900, 0, 0), (33, 64, 900, 0, 3)])
+def test_few_rows_as_they_stand_and_packed(M, K, V, pad, shift, reduction):
+    # up to 64 rows are read where they lie if a tensor map can (whole 16-byte rows), with ignored and
+    # bad targets among them; odd weights are copied first
+    h, w, t = make_head(M, K, V, BF, pad=pad, shift=shift, ignored=0.3)
+    if M > 5:
+        t[2], t[4] = V + 5, -7
+    ref = HeadRef(h, w, t, reduction=reduction)
+    gbce.last_error()
+    loss, row, lse = gbce.linear_ce_fwd(h, w, t, reduction=reduction)
+    assert gbce.last_error() == (gbce.ERR_BAD_TARGET if M > 5 else gbce.OK)
+    near(row, ref.row_loss, ref.row_tol, "row loss")
+    near(lse, ref.lse_out, ref.lse_tol, "lse")
+    if loss is not None:
+        near(loss, ref.loss, ref.loss_tol, "loss")
