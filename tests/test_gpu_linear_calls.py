@@ -1,6 +1,9 @@
 """Calls of the output-layer and router operators as programs make them: refusals on the GPU, captured
 graphs, several streams and threads, another current device, a wait that runs out (GPU)."""
 import ctypes
+import os
+import subprocess
+import sys
 import threading
 
 import pytest
@@ -224,3 +227,98 @@ def test_a_wait_that_runs_out_ends_the_call(M, drop):
     got = step(h, w, t)
     assert gbce.last_error() == gbce.OK
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+FIRST_CALLS = r"""
+import os, sys
+sys.path[:0] = [os.getcwd(), os.path.join(os.getcwd(), "tests")]
+import torch
+import cross_entropy_loss_ce_gb300 as gbce
+from head_ref import HeadRef, MoeRef, make_head, near
+torch.zeros(1, device="cuda")
+cases = [make_head(M, 72, 900, torch.bfloat16, ignored=0.2) for M in (20, 300, 1300)]
+x = torch.randn(3000, 48, device="cuda")
+ex = x.topk(4, 1).indices.contiguous()
+graph, outs = torch.cuda.CUDAGraph(), []
+with torch.cuda.graph(graph):
+    for h, w, t in cases:
+        loss, row, lse = gbce.linear_ce_fwd(h, w, t)
+        outs.append((loss, row, *gbce.linear_ce_bwd(h, w, t, lse), *gbce.linear_greedy(h, w)))
+    moe = gbce.moe_balance(x, ex, 0.01, 0.001)
+graph.replay()
+torch.cuda.synchronize()
+for (h, w, t), (loss, row, dh, dw, tok, lp) in zip(cases, outs):
+    ref = HeadRef(h, w, t)
+    near(loss, ref.loss, ref.loss_tol, "loss")
+    near(dh, ref.d_hidden, ref.dh_tol, "d_hidden")
+    near(dw, ref.d_weight, ref.dw_tol, "d_weight")
+    near(lp, ref.logprob, 2 * ref.D + 2.0 ** -19 * (1 + ref.lse.abs()), "logprob")
+ref = MoeRef(x, ex, 0.01, 0.001)
+assert torch.equal(moe[1], ref.counts)
+near(moe[0], ref.loss, ref.loss_tol, "balance loss")
+near(moe[2], ref.grad, ref.grad_tol, "balance gradient")
+print("captured first calls: ok")
+"""
+
+
+def test_a_process_whose_first_calls_are_captured():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured first calls: ok" in r.stdout, r.stdout + r.stderr
+
+
+def test_weights_past_32_bit_offsets():
+    # 1.1 million classes of 2048: 2.25e9 values, the last rows beyond 2^31
+    V, K, M = 1_100_000, 2048, 5
+    g = torch.Generator(device="cuda").manual_seed(3)
+    w = torch.empty(V, K, device="cuda", dtype=BF)
+    for i in range(0, V, 100_000):
+        w[i:i + 100_000] = torch.randn(100_000, K, device="cuda", generator=g).to(BF) / 64
+    t = torch.tensor([V - 1, 3, V - 40_000, -100, 600_000], device="cuda")
+    h = (w[t.clamp_min(0)].float() * 40).to(BF)
+    h[3] = (w[V - 7].float() * 40).to(BF)
+    tokens, logprob = gbce.linear_greedy(h, w)
+    assert tokens.tolist() == [V - 1, 3, V - 40_000, V - 7, 600_000]
+    loss, row, lse = gbce.linear_ce_fwd(h, w, t, reduction="sum")
+    x = torch.cat([h.double() @ w[i:i + 100_000].double().T for i in range(0, V, 100_000)], 1)
+    want = torch.logsumexp(x, 1)
+    D = (K / 16 + 8) * 2.0 ** -23 * max(float((h[i].abs().double() @ w[:1000].abs().double().T).amax()) for i in range(M)) * 4
+    keep = t >= 0
+    near(lse[keep], want[keep], D + 2.0 ** -20 * (1 + want[keep].abs()), "lse")
+    near(logprob, x.amax(1) - want, 2 * D + 2.0 ** -19 * (1 + want.abs()), "logprob")
+    dh, dw = gbce.linear_ce_bwd(h, w, t, lse, reduction="sum")
+    p = torch.exp(x - want[:, None]) * keep[:, None]
+    p[keep, t[keep]] -= 1
+    for rows in (slice(0, 8), slice(600_000, 600_004), slice(V - 40_000, V - 39_996), slice(V - 8, V)):
+        A = (p[:, rows].abs() + 1e-6).T @ h.double().abs()
+        near(dw[rows], p[:, rows].T @ h.double(), (2.0 ** -8 + 2 * D + 2.0 ** -18) * A * 2, "d_weight")
+    A = torch.zeros(M, K, device="cuda", dtype=torch.float64)
+    want_dh = torch.zeros_like(A)
+    for i in range(0, V, 100_000):
+        block = w[i:i + 100_000].double()
+        want_dh += p[:, i:i + 100_000] @ block
+        A += p[:, i:i + 100_000].abs() @ block.abs()
+    near(dh, want_dh, (2.0 ** -7 + 2 * D) * A + 2.0 ** -8 * want_dh.abs() + 2.0 ** -18 * w[t.clamp_min(0)].double().abs(), "d_hidden")
+
+
+def test_router_logits_past_32_bit_offsets():
+    # 2.1 million tokens of 1024 experts: 2.15e9 values
+    T, E, k = 2_100_000, 1024, 2
+    x = torch.empty(T, E, device="cuda", dtype=BF)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    for i in range(0, T, 300_000):
+        x[i:i + 300_000] = torch.randn(300_000, E, device="cuda", generator=g).to(BF)
+    ex = torch.randint(0, E, (T, k), device="cuda", generator=g)
+    ex[:, 0] = ex[:, 0] // 2  # the lower half is chosen more
+    ex[-1] = -1
+    loss, counts, grad = gbce.moe_balance(x, ex, 1.0, 0.0, grad_scale=1e6)
+    assert torch.equal(counts, torch.bincount(ex[:-1].reshape(-1), minlength=E))
+    n, f = T - 1, counts.double()
+    total = sum(float((torch.softmax(x[i:i + 100_000].double(), 1)[:min(100_000, n - i)] @ f).sum()) for i in range(0, T, 100_000))
+    assert abs(float(loss) - E / (k * n * n) * total) <= 2.0 ** -19
+    last = x[-50:].double()
+    p, c = torch.softmax(last, 1), f - f.mean()
+    want = 1e6 * E / (k * n * n) * p * (c - (p @ c)[:, None])
+    want[-1] = 0
+    size = 1e6 * E / (k * n * n) * p * (c.abs() + (p @ c.abs())[:, None])
+    near(grad[-50:], want, 2.0 ** -19 * size + 2.0 ** -8 * want.abs() + 2.0 ** -126, "grad")
