@@ -216,10 +216,14 @@ __device__ __forceinline__ void stats_chunk(float (&x)[N], int c0, int limit, fl
         for (int i = 0; i < 32; ++i)
             x[OFF + i] = c0 + i < limit ? x[OFF + i] : -INFINITY;
     }
-    float mc = x[OFF];
+    // four chains each for the maximum and the sum: two warps a scheduler do not
+    // hide the latency of one (8192 x 32000, K 512, where this work outlasts the
+    // tile's products: forward 199 us with one and two chains, 184 so)
+    float top[4] = {x[OFF], x[OFF + 1], x[OFF + 2], x[OFF + 3]};
 #pragma unroll
-    for (int i = 1; i < 32; ++i)
-        mc = fmaxf(mc, x[OFF + i]);
+    for (int i = 4; i < 32; ++i)
+        top[i & 3] = fmaxf(top[i & 3], x[OFF + i]);
+    const float mc = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
     if (mc > m) {
         if constexpr (GREEDY) {
             int at = 31;
@@ -237,13 +241,11 @@ __device__ __forceinline__ void stats_chunk(float (&x)[N], int c0, int limit, fl
         m = mc;
     }
     const float s = finite_shift(m);
-    float d0 = 0.f, d1 = 0.f;
+    float sum[4] = {};
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-        d0 += exp2_shift(x[OFF + i], s);
-        d1 += exp2_shift(x[OFF + i + 1], s);
-    }
-    d += d0 + d1;
+    for (int i = 0; i < 32; ++i)
+        sum[i & 3] += exp2_shift(x[OFF + i], s);
+    d += (sum[0] + sum[1]) + (sum[2] + sum[3]);
 }
 
 // A warp's 32 x 32 block of finished values, a thread one row, rounded once and
@@ -541,31 +543,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             const uint32_t lanes = tmem + half * 128 + (static_cast<uint32_t>(ew * 32) << 16);
             if constexpr (CHUNKED) {
                 float x[128];
-                for (int kb0 = 0; kb0 < un.k1; kb0 += kChunk, ++it) {
+                // what a row needs is loaded while its sums are still on their way
+                [[maybe_unused]] int y = -1;
+                if constexpr (E == Epi::Stats)
+                    y = live ? a.tgt[row] - c0 : -1;
+                const auto drain = [&](auto first) {
                     const int acc = it & 1;
                     if (!bar_wait<true>(tfull + 8 * acc, (it >> 1) & 1, dead))
                         return false;
+                    ++it;
                     tc_fence_after();
-                    uint32_t buf[2][16];
-                    tmem_ld16(lanes + acc * kPairN, buf[0]);
+                    const uint32_t src = lanes + acc * kPairN;
+                    if constexpr (decltype(first)::value) {
+                        tmem_ld32_into<0>(src, x);
+                        tmem_ld32_into<32>(src + 32, x);
+                        tmem_ld32_into<64>(src + 64, x);
+                        tmem_ld32_into<96>(src + 96, x);
+                        tmem_wait_into(x);
+                    } else {
+                        uint32_t buf[2][16];
+                        tmem_ld16(src, buf[0]);
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        tmem_wait_ld(buf[c & 1]);
-                        if (c + 1 < 8)
-                            tmem_ld16(lanes + acc * kPairN + 16 * (c + 1), buf[(c + 1) & 1]);
+                        for (int c = 0; c < 8; ++c) {
+                            tmem_wait_ld(buf[c & 1]);
+                            if (c + 1 < 8)
+                                tmem_ld16(src + 16 * (c + 1), buf[(c + 1) & 1]);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float v = __uint_as_float(buf[c & 1][i]);
-                            x[16 * c + i] = kb0 ? x[16 * c + i] + v : v;
+                            for (int i = 0; i < 16; ++i)
+                                x[16 * c + i] += __uint_as_float(buf[c & 1][i]);
                         }
                     }
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0)
                         bar_arrive_cluster(tempty0 + 8 * acc);
-                }
+                    return true;
+                };
+                if (!drain(std::true_type{}))
+                    return false;
+                for (int kb0 = kChunk; kb0 < un.k1; kb0 += kChunk)
+                    if (!drain(std::false_type{}))
+                        return false;
                 if constexpr (E == Epi::Stats) {  // the target's term is left out
-                    const int y = live ? a.tgt[row] - c0 : -1;
                     if (y >= 0 && y < 128) {
 #pragma unroll
                         for (int i = 0; i < 128; ++i)
@@ -586,11 +605,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         a.part[at] = make_float2(m == -INFINITY ? m : shift_of(m), d);
                 }
             } else {
-                const int acc = it & 1;
-                if (!bar_wait<true>(tfull + 8 * acc, (it >> 1) & 1, dead))
-                    return false;
-                ++it;
-                tc_fence_after();
                 [[maybe_unused]] int y = -1, inside = 0;  // columns with a gradient: none of an unlisted row
                 [[maybe_unused]] float l2 = 0.f, rs = 0.f, gy = 0.f;
                 if constexpr (E == Epi::Grad)
@@ -601,6 +615,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         rs = a.rs[row];
                         gy = a.gy[row];
                     }
+                const int acc = it & 1;
+                if (!bar_wait<true>(tfull + 8 * acc, (it >> 1) & 1, dead))
+                    return false;
+                ++it;
+                tc_fence_after();
                 [[maybe_unused]] const int part = static_cast<int>(rank) * 8 + warp - 4;
                 // where this lane's share of each block goes, for blocks that are whole
                 const int row0 = row - lane;

@@ -216,6 +216,34 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[N])
         asm volatile("" : "+r"(r[i]));
 }
 
+// 32 columns straight into x[OFF ..] (issue only).
+template <int OFF, int N>
+__device__ __forceinline__ void tmem_ld32_into(uint32_t addr, float (&x)[N])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=f"(x[OFF + 0]), "=f"(x[OFF + 1]), "=f"(x[OFF + 2]), "=f"(x[OFF + 3]),
+          "=f"(x[OFF + 4]), "=f"(x[OFF + 5]), "=f"(x[OFF + 6]), "=f"(x[OFF + 7]),
+          "=f"(x[OFF + 8]), "=f"(x[OFF + 9]), "=f"(x[OFF + 10]), "=f"(x[OFF + 11]),
+          "=f"(x[OFF + 12]), "=f"(x[OFF + 13]), "=f"(x[OFF + 14]), "=f"(x[OFF + 15]),
+          "=f"(x[OFF + 16]), "=f"(x[OFF + 17]), "=f"(x[OFF + 18]), "=f"(x[OFF + 19]),
+          "=f"(x[OFF + 20]), "=f"(x[OFF + 21]), "=f"(x[OFF + 22]), "=f"(x[OFF + 23]),
+          "=f"(x[OFF + 24]), "=f"(x[OFF + 25]), "=f"(x[OFF + 26]), "=f"(x[OFF + 27]),
+          "=f"(x[OFF + 28]), "=f"(x[OFF + 29]), "=f"(x[OFF + 30]), "=f"(x[OFF + 31])
+        : "r"(addr));
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_wait_into(float (&x)[N])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        asm volatile("" : "+f"(x[i]));
+}
+
 // Shared-memory descriptor of a 16-bit operand tile in 128-byte-swizzled atoms
 // of 8 rows x 128 bytes.  K-major (rows run along K): `sbo` = bytes from one
 // group of 8 rows to the next.  MN-major (rows run along M or N, 64 values
