@@ -1039,7 +1039,7 @@ struct PrepArgs {
 // What a CTA knows of the listed rows after prep_rows.
 struct Listed {
     int rows;
-    float one, inv;  // the factor that all rows share, and the power of two it is relative to
+    float inv;  // of a row's own factor: the power of two that it is relative to
 };
 
 // By all NT threads of a CTA.  `write`: this CTA writes the call's lists and
@@ -1057,7 +1057,9 @@ __device__ __forceinline__ Listed prep_rows(const PrepArgs &a, bool write, int *
     // each warp owns a contiguous range of rows: counts first, then the list
     const int64_t per = ((a.M + NT - 1) / NT) * 32;
     const int64_t lo = min(per * warp, a.M), hi = min(lo + per, a.M);
-    const float one = BWD && a.grad_scale && a.reduction != kReduceNone ? __ldg(a.grad_scale) : 1.f;
+    // a factor of the row's own goes into its entries of G; one that all rows share is
+    // applied to the sums in fp32, so that an entry of -1 stays one in 16 bits
+    const bool own = BWD && a.grad_scale && a.reduction == kReduceNone;
     int rows = 0, n = 0;
     float top = 0.f;
     bool bad = false;
@@ -1068,8 +1070,8 @@ __device__ __forceinline__ Listed prep_rows(const PrepArgs &a, bool write, int *
             ++n;
             if (y >= 0 && y < a.V) {
                 ++rows;
-                if (BWD && a.grad_scale) {
-                    const float g = fabsf(a.reduction == kReduceNone ? __ldg(a.grad_scale + i) : one);
+                if (own) {
+                    const float g = fabsf(__ldg(a.grad_scale + i));
                     top = g > top ? g : top;  // a NaN factor leaves the scale alone
                 }
             } else {
@@ -1091,7 +1093,7 @@ __device__ __forceinline__ Listed prep_rows(const PrepArgs &a, bool write, int *
     }
     __syncthreads();
     int at = 0;
-    Listed list{0, one, 1.f};
+    Listed list{0, 1.f};
     int n_all = 0;
     top = 0.f;
 #pragma unroll 8
@@ -1101,17 +1103,17 @@ __device__ __forceinline__ Listed prep_rows(const PrepArgs &a, bool write, int *
         n_all += warp_n[w];
         top = fmaxf(top, warp_max[w]);
     }
-    // factors relative to a power of two at or above the largest, so that their
+    // rows' factors relative to a power of two at or above the largest, so that their
     // 16-bit products with (p - onehot) stay in range whatever the loss scale
     if (BWD) {
         int e = 0;
-        if (a.grad_scale && top > 0.f && top < INFINITY)
+        if (top > 0.f && top < INFINITY)
             frexpf(top, &e);
         e = min(max(e, -100), 127);
         list.inv = ldexpf(a.head, -e);
         if (write && threadIdx.x == 0)
             *a.alpha = (a.reduction == kReduceMean ? 1.f / static_cast<float>(max(n_all, 1)) : 1.f) *
-                       ldexpf(1.f / a.head, e);
+                       (a.grad_scale && !own ? __ldg(a.grad_scale) : 1.f) * ldexpf(1.f / a.head, e);
         if (write)
             for (int i = threadIdx.x; i < kSplitCounters; i += NT)
                 a.arrived[i] = 0u;
@@ -1137,7 +1139,7 @@ __device__ __forceinline__ Listed prep_rows(const PrepArgs &a, bool write, int *
             const int64_t i = i0 + 32 * r + lane;
             y[r] = i < hi ? __ldg(a.targets + i) : a.ignore_index;
             lse[r] = BWD && write && i < hi ? __ldg(a.lse_in + i) : 0.f;
-            g[r] = BWD && write && i < hi && a.grad_scale && a.reduction == kReduceNone ? __ldg(a.grad_scale + i) : one;
+            g[r] = own && write && i < hi ? __ldg(a.grad_scale + i) : 1.f;
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -1346,7 +1348,7 @@ __global__ void __launch_bounds__(NT) lin_start_kernel(const GatherArgs a, const
         a, list.rows, blockIdx.x * int64_t{NT / 32} + (threadIdx.x >> 5), gridDim.x * int64_t{NT / 32},
         [&](int64_t i) { return int64_t{idx[i]}; }, [&](int64_t i) { return int64_t{tgt[i]}; },
         [&](int64_t i, float x) {
-            const float g = p.grad_scale && p.reduction == kReduceNone ? p.grad_scale[idx[i]] : list.one;
+            const float g = p.grad_scale && p.reduction == kReduceNone ? p.grad_scale[idx[i]] : 1.f;
             return target_entry(x, p.lse_in[idx[i]] * kLog2e, g * list.inv);
         });
 }

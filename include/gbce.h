@@ -452,9 +452,10 @@ GBCE_API int linear_ce_fwd(const void *hidden, int64_t hidden_stride, const void
  *                   G[r, v] = (exp(x[r, v] - lse_r) - [v == t_r]) k_r,
  *                   k_r = grad_scale / n (mean), grad_scale (sum), grad_scale[r] (none)
  *
- * G is formed a piece of the vocabulary at a time and rounded once to dtype (its
- * factors relative to a power of two at or above the largest, so fp16 keeps
- * small ones); both products are summed in fp32 and rounded once.  Both
+ * G is formed a piece of the vocabulary at a time and rounded once to dtype.  Of
+ * k_r it holds a factor of the row's own (none), relative to a power of two at or
+ * above the largest, so fp16 keeps small ones; a factor of all rows (mean, sum) is
+ * applied to the sums.  Both products are summed in fp32 and rounded once.  Both
  * gradients are written, not added to.  Scratch: the counted rows' hidden states, up to
  * 512 MB of G (more only when M exceeds 2^20 rows), M x K floats when the
  * vocabulary takes several pieces, up to 168 MB of partial sums, and the
