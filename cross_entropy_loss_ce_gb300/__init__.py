@@ -7,6 +7,10 @@ CUDA stream from torch, and calls the library.  Every step of the computation
 runs in the library's own CUDA kernels; there is no CPU or PyTorch fallback.
 Loading fails loudly when the library has not been built
 (``python -m cross_entropy_loss_ce_gb300.build``).
+
+A call with ``stream=`` works as one under ``torch.cuda.stream(stream)``: it reads its
+operands, and makes its outputs, on that stream.  Operands from another stream have to
+be ready on it, and kept until it is done; outputs are used elsewhere after it.
 """
 import ctypes
 import os
@@ -167,7 +171,7 @@ def ce_fwd_bwd(logits: torch.Tensor, targets: torch.Tensor, ignore_index: int = 
     if M and (not targets.is_cuda or not targets.is_contiguous()):
         raise ValueError("targets must be a contiguous CUDA tensor")
     if loss is None:
-        loss = torch.empty((), dtype=torch.float32, device=logits.device)
+        loss = _empty((), torch.float32, logits.device, stream)
     elif loss.dtype != torch.float32 or loss.numel() != 1 or not loss.is_cuda:
         raise ValueError("loss must be a one-element float32 CUDA tensor")
     dev = _call_device(("logits", logits), ("targets", targets if M else None), ("loss", loss))
@@ -179,10 +183,26 @@ def ce_fwd_bwd(logits: torch.Tensor, targets: torch.Tensor, ignore_index: int = 
     return loss
 
 
-def _device_floats(v, n: int, device, name: str):
-    """A float32 CUDA tensor of n values on `device` from a tensor or a number."""
+def _empty(shape, dtype, device, stream):
+    """An output that a call makes for itself.  Like all that it allocates or fills, it belongs
+    to the call's stream: made on the current stream, it might be a block that work queued there
+    has yet to leave.  The current stream is noted as its user, so its memory is not given to a
+    later call of the stream while work queued here by the time it is dropped still reads it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        out = torch.empty(shape, dtype=dtype, device=device)
+    if out.is_cuda:
+        out.record_stream(torch.cuda.current_stream(out.device))
+    return out
+
+
+def _device_floats(v, n: int, device, name: str, stream):
+    """A float32 CUDA tensor of n values on `device` from a tensor or a number (filled on the
+    call's stream)."""
     if not torch.is_tensor(v):
-        v = torch.full((n,), float(v), dtype=torch.float32, device=device)
+        with torch.cuda.stream(stream):  # None: the current one
+            v = torch.full((n,), float(v), dtype=torch.float32, device=device)
     if v.dtype != torch.float32 or not v.is_cuda or v.numel() != n or not v.is_contiguous():
         raise ValueError(f"{name} must be {n} contiguous float32 CUDA value(s)")
     return v
@@ -207,12 +227,12 @@ def ce_fwd_bwd_ex(logits: torch.Tensor, targets: torch.Tensor, ignore_index: int
         raise ValueError("targets must be a contiguous CUDA tensor")
     dev = logits.device
     if reduction != "none" and loss is None:
-        loss = torch.empty((), dtype=torch.float32, device=dev)
+        loss = _empty((), torch.float32, dev, stream)
     if (want_row_loss or reduction == "none") and row_loss is None:
-        row_loss = torch.empty((M,), dtype=torch.float32, device=dev)
+        row_loss = _empty((M,), torch.float32, dev, stream)
     gs = None
     if grad_scale is not None:
-        gs = _device_floats(grad_scale, M if reduction == "none" else 1, dev, "grad_scale")
+        gs = _device_floats(grad_scale, M if reduction == "none" else 1, dev, "grad_scale", stream)
     dev = _call_device(("logits", logits), ("targets", targets if M else None), ("loss", loss),
                        ("row_loss", row_loss), ("grad_scale", gs))
     with _OnDevice(dev):
@@ -230,7 +250,7 @@ def scale_rows(x: torch.Tensor, scale, stream=None) -> torch.Tensor:
     or one value per row ([M]).  A single scale of 1 costs only the launch."""
     xp, stride, M, N = _matrix(x, "x")
     per_row = torch.is_tensor(scale) and scale.numel() == M and M != 1
-    sc = _device_floats(scale, M if per_row else 1, x.device, "scale")
+    sc = _device_floats(scale, M if per_row else 1, x.device, "scale", stream)
     dev = _call_device(("x", x), ("scale", sc))
     with _OnDevice(dev):
         rc = load_library().scale_rows(xp, stride, M, N, DTYPES[x.dtype], sc.data_ptr(),
@@ -306,7 +326,7 @@ def softmax_fwd_ex(x: torch.Tensor, y: torch.Tensor = None, status: torch.Tensor
     int32 CUDA tensor the caller cleared) gets STATUS_TIMEOUT when one of the
     call's bounded waits gave up."""
     if y is None:
-        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+        y = _empty(x.shape, x.dtype, x.device, stream)
     xp, xs, M, N = _matrix(x, "x")
     yp, ys, My, Ny = _matrix(y, "y")
     if (My, Ny) != (M, N) or y.dtype != x.dtype:
@@ -330,7 +350,7 @@ def softmax_bwd_ex(y: torch.Tensor, dy: torch.Tensor, dx: torch.Tensor = None,
                    status: torch.Tensor = None, stream=None) -> torch.Tensor:
     """softmax_bwd with a status word of the call's own (as softmax_fwd_ex)."""
     if dx is None:
-        dx = torch.empty_like(dy, memory_format=torch.contiguous_format)
+        dx = _empty(dy.shape, dy.dtype, dy.device, stream)
     yp, ys, M, N = _matrix(y, "y")
     dp, ds, Md, Nd = _matrix(dy, "dy")
     xp, xs, Mx, Nx = _matrix(dx, "dx")
@@ -455,7 +475,7 @@ def ce_fwd_bwd_host(logits_host: torch.Tensor, targets_host: torch.Tensor,
         raise ValueError("targets_host must be a contiguous int64 tensor of shape [M]")
     hs = logits_host.stride(0) if M > 1 else V
     if grad is None:
-        grad = torch.empty((M, V), dtype=logits_host.dtype, device="cuda")
+        grad = _empty((M, V), logits_host.dtype, "cuda", stream)
     gp, gs, Mg, Vg = _matrix(grad, "grad")
     if (Mg, Vg) != (M, V) or grad.dtype != logits_host.dtype:
         raise ValueError("grad must match the logits' shape and dtype")
@@ -493,7 +513,7 @@ def ce_fwd_bwd_noalloc(logits: torch.Tensor, targets: torch.Tensor, ignore_index
     if M and (not targets.is_cuda or not targets.is_contiguous()):
         raise ValueError("targets must be a contiguous CUDA tensor")
     if loss is None:
-        loss = torch.empty((), dtype=torch.float32, device=logits.device)
+        loss = _empty((), torch.float32, logits.device, stream)
     elif loss.dtype != torch.float32 or loss.numel() != 1 or not loss.is_cuda:
         raise ValueError("loss must be a one-element float32 CUDA tensor")
     dev = _call_device(("logits", logits), ("targets", targets if M else None), ("loss", loss))
@@ -582,12 +602,12 @@ def linear_ce_fwd(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Ten
     if reduction == "none":
         loss = None
     elif loss is None:
-        loss = torch.empty((), dtype=torch.float32, device=dev)
+        loss = _empty((), torch.float32, dev, stream)
     elif loss.dtype != torch.float32 or loss.numel() != 1:
         raise ValueError("loss must be a one-element float32 CUDA tensor")
-    row_loss = torch.empty((M,), dtype=torch.float32, device=dev) if row_loss is None else \
+    row_loss = _empty((M,), torch.float32, dev, stream) if row_loss is None else \
         _row_values(row_loss, M, "row_loss")
-    lse = torch.empty((M,), dtype=torch.float32, device=dev) if lse is None else \
+    lse = _empty((M,), torch.float32, dev, stream) if lse is None else \
         _row_values(lse, M, "lse")
     dev = _call_device(("hidden", hidden), ("weight", weight), ("targets", ids), ("loss", loss),
                        ("row_loss", row_loss), ("lse", lse))
@@ -621,7 +641,7 @@ def linear_ce_bwd(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Ten
         if not want:
             out = None
         elif out is None:
-            out = torch.empty(like.shape, dtype=like.dtype, device=dev)
+            out = _empty(like.shape, like.dtype, dev, stream)
         elif out.shape != like.shape or out.dtype != like.dtype:
             raise ValueError(f"{name} must have the shape and dtype of {name[2:]}")
         else:
@@ -632,7 +652,7 @@ def linear_ce_bwd(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Ten
         _apart("d_hidden", d_hidden, ("d_weight", d_weight))
     gs = None
     if grad_scale is not None:
-        gs = _device_floats(grad_scale, M if reduction == "none" else 1, dev, "grad_scale")
+        gs = _device_floats(grad_scale, M if reduction == "none" else 1, dev, "grad_scale", stream)
     dhp, dhs = _rows(d_hidden, "d_hidden")[:2] if d_hidden is not None else (None, 0)
     dwp, dws = _rows(d_weight, "d_weight")[:2] if d_weight is not None else (None, 0)
     dev = _call_device(("hidden", hidden), ("weight", weight), ("targets", ids), ("lse", lse),
@@ -657,10 +677,10 @@ def linear_greedy(hidden: torch.Tensor, weight: torch.Tensor, tokens: torch.Tens
     hp, hs, wp, ws, M, K, V = _head(hidden, weight)
     dev = hidden.device
     if tokens is None:
-        tokens = torch.empty((M,), dtype=torch.int64, device=dev)
+        tokens = _empty((M,), torch.int64, dev, stream)
     elif tokens.dtype != torch.int64 or tokens.shape != (M,) or not tokens.is_contiguous():
         raise ValueError("tokens must be contiguous int64 of shape [M]")
-    logprob = torch.empty((M,), dtype=torch.float32, device=dev) if logprob is None else \
+    logprob = _empty((M,), torch.float32, dev, stream) if logprob is None else \
         _row_values(logprob, M, "logprob")
     dev = _call_device(("hidden", hidden), ("weight", weight), ("tokens", tokens), ("logprob", logprob))
     with _OnDevice(dev):
@@ -758,15 +778,15 @@ def moe_balance(logits: torch.Tensor, experts: torch.Tensor, balance_coef: float
     if not want_grad:
         grad = None
     elif grad is None:
-        grad = torch.empty((T, E), dtype=logits.dtype, device=dev)
+        grad = _empty((T, E), logits.dtype, dev, stream)
         gp, gstride = grad.data_ptr(), E
     elif grad.shape != logits.shape or grad.dtype != logits.dtype:
         raise ValueError("grad must match the logits' shape and dtype")
     else:
         gp, gstride = _rows(grad, "grad")[:2]
-    gs = None if grad_scale is None else _device_floats(grad_scale, 1, dev, "grad_scale")
-    loss = torch.empty((), dtype=torch.float32, device=dev) if want_loss else None
-    counts = torch.empty((E,), dtype=torch.int64, device=dev)
+    gs = None if grad_scale is None else _device_floats(grad_scale, 1, dev, "grad_scale", stream)
+    loss = _empty((), torch.float32, dev, stream) if want_loss else None
+    counts = _empty((E,), torch.int64, dev, stream)
     dev = _call_device(("logits", logits), ("experts", experts if T else None), ("grad", grad),
                        ("grad_scale", gs))
     with _OnDevice(dev):

@@ -100,6 +100,20 @@ def test_host_logits_into_a_gradient_of_the_call():
     assert torch.equal(got, want) and torch.equal(mine, loss)
 
 
+def test_an_output_dropped_while_the_current_stream_reads_it():
+    x, other = torch.randn(300, 700, device="cuda"), torch.zeros(300, 700, device="cuda")
+    want, side = torch.softmax(x, 1), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    y = gbce.softmax_fwd(x, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda._sleep(BUSY)
+    read = y * 1.0
+    del y
+    again = gbce.softmax_fwd(other, stream=side)
+    torch.cuda.synchronize()
+    assert torch.allclose(read, want, rtol=1e-5) and torch.allclose(again, torch.full_like(x, 1 / 700), rtol=1e-5)
+
+
 def test_a_side_stream_that_captures():
     h, w, t, lse = head()
     want = gbce.linear_ce_bwd(h, w, t, lse, 2.0)
