@@ -70,13 +70,15 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.linear_ce_fwd.argtypes = [p, i64, p, i64, p, p, p, p, i64, i64, i64, i64, ci, ci, p]
         lib.linear_ce_bwd.argtypes = [p, i64, p, i64, p, p, p, p, i64, p, i64, i64, i64, i64, i64,
                                       ci, ci, p]
+        lib.linear_ce_bwd_ex.argtypes = [p, i64, p, i64, p, p, p, p, p, i64, p, i64, i64, i64, i64, i64,
+                                         ci, ci, p]
         lib.linear_greedy.argtypes = [p, i64, p, i64, p, p, i64, i64, i64, ci, p]
         lib.moe_balance.argtypes = [p, i64, p, i64, p, p, p, i64, p, i64, i64, i64, ctypes.c_float,
                                     ctypes.c_float, ci, p]
         for f in ("ce_fwd_bwd", "softmax_fwd", "softmax_bwd", "gbce_last_error",
                   "gbce_timing_enable", "gbce_timing_read", "ce_fwd_bwd_ex", "scale_rows",
-                  "softmax_bwd_bsr", "linear_ce_fwd", "linear_ce_bwd", "linear_greedy",
-                  "moe_balance"):
+                  "softmax_bwd_bsr", "linear_ce_fwd", "linear_ce_bwd", "linear_ce_bwd_ex",
+                  "linear_greedy", "moe_balance"):
             getattr(lib, f).restype = ci
         _lib = lib
     return _lib
@@ -623,10 +625,13 @@ def linear_ce_fwd(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Ten
 def linear_ce_bwd(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor,
                   lse: torch.Tensor, grad_scale=None, ignore_index: int = -100,
                   reduction: str = "mean", want_hidden: bool = True, want_weight: bool = True,
-                  d_hidden: torch.Tensor = None, d_weight: torch.Tensor = None, stream=None):
+                  d_hidden: torch.Tensor = None, d_weight: torch.Tensor = None, stream=None,
+                  row_loss: torch.Tensor = None):
     """(d_hidden, d_weight) of linear_ce_fwd's loss, in the operands' type.
 
-    ``lse`` is what the forward returned; ``grad_scale`` the incoming gradient
+    ``lse`` and ``row_loss`` are what the forward returned; without the row losses
+    the gradients of nearly certain rows lose their precision (a loss of 1e-4 about 1%
+    of it, one of 1e-6 all: it is less than a step of lse).  ``grad_scale`` the incoming gradient
     (None, a number or a float32 CUDA tensor: one value, or one per row for
     'none').  A gradient that is not wanted is None and costs nothing.
     """
@@ -635,6 +640,8 @@ def linear_ce_bwd(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Ten
         raise ValueError(f"reduction must be one of {sorted(REDUCTIONS)}")
     ids = _class_ids(targets, M)
     lse = _row_values(lse, M, "lse")
+    if row_loss is not None:
+        row_loss = _row_values(row_loss, M, "row_loss")
     dev, outs = hidden.device, []
     for name, want, out, like in (("d_hidden", want_hidden, d_hidden, hidden),
                                   ("d_weight", want_weight, d_weight, weight)):
@@ -656,14 +663,14 @@ def linear_ce_bwd(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Ten
     dhp, dhs = _rows(d_hidden, "d_hidden")[:2] if d_hidden is not None else (None, 0)
     dwp, dws = _rows(d_weight, "d_weight")[:2] if d_weight is not None else (None, 0)
     dev = _call_device(("hidden", hidden), ("weight", weight), ("targets", ids), ("lse", lse),
-                       ("grad_scale", gs if M else None), ("d_hidden", d_hidden),
-                       ("d_weight", d_weight))
+                       ("row_loss", row_loss), ("grad_scale", gs if M else None),
+                       ("d_hidden", d_hidden), ("d_weight", d_weight))
     if d_hidden is None and d_weight is None:
         return None, None
     with _OnDevice(dev):
-        rc = load_library().linear_ce_bwd(
-            hp, hs, wp, ws, targets.data_ptr(), lse.data_ptr(), _ptr(gs), dhp, dhs, dwp, dws, M, K, V,
-            int(ignore_index), DTYPES[hidden.dtype], REDUCTIONS[reduction],
+        rc = load_library().linear_ce_bwd_ex(
+            hp, hs, wp, ws, targets.data_ptr(), lse.data_ptr(), _ptr(row_loss), _ptr(gs), dhp, dhs,
+            dwp, dws, M, K, V, int(ignore_index), DTYPES[hidden.dtype], REDUCTIONS[reduction],
             _stream_handle(stream, dev))
     _check(rc, "linear_ce_bwd")
     return d_hidden, d_weight
@@ -698,25 +705,26 @@ def _unit_rows(t):
 
 class FusedLinearCrossEntropy(torch.autograd.Function):
     """Autograd form of linear_ce_fwd / linear_ce_bwd.  Saves the hidden states,
-    the weights and one number per row; nothing is overwritten, so backward may
+    the weights and two numbers per row; nothing is overwritten, so backward may
     run more than once."""
 
     @staticmethod
     def forward(ctx, hidden, weight, targets, ignore_index=-100, reduction="mean"):
         h, w = _unit_rows(hidden.detach()), _unit_rows(weight.detach())
         loss, row_loss, lse = linear_ce_fwd(h, w, targets, ignore_index, reduction)
-        ctx.save_for_backward(h, w, targets, lse)
+        # a copy where the row losses are the output: a caller may change those
+        ctx.save_for_backward(h, w, targets, lse, row_loss.clone() if reduction == "none" else row_loss)
         ctx.ignore_index, ctx.reduction = ignore_index, reduction
         return row_loss if reduction == "none" else loss
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad_output):
-        h, w, targets, lse = ctx.saved_tensors
+        h, w, targets, lse, row_loss = ctx.saved_tensors
         gs = grad_output.detach().to(torch.float32).contiguous().reshape(-1)
         dh, dw = linear_ce_bwd(h, w, targets, lse, gs, ctx.ignore_index, ctx.reduction,
                                want_hidden=ctx.needs_input_grad[0],
-                               want_weight=ctx.needs_input_grad[1])
+                               want_weight=ctx.needs_input_grad[1], row_loss=row_loss)
         return dh, dw, None, None, None
 
 

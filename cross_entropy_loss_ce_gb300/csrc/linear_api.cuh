@@ -434,8 +434,8 @@ cudaError_t launch_linear_fwd(const Call &call, const HeadShape &s, const HeadSc
 
 cudaError_t launch_linear_bwd(const Call &call, const HeadShape &s, const HeadScratch &r,
                               const void *hidden, int64_t hs, const void *weight, int64_t ws,
-                              void *d_hidden, int64_t dhs, void *d_weight, int64_t dws,
-                              const PrepArgs &prep)
+                              const float *row_loss, void *d_hidden, int64_t dhs, void *d_weight,
+                              int64_t dws, const PrepArgs &prep)
 {
     GatherArgs g{};
     g.src = hidden;
@@ -444,6 +444,7 @@ cudaError_t launch_linear_bwd(const Call &call, const HeadShape &s, const HeadSc
     g.w = weight;
     g.ws = ws;
     g.gy = r.gy;
+    g.row_loss = row_loss;
     g.zero = d_hidden;
     g.zs = dhs;
     g.M = s.M;
@@ -604,6 +605,18 @@ extern "C" int linear_ce_bwd(const void *hidden, int64_t hidden_stride, const vo
                              void *d_weight, int64_t d_weight_stride, int64_t M, int64_t K, int64_t V,
                              int64_t ignore_index, int dtype, int reduction, gbce_stream_t stream)
 {
+    return linear_ce_bwd_ex(hidden, hidden_stride, weight, weight_stride, targets, lse, nullptr, grad_scale,
+                            d_hidden, d_hidden_stride, d_weight, d_weight_stride, M, K, V, ignore_index, dtype,
+                            reduction, stream);
+}
+
+extern "C" int linear_ce_bwd_ex(const void *hidden, int64_t hidden_stride, const void *weight,
+                                int64_t weight_stride, const int64_t *targets, const float *lse,
+                                const float *row_loss, const float *grad_scale, void *d_hidden,
+                                int64_t d_hidden_stride, void *d_weight, int64_t d_weight_stride, int64_t M,
+                                int64_t K, int64_t V, int64_t ignore_index, int dtype, int reduction,
+                                gbce_stream_t stream)
+{
     int st = check_head(hidden, hidden_stride, weight, weight_stride, M, K, V, dtype);
     if (st)
         return st;
@@ -615,7 +628,7 @@ extern "C" int linear_ce_bwd(const void *hidden, int64_t hidden_stride, const vo
         return st;
     if (d_weight && (st = check_matrix(d_weight, d_weight_stride, V, K, dtype)))
         return st;
-    if (!aligned_to(targets, 8) || !aligned_to(lse, 4) || !aligned_to(grad_scale, 4))
+    if (!aligned_to(targets, 8) || !aligned_to(lse, 4) || !aligned_to(row_loss, 4) || !aligned_to(grad_scale, 4))
         return GBCE_ERR_ALIGN;
     if (M == 0 && !d_weight)
         return GBCE_OK;
@@ -652,7 +665,7 @@ extern "C" int linear_ce_bwd(const void *hidden, int64_t hidden_stride, const vo
     prep.arrived = r.arrived;
     prep.head = dtype == GBCE_F16 ? 16384.f : 1.f;
     return map_error(scratch.release(launch_linear_bwd(call, s, r, hidden, hidden_stride, weight,
-                                                       weight_stride, M > 0 ? d_hidden : nullptr,
+                                                       weight_stride, row_loss, M > 0 ? d_hidden : nullptr,
                                                        d_hidden_stride, d_weight, d_weight_stride, prep)));
 }
 

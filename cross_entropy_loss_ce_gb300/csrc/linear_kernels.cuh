@@ -24,7 +24,8 @@
 // target's, the arg max's) is formed again as an fp32 dot product of two rows
 // (0.5% of the time at 8192 rows), and the sums leave its term out, so that the
 // loss ln(1 + others / e^x_y) of a likely target and (p_y - 1) keep their
-// precision.  And logits are summed in tensor memory over kChunk k-steps (1024
+// precision (the backward takes p_y from the row's loss: an fp32 lse of 20 has
+// lost a loss of 1e-6).  And logits are summed in tensor memory over kChunk k-steps (1024
 // of K) at a time, these sums in registers.  Emptying an accumulator takes
 // tensor-memory cycles from the running instructions: 8192 x 128256, K 4096
 // takes 4.90 ms unsplit, 5.04-5.22 in runs of 1024, 5.29 of 512, 5.86 of 256.
@@ -1210,7 +1211,7 @@ struct GatherArgs {
     int64_t K;
     int pad;
     int vec;            // src allows 16-byte loads
-    // targets' logits
+    // targets' logits, or (backward) the rows' losses in their place
     const void *w;      // NULL: none
     int64_t ws;
     int wvec;           // w and src allow 16-byte loads
@@ -1222,6 +1223,7 @@ struct GatherArgs {
     int zvec;           // zero allows 16-byte stores
     int64_t M, V, ignore_index;
     const int64_t *targets;
+    const float *row_loss;  // NULL: none given
 };
 
 // The 16 bytes that begin `off` (even, < 16) bytes into the aligned v[0], v[1].
@@ -1244,11 +1246,11 @@ __device__ __forceinline__ uint4 shifted_vector(const uint4 *v, int off)
     return make_uint4(x[0], x[1], x[2], x[3]);
 }
 
-// By one warp of `step`; row_of(i) and target_of(i) of the n listed rows,
-// entry_of(i, x_y) the backward's entry of its target.
-template <typename T, typename RowOf, typename TargetOf, typename EntryOf>
+// By one warp of `step`; row_of(i), target_of(i) and (backward) lse_of(i) of the n
+// listed rows, entry_of(i, ln p_y) the backward's entry of its target.
+template <typename T, typename RowOf, typename TargetOf, typename LseOf, typename EntryOf>
 __device__ __forceinline__ void gather_rows(const GatherArgs &a, int64_t n, int64_t first, int64_t step,
-                                            RowOf row_of, TargetOf target_of, EntryOf entry_of)
+                                            RowOf row_of, TargetOf target_of, LseOf lse_of, EntryOf entry_of)
 {
     const int lane = threadIdx.x & 31;
     const int64_t rows = (n + a.pad - 1) / a.pad * a.pad;
@@ -1282,13 +1284,16 @@ __device__ __forceinline__ void gather_rows(const GatherArgs &a, int64_t n, int6
                 v[i] = 8 * j + i < a.K ? s[8 * j + i] : zero_value;
             reinterpret_cast<uint4 *>(d)[j] = *reinterpret_cast<const uint4 *>(v);
         }
-        if (a.w) {
+        if (a.row_loss) {
+            if (lane == 0)
+                a.gy[i] = entry_of(i, -__ldg(a.row_loss + row_of(i)));
+        } else if (a.w) {
             const float x = row_dot<T, 32>(s, static_cast<const T *>(a.w) + target_of(i) * a.ws, a.K, a.wvec);
             if (lane == 0) {
                 if (a.xy)
                     a.xy[i] = x;
                 else
-                    a.gy[i] = entry_of(i, x);
+                    a.gy[i] = entry_of(i, x - lse_of(i));
             }
         }
     }
@@ -1304,12 +1309,6 @@ __device__ __forceinline__ void gather_rows(const GatherArgs &a, int64_t n, int6
             for (int64_t j = whole * 8 + lane; j < a.K; j += 32)
                 z[j] = zero_value;
         }
-}
-
-// (e^(x_y - lse) - 1) times the row's factor, from the difference itself.
-__device__ __forceinline__ float target_entry(float x, float l2, float rs)
-{
-    return expm1f(fmaf(x, kLog2e, -l2) * kLn2) * rs;
 }
 
 constexpr int kFewRows = 64;  // rows that skinny_kernel takes
@@ -1330,7 +1329,7 @@ __global__ void __launch_bounds__(NT) lin_gather_kernel(const GatherArgs a, cons
     gather_rows<T>(
         a, *p.rows_out, blockIdx.x * int64_t{NT / 32} + (threadIdx.x >> 5), gridDim.x * int64_t{NT / 32},
         [&](int64_t i) { return int64_t{p.idx[i]}; }, [&](int64_t i) { return int64_t{p.tgt[i]}; },
-        [&](int64_t i, float x) { return target_entry(x, p.l2[i], p.rs[i]); });
+        [&](int64_t i) { return p.lse_in[p.idx[i]]; }, [&](int64_t i, float lnp) { return expm1f(lnp) * p.rs[i]; });
 }
 
 // Up to kStartRows rows: every CTA lists them for itself (8 KB of targets from
@@ -1347,9 +1346,10 @@ __global__ void __launch_bounds__(NT) lin_start_kernel(const GatherArgs a, const
     gather_rows<T>(
         a, list.rows, blockIdx.x * int64_t{NT / 32} + (threadIdx.x >> 5), gridDim.x * int64_t{NT / 32},
         [&](int64_t i) { return int64_t{idx[i]}; }, [&](int64_t i) { return int64_t{tgt[i]}; },
-        [&](int64_t i, float x) {
+        [&](int64_t i) { return p.lse_in[idx[i]]; },
+        [&](int64_t i, float lnp) {
             const float g = p.grad_scale && p.reduction == kReduceNone ? p.grad_scale[idx[i]] : 1.f;
-            return target_entry(x, p.lse_in[idx[i]] * kLog2e, g * list.inv);
+            return expm1f(lnp) * (g * list.inv);
         });
 }
 
@@ -1361,7 +1361,8 @@ __global__ void __launch_bounds__(NT) lin_pack_kernel(const GatherArgs a, int64_
     wait_prerequisite_grid();
     gather_rows<T>(
         a, n, blockIdx.x * int64_t{NT / 32} + (threadIdx.x >> 5), gridDim.x * int64_t{NT / 32},
-        [](int64_t i) { return i; }, [](int64_t) { return int64_t{0}; }, [](int64_t, float) { return 0.f; });
+        [](int64_t i) { return i; }, [](int64_t) { return int64_t{0}; }, [](int64_t) { return 0.f; },
+        [](int64_t, float) { return 0.f; });
 }
 
 // ---------------------------------------------------------------------------

@@ -442,7 +442,8 @@ GBCE_API int linear_ce_fwd(const void *hidden, int64_t hidden_stride, const void
  * linear_ce_bwd -- gradients of linear_ce_fwd's loss.
  *
  *   hidden .. targets, M, K, V, ignore_index, dtype, reduction: as given to the forward.
- *   lse           [M] floats that linear_ce_fwd wrote.
+ *   lse           [M] floats that linear_ce_fwd wrote.  (linear_ce_bwd_ex takes its
+ *                 row losses too: nearly certain rows need them.)
  *   grad_scale    the incoming gradient: NULL (1), one float (mean, sum), or
  *                 one per row (none).
  *   d_hidden      [M, d_hidden_stride] of dtype or NULL: sum_v G[r, v] W[v, :], zeros
@@ -466,6 +467,24 @@ GBCE_API int linear_ce_bwd(const void *hidden, int64_t hidden_stride, const void
                            const float *grad_scale, void *d_hidden, int64_t d_hidden_stride,
                            void *d_weight, int64_t d_weight_stride, int64_t M, int64_t K, int64_t V,
                            int64_t ignore_index, int dtype, int reduction, gbce_stream_t stream);
+
+/*
+ * linear_ce_bwd_ex -- linear_ce_bwd with the forward's row losses.
+ *
+ *   row_loss      [M] floats that linear_ce_fwd wrote, or NULL (the same as
+ *                 linear_ce_bwd).
+ *
+ * A target's entry is then p - 1 = expm1(-row_loss), with the row loss's relative
+ * precision.  Without them it is expm1(x - lse), off by half a step of lse: 1e-6
+ * for an lse of 16 to 32, as much as the whole entry of a row whose loss is 1e-6,
+ * 1% of one of 1e-4.  Other arguments, results and errors: as for linear_ce_bwd.
+ */
+GBCE_API int linear_ce_bwd_ex(const void *hidden, int64_t hidden_stride, const void *weight,
+                              int64_t weight_stride, const int64_t *targets, const float *lse,
+                              const float *row_loss, const float *grad_scale, void *d_hidden,
+                              int64_t d_hidden_stride, void *d_weight, int64_t d_weight_stride, int64_t M,
+                              int64_t K, int64_t V, int64_t ignore_index, int dtype, int reduction,
+                              gbce_stream_t stream);
 
 /*
  * linear_greedy -- the most probable class of each row of H W^T and its

@@ -39,3 +39,93 @@ def test_a_factor_of_all_rows_is_not_rounded_with_the_entries(M, reduction, fact
     want = k * (p - hot).T @ h.double()
     tol = abs(k) * ((p * hot + U[dtype] * p + 2.0 ** -18 * (p + hot)).T @ h.double().abs()) + 2.0 ** -38 * abs(k)
     near(dw[t], want[t], tol[t] + half_step(want[t].abs() + tol[t], dtype), "weight rows of the targets")
+
+
+# --- nearly certain targets ----------------------------------------------------------------------
+
+
+def certain(M, V, dtype, top, losses):
+    """Rows whose target's logit is about ``top`` and whose loss is about losses[r % len]: x = base_r for all
+    classes but the target (a column of ones in the weights), plus a little noise."""
+    g = torch.Generator().manual_seed(M + V)
+    n = len(losses)
+    h, w = torch.zeros(M, 64), torch.zeros(V, 64)
+    w[:, 0] = 1.0
+    t = torch.arange(M) % n * 3 + 1
+    r = torch.arange(M) % n
+    base = top + torch.log(torch.tensor(losses, dtype=torch.float64) / V)[r]
+    h[:, 0] = base.float().to(dtype).float()
+    h[torch.arange(M), 1 + r] = 1.0
+    w[torch.arange(n) * 3 + 1, 1 + torch.arange(n)] = (top - h[:n, 0]).to(dtype).float()
+    h[:, 32:] = torch.randn(M, 32, generator=g) * 0.25
+    w[:, 32:] = torch.randn(V, 32, generator=g) * 0.25
+    return h.to(dtype).cuda(), w.to(dtype).cuda(), t.cuda()
+
+
+def certain_tolerances(h, w, t, k):
+    """The gradients in 64 bits and their tolerances by |p - onehot|: every entry of G is off by half a step
+    of its type (fp16 ones below the smallest normal by 2^-25 / 2^14 at most), by the error of a logit
+    against its row's lse, 2 (K / 16 + 8) 2^-23 max |h||w| (head_ref), by four roundings of lse's size and a few
+    others (2^-19); sums over 60 classes or the rows in fp32, and half a step of the result."""
+    a, b = h.double(), w.double()
+    x = a @ b.T
+    lse = torch.logsumexp(x, 1)
+    p = torch.exp(x - lse[:, None])
+    hot = torch.zeros_like(p).scatter_(1, t[:, None], 1.0)
+    entry = torch.where(hot > 0, torch.expm1(x - lse[:, None]), p)
+    # p - 1 from the others, where x - lse cancels in 64 bits too
+    entry = torch.where(hot > 0, -(p * (1 - hot)).sum(1, keepdim=True), entry)
+    D = (h.shape[1] / 16 + 8) * 2.0 ** -23 * (a.abs() @ b.abs().T).amax(1)
+    rel = U[h.dtype] + 2 * D + 4 * lse.abs() * 2.0 ** -24 + 2.0 ** -19
+    E = entry.abs()
+    tiny = 2.0 ** -39 if h.dtype == F16 else 2.0 ** -126
+    both = []
+    for want, bound, flat, n in ((entry @ b, (rel[:, None] * E) @ b.abs(), b.abs().sum(0), w.shape[0]),
+                                 (entry.T @ a, (rel[:, None] * E).T @ a.abs(), a.abs().sum(0), h.shape[0])):
+        size = E @ b.abs() if want.shape == h.shape else E.T @ a.abs()
+        tol = k * (bound + (n / 16 + 8) * 2.0 ** -23 * size + tiny * flat)
+        both.append((k * want, tol + half_step(k * want.abs() + tol, h.dtype)))
+    return both
+
+
+LOSSES = [1e-2, 1e-3, 1e-4, 1e-5, 1e-6]
+
+
+@pytest.mark.parametrize("dtype", [BF, F16])
+@pytest.mark.parametrize("M", [10, 300])
+@pytest.mark.parametrize("top", [20.0, 100.0])
+def test_nearly_certain_targets(M, top, dtype):
+    h, w, t = certain(M, 60, dtype, top, LOSSES)
+    factor = 1024.0  # a loss scale: fp16 results stay normal numbers
+    (dh, dh_tol), (dw, dw_tol) = certain_tolerances(h, w, t, factor)
+    a, b = h.clone().requires_grad_(), w.clone().requires_grad_()
+    rows = gbce.linear_cross_entropy(a, b, t, reduction="none")
+    rows = rows.detach()
+    assert float(rows.min()) < 4e-6 and float(rows.max()) < 4e-2
+    loss = gbce.linear_cross_entropy(a, b, t, reduction="sum")
+    (loss * factor).backward()
+    near(a.grad, dh, dh_tol, "d_hidden")
+    near(b.grad, dw, dw_tol, "d_weight")
+    _, row, lse = gbce.linear_ce_fwd(h, w, t, reduction="sum")
+    raw = gbce.linear_ce_bwd(h, w, t, lse, factor, reduction="sum", row_loss=row)
+    assert torch.equal(raw[0], a.grad) and torch.equal(raw[1], b.grad)
+
+
+def test_row_losses_of_another_shape_or_type_are_refused():
+    h, w, t = make_head(8, 64, 100, BF)
+    _, row, lse = gbce.linear_ce_fwd(h, w, t)
+    for wrong in (row[:4], row.double(), row[:, None]):
+        with pytest.raises(ValueError, match="row_loss"):
+            gbce.linear_ce_bwd(h, w, t, lse, row_loss=wrong)
+
+
+def test_row_losses_that_a_program_changes_in_place():
+    # the rows that linear_cross_entropy returns are the caller's: masking them in place changes no gradient
+    h, w, t = make_head(50, 64, 300, BF, ignored=0.2)
+    g = torch.rand(50, device="cuda")
+    grads = []
+    for change in (False, True):
+        a, b = h.clone().requires_grad_(), w.clone().requires_grad_()
+        rows = gbce.linear_cross_entropy(a, b, t, reduction="none")
+        grads.append(torch.autograd.grad((rows.mul_(g) if change else rows * g).sum(), (a, b)))
+    assert all(torch.equal(p, q) for p, q in zip(*grads))
