@@ -202,7 +202,7 @@ def _own(s):
     if case["op"] == "fwd":
         return {"loss": loss, "row_loss": row, "lse": lse}
     dh, dw = gbce.linear_ce_bwd(s["hidden"], s["weight"], s["targets"], lse, s["grad"], IGNORE,
-                                case["reduction"])
+                                case["reduction"], row_loss=row)
     return {"loss": loss, "row_loss": row, "d_hidden": dh, "d_weight": dw}
 
 
