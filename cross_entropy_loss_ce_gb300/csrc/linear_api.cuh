@@ -89,7 +89,7 @@ struct HeadScratch {
     float2 *part;
     float4 *best;
     unsigned short *g;
-    float *acc, *slices;
+    float *acc, *slices, *runs;
 };
 
 struct HeadShape {
@@ -103,6 +103,8 @@ struct HeadShape {
     int64_t vp;         // backward: vocabulary rows of a piece
     int64_t pieces;
     int64_t slices;     // slices of split tiles, at most, of either gradient
+    int grad_run, sum_run;  // backward: k-steps that tensor memory adds up at a time
+    int64_t run_pairs;  // backward: CTA pairs with tiles of several runs
 };
 
 enum class HeadOp { Fwd, Bwd, Greedy };
@@ -133,6 +135,8 @@ HeadScratch carve(Carver &c, const HeadShape &s, HeadOp op, bool want_hidden)
             r.acc = c.take<float>(s.mp * round_up(s.K, kPairN));
         r.arrived = c.take<unsigned>(kSplitCounters);
         r.slices = c.take<float>(2 * s.slices * kPairM * kPairN);
+        if (s.run_pairs)
+            r.runs = c.take<float>(s.run_pairs * kPairM * kPairN);
     } else {
         if (op == HeadOp::Fwd) {
             r.part = c.take<float2>(s.parts * s.mp);
@@ -302,6 +306,11 @@ HeadShape head_shape(const Call &call, const void *hidden, int64_t hs, const voi
         const int64_t rows = s.mp > s.vp ? s.mp : s.vp;
         const int64_t units = rows / kPairM * ((K + kPairN - 1) / kPairN) * kSplitMax;
         s.slices = units < kSplitUnits ? units : kSplitUnits;
+        const int scale = call.dtype == GBCE_BF16 ? kBf16Runs : 1;
+        s.grad_run = kGradRun * scale;
+        s.sum_run = kSumRun * scale;
+        if (K > s.grad_run * int64_t{kPairK} || rows > s.sum_run * int64_t{kPairK})
+            s.run_pairs = call.sms / 2;
     }
     return s;
 }
@@ -482,6 +491,8 @@ cudaError_t launch_linear_bwd(const Call &call, const HeadShape &s, const HeadSc
         a->acc = r.acc;
         a->slices = r.slices;
         a->arrived = r.arrived;
+        a->run = a == &grad ? s.grad_run : s.sum_run;
+        a->runs = r.runs;
     }
     grad.kblocks = static_cast<int>((s.K + 63) / 64);
     dw.tiles_n = d_weight ? tiles_k : 0;  // none: no tiles

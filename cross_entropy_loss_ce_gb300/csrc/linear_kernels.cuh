@@ -29,7 +29,14 @@
 // of K) at a time, these sums in registers.  Emptying an accumulator takes
 // tensor-memory cycles from the running instructions: 8192 x 128256, K 4096
 // takes 4.90 ms unsplit, 5.04-5.22 in runs of 1024, 5.29 of 512, 5.86 of 256.
-// The gradient products and their logits, which end in 16 bits, are not split.
+// The gradient products and their logits end in 16 bits; they are split where the
+// axis is so long that what is cut off comes near half a step of that type.  A sum
+// of one sign loses 0.6 to 0.8 of a step of 2^-23 for each 16 of the axis (measured:
+// a logit of 32 from K = 131072 was low by 0.024, the hidden gradient of 524288
+// classes by 2.3e-3 of its sums, the weights' of 262144 rows by 1.6e-3; half a step
+// of fp16 is 4.9e-4).  So sums over classes and rows are split after 16384 (fp16) and
+// 131072 (bf16) of them, which lose a quarter of half a step at most, and logits
+// after 2048 and 16384 of K: those of 32 move their p by less than half a step.
 //
 // skinny_kernel is the forward for at most 64 rows, where reading W once is the
 // whole cost: W's rows take the M side of the instruction, so a tile is 128
@@ -53,6 +60,8 @@ constexpr int kPairStageBytes = 2 * 128 * kPairK * 2;   // per CTA: 128 rows of 
 constexpr int kPairThreads = 384;
 constexpr int kPairSmem = kPairStages * kPairStageBytes + 1024;
 constexpr int kChunk = 16;                              // k-steps of a logit summed in tensor memory
+constexpr int kGradRun = 32, kSumRun = 256;             // ... of the backward's logits and of its sums in fp16;
+constexpr int kBf16Runs = 8;                            // in bf16 8 times as many
 constexpr int kBand = 8;                                // tiles of M that share a sweep over N
 
 enum class Epi { Stats, Greedy, Grad, Both };  // Both: the two gradient products
@@ -64,6 +73,8 @@ struct PairArgs {
     int tiles_m;        // dW: tiles of the piece's classes; else from n
     int tiles_n;
     int kblocks;        // 64-wide steps along K; dW: from n
+    int run;            // Grad, Both: k-steps summed in tensor memory at a time
+    float *runs;        // ... sums of earlier runs, kPairM x kPairN for each pair (NULL: no tile has two)
     int b_row0;         // Grad, dH: the piece's first row of W
     unsigned *fail;
     int drop_copy;      // failure-path tests: the k-step whose A block CTA 0 leaves out, else -1
@@ -498,7 +509,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             each_unit([&](const Unit &un, int, int, bool dw) {
                 const uint32_t idesc = BOTH && dw ? kIdescW : kIdesc;
                 const uint32_t lbo_a = BOTH && dw ? 8192 : 16, step_a = BOTH && dw ? 128 : 2;
-                const int run = CHUNKED ? kChunk : max(un.k1 - un.k0, 1);  // k-steps that stay in tensor memory
+                const int run = CHUNKED ? kChunk : (BOTH && dw ? w : a).run;  // k-steps that stay in tensor memory
                 for (int kb0 = un.k0; kb0 < un.k1 || kb0 == 0; kb0 += run, ++it) {
                     const int acc = it & 1;
                     if (!bar_wait<true>(tempty + 8 * acc, ((it >> 1) & 1) ^ 1, dead))
@@ -616,12 +627,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         rs = a.rs[row];
                         gy = a.gy[row];
                     }
+                const int part = static_cast<int>(rank) * 8 + warp - 4;
+                // all runs but the last one are added up where this thread alone reads them
+                bool more = false;
+                for (int k1 = un.k0 + p.run; k1 < un.k1; k1 += p.run) {
+                    const int acc = it & 1;
+                    if (!bar_wait<true>(tfull + 8 * acc, (it >> 1) & 1, dead))
+                        return false;
+                    ++it;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t r[32];
+                        tmem_ld32(lanes + acc * kPairN + 32 * c, r);
+                        tmem_wait_ld(r);
+                        float f[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            f[i] = __uint_as_float(r[i]);
+                        if (more)
+                            add_block(f, block_at(p.runs, pair, part, c));
+                        put_block(block_at(p.runs, pair, part, c), f);
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        bar_arrive_cluster(tempty0 + 8 * acc);
+                    more = true;
+                }
                 const int acc = it & 1;
                 if (!bar_wait<true>(tfull + 8 * acc, (it >> 1) & 1, dead))
                     return false;
                 ++it;
                 tc_fence_after();
-                [[maybe_unused]] const int part = static_cast<int>(rank) * 8 + warp - 4;
                 // where this lane's share of each block goes, for blocks that are whole
                 const int row0 = row - lane;
                 T *to[4];
@@ -645,15 +683,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     tmem_wait_ld(r);
                     const int col = c0 + 32 * c;
                     float f[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        f[i] = __uint_as_float(r[i]);
+                    if (more)
+                        add_block(f, block_at(p.runs, pair, part, c));
                     if constexpr (E == Epi::Grad) {
                         if (col + 32 <= inside) {
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                f[i] = exp2_shift(__uint_as_float(r[i]), l2) * rs;
+                                f[i] = exp2_shift(f[i], l2) * rs;
                         } else {
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                f[i] = col + i < inside ? exp2_shift(__uint_as_float(r[i]), l2) * rs : 0.f;
+                                f[i] = col + i < inside ? exp2_shift(f[i], l2) * rs : 0.f;
                         }
                         if (y >= col && y < col + 32) {
 #pragma unroll
@@ -662,9 +705,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         }
                         store_whole_block(to, 32 * c, f, turn[warp - 4]);
                     } else if (whole) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            f[i] = __uint_as_float(r[i]);
                         if (!dw && !p.first)
                             add_block(f, block_at(p.acc, un.tile, part, c));
 #pragma unroll
@@ -672,9 +712,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                             f[i] *= alpha;
                         store_whole_block(to, 32 * c, f, turn[warp - 4]);
                     } else {
+                        if (!un.k1) {  // no step: nothing was added up
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            f[i] = un.k1 ? __uint_as_float(r[i]) : 0.f;
+                            for (int i = 0; i < 32; ++i)
+                                f[i] = 0.f;
+                        }
                         if (un.slice >= 0)
                             put_block(block_at(p.slices, un.slice, part, c), f);
                         else if (dw)

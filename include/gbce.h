@@ -459,8 +459,9 @@ GBCE_API int linear_ce_fwd(const void *hidden, int64_t hidden_stride, const void
  * applied to the sums.  Both products are summed in fp32 and rounded once.  Both
  * gradients are written, not added to.  Scratch: the counted rows' hidden states, up to
  * 512 MB of G (more only when M exceeds 2^20 rows), M x K floats when the
- * vocabulary takes several pieces, up to 168 MB of partial sums, and the
- * weights' copy as in the forward.
+ * vocabulary takes several pieces, up to 168 MB of partial sums (20 MB more when
+ * sums are so long that they are taken in runs), and the weights' copy as in the
+ * forward.
  */
 GBCE_API int linear_ce_bwd(const void *hidden, int64_t hidden_stride, const void *weight,
                            int64_t weight_stride, const int64_t *targets, const float *lse,

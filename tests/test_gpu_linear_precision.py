@@ -129,3 +129,86 @@ def test_row_losses_that_a_program_changes_in_place():
         rows = gbce.linear_cross_entropy(a, b, t, reduction="none")
         grads.append(torch.autograd.grad((rows.mul_(g) if change else rows * g).sum(), (a, b)))
     assert all(torch.equal(p, q) for p, q in zip(*grads))
+
+
+# --- long sums -----------------------------------------------------------------------------------
+#
+# The tensor cores cut every addition (16 products of the axis at a time) toward zero, by one step, 2^-23 of
+# the sum or of the largest product, at most (as head_ref has it, whose bounds go by the sum of the products'
+# sizes too); N additions lose up to N 2^-23 of that, in one direction, which no rounding to nearest does.
+
+
+@pytest.mark.parametrize("dtype,K,run", [(F16, 131072, 2048), (BF, 1 << 20, 16384), (F16, 5000, 2048), (F16, 4160, 2048)])
+def test_wide_hidden_states(dtype, K, run):
+    # logits of about 32 from products of one sign; the tensor cores add up `run` of K at most.  An entry of G:
+    # half a step, the error of its logit (run / 16 + 8 additions) against the forward's lse (1024 / 16 + 8).
+    M, V = 70, 300
+    g = torch.Generator("cuda").manual_seed(K)
+    h = (0.5 + torch.rand(M, K, device="cuda", generator=g)).to(dtype)
+    size = 32.0 / K * (1 + 0.02 * torch.randn(V, 1, device="cuda", generator=g))
+    w = (size * (0.5 + torch.rand(V, K, device="cuda", generator=g))).to(dtype)
+    t = torch.arange(M, device="cuda") + 200
+    factor = 4096.0 if dtype == F16 else 1.0
+    _, _, lse = gbce.linear_ce_fwd(h, w, t, reduction="sum")
+    dh, dw = gbce.linear_ce_bwd(h, w, t, lse, factor, reduction="sum")
+    a, b = h.double(), w.double()
+    x = a @ b.T
+    p = torch.exp(x - torch.logsumexp(x, 1, keepdim=True))
+    hot = torch.zeros_like(p).scatter_(1, t[:, None], 1.0)
+    reach = float(x.amax())
+    rel = U[dtype] + ((run / 16 + 8) + (1024 / 16 + 8)) * 2.0 ** -23 * reach + 2.0 ** -18
+    tiny = factor * 2.0 ** -39 if dtype == F16 else 0.0
+    tol = factor * rel * (p + hot).T @ a + tiny * a.sum(0)
+    want = factor * (p - hot).T @ a
+    near(dw, want, tol + half_step(want.abs() + tol, dtype), "d_weight")
+    tol = factor * rel * (p + hot) @ b + tiny * b.sum(0)
+    want = factor * (p - hot) @ b
+    near(dh, want, tol + half_step(want.abs() + tol, dtype), "d_hidden")
+
+
+def test_hidden_gradient_of_many_classes():
+    # 524288 classes, 76 tiles of two rows of tiles: no tile is cut.  Only the first 64 columns of the hidden
+    # states hold anything (cheap logits); the gradient's are all sums over the classes of p W, of one sign.
+    # At most 16384 classes are added on the tensor cores: 1024 additions, 2^-13 of the sizes added.  Those are
+    # the sum of p W and the target's W (its entry is -1): once that stands in a run's sum, its steps are what
+    # the others are cut to.
+    M, K, V = 512, 9728, 524288
+    g = torch.Generator("cuda").manual_seed(1)
+    h = torch.zeros(M, K, device="cuda", dtype=F16)
+    h[:, :64] = 0.3 * torch.randn(M, 64, device="cuda", generator=g).to(F16)
+    w = torch.empty(V, K, device="cuda", dtype=F16)
+    for i in range(0, V, 32768):
+        w[i:i + 32768] = 0.5 + torch.rand(32768, K, device="cuda", generator=g).to(F16)
+    t = torch.randint(0, V, (M,), device="cuda", generator=g)
+    _, _, lse = gbce.linear_ce_fwd(h, w, t, reduction="sum")
+    dh, _ = gbce.linear_ce_bwd(h, w, t, lse, None, reduction="sum", want_weight=False)
+    rows = torch.arange(0, M, 64, device="cuda")
+    x = h[rows, :64].double() @ w[:, :64].double().T
+    p = torch.softmax(x, 1)
+    sums = torch.zeros(len(rows), K, device="cuda", dtype=torch.float64)
+    for i in range(0, V, 32768):
+        sums += p[:, i:i + 32768] @ w[i:i + 32768].double()
+    target = w[t[rows]].double()
+    off = (dh[rows].double() - (sums - target)) / (sums + target)
+    assert abs(float(off.mean())) <= 2.0 ** -13
+    assert float(off.abs().max()) <= 1024 * 2.0 ** -23 + 2 * U[F16]
+
+
+def test_weight_gradient_of_many_rows():
+    # the same for the weights of classes that are no target: 262144 rows, 76 tiles; at most 16384 rows are
+    # added on the tensor cores
+    M, K, V = 262144, 4864, 1024
+    g = torch.Generator("cuda").manual_seed(2)
+    h = 0.5 + torch.rand(M, K, device="cuda", generator=g).to(F16)
+    h[:, :64] = torch.randn(M, 64, device="cuda", generator=g).to(F16)
+    w = torch.zeros(V, K, device="cuda", dtype=F16)
+    w[:, :64] = 0.125 * torch.randn(V, 64, device="cuda", generator=g).to(F16)
+    t = torch.zeros(M, device="cuda", dtype=torch.int64)
+    _, _, lse = gbce.linear_ce_fwd(h, w, t, reduction="sum")
+    _, dw = gbce.linear_ce_bwd(h, w, t, lse, None, reduction="sum", want_hidden=False)
+    p = torch.softmax(h[:, :64].double() @ w[:, :64].double().T, 1)
+    some = slice(100, 164)
+    want = p[:, some].T @ h[:, 4000:4512].double()
+    off = (dw[some, 4000:4512].double() - want) / want
+    assert abs(float(off.mean())) <= 2.0 ** -13
+    assert float(off.abs().max()) <= 1024 * 2.0 ** -23 + 2 * U[F16] + 2.0 ** -18
