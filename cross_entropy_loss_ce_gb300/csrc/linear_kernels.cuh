@@ -1115,7 +1115,7 @@ __device__ __forceinline__ Listed prep_rows(const PrepArgs &a, bool write, int *
                 ++rows;
                 if (own) {
                     const float g = fabsf(__ldg(a.grad_scale + i));
-                    top = g > top ? g : top;  // a NaN factor leaves the scale alone
+                    top = g > top && g < INFINITY ? g : top;  // NaN and infinity stay in their rows
                 }
             } else {
                 bad = true;
@@ -1150,7 +1150,7 @@ __device__ __forceinline__ Listed prep_rows(const PrepArgs &a, bool write, int *
     // 16-bit products with (p - onehot) stay in range whatever the loss scale
     if (BWD) {
         int e = 0;
-        if (top > 0.f && top < INFINITY)
+        if (top > 0.f)
             frexpf(top, &e);
         e = min(max(e, -100), 127);
         list.inv = ldexpf(a.head, -e);

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import cross_entropy_loss_ce_gb300 as gbce
-from head_ref import U, make_head, near
+from head_ref import HeadRef, U, make_head, near
 
 pytestmark = pytest.mark.gpu
 BF, F16 = torch.bfloat16, torch.float16
@@ -212,3 +212,16 @@ def test_weight_gradient_of_many_rows():
     off = (dw[some, 4000:4512].double() - want) / want
     assert abs(float(off.mean())) <= 2.0 ** -13
     assert float(off.abs().max()) <= 1024 * 2.0 ** -23 + 2 * U[F16] + 2.0 ** -18
+
+
+@pytest.mark.parametrize("dtype", [BF, F16])
+def test_an_infinite_factor_stays_in_its_row(dtype):
+    h, w, t = make_head(70, 64, 300, dtype)
+    g = torch.full((70,), 100.0, device="cuda")
+    g[7], g[9] = float("inf"), float("nan")
+    ref = HeadRef(h, w, t, reduction="none", grad=torch.where(torch.isfinite(g), g, 1.0))
+    _, _, lse = gbce.linear_ce_fwd(h, w, t, reduction="none")
+    dh, _ = gbce.linear_ce_bwd(h, w, t, lse, g, reduction="none")
+    ok = torch.isfinite(g)
+    near(dh[ok], ref.d_hidden[ok], ref.dh_tol[ok], "rows of finite factors")
+    assert not bool(torch.isfinite(dh[~ok]).any())
