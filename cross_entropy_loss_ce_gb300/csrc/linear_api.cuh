@@ -674,7 +674,7 @@ extern "C" int linear_ce_bwd_ex(const void *hidden, int64_t hidden_stride, const
     prep.rs = r.rs;
     prep.alpha = r.alpha;
     prep.arrived = r.arrived;
-    prep.head = dtype == GBCE_F16 ? 16384.f : 1.f;
+    prep.head = dtype == GBCE_F16 ? 16384.f : 2.f;
     return map_error(scratch.release(launch_linear_bwd(call, s, r, hidden, hidden_stride, weight,
                                                        weight_stride, row_loss, M > 0 ? d_hidden : nullptr,
                                                        d_hidden_stride, d_weight, d_weight_stride, prep)));

@@ -1076,7 +1076,8 @@ struct PrepArgs {
     const float *lse_in, *grad_scale;
     float *l2, *rs, *alpha;
     unsigned *arrived;  // counters of split tiles
-    float head;      // power of two that keeps 16-bit G in range (fp16: 2^14)
+    float head;      // power of two that keeps 16-bit G in range (fp16: 2^14; bf16: 2, so that a factor's
+                     // inverse scale is a normal number up to the end of fp32)
 };
 
 // What a CTA knows of the listed rows after prep_rows.

@@ -225,3 +225,15 @@ def test_an_infinite_factor_stays_in_its_row(dtype):
     ok = torch.isfinite(g)
     near(dh[ok], ref.d_hidden[ok], ref.dh_tol[ok], "rows of finite factors")
     assert not bool(torch.isfinite(dh[~ok]).any())
+
+
+def test_factors_at_the_top_of_fp32():
+    # 1.2e38 lies between 2^126 and 2^127
+    h, w, t = make_head(70, 64, 300, BF, spread=0.1)
+    g = torch.full((70,), 1.2e38, device="cuda")
+    w.mul_(0.25)
+    ref = HeadRef(h, w, t, reduction="none", grad=g)
+    _, _, lse = gbce.linear_ce_fwd(h, w, t, reduction="none")
+    dh, dw = gbce.linear_ce_bwd(h, w, t, lse, g, reduction="none")
+    near(dh, ref.d_hidden, ref.dh_tol, "d_hidden")
+    near(dw, ref.d_weight, ref.dw_tol, "d_weight")
