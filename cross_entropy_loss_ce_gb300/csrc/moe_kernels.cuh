@@ -28,6 +28,7 @@ constexpr int kMoeThreads = 256;
 constexpr int kMoeMaxExperts = 1024;
 constexpr int kMoeMaxSlots = 64;
 constexpr int kMoeMaxCtas = 2048;
+constexpr float kMoeFar = 1048576.f;  // logits from here on are taken about their row's maximum first
 
 // Zeroed before a moe_count_kernel of several CTAs.
 struct MoeTotals {
@@ -314,6 +315,15 @@ __global__ void __launch_bounds__(NT) moe_rows_kernel(const MoeArgs a)
         for (int i = 1; i < NJ * VEC; ++i)
             m = fmaxf(m, x[i]);
         m = group_max<LPT>(m);
+        // about the maximum itself where its shift's rounding, 2^-24 of it in log2 units,
+        // might outgrow exp2's range, or the shift fp32's (rows of a type's lowest value)
+        const float far = fabsf(m) > kMoeFar && fabsf(m) < INFINITY ? m : 0.f;
+        if (far != 0.f) {
+#pragma unroll
+            for (int i = 0; i < NJ * VEC; ++i)
+                x[i] -= far;
+            m = 0.f;
+        }
         const float s = m == -INFINITY ? 0.f : shift_of(m);
         float d = 0.f, q = 0.f;
 #pragma unroll
@@ -325,7 +335,7 @@ __global__ void __launch_bounds__(NT) moe_rows_kernel(const MoeArgs a)
         d = group_sum<LPT>(d);
         q = group_sum<LPT>(q);
         const float inv = 1.f / d, dot = q * inv;
-        const float lse = fmaf(s, kLn2, logf(d));
+        const float lse = far + fmaf(s, kLn2, logf(d));
         if (live && sub == 0) {
             const float v = fmaf(ka, fmean + dot, a.z * lse * lse);
             const float sum = part + v;
