@@ -289,6 +289,7 @@ __global__ void __launch_bounds__(NT) moe_rows_kernel(const MoeArgs a)
     const float ka = a.balance * static_cast<float>(a.E) / static_cast<float>(a.k) * per_n;  // a E / (k n)
     const float gscale = a.grad ? (a.grad_scale ? __ldg(a.grad_scale) : 1.f) * per_n : 0.f;
     const float ga = ka * gscale, gz = 2.f * a.z * gscale;
+    const float la = ka * per_n, lz = a.z * per_n;  // of the loss: terms over n stay in range as long as their sum
 
     float part = 0.f, carry = 0.f;
     bool counted = t < a.T && mask[t];
@@ -337,7 +338,7 @@ __global__ void __launch_bounds__(NT) moe_rows_kernel(const MoeArgs a)
         const float inv = 1.f / d, dot = q * inv;
         const float lse = far + fmaf(s, kLn2, logf(d));
         if (live && sub == 0) {
-            const float v = fmaf(ka, fmean + dot, a.z * lse * lse);
+            const float v = fmaf(la, fmean + dot, lz * lse * lse);
             const float sum = part + v;
             carry += fabsf(part) >= fabsf(v) ? (part - sum) + v : (v - sum) + part;
             part = sum;
@@ -361,7 +362,8 @@ __global__ void __launch_bounds__(NT) moe_rows_kernel(const MoeArgs a)
     if (!a.loss)
         return;
 
-    double total = static_cast<double>(part) + static_cast<double>(carry);
+    // an infinite sum has no rounding errors to carry (inf - inf)
+    double total = static_cast<double>(part) + (fabsf(part) < INFINITY ? static_cast<double>(carry) : 0.0);
     const auto add_up = [&]() {  // over the CTA, in thread 0
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1)
@@ -393,7 +395,7 @@ __global__ void __launch_bounds__(NT) moe_rows_kernel(const MoeArgs a)
         add_up();
     }
     if (threadIdx.x == 0)
-        *a.loss = bad ? __int_as_float(0x7fc00000) : static_cast<float>(total / n);
+        *a.loss = bad || n == 0 ? __int_as_float(0x7fc00000) : static_cast<float>(total);
 }
 
 }  // namespace gbce

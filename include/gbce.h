@@ -527,8 +527,10 @@ GBCE_API int linear_greedy(const void *hidden, int64_t hidden_stride, const void
  *                 1 <= k <= 64.
  *
  * A slot outside [-1, E) raises GBCE_ERR_BAD_TARGET: its token does not count,
- * and the loss is NaN.  Arithmetic is fp32 with fp64 sums over tokens; results
- * do not depend on the order of execution.
+ * and the loss is NaN.  Arithmetic is fp32; each thread adds its tokens' losses
+ * with their rounding errors carried, and the threads' sums are added in fp64, in
+ * an order that T, E and the device fix: results do not depend on the order of
+ * execution.
  */
 GBCE_API int moe_balance(const void *logits, int64_t logits_stride, const int64_t *experts,
                          int64_t experts_stride, int64_t *counts, float *loss, void *grad,

@@ -40,3 +40,20 @@ def test_logits_of_any_size(T, size):
     assert torch.equal(counts, ref.counts)
     near(loss, ref.loss, ref.loss_tol, "loss")
     near(grad, ref.grad, ref.grad_tol, "grad")
+
+
+@pytest.mark.parametrize("T", [40, 600])
+def test_a_row_loss_past_the_range_of_fp32(T):
+    # a logit of 1e22: z_coef lse^2 is 1e41, past fp32, and over 40 tokens the loss is too: infinite, not NaN.
+    # Over 600 it is 1.7e38, which fp32 holds.  Every gradient is finite.
+    x = torch.randn(T, 8, device="cuda", generator=torch.Generator("cuda").manual_seed(T))
+    ex = x.topk(2, 1).indices.contiguous()
+    x[T // 2, 3] = 1e22
+    ref = MoeRef(x, ex, 0.01, 0.001)
+    loss, counts, grad = gbce.moe_balance(x, ex, 0.01, 0.001)
+    if T == 40:
+        assert float(ref.loss.float()) == float("inf") and float(loss) == float("inf")
+    else:
+        near(loss, ref.loss, ref.loss_tol, "loss")
+    assert torch.equal(counts, ref.counts)
+    near(grad, ref.grad, ref.grad_tol, "grad")
