@@ -570,15 +570,26 @@ def _row_values(t, M, name):
 
 
 def _apart(name, out, *inputs):
-    """Raises ValueError when the matrix ``out`` shares memory with an input."""
+    """Raises ValueError when the matrix ``out`` shares memory with an input.  (Columns of one
+    buffer share none: rows of one stride, side by side.)"""
     def span(t):
         last = sum((n - 1) * s for n, s in zip(t.shape, t.stride())) if t.numel() else -1
         return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
     lo, hi = span(out)
     for other, t in inputs:
+        if t is None:
+            continue
         a, b = span(t)
-        if lo < b and a < hi:
-            raise ValueError(f"{name} shares memory with {other}")
+        if not (lo < b and a < hi):
+            continue
+        if out.dim() == t.dim() == 2 and out.shape[0] > 1 and t.shape[0] > 1:
+            step = out.stride(0) * out.element_size()
+            beside = (a - lo) % step if step else 0
+            if step == t.stride(0) * t.element_size() and \
+                    beside >= out.shape[1] * out.element_size() and \
+                    beside + t.shape[1] * t.element_size() <= step:
+                continue
+        raise ValueError(f"{name} shares memory with {other}")
 
 
 def _ptr(t):
@@ -652,7 +663,9 @@ def linear_ce_bwd(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Ten
         elif out.shape != like.shape or out.dtype != like.dtype:
             raise ValueError(f"{name} must have the shape and dtype of {name[2:]}")
         else:
-            _apart(name, out, ("hidden", hidden), ("weight", weight))
+            _apart(name, out, ("hidden", hidden), ("weight", weight), ("targets", targets),
+                   ("lse", lse), ("row_loss", row_loss),
+                   ("grad_scale", grad_scale if torch.is_tensor(grad_scale) else None))
         outs.append(out)
     d_hidden, d_weight = outs
     if d_hidden is not None and d_weight is not None:
@@ -771,7 +784,7 @@ def moe_balance(logits: torch.Tensor, experts: torch.Tensor, balance_coef: float
     + z_coef * mean_t logsumexp(logits_t)^2 over the n tokens with a slot in use;
     counts is [E] int64; grad is d(loss)/d(logits) times grad_scale (a number or a
     one-element float32 CUDA tensor), written to ``grad`` when given (which may be
-    ``logits``).  loss and grad are None when not wanted.
+    ``logits`` itself, and shares no memory with the operands otherwise).  loss and grad are None when not wanted.
     """
     lp, ls, T, E = _rows(logits, "logits")
     if experts.dtype != torch.int64 or experts.dim() != 2 or experts.shape[0] != T or \
@@ -792,6 +805,10 @@ def moe_balance(logits: torch.Tensor, experts: torch.Tensor, balance_coef: float
         raise ValueError("grad must match the logits' shape and dtype")
     else:
         gp, gstride = _rows(grad, "grad")[:2]
+        if gp != lp or (gstride != ls and T > 1):  # a row is read while others are written
+            _apart("grad", grad, ("logits", logits))
+        _apart("grad", grad, ("experts", experts),
+               ("grad_scale", grad_scale if torch.is_tensor(grad_scale) else None))
     gs = None if grad_scale is None else _device_floats(grad_scale, 1, dev, "grad_scale", stream)
     loss = _empty((), torch.float32, dev, stream) if want_loss else None
     counts = _empty((E,), torch.int64, dev, stream)

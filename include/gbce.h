@@ -521,8 +521,9 @@ GBCE_API int linear_greedy(const void *hidden, int64_t hidden_stride, const void
  *                 log-sum-exp (NaN when n == 0).
  *   grad          [T, grad_stride] of dtype or NULL: dL/dlogits times *grad_scale
  *                 (1 when that is NULL), zeros for tokens that do not count.  f is
- *                 a constant.  May be logits itself (same stride).  At least one
- *                 of loss and grad is given.
+ *                 a constant.  May be logits itself (same stride); other overlaps
+ *                 with the operands are not allowed.  At least one of loss and grad
+ *                 is given.
  *   T, E, k       tokens, experts and slots: T <= 2^27 - 1, 1 <= E <= 1024,
  *                 1 <= k <= 64.
  *
