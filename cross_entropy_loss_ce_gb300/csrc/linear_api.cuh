@@ -450,7 +450,7 @@ cudaError_t launch_linear_bwd(const Call &call, const HeadShape &s, const HeadSc
     g.src = hidden;
     g.ss = hs;
     g.dst = r.h;
-    g.w = weight;
+    g.w = row_loss ? nullptr : weight;
     g.ws = ws;
     g.gy = r.gy;
     g.row_loss = row_loss;

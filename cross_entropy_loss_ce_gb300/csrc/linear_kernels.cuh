@@ -1306,6 +1306,8 @@ __device__ __forceinline__ void gather_rows(const GatherArgs &a, int64_t n, int6
             continue;
         }
         const T *s = static_cast<const T *>(a.src) + row_of(i) * a.ss;
+        // on its way while the row is copied
+        const float known = a.row_loss ? __ldg(a.row_loss + row_of(i)) : a.gy ? lse_of(i) : 0.f;
         const int off = static_cast<int>(reinterpret_cast<uintptr_t>(s) & 15);
         const uint4 *s0 = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(s) - off);
         int64_t done = 0;
@@ -1327,17 +1329,16 @@ __device__ __forceinline__ void gather_rows(const GatherArgs &a, int64_t n, int6
                 v[i] = 8 * j + i < a.K ? s[8 * j + i] : zero_value;
             reinterpret_cast<uint4 *>(d)[j] = *reinterpret_cast<const uint4 *>(v);
         }
-        if (a.row_loss) {
-            if (lane == 0)
-                a.gy[i] = entry_of(i, -__ldg(a.row_loss + row_of(i)));
-        } else if (a.w) {
+        if (a.w) {
             const float x = row_dot<T, 32>(s, static_cast<const T *>(a.w) + target_of(i) * a.ws, a.K, a.wvec);
             if (lane == 0) {
                 if (a.xy)
                     a.xy[i] = x;
                 else
-                    a.gy[i] = entry_of(i, x - lse_of(i));
+                    a.gy[i] = entry_of(i, x - known);
             }
+        } else if (a.row_loss && lane == 0) {
+            a.gy[i] = entry_of(i, -known);
         }
     }
     if (a.zero)
