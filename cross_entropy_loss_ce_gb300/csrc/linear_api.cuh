@@ -104,7 +104,8 @@ struct HeadShape {
     int64_t pieces;
     int64_t slices;     // slices of split tiles, at most, of either gradient
     int grad_run, sum_run;  // backward: k-steps that tensor memory adds up at a time
-    int64_t run_pairs;  // backward: CTA pairs with tiles of several runs
+    bool grad_runs, sum_runs;  // ... of a longer axis, with sums of earlier runs for run_pairs pairs
+    int64_t run_pairs;
 };
 
 enum class HeadOp { Fwd, Bwd, Greedy };
@@ -189,14 +190,14 @@ cudaError_t launch_kernel(const Call &call, bool early, void (*fn)(Args...), int
     return cudaLaunchKernelEx(&cfg, fn, static_cast<Args>(args)...);
 }
 
-template <Epi E>
+template <Epi E, bool RUNS = false>
 cudaError_t launch_pair(const Call &call, PairArgs a, const PairArgs &w, int64_t max_tiles,
                         bool early = true)
 {
     a.drop_copy = g_drop_copy.load(std::memory_order_relaxed);
     using Fn = void (*)(const PairArgs, const PairArgs);
-    const Fn fn = call.dtype == GBCE_BF16 ? static_cast<Fn>(pair_gemm_kernel<E, __nv_bfloat16>)
-                                          : static_cast<Fn>(pair_gemm_kernel<E, __half>);
+    const Fn fn = call.dtype == GBCE_BF16 ? static_cast<Fn>(pair_gemm_kernel<E, RUNS, __nv_bfloat16>)
+                                          : static_cast<Fn>(pair_gemm_kernel<E, RUNS, __half>);
     const cudaError_t e = configure_smem(reinterpret_cast<const void *>(fn), call.device, kPairSmem);
     if (e != cudaSuccess)
         return e;
@@ -309,8 +310,9 @@ HeadShape head_shape(const Call &call, const void *hidden, int64_t hs, const voi
         const int scale = call.dtype == GBCE_BF16 ? kBf16Runs : 1;
         s.grad_run = kGradRun * scale;
         s.sum_run = kSumRun * scale;
-        if (K > s.grad_run * int64_t{kPairK} || rows > s.sum_run * int64_t{kPairK})
-            s.run_pairs = call.sms / 2;
+        s.grad_runs = K > s.grad_run * int64_t{kPairK};
+        s.sum_runs = rows > s.sum_run * int64_t{kPairK};
+        s.run_pairs = s.grad_runs || s.sum_runs ? call.sms / 2 : 0;
     }
     return s;
 }
@@ -511,7 +513,9 @@ cudaError_t launch_linear_bwd(const Call &call, const HeadShape &s, const HeadSc
         grad.b_row0 = dh.b_row0 = static_cast<int>(v0);
         grad.V = vn;
         grad.tiles_n = tiles_v;
-        if ((e = launch_pair<Epi::Grad>(call, grad, grad, s.mp / kPairM * tiles_v)) != cudaSuccess)
+        const int64_t tiles = s.mp / kPairM * tiles_v;
+        if ((e = s.grad_runs ? launch_pair<Epi::Grad, true>(call, grad, grad, tiles)
+                             : launch_pair<Epi::Grad>(call, grad, grad, tiles)) != cudaSuccess)
             return e;
         if (d_weight) {
             dw.out = static_cast<unsigned short *>(d_weight) + v0 * dws;
@@ -521,7 +525,8 @@ cudaError_t launch_linear_bwd(const Call &call, const HeadShape &s, const HeadSc
         dh.kblocks = tiles_v * (kPairN / kPairK);  // G holds zeros up to whole tiles
         dh.first = p == 0;
         dh.last = p == s.pieces - 1;
-        if ((e = launch_pair<Epi::Both>(call, dh, dw, 0)) != cudaSuccess)
+        if ((e = s.sum_runs ? launch_pair<Epi::Both, true>(call, dh, dw, 0)
+                            : launch_pair<Epi::Both>(call, dh, dw, 0)) != cudaSuccess)
             return e;
     }
     return cudaSuccess;

@@ -73,8 +73,8 @@ struct PairArgs {
     int tiles_m;        // dW: tiles of the piece's classes; else from n
     int tiles_n;
     int kblocks;        // 64-wide steps along K; dW: from n
-    int run;            // Grad, Both: k-steps summed in tensor memory at a time
-    float *runs;        // ... sums of earlier runs, kPairM x kPairN for each pair (NULL: no tile has two)
+    int run;            // RUNS: k-steps summed in tensor memory at a time
+    float *runs;        // ... sums of earlier runs, kPairM x kPairN for each pair
     int b_row0;         // Grad, dH: the piece's first row of W
     unsigned *fail;
     int drop_copy;      // failure-path tests: the k-step whose A block CTA 0 leaves out, else -1
@@ -380,7 +380,9 @@ __device__ __forceinline__ void finish_block(const PairArgs &a, float (&f)[32], 
                 turn, [&](int r) { return WEIGHT ? row0 + r : int64_t{a.idx[row0 + r]}; });
 }
 
-template <Epi E, typename T>
+// RUNS: axes longer than a.run (the others' tiles are one run each; the loop over runs
+// in their kernel too cost 2% of the backward of 1 row of 128256 x 2048 and of 256 of 32000)
+template <Epi E, bool RUNS, typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     pair_gemm_kernel(const __grid_constant__ PairArgs a, const __grid_constant__ PairArgs w)
 {
@@ -509,7 +511,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             each_unit([&](const Unit &un, int, int, bool dw) {
                 const uint32_t idesc = BOTH && dw ? kIdescW : kIdesc;
                 const uint32_t lbo_a = BOTH && dw ? 8192 : 16, step_a = BOTH && dw ? 128 : 2;
-                const int run = CHUNKED ? kChunk : (BOTH && dw ? w : a).run;  // k-steps that stay in tensor memory
+                const int run = CHUNKED ? kChunk : RUNS ? a.run : max(un.k1 - un.k0, 1);  // k-steps that stay in tensor memory
                 for (int kb0 = un.k0; kb0 < un.k1 || kb0 == 0; kb0 += run, ++it) {
                     const int acc = it & 1;
                     if (!bar_wait<true>(tempty + 8 * acc, ((it >> 1) & 1) ^ 1, dead))
@@ -627,10 +629,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         rs = a.rs[row];
                         gy = a.gy[row];
                     }
-                const int part = static_cast<int>(rank) * 8 + warp - 4;
+                [[maybe_unused]] const int part = static_cast<int>(rank) * 8 + warp - 4;
                 // all runs but the last one are added up where this thread alone reads them
-                bool more = false;
-                for (int k1 = un.k0 + p.run; k1 < un.k1; k1 += p.run) {
+                [[maybe_unused]] bool more = false;
+                for (int k1 = un.k0 + a.run; RUNS && k1 < un.k1; k1 += a.run) {
                     const int acc = it & 1;
                     if (!bar_wait<true>(tfull + 8 * acc, (it >> 1) & 1, dead))
                         return false;
@@ -646,8 +648,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         for (int i = 0; i < 32; ++i)
                             f[i] = __uint_as_float(r[i]);
                         if (more)
-                            add_block(f, block_at(p.runs, pair, part, c));
-                        put_block(block_at(p.runs, pair, part, c), f);
+                            add_block(f, block_at(a.runs, pair, part, c));
+                        put_block(block_at(a.runs, pair, part, c), f);
                     }
                     tc_fence_before();
                     __syncwarp();
@@ -686,8 +688,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
                         f[i] = __uint_as_float(r[i]);
-                    if (more)
-                        add_block(f, block_at(p.runs, pair, part, c));
+                    if (RUNS && more)
+                        add_block(f, block_at(a.runs, pair, part, c));
                     if constexpr (E == Epi::Grad) {
                         if (col + 32 <= inside) {
 #pragma unroll
