@@ -423,11 +423,15 @@ GBCE_API int gbce_pool_reserved(int device, uint64_t *bytes);
  *   dtype         GBCE_BF16 or GBCE_F16 (GBCE_F32 is refused: GBCE_ERR_DTYPE).
  *   reduction     a gbce_reduction.
  *
- * Products of 16-bit values are summed in fp32 on the tensor cores; everything
- * after them is fp32.  Ignored rows take no part in the products, so a batch
- * costs what its counted rows cost.  A target outside [0, V) that is not
+ * Products of 16-bit values are summed in fp32 on the tensor cores, which cut each
+ * addition toward zero, 1024 of K at a time; everything after them is fp32, and the
+ * target's logit is formed by fp32 arithmetic alone.  Ignored rows take no part in
+ * the products of more than 64 rows, so such a batch costs what its counted rows
+ * cost; up to 64 rows, whose time is the reading of the weights, all are multiplied
+ * (unless they have to be copied for alignment).  A target outside [0, V) that is not
  * ignore_index raises GBCE_ERR_BAD_TARGET: its row loss and lse are NaN.
- * NaN or infinite logits make their row's loss NaN.
+ * NaN or infinite logits make their row's loss NaN; finite ones past about 10^9
+ * in size may make it infinite or NaN.
  *
  * Scratch comes from the library's pool on `stream` (gbce_pool_reserved) and stays in
  * the pool: the counted rows' hidden states, 8 bytes per row and 128 classes,
@@ -455,8 +459,12 @@ GBCE_API int linear_ce_fwd(const void *hidden, int64_t hidden_stride, const void
  *
  * G is formed a piece of the vocabulary at a time and rounded once to dtype.  Of
  * k_r it holds a factor of the row's own (none), relative to a power of two at or
- * above the largest, so fp16 keeps small ones; a factor of all rows (mean, sum) is
- * applied to the sums.  Both products are summed in fp32 and rounded once.  Both
+ * above the largest finite one, so fp16 keeps small ones; a factor of all rows (mean,
+ * sum) is applied to the sums.  Where a gradient entry hangs on one or two entries
+ * of G (a weight row of a rare target, a hidden row that is sure of a wrong class),
+ * G's rounding adds to the result's own: up to two half steps in all.  Both products
+ * are summed in fp32 (on the tensor cores as above: 16384 rows or classes at a time
+ * in fp16, 131072 in bf16; the logits 2048 and 16384 of K) and rounded once.  Both
  * gradients are written, not added to.  Scratch: the counted rows' hidden states, up to
  * 512 MB of G (more only when M exceeds 2^20 rows), M x K floats when the
  * vocabulary takes several pieces, up to 168 MB of partial sums (20 MB more when
