@@ -1159,7 +1159,8 @@ __device__ __forceinline__ Listed prep_rows(const PrepArgs &a, bool write, int *
         list.inv = ldexpf(a.head, -e);
         if (write && threadIdx.x == 0)
             *a.alpha = (a.reduction == kReduceMean ? 1.f / static_cast<float>(max(n_all, 1)) : 1.f) *
-                       (a.grad_scale && !own ? __ldg(a.grad_scale) : 1.f) * ldexpf(1.f / a.head, e);
+                       // no row: zeros, which a factor of NaN must not touch
+                       (a.grad_scale && !own && list.rows ? __ldg(a.grad_scale) : 1.f) * ldexpf(1.f / a.head, e);
         if (write)
             for (int i = threadIdx.x; i < kSplitCounters; i += NT)
                 a.arrived[i] = 0u;

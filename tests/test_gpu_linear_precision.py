@@ -237,3 +237,15 @@ def test_factors_at_the_top_of_fp32():
     dh, dw = gbce.linear_ce_bwd(h, w, t, lse, g, reduction="none")
     near(dh, ref.d_hidden, ref.dh_tol, "d_hidden")
     near(dw, ref.d_weight, ref.dw_tol, "d_weight")
+
+
+@pytest.mark.parametrize("M", [5, 300])
+@pytest.mark.parametrize("factor", [float("nan"), float("inf")])
+def test_no_counted_row_leaves_zeros_whatever_the_factor(M, factor):
+    # the mean of no row is NaN, and so may be what comes back
+    h, w, t = make_head(M, 64, 300, BF)
+    t.fill_(-100)
+    for reduction in ("mean", "sum", "none"):
+        _, row, lse = gbce.linear_ce_fwd(h, w, t, reduction=reduction)
+        dh, dw = gbce.linear_ce_bwd(h, w, t, lse, factor, reduction=reduction, row_loss=row)
+        assert not bool(dh.any()) and not bool(dw.any())
