@@ -573,11 +573,11 @@ def _apart(name, out, *inputs):
     """Raises ValueError when the matrix ``out`` shares memory with an input.  (Columns of one
     buffer share none: rows of one stride, side by side.)"""
     def span(t):
-        last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+        last = sum((n - 1) * s for n, s in zip(t.shape, t.stride())) if t.numel() else -1
         return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
     lo, hi = span(out)
     for other, t in inputs:
-        if t is None or not (t.numel() and out.numel()):
+        if t is None:
             continue
         a, b = span(t)
         if not (lo < b and a < hi):

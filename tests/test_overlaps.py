@@ -49,11 +49,6 @@ def test_columns_of_one_buffer_and_other_types():
     gbce._apart("grad", wide, ("experts", None))
 
 
-def test_tensors_without_elements_share_nothing():
-    _, wide = views()
-    assert not refused(wide, wide[5:5]) and not refused(wide[5:5], wide) and not refused(wide, wide[5, 3:3])
-
-
 gpu = pytest.mark.gpu
 
 
