@@ -1,5 +1,6 @@
 """Fused hard-label cross-entropy and row softmax on GB300 (sm_103a), the
-cross-entropy of hidden states through an output layer, and a router's balance loss.
+cross-entropy of hidden states through an output layer, a router's balance loss, its
+tokens sorted by expert and back, and the norm of all gradients.
 
 Thin ctypes binding of ``_lib/libgbce.so`` (C ABI in ``include/gbce.h``): it
 checks tensor shapes, takes raw device pointers, row strides and the current
@@ -22,9 +23,10 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "lib
 GBCE_F32, GBCE_BF16, GBCE_F16 = 0, 1, 2
 DTYPES = {torch.float32: GBCE_F32, torch.bfloat16: GBCE_BF16, torch.float16: GBCE_F16}
 REDUCTIONS = {"mean": 0, "sum": 1, "none": 2}
+NORMS = {2.0: 0, 1.0: 1, float("inf"): 2}
 
 OK, ERR_NULL, ERR_SIZE, ERR_DTYPE, ERR_ALIGN, ERR_CUDA, ERR_BAD_TARGET, ERR_TIMEOUT, \
-    ERR_NO_DEVICE, ERR_REDUCTION, ERR_BAD_TABLE = range(11)
+    ERR_NO_DEVICE, ERR_REDUCTION, ERR_BAD_TABLE, ERR_OVERLAP = range(12)
 # bits a call ORs into its own status word (gbce_status_bit)
 STATUS_TIMEOUT, STATUS_BAD_TABLE = 1, 2
 
@@ -75,10 +77,20 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.linear_greedy.argtypes = [p, i64, p, i64, p, p, i64, i64, i64, ci, p]
         lib.moe_balance.argtypes = [p, i64, p, i64, p, p, p, i64, p, i64, i64, i64, ctypes.c_float,
                                     ctypes.c_float, ci, p]
+        lib.moe_plan_rows.argtypes = [i64, i64, i64, i64]
+        lib.moe_plan_rows.restype = i64
+        lib.moe_sort.argtypes = [p, i64, p, p, p, p, i64, i64, i64, i64, p]
+        lib.moe_dispatch.argtypes = [p, i64, p, p, p, i64, i64, i64, i64, i64, ci, p]
+        lib.moe_combine.argtypes = [p, i64, p, p, i64, ci, p, i64, i64, i64, i64, i64, ci, p]
+        lib.moe_combine_bwd.argtypes = [p, i64, p, i64, p, p, p, i64, ci, p, i64, p, i64, i64, i64, i64,
+                                        i64, ci, p]
+        lib.grad_norm.argtypes = [p, p, p, i64, ci, p, p]
+        lib.clip_grad_norm.argtypes = [p, p, p, p, i64, ci, ctypes.c_double, ctypes.c_double, p, p]
         for f in ("ce_fwd_bwd", "softmax_fwd", "softmax_bwd", "gbce_last_error",
                   "gbce_timing_enable", "gbce_timing_read", "ce_fwd_bwd_ex", "scale_rows",
                   "softmax_bwd_bsr", "linear_ce_fwd", "linear_ce_bwd", "linear_ce_bwd_ex",
-                  "linear_greedy", "moe_balance"):
+                  "linear_greedy", "moe_balance", "moe_sort", "moe_dispatch", "moe_combine",
+                  "moe_combine_bwd", "grad_norm", "clip_grad_norm"):
             getattr(lib, f).restype = ci
         _lib = lib
     return _lib
@@ -853,3 +865,330 @@ def moe_balance_loss(logits: torch.Tensor, experts: torch.Tensor, balance_coef: 
                          f"{tuple(experts.shape[:-1])}")
     return MoeBalance.apply(logits.reshape(-1, logits.shape[-1]),
                             experts.reshape(-1, experts.shape[-1]).contiguous(), balance_coef, z_coef)
+
+
+# ---------------------------------------------------------------------------
+# a router's tokens sorted by expert and back
+
+
+class MoePlan:
+    """Where a router's tokens go: ``position`` [T, k], ``source`` [R], ``offsets`` [E + 1] and
+    ``counts`` [E], all int32 on one device, as moe_sort makes them (expert e's rows are
+    offsets[e] .. offsets[e] + counts[e], offsets[e + 1] being a multiple of ``align``)."""
+    __slots__ = ("_position", "_source", "_offsets", "_counts", "_buffer", "_places", "tokens",
+                 "slots", "rows", "experts", "align", "device")
+
+    def __init__(self, position, source, offsets, counts, align: int = 1):
+        for name, t, dim in (("position", position, 2), ("source", source, 1), ("offsets", offsets, 1),
+                             ("counts", counts, 1)):
+            if t.dtype != torch.int32 or t.dim() != dim or not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous int32, {dim}-D")
+        if offsets.shape[0] != counts.shape[0] + 1:
+            raise ValueError("offsets must hold one value more than counts")
+        self._position, self._source, self._offsets, self._counts = position, source, offsets, counts
+        self._buffer = None
+        self._places = position.data_ptr(), source.data_ptr()
+        self.tokens, self.slots = position.shape
+        self.rows, self.experts, self.align = source.shape[0], counts.shape[0], align
+        self.device = _call_device(("position", position), ("source", source), ("offsets", offsets),
+                                   ("counts", counts))
+
+    @classmethod
+    def _packed(cls, T, k, rows, E, align, device, stream):
+        """A plan whose four parts are one buffer, each from a 16-byte boundary; a part is made
+        a tensor when it is asked for."""
+        self = cls.__new__(cls)
+        source = (T * k + 3) // 4 * 4
+        offsets = source + (rows + 3) // 4 * 4
+        counts = offsets + (E + 4) // 4 * 4
+        self._buffer = _empty((counts + E,), torch.int32, device, stream)
+        self._position = self._source = self._offsets = self._counts = None
+        p = self._buffer.data_ptr()
+        self._places = p, p + 4 * source, p + 4 * offsets, p + 4 * counts
+        self.tokens, self.slots, self.rows, self.experts = T, k, rows, E
+        self.align, self.device = align, self._buffer.device
+        return self
+
+    def _part(self, i, *shape):
+        return self._buffer.as_strided(shape, (shape[1], 1) if len(shape) == 2 else (1,),
+                                       (self._places[i] - self._places[0]) // 4)
+
+    @property
+    def position(self):
+        if self._position is None:
+            self._position = self._part(0, self.tokens, self.slots)
+        return self._position
+
+    @property
+    def source(self):
+        if self._source is None:
+            self._source = self._part(1, self.rows)
+        return self._source
+
+    @property
+    def offsets(self):
+        if self._offsets is None:
+            self._offsets = self._part(2, self.experts + 1)
+        return self._offsets
+
+    @property
+    def counts(self):
+        if self._counts is None:
+            self._counts = self._part(3, self.experts)
+        return self._counts
+
+
+def moe_sort(experts: torch.Tensor, n_experts: int, align: int = 1, stream=None) -> MoePlan:
+    """The plan by which tokens go to ``experts`` [T, k] (int64, -1 for an empty slot) of
+    ``n_experts``, each expert's rows padded to a multiple of ``align``: slots sorted by expert,
+    an expert's in their order."""
+    if experts.dtype != torch.int64 or experts.dim() != 2 or experts.shape[1] < 1:
+        raise ValueError("experts must be int64 of shape [T, k]")
+    T, k = experts.shape
+    es, unit = experts.stride()
+    if (k > 1 and unit != 1) or (T > 1 and es < k):
+        raise ValueError("experts needs unit column stride and rows that do not overlap")
+    dev = _call_device(("experts", experts))
+    lib = load_library()
+    rows = lib.moe_plan_rows(T, n_experts, k, align)
+    if rows < 0:
+        raise GbceError(ERR_SIZE, "moe_sort")
+    plan = MoePlan._packed(T, k, rows, n_experts, align, dev, stream)
+    with _OnDevice(dev):
+        rc = lib.moe_sort(experts.data_ptr(), max(es, k), *plan._places, T, n_experts, k, align,
+                          _stream_handle(stream, dev))
+    _check(rc, "moe_sort")
+    return plan
+
+
+def _plan_matrix(t, rows, plan, name):
+    """Pointer and row stride of a matrix with `rows` rows on the plan's device."""
+    p, step, n, _ = _rows(t, name)
+    if n != rows:
+        raise ValueError(f"{name} has {n} rows, the plan asks for {rows}")
+    if t.device != plan.device:
+        raise ValueError(f"{name} is on {t.device}, the plan on {plan.device}")
+    return p, step
+
+
+def _plan_output(out, name, rows, H, like, plan, stream, *inputs):
+    """(out, pointer, row stride): allocated when None, else checked against the inputs."""
+    if out is None:
+        out = _empty((rows, H), like.dtype, plan.device, stream)
+        return out, out.data_ptr(), H
+    p, step = _plan_matrix(out, rows, plan, name)
+    if out.shape[1] != H or out.dtype != like.dtype:
+        raise ValueError(f"{name} must be {like.dtype} of {H} columns")
+    _apart(name, out, *inputs, ("position", plan.position), ("source", plan.source))
+    return out, p, step
+
+
+def _plan_weights(w, plan, like, name):
+    """(pointer, row stride, dtype) of a [T, k] matrix of float32 or of the rows' type."""
+    if w.dtype != torch.float32 and w.dtype != like.dtype:
+        raise TypeError(f"{name} must be float32 or {like.dtype}, not {w.dtype}")
+    p, step = _plan_matrix(w, plan.tokens, plan, name)
+    if w.shape[1] != plan.slots:
+        raise ValueError(f"{name} must have {plan.slots} columns, one for each slot")
+    return p, step, DTYPES[w.dtype]
+
+
+def moe_dispatch(x: torch.Tensor, plan: MoePlan, out: torch.Tensor = None, stream=None) -> torch.Tensor:
+    """Rows of ``x`` [T, H] in the plan's order, [R, H]: row position[t, j] is x[t]; rows that
+    are no slot's are zeros.  (Its gradient is moe_combine without weights.)"""
+    xp, xs = _plan_matrix(x, plan.tokens, plan, "x")
+    H = x.shape[1]
+    out, op, os_ = _plan_output(out, "out", plan.rows, H, x, plan, stream, ("x", x))
+    with _OnDevice(plan.device):
+        rc = load_library().moe_dispatch(xp, xs, plan._places[0], plan._places[1], op, os_, plan.tokens, H,
+                                         plan.slots, plan.rows, DTYPES[x.dtype],
+                                         _stream_handle(stream, plan.device))
+    _check(rc, "moe_dispatch")
+    return out
+
+
+def moe_combine(y: torch.Tensor, plan: MoePlan, weights: torch.Tensor = None, out: torch.Tensor = None,
+                stream=None) -> torch.Tensor:
+    """Rows of ``y`` [R, H] back by token, [T, H]: row t is the sum over t's slots of
+    weights[t, j] * y[position[t, j]] (weights [T, k] in float32 or y's type; None: 1)."""
+    yp, ys = _plan_matrix(y, plan.rows, plan, "y")
+    H = y.shape[1]
+    wp, ws, wt = (None, 0, 0) if weights is None else _plan_weights(weights, plan, y, "weights")
+    out, op, os_ = _plan_output(out, "out", plan.tokens, H, y, plan, stream, ("y", y), ("weights", weights))
+    with _OnDevice(plan.device):
+        rc = load_library().moe_combine(yp, ys, plan._places[0], wp, ws, wt, op, os_, plan.tokens, H,
+                                        plan.slots, plan.rows, DTYPES[y.dtype],
+                                        _stream_handle(stream, plan.device))
+    _check(rc, "moe_combine")
+    return out
+
+
+def moe_combine_bwd(d_out: torch.Tensor, y: torch.Tensor, plan: MoePlan, weights: torch.Tensor,
+                    want_y: bool = True, want_weights: bool = True, d_y: torch.Tensor = None,
+                    d_weights: torch.Tensor = None, stream=None):
+    """(d_y, d_weights) of moe_combine with weights, for the incoming ``d_out`` [T, H]; rows of
+    d_y that are no slot's are zeros, and so are the gradients of empty slots' weights.  A
+    gradient that is not wanted is None."""
+    dp, ds = _plan_matrix(d_out, plan.tokens, plan, "d_out")
+    yp, ys = _plan_matrix(y, plan.rows, plan, "y")
+    H = y.shape[1]
+    if d_out.shape[1] != H or d_out.dtype != y.dtype:
+        raise ValueError(f"d_out must be {y.dtype} of {H} columns, as y")
+    wp, ws, wt = _plan_weights(weights, plan, y, "weights")
+    inputs = ("d_out", d_out), ("y", y), ("weights", weights)
+    dyp, dys, dwp, dws = None, 0, None, 0
+    if want_y:
+        d_y, dyp, dys = _plan_output(d_y, "d_y", plan.rows, H, y, plan, stream, *inputs)
+    else:
+        d_y = None
+    if want_weights:
+        d_weights, dwp, dws = _plan_output(d_weights, "d_weights", plan.tokens, plan.slots, weights, plan,
+                                           stream, *inputs, ("d_y", d_y))
+    else:
+        d_weights = None
+    if d_y is None and d_weights is None:
+        return None, None
+    with _OnDevice(plan.device):
+        rc = load_library().moe_combine_bwd(dp, ds, yp, ys, plan._places[0], plan._places[1], wp, ws, wt, dyp,
+                                            dys, dwp, dws, plan.tokens, H, plan.slots, plan.rows,
+                                            DTYPES[y.dtype], _stream_handle(stream, plan.device))
+    _check(rc, "moe_combine_bwd")
+    return d_y, d_weights
+
+
+class DispatchTokens(torch.autograd.Function):
+    """Autograd form of moe_dispatch."""
+
+    @staticmethod
+    def forward(ctx, x, plan):
+        ctx.plan = plan
+        return moe_dispatch(_unit_rows(x.detach()), plan)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_output):
+        return moe_combine(_unit_rows(grad_output.detach()), ctx.plan), None
+
+
+class CombineTokens(torch.autograd.Function):
+    """Autograd form of moe_combine; saves the rows and the weights, so backward may run more
+    than once."""
+
+    @staticmethod
+    def forward(ctx, y, plan, weights=None):
+        y = _unit_rows(y.detach())
+        w = None if weights is None else _unit_rows(weights.detach())
+        ctx.plan = plan
+        ctx.save_for_backward(*(() if w is None else (y, w)))
+        return moe_combine(y, plan, w)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_output):
+        g = _unit_rows(grad_output.detach())
+        if not ctx.saved_tensors:
+            return moe_dispatch(g, ctx.plan), None, None
+        y, w = ctx.saved_tensors
+        dy, dw = moe_combine_bwd(g, y, ctx.plan, w, want_y=ctx.needs_input_grad[0],
+                                 want_weights=ctx.needs_input_grad[2])
+        return dy, None, dw
+
+
+def dispatch_tokens(x: torch.Tensor, plan: MoePlan) -> torch.Tensor:
+    """moe_dispatch of ``x`` [..., H], differentiable (the leading sizes hold the plan's tokens)."""
+    return DispatchTokens.apply(x.reshape(-1, x.shape[-1]), plan)
+
+
+def combine_tokens(y: torch.Tensor, plan: MoePlan, weights: torch.Tensor = None) -> torch.Tensor:
+    """moe_combine of ``y`` [R, H] with ``weights`` [T, k] or None, differentiable in both:
+    [T, H].  (Captured into a CUDA graph with its backward: as for linear_cross_entropy.)"""
+    return CombineTokens.apply(y, plan, weights)
+
+
+# ---------------------------------------------------------------------------
+# the norm of all gradients
+
+
+def _dense(t):
+    """Do the tensor's values fill one stretch of memory, in whatever order of its axes?"""
+    if t.is_contiguous():
+        return True
+    step = 1
+    for size, stride in sorted(zip(t.shape, t.stride()), key=lambda p: p[1]):
+        if size != 1 and stride != step:
+            return False
+        step *= size
+    return True
+
+
+def _tensor_list(tensors, name):
+    """(tensors that are not None, device, pointers, sizes, types) of a call on many tensors."""
+    if torch.is_tensor(tensors):
+        tensors = [tensors]
+    tensors = [t for t in tensors if t is not None]
+    pointers, sizes, types, dev = [], [], [], None
+    for t in tensors:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be CUDA tensors")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"{name} are on {dev} and {t.device}")
+        kind = DTYPES.get(t.dtype)
+        if kind is None:
+            raise TypeError(f"{name} must be float32, bfloat16 or float16, not {t.dtype}")
+        if not _dense(t):
+            raise ValueError(f"{name} must each fill one stretch of memory, not strides {t.stride()} "
+                             f"of shape {tuple(t.shape)}")
+        pointers.append(t.data_ptr())
+        sizes.append(t.numel())
+        types.append(kind)
+    return tensors, dev, pointers, sizes, types
+
+
+def _norm_call(where, tensors, norm_type, norm, stream, max_norm=None, eps=0.0, outs=None):
+    kind = NORMS.get(float(norm_type))
+    if kind is None:
+        raise ValueError(f"norm_type must be 1, 2 or inf, not {norm_type}")
+    given = [t is not None for t in tensors] if outs is not None and not torch.is_tensor(tensors) else None
+    tensors, dev, pointers, sizes, types = _tensor_list(tensors, "tensors")
+    if norm is None:
+        norm = _empty((), torch.float32, dev if dev is not None else "cuda", stream)
+    elif norm.dtype != torch.float32 or norm.numel() != 1:
+        raise ValueError("norm must be a one-element float32 CUDA tensor")
+    dev = _call_device(("norm", norm), ("tensors", tensors[0] if tensors else None))
+    n = len(tensors)
+    args = [(ctypes.c_void_p * n)(*pointers), (ctypes.c_int64 * n)(*sizes), (ctypes.c_int * n)(*types), n, kind]
+    if max_norm is not None:
+        if outs is None:
+            args.insert(1, args[0])
+        else:
+            outs = [outs] if torch.is_tensor(outs) else list(outs)
+            if given is not None and len(outs) == len(given):
+                outs = [o for o, there in zip(outs, given) if there]
+            if len(outs) != n:
+                raise ValueError(f"{len(outs)} outs for {n} tensors")
+            for o, t in zip(outs, tensors):
+                if o.shape != t.shape or o.dtype != t.dtype or o.device != dev or o.stride() != t.stride():
+                    raise ValueError("outs must match the tensors in shape, strides, dtype and device")
+            args.insert(1, (ctypes.c_void_p * n)(*[o.data_ptr() for o in outs]))
+        args += [float(max_norm), float(eps)]
+    with _OnDevice(dev):
+        rc = getattr(load_library(), where)(*args, norm.data_ptr(), _stream_handle(stream, dev))
+    _check(rc, where)
+    return norm
+
+
+def grad_norm(tensors, norm_type: float = 2.0, norm: torch.Tensor = None, stream=None) -> torch.Tensor:
+    """The norm (1, 2 or inf) of all ``tensors`` (float32, bfloat16 and float16 in any mixture;
+    None entries are passed over) taken as one vector: a 0-dim float32 CUDA tensor.  Each tensor
+    fills one stretch of memory, in whatever order of its axes; nothing is synchronised."""
+    return _norm_call("grad_norm", tensors, norm_type, norm, stream)
+
+
+def clip_grad_norm(tensors, max_norm: float, norm_type: float = 2.0, eps: float = 1e-6, outs=None,
+                   norm: torch.Tensor = None, stream=None) -> torch.Tensor:
+    """Scales ``tensors`` by min(1, max_norm / (norm + eps)), in place or into ``outs`` (one for
+    each tensor, of the same shape, strides and type), and returns the norm they had, as
+    grad_norm does.  Where the norm keeps the limit, tensors in place are not written."""
+    return _norm_call("clip_grad_norm", tensors, norm_type, norm, stream, max_norm, eps, outs)

@@ -1045,8 +1045,9 @@ extern "C" const char *gbce_status_string(int status)
     case GBCE_ERR_BAD_TARGET: return "a target is outside [0, V) and is not ignore_index";
     case GBCE_ERR_TIMEOUT: return "a bounded wait for an asynchronous copy gave up";
     case GBCE_ERR_NO_DEVICE: return "no usable CUDA device";
-    case GBCE_ERR_REDUCTION: return "reduction is not a gbce_reduction";
+    case GBCE_ERR_REDUCTION: return "reduction is not a gbce_reduction, or kind not a gbce_norm";
     case GBCE_ERR_BAD_TABLE: return "a block-sparse look-up table entry is malformed";
+    case GBCE_ERR_OVERLAP: return "an output shares memory with another tensor of the call";
     default: return "unknown status";
     }
 }
@@ -1329,3 +1330,5 @@ extern "C" int ce_fwd_bwd_host(const void *logits_host, int64_t host_stride,
 
 #include "linear_api.cuh"
 #include "moe_api.cuh"
+#include "permute_api.cuh"
+#include "norm_api.cuh"

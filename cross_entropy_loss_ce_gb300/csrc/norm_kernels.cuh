@@ -1,0 +1,355 @@
+// The norm of many tensors taken as one vector, and the tensors scaled so that
+// it keeps a limit:
+//   n = (sum g^2)^(1/2), sum |g| or max |g|
+//   out = f g,  f = min(1, max_norm / (n + eps))
+//
+// The factor needs every value before the first result, so the clipped form
+// reads twice and writes once; tensors that fit in L2 come from HBM once.  The
+// tensors are cut into tiles of 32 KB and a grid of the device's size takes
+// them in turn, whatever tensor they are of: many small tensors cost what one
+// of their size costs.  The table of tensors travels in the kernel's
+// parameters, so a call copies nothing to the device and can be captured.
+//
+// Sums: a thread adds the values of a tile that it holds (32 or 64) in fp32,
+// and the tiles' sums in fp32 with the rounding errors carried (two words); the
+// threads' sums are added in fp64 in an order that the sizes and the device
+// fix.  A tile's sum below 2^-92 may have lost terms to fp32's range (64 squares
+// below 2^-126), one above 2^100 nearly so: it is taken again from values times
+// a power of two.  (fp32 numbers below 2^-126 count as 0.)
+#pragma once
+
+#include "row_kernels.cuh"
+
+namespace gbce {
+
+constexpr int kNormThreads = 256;
+constexpr int kNormCtasPerSm = 4;
+constexpr int kNormVecs = 8;                             // 16-byte vectors of a tile that a thread holds
+constexpr int64_t kNormTileVecs = kNormThreads * kNormVecs;
+constexpr int kNormSmallTable = 64, kNormTable = 1024;   // tensors of a launch
+constexpr float kNormLow = 0x1p-92f, kNormHigh = 0x1p100f;
+constexpr float kNormUp = 0x1p64f, kNormDown = 0x1p-70f;
+
+enum NormKind { kNormTwo = 0, kNormOne = 1, kNormMax = 2 };
+
+template <int N>
+struct NormTable {
+    const char *in[N];
+    char *out[N];
+    int64_t values[N];
+    int first[N + 1];      // tiles before each tensor's; first[tensors]: all
+    unsigned char type[N];
+    int tensors;
+};
+
+template <typename T>
+struct NormGeom {
+    int head;       // values before the first 16-byte boundary
+    int64_t vecs, tail_start, values;
+};
+
+template <typename T>
+__host__ __device__ __forceinline__ NormGeom<T> norm_geom(const void *p, int64_t values)
+{
+    constexpr int V = 16 / sizeof(T);
+    NormGeom<T> g;
+    const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u);
+    g.head = mis ? (16 - mis) / static_cast<int>(sizeof(T)) : 0;
+    if (g.head > values)
+        g.head = static_cast<int>(values);
+    g.vecs = (values - g.head) / V;
+    g.tail_start = g.head + g.vecs * V;
+    g.values = values;
+    return g;
+}
+
+// The tensor that a tile is of: the last one whose first tile is not behind it.
+template <int N>
+__device__ __forceinline__ int norm_tensor(const NormTable<N> &a, int tile)
+{
+    int lo = 0, hi = a.tensors;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (a.first[mid] <= tile)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+// What a thread has seen: a compensated sum and the sums out of its range, or
+// the largest magnitude's bits (a NaN's are above all others).
+struct NormSum {
+    float sum = 0.f, carry = 0.f;
+    double more = 0.0;
+    unsigned top = 0;
+};
+
+template <int KIND>
+__device__ __forceinline__ void norm_value(float x, float &s, unsigned &top)
+{
+    if constexpr (KIND == kNormTwo)
+        s = fmaf(x, x, s);
+    else if constexpr (KIND == kNormOne)
+        s += fabsf(x);
+    else
+        top = max(top, __float_as_uint(x) & 0x7fffffffu);
+}
+
+// Adds one tile's sum, or tells that it is out of range.
+template <int KIND>
+__device__ __forceinline__ bool norm_add(NormSum &a, float s)
+{
+    if constexpr (KIND == kNormMax)
+        return true;
+    if (!(s < kNormHigh) || (KIND == kNormTwo && s < kNormLow))
+        return false;
+    const float t = a.sum + s;
+    a.carry += a.sum >= s ? (a.sum - t) + s : (s - t) + a.sum;
+    a.sum = t;
+    return true;
+}
+
+template <int KIND, typename T>
+__device__ __forceinline__ void norm_tile(const void *p, int64_t values, int64_t tile, NormSum &sum)
+{
+    using E = Elem<T>;
+    constexpr int V = E::kPerVec;
+    const NormGeom<T> g = norm_geom<T>(p, values);
+    const T *x = static_cast<const T *>(p);
+    const uint4 *v = reinterpret_cast<const uint4 *>(x + g.head);
+    const uint4 *mine = v + tile * kNormTileVecs + threadIdx.x;
+    const int64_t left = g.vecs - tile * kNormTileVecs - static_cast<int>(threadIdx.x);  // of this thread's on
+    const int here = static_cast<int>(left < kNormTileVecs ? left : kNormTileVecs);
+    const auto load = [&](int i) {
+        return i * kNormThreads < here ? __ldg(mine + i * kNormThreads) : make_uint4(0, 0, 0, 0);
+    };
+    uint4 raw[kNormVecs];
+#pragma unroll
+    for (int i = 0; i < kNormVecs; ++i)
+        raw[i] = load(i);
+    float s = 0.f, edge = 0.f;
+    if (tile == 0) {  // up to 14 values before and behind the vectors
+        const int tail = static_cast<int>(g.values - g.tail_start);
+        const int i = static_cast<int>(threadIdx.x);
+        if (i < g.head)
+            edge = E::load(x + i);
+        else if (i - g.head < tail)
+            edge = E::load(x + g.tail_start + (i - g.head));
+        norm_value<KIND>(edge, s, sum.top);
+    }
+#pragma unroll
+    for (int i = 0; i < kNormVecs; ++i) {
+        float f[V];
+        E::unpack(raw[i], f);
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            norm_value<KIND>(f[e], s, sum.top);
+    }
+    if (!norm_add<KIND>(sum, s)) {
+        unsigned any = __float_as_uint(edge);
+#pragma unroll
+        for (int i = 0; i < kNormVecs; ++i)
+            any |= raw[i].x | raw[i].y | raw[i].z | raw[i].w;
+        if (any) {  // not the zeros of rows that no token used
+            const float by = s < kNormLow ? kNormUp : kNormDown;
+            s = 0.f;
+            norm_value<KIND>(edge * by, s, sum.top);
+#pragma unroll 1
+            for (int i = 0; i < kNormVecs; ++i) {
+                float f[V];
+                E::unpack(load(i), f);
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    norm_value<KIND>(f[e] * by, s, sum.top);
+            }
+            const double back = 1.0 / static_cast<double>(by);
+            sum.more += static_cast<double>(s) * (KIND == kNormTwo ? back * back : back);
+        }
+    }
+}
+
+// Sum (or maximum, a NaN above all) over the CTA, in thread 0.
+template <int KIND>
+__device__ __forceinline__ double norm_reduce(double v)
+{
+    __shared__ double part[kNormThreads / 32];
+    const auto join = [](double a, double b) {
+        return KIND == kNormMax ? (a >= b || a != a ? a : b) : a + b;
+    };
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+        v = join(v, __shfl_xor_sync(0xffffffffu, v, off));
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0)
+        part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = part[0];
+    for (int w = 1; w < kNormThreads / 32; ++w)
+        v = join(v, part[w]);
+    return v;
+}
+
+// One number a CTA: its tiles' sum or maximum.
+template <int KIND, int N>
+__global__ void __launch_bounds__(kNormThreads, kNormCtasPerSm) norm_parts_kernel(const __grid_constant__ NormTable<N> a, double *part)
+{
+    wait_prerequisite_grid();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    NormSum sum;
+    const int tiles = a.first[a.tensors];
+    for (int tile = blockIdx.x; tile < tiles; tile += static_cast<int>(gridDim.x)) {
+        const int i = norm_tensor(a, tile);
+        const int64_t at = tile - a.first[i];
+        switch (a.type[i]) {
+        case 0: norm_tile<KIND, float>(a.in[i], a.values[i], at, sum); break;
+        case 1: norm_tile<KIND, __nv_bfloat16>(a.in[i], a.values[i], at, sum); break;
+        default: norm_tile<KIND, __half>(a.in[i], a.values[i], at, sum);
+        }
+    }
+    double v = KIND == kNormMax ? static_cast<double>(__uint_as_float(sum.top))
+                                : static_cast<double>(sum.sum) + static_cast<double>(sum.carry) + sum.more;
+    v = norm_reduce<KIND>(v);
+    if (threadIdx.x == 0)
+        part[blockIdx.x] = v;
+}
+
+// The norm from the CTAs' numbers, the same in every thread.
+template <int KIND>
+__device__ __forceinline__ double norm_total(const double *part, int parts)
+{
+    double v = 0.0;
+    for (int i = threadIdx.x; i < parts; i += kNormThreads) {
+        const double p = __ldcg(part + i);
+        v = KIND == kNormMax ? (v >= p || v != v ? v : p) : v + p;
+    }
+    v = norm_reduce<KIND>(v);
+    return KIND == kNormTwo ? sqrt(v) : v;
+}
+
+template <int KIND>
+__global__ void __launch_bounds__(kNormThreads) norm_finish_kernel(const double *part, int parts, float *norm)
+{
+    wait_prerequisite_grid();
+    const double n = norm_total<KIND>(part, parts);
+    if (threadIdx.x == 0)
+        *norm = static_cast<float>(n);
+}
+
+// f as two fp32 factors, the second a power of two: 1, or 2^-100 where f is
+// below fp32's normal numbers.
+struct NormFactor {
+    float f, power;
+    bool copy;
+};
+
+// n values of memory that starts at another place within 16 bytes than its
+// result: one value at a time, kNormValues of a thread in flight.
+constexpr int kNormValues = 16;
+
+template <typename T>
+__device__ __noinline__ void scale_apart(const T *x, T *y, int n, const NormFactor by)
+{
+    using E = Elem<T>;
+#pragma unroll 1
+    for (int i0 = threadIdx.x; i0 < n; i0 += kNormValues * kNormThreads) {
+        T raw[kNormValues];
+#pragma unroll
+        for (int i = 0; i < kNormValues; ++i)
+            if (i0 + i * kNormThreads < n)
+                raw[i] = x[i0 + i * kNormThreads];
+#pragma unroll
+        for (int i = 0; i < kNormValues; ++i) {
+            if (i0 + i * kNormThreads >= n)
+                continue;
+            if (by.copy)
+                y[i0 + i * kNormThreads] = raw[i];
+            else
+                E::store(y + i0 + i * kNormThreads, E::load(&raw[i]) * by.f * by.power);
+        }
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void scale_tile(const void *p, void *q, int64_t values, int64_t tile, const NormFactor &by)
+{
+    using E = Elem<T>;
+    constexpr int V = E::kPerVec;
+    const NormGeom<T> g = norm_geom<T>(p, values);
+    const T *x = static_cast<const T *>(p);
+    T *y = static_cast<T *>(q);
+    const auto one = [&](int64_t i) {
+        if (by.copy)
+            y[i] = x[i];
+        else
+            E::store(y + i, E::load(x + i) * by.f * by.power);
+    };
+    if (tile == 0) {
+        const int tail = static_cast<int>(g.values - g.tail_start);
+        const int i = static_cast<int>(threadIdx.x);
+        if (i < g.head)
+            one(i);
+        else if (i - g.head < tail)
+            one(g.tail_start + (i - g.head));
+    }
+    if (((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(q)) & 15u) == 0) {
+        const int64_t at = tile * kNormTileVecs + threadIdx.x;
+        const uint4 *v = reinterpret_cast<const uint4 *>(x + g.head) + at;
+        uint4 *o = reinterpret_cast<uint4 *>(y + g.head) + at;
+        const int here = static_cast<int>(g.vecs - at < kNormTileVecs ? g.vecs - at : kNormTileVecs);
+        uint4 raw[kNormVecs];
+#pragma unroll
+        for (int i = 0; i < kNormVecs; ++i)
+            if (i * kNormThreads < here)
+                raw[i] = __ldcs(v + i * kNormThreads);
+#pragma unroll
+        for (int i = 0; i < kNormVecs; ++i) {
+            if (i * kNormThreads >= here)
+                continue;
+            if (!by.copy) {
+                float w[V];
+                E::unpack(raw[i], w);
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    w[e] = w[e] * by.f * by.power;
+                raw[i] = E::pack(w);
+            }
+            __stcs(o + i * kNormThreads, raw[i]);
+        }
+        return;
+    }
+    const int64_t at = g.head + tile * kNormTileVecs * V;
+    scale_apart(x + at, y + at, static_cast<int>(g.tail_start - at < kNormTileVecs * V ? g.tail_start - at : kNormTileVecs * V), by);
+}
+
+// The tiles in the opposite order: those that the norm read last are still in L2.
+template <int KIND, int N>
+__global__ void __launch_bounds__(kNormThreads, kNormCtasPerSm) norm_scale_kernel(const __grid_constant__ NormTable<N> a, const double *part,
+                                                                  int parts, float *norm, double max_norm, double eps,
+                                                                  bool in_place)
+{
+    wait_prerequisite_grid();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const double n = norm_total<KIND>(part, parts);
+    if (norm && blockIdx.x == 0 && threadIdx.x == 0)
+        *norm = static_cast<float>(n);
+    double f = max_norm / (n + eps);
+    f = f >= 1.0 ? 1.0 : f;  // a NaN stays one
+    if (in_place && f == 1.0)
+        return;
+    const bool low = f > 0.0 && f < 0x1p-126;
+    const NormFactor by{static_cast<float>(low ? f * 0x1p100 : f), low ? 0x1p-100f : 1.f, f == 1.0};
+    const int tiles = a.first[a.tensors];
+    for (int tile = tiles - 1 - static_cast<int>(blockIdx.x); tile >= 0; tile -= static_cast<int>(gridDim.x)) {
+        const int i = norm_tensor(a, tile);
+        const int64_t at = tile - a.first[i];
+        switch (a.type[i]) {
+        case 0: scale_tile<float>(a.in[i], a.out[i], a.values[i], at, by); break;
+        case 1: scale_tile<__nv_bfloat16>(a.in[i], a.out[i], a.values[i], at, by); break;
+        default: scale_tile<__half>(a.in[i], a.out[i], a.values[i], at, by);
+        }
+    }
+}
+
+}  // namespace gbce

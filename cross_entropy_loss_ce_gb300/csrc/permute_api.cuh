@@ -1,0 +1,331 @@
+// Host side of moe_sort, moe_dispatch, moe_combine and moe_combine_bwd:
+// argument checks, launch shapes and the launches of permute_kernels.cuh.
+// Part of gbce.cu.
+#pragma once
+
+#include "permute_kernels.cuh"
+
+namespace gbce {
+namespace {
+
+constexpr int64_t kSortRound = 1024 * kSortItems;   // slots that one CTA ranks at once
+constexpr int64_t kSortMaxPerCta = int64_t{1} << kSortRankBits;
+constexpr int kMaxAlign = 1024;
+constexpr int64_t kPermuteMaxCols = int64_t{1} << 24;
+constexpr int64_t kPermuteWarpsPerSm = 16;  // fewer warps than that: a lane takes one unit, not several
+
+// Rows of a plan, or -1 where they pass 2^31 - 1.
+int64_t plan_rows(int64_t T, int64_t E, int64_t k, int64_t align)
+{
+    const int64_t slots = T * k;
+    const int64_t rows = round_up(slots + (E < slots ? E : slots) * (align - 1), align);
+    return rows > INT32_MAX ? -1 : rows;
+}
+
+int check_plan(int64_t T, int64_t E, int64_t k, int64_t align)
+{
+    if (T < 0 || T > kMaxRows || E < 1 || E > kSortMaxExperts || k < 1 || k > kMoeMaxSlots || align < 1 ||
+        align > kMaxAlign || T * k > INT32_MAX || plan_rows(T, E, k, align) < 0)
+        return GBCE_ERR_SIZE;
+    return GBCE_OK;
+}
+
+int sort_rank_smem(int E, int threads, bool all)
+{
+    return (all ? 2 * E + 1 : E) * 4 + sort_hist_stride(E) * 2 * (threads / 32 + 1);
+}
+
+cudaError_t launch_sort(const Call &call, SortArgs a)
+{
+    cudaError_t e;
+    if (a.n <= kSortRound) {
+        const int threads = a.n <= 32 * kSortItems ? 32 : (a.n <= 256 * kSortItems ? 256 : 1024);
+        const int smem = sort_rank_smem(a.E, threads, true);
+        a.per_cta = threads * kSortItems;
+        if ((e = configure_smem(reinterpret_cast<const void *>(sort_rank_kernel<true>), call.device,
+                                sort_rank_smem(kSortMaxExperts, 1024, true))) != cudaSuccess)
+            return e;
+        return launch_kernel(call, false, sort_rank_kernel<true>, 1, threads, smem, a);
+    }
+    const int64_t rounds = (a.n + kSortRound - 1) / kSortRound;
+    a.per_cta = (rounds + call.sms - 1) / call.sms * kSortRound;
+    if (a.per_cta > kSortMaxPerCta)
+        a.per_cta = kSortMaxPerCta;
+    const int64_t ctas = (a.n + a.per_cta - 1) / a.per_cta;
+    PoolScratch scratch(call.stream);
+    if ((e = scratch.get(call.device, static_cast<size_t>(ctas) * a.E * sizeof(int))) != cudaSuccess)
+        return e;
+    a.table = static_cast<int *>(scratch.p);
+    e = configure_smem(reinterpret_cast<const void *>(sort_rank_kernel<false>), call.device,
+                       sort_rank_smem(kSortMaxExperts, 1024, false));
+    if (e == cudaSuccess)
+        e = launch_kernel(call, false, sort_rank_kernel<false>, ctas, 1024, sort_rank_smem(a.E, 1024, false), a);
+    if (e == cudaSuccess)
+        e = launch_kernel(call, true, sort_place_kernel, ctas, 1024, (3 * a.E + 1) * 4, a);
+    return scratch.release(e);
+}
+
+int check_permute(int64_t T, int64_t H, int64_t k, int64_t rows, int dtype)
+{
+    const int st = check_common(T, H, dtype);
+    if (st)
+        return st;
+    return H > kPermuteMaxCols || k < 1 || k > kMoeMaxSlots || T * k > INT32_MAX || rows < 0 || rows > INT32_MAX
+               ? GBCE_ERR_SIZE
+               : GBCE_OK;
+}
+
+// Rows of two matrices are made of whole units of `bytes`, and start on them.
+bool in_units(size_t bytes, size_t es, int64_t H, const void *a, int64_t sa, const void *b, int64_t sb)
+{
+    const int64_t v = static_cast<int64_t>(bytes / es);
+    return H % v == 0 && aligned_to(a, bytes) && sa % v == 0 && aligned_to(b, bytes) && sb % v == 0;
+}
+
+unsigned token_ctas(int64_t warps)
+{
+    const int64_t ctas = (warps + kPermuteThreads / 32 - 1) / (kPermuteThreads / 32);
+    return static_cast<unsigned>(ctas < (1 << 30) ? ctas : (1 << 30));
+}
+
+// CTAs that look for rows that are no slot's, 256 of them at a time.
+int64_t zero_ctas(const Call &call, int64_t rows)
+{
+    const int64_t ctas = (rows + kPermuteThreads - 1) / kPermuteThreads;
+    return ctas < 2 * call.sms ? ctas : 2 * call.sms;
+}
+
+template <typename Raw, int U>
+cudaError_t launch_dispatch_as(const Call &call, PermuteArgs a, size_t es)
+{
+    const int64_t v = static_cast<int64_t>(sizeof(Raw) / es);
+    a.units = static_cast<int>(a.H / v);
+    a.segs = (a.units + 32 * U - 1) / (32 * U);
+    a.token_ctas = token_ctas(a.T * a.segs);
+    return launch_kernel(call, false, dispatch_kernel<Raw, U>, a.token_ctas + zero_ctas(call, a.rows),
+                         kPermuteThreads, 0, a, a.is / v, a.os / v);
+}
+
+cudaError_t launch_dispatch(const Call &call, const PermuteArgs &a)
+{
+    const size_t es = elem_size(call.dtype);
+    if (in_units(16, es, a.H, a.in, a.is, a.out, a.os)) {
+        const int64_t warps = a.T * ((a.H * static_cast<int64_t>(es) / 16 + 127) / 128);
+        return warps < kPermuteWarpsPerSm * call.sms ? launch_dispatch_as<uint4, 1>(call, a, es)
+                                                     : launch_dispatch_as<uint4, 4>(call, a, es);
+    }
+    if (in_units(4, es, a.H, a.in, a.is, a.out, a.os))
+        return launch_dispatch_as<unsigned, 8>(call, a, es);
+    return launch_dispatch_as<unsigned short, 8>(call, a, es);
+}
+
+template <typename T>
+cudaError_t launch_combine(const Call &call, PermuteArgs a)
+{
+    constexpr int V = Elem<T>::kPerVec;
+    const auto go = [&](void (*fn)(const PermuteArgs), int vec, int u) {
+        a.units = static_cast<int>(a.H / vec);
+        a.segs = (a.units + 32 * u - 1) / (32 * u);
+        return launch_kernel(call, false, fn, token_ctas(a.T * a.segs), kPermuteThreads, 0, a);
+    };
+    if (!in_units(16, sizeof(T), a.H, a.in, a.is, a.out, a.os))
+        return go(combine_kernel<T, 1, 4>, 1, 4);
+    return a.T * ((a.H / V + 63) / 64) < kPermuteWarpsPerSm * call.sms ? go(combine_kernel<T, V, 1>, V, 1)
+                                                                       : go(combine_kernel<T, V, 2>, V, 2);
+}
+
+template <typename T>
+cudaError_t launch_combine_bwd(const Call &call, PermuteArgs a)
+{
+    constexpr int V = Elem<T>::kPerVec;
+    const void *other = a.d_weights ? a.in : a.d_out;
+    const int64_t other_stride = a.d_weights ? a.is : a.ds;
+    const bool wide = in_units(16, sizeof(T), a.H, a.d_out, a.ds, other, other_stride) &&
+                      (!a.out || in_units(16, sizeof(T), a.H, a.out, a.os, a.out, a.os));
+    a.units = static_cast<int>(wide ? a.H / V : a.H);
+    constexpr int kWarps = kPermuteThreads / 32;
+    a.segs = a.T >= kPermuteWarpsPerSm * call.sms || a.units <= 32 ? 1 : kWarps;
+    a.token_ctas = token_ctas(a.T * a.segs);
+    const int64_t grid = a.token_ctas + (a.out ? zero_ctas(call, a.rows) : 0);
+    void (*fn)(const PermuteArgs) = nullptr;
+    if (wide)
+        fn = a.k <= 4 ? combine_bwd_kernel<T, V, 4> : combine_bwd_kernel<T, V, 8>;
+    else
+        fn = a.k <= 4 ? combine_bwd_kernel<T, 1, 4> : combine_bwd_kernel<T, 1, 8>;
+    return launch_kernel(call, false, fn, grid, kPermuteThreads, 0, a);
+}
+
+int check_weights(const void *w, int64_t stride, int wdtype, int64_t k, int dtype)
+{
+    if (!w)
+        return GBCE_OK;
+    if (wdtype != GBCE_F32 && wdtype != dtype)
+        return GBCE_ERR_DTYPE;
+    if (stride < k || stride > kMaxStride)
+        return GBCE_ERR_SIZE;
+    return aligned_to(w, elem_size(wdtype)) ? GBCE_OK : GBCE_ERR_ALIGN;
+}
+
+}  // namespace
+}  // namespace gbce
+
+extern "C" int64_t moe_plan_rows(int64_t T, int64_t E, int64_t k, int64_t align)
+{
+    return check_plan(T, E, k, align) ? -1 : plan_rows(T, E, k, align);
+}
+
+extern "C" int moe_sort(const int64_t *experts, int64_t experts_stride, int32_t *position, int32_t *source,
+                        int32_t *offsets, int32_t *counts, int64_t T, int64_t E, int64_t k, int64_t align,
+                        gbce_stream_t stream)
+{
+    const int st = check_plan(T, E, k, align);
+    if (st)
+        return st;
+    if (experts_stride < k || experts_stride > kMaxStride)
+        return GBCE_ERR_SIZE;
+    if (!offsets || !counts || (T > 0 && (!experts || !position || !source)))
+        return GBCE_ERR_NULL;
+    if (!aligned_to(experts, 8) || !aligned_to(position, 4) || !aligned_to(source, 4) || !aligned_to(offsets, 4) ||
+        !aligned_to(counts, 4))
+        return GBCE_ERR_ALIGN;
+    Call call;
+    const cudaError_t e = begin_call(&call, GBCE_F32, stream);
+    if (e != cudaSuccess)
+        return map_error(e);
+    SortArgs a{};
+    a.experts = experts;
+    a.es = experts_stride;
+    a.n = T * k;
+    a.E = static_cast<int>(E);
+    a.k = static_cast<int>(k);
+    a.align = static_cast<int>(align);
+    a.rows = static_cast<int>(plan_rows(T, E, k, align));
+    a.position = position;
+    a.source = source;
+    a.offsets = offsets;
+    a.counts = counts;
+    return map_error(launch_sort(call, a));
+}
+
+extern "C" int moe_dispatch(const void *x, int64_t x_stride, const int32_t *position, const int32_t *source,
+                            void *out, int64_t out_stride, int64_t T, int64_t H, int64_t k, int64_t rows,
+                            int dtype, gbce_stream_t stream)
+{
+    int st = check_permute(T, H, k, rows, dtype);
+    if (st)
+        return st;
+    if ((T > 0 && !position) || (rows > 0 && !source))
+        return GBCE_ERR_NULL;
+    if ((st = check_matrix(x, x_stride, T, H, dtype)) || (st = check_matrix(out, out_stride, rows, H, dtype)))
+        return st;
+    if (!aligned_to(position, 4) || !aligned_to(source, 4))
+        return GBCE_ERR_ALIGN;
+    if (rows == 0)
+        return GBCE_OK;
+    Call call;
+    const cudaError_t e = begin_call(&call, dtype, stream);
+    if (e != cudaSuccess)
+        return map_error(e);
+    PermuteArgs a{};
+    a.in = x;
+    a.is = x_stride;
+    a.out = out;
+    a.os = out_stride;
+    a.position = position;
+    a.source = source;
+    a.T = T;
+    a.H = H;
+    a.k = static_cast<int>(k);
+    a.rows = static_cast<int>(rows);
+    return map_error(launch_dispatch(call, a));
+}
+
+extern "C" int moe_combine(const void *y, int64_t y_stride, const int32_t *position, const void *weights,
+                           int64_t weights_stride, int weights_dtype, void *out, int64_t out_stride, int64_t T,
+                           int64_t H, int64_t k, int64_t rows, int dtype, gbce_stream_t stream)
+{
+    int st = check_permute(T, H, k, rows, dtype);
+    if (st || (st = check_weights(weights, weights_stride, weights_dtype, k, dtype)))
+        return st;
+    if (T > 0 && !position)
+        return GBCE_ERR_NULL;
+    if ((st = check_matrix(y, y_stride, rows, H, dtype)) || (st = check_matrix(out, out_stride, T, H, dtype)))
+        return st;
+    if (!aligned_to(position, 4))
+        return GBCE_ERR_ALIGN;
+    if (T == 0)
+        return GBCE_OK;
+    Call call;
+    const cudaError_t e = begin_call(&call, dtype, stream);
+    if (e != cudaSuccess)
+        return map_error(e);
+    PermuteArgs a{};
+    a.in = y;
+    a.is = y_stride;
+    a.out = out;
+    a.os = out_stride;
+    a.position = position;
+    a.weights = weights;
+    a.ws = weights_stride;
+    a.weights_f32 = weights_dtype == GBCE_F32;
+    a.T = T;
+    a.H = H;
+    a.k = static_cast<int>(k);
+    a.rows = static_cast<int>(rows);
+    switch (dtype) {
+    case GBCE_F32: return map_error(launch_combine<float>(call, a));
+    case GBCE_F16: return map_error(launch_combine<__half>(call, a));
+    default: return map_error(launch_combine<__nv_bfloat16>(call, a));
+    }
+}
+
+extern "C" int moe_combine_bwd(const void *d_out, int64_t d_out_stride, const void *y, int64_t y_stride,
+                               const int32_t *position, const int32_t *source, const void *weights,
+                               int64_t weights_stride, int weights_dtype, void *d_y, int64_t d_y_stride,
+                               void *d_weights, int64_t d_weights_stride, int64_t T, int64_t H, int64_t k,
+                               int64_t rows, int dtype, gbce_stream_t stream)
+{
+    int st = check_permute(T, H, k, rows, dtype);
+    if (st || (st = check_weights(weights, weights_stride, weights_dtype, k, dtype)) ||
+        (st = check_weights(d_weights, d_weights_stride, weights_dtype, k, dtype)))
+        return st;
+    if ((T > 0 && (!position || !weights)) || (d_y && rows > 0 && !source) || (!d_y && !d_weights && T > 0 && rows > 0))
+        return GBCE_ERR_NULL;
+    if ((st = check_matrix(d_out, d_out_stride, T, H, dtype)))
+        return st;
+    if (d_weights && (st = check_matrix(y, y_stride, rows, H, dtype)))
+        return st;
+    if (d_y && (st = check_matrix(d_y, d_y_stride, rows, H, dtype)))
+        return st;
+    if (!aligned_to(position, 4) || !aligned_to(source, 4))
+        return GBCE_ERR_ALIGN;
+    if (T == 0 && (!d_y || rows == 0))
+        return GBCE_OK;
+    Call call;
+    const cudaError_t e = begin_call(&call, dtype, stream);
+    if (e != cudaSuccess)
+        return map_error(e);
+    PermuteArgs a{};
+    a.in = y;
+    a.is = y_stride;
+    a.out = rows > 0 ? d_y : nullptr;
+    a.os = d_y_stride;
+    a.d_out = d_out;
+    a.ds = d_out_stride;
+    a.position = position;
+    a.source = source;
+    a.weights = weights;
+    a.ws = weights_stride;
+    a.weights_f32 = weights_dtype == GBCE_F32;
+    a.d_weights = d_weights;
+    a.dws = d_weights_stride;
+    a.T = T;
+    a.H = H;
+    a.k = static_cast<int>(k);
+    a.rows = static_cast<int>(rows);
+    switch (dtype) {
+    case GBCE_F32: return map_error(launch_combine_bwd<float>(call, a));
+    case GBCE_F16: return map_error(launch_combine_bwd<__half>(call, a));
+    default: return map_error(launch_combine_bwd<__nv_bfloat16>(call, a));
+    }
+}

@@ -1,6 +1,7 @@
 /*
  * gbce: fused hard-label cross-entropy and row softmax for NVIDIA GB300 (sm_103a),
- * the cross-entropy of hidden states through an output layer, and a router's balance loss.
+ * the cross-entropy of hidden states through an output layer, a router's balance loss, its
+ * tokens sorted by expert and back, and the norm of all gradients.
  *
  * Plain C ABI.  Every pointer argument of the compute calls is DEVICE memory
  * owned by the caller; the library keeps no reference after a call returns.
@@ -78,8 +79,16 @@ enum gbce_status {
     GBCE_ERR_BAD_TARGET = 6,  /* device flag: a target outside [0, V) that is not ignore_index */
     GBCE_ERR_TIMEOUT = 7,     /* device flag: a bounded wait on an asynchronous copy gave up */
     GBCE_ERR_NO_DEVICE = 8,   /* no usable CUDA device */
-    GBCE_ERR_REDUCTION = 9,   /* reduction is not a gbce_reduction */
-    GBCE_ERR_BAD_TABLE = 10   /* device flag: a block-sparse look-up table entry is malformed */
+    GBCE_ERR_REDUCTION = 9,   /* reduction is not a gbce_reduction, or kind not a gbce_norm */
+    GBCE_ERR_BAD_TABLE = 10,  /* device flag: a block-sparse look-up table entry is malformed */
+    GBCE_ERR_OVERLAP = 11     /* an output shares memory with another tensor (clip_grad_norm) */
+};
+
+/* Norms of grad_norm and clip_grad_norm. */
+enum gbce_norm {
+    GBCE_NORM_TWO = 0, /* (sum g^2)^(1/2) */
+    GBCE_NORM_ONE = 1, /* sum |g| */
+    GBCE_NORM_MAX = 2  /* max |g| */
 };
 
 /*
@@ -398,8 +407,8 @@ GBCE_API const char *gbce_status_string(int status);
  * gbce_pool_reserved -- device memory, in bytes, that the library's scratch
  * pool holds on `device` (reserved from the driver and kept for reuse), or 0
  * in *bytes when no call on that device has needed the pool yet.  The pool
- * serves ce_fwd_bwd, ce_fwd_bwd_ex, ce_fwd_bwd_host, the linear_* calls and
- * moe_balance; ce_fwd_bwd_noalloc
+ * serves ce_fwd_bwd, ce_fwd_bwd_ex, ce_fwd_bwd_host, the linear_* calls,
+ * moe_balance, moe_sort, grad_norm and clip_grad_norm; ce_fwd_bwd_noalloc
  * and the softmax calls never create it.  For diagnostics; no launch, no sync.
  */
 GBCE_API int gbce_pool_reserved(int device, uint64_t *bytes);
@@ -545,6 +554,130 @@ GBCE_API int moe_balance(const void *logits, int64_t logits_stride, const int64_
                          int64_t experts_stride, int64_t *counts, float *loss, void *grad,
                          int64_t grad_stride, const float *grad_scale, int64_t T, int64_t E, int64_t k,
                          float balance_coef, float z_coef, int dtype, gbce_stream_t stream);
+
+/*
+ * moe_plan_rows -- rows R of the plan that moe_sort makes: enough for T k slots
+ * over any of E experts, T k + min(E, T k) (align - 1) rounded up to a multiple of
+ * align.  -1 for sizes that moe_sort refuses.  No device is needed.
+ */
+GBCE_API int64_t moe_plan_rows(int64_t T, int64_t E, int64_t k, int64_t align);
+
+/*
+ * moe_sort -- the slots of a mixture-of-experts router sorted by expert: the plan
+ * by which moe_dispatch takes tokens to their experts and moe_combine back.
+ *
+ *   experts       [T, experts_stride] int64, rows of k slots: the expert of each
+ *                 slot, or -1 for an empty one (padding, a dropped token), as
+ *                 moe_balance takes them.  The same expert may stand twice.
+ *   position      [T, k] int32: the row of each slot t k + j,
+ *                 offsets[e] + the slots before it that hold the same e; -1 for empty slots.
+ *   source        [R] int32, R = moe_plan_rows: the slot of each row, -1 for rows
+ *                 that are no slot's (behind an expert's slots, behind the last expert).
+ *   offsets       [E + 1] int32: where each expert's rows begin, each a multiple of
+ *                 align; offsets[E] is where the last one's end.
+ *   counts        [E] int32: slots of each expert.
+ *   T, E, k       as for moe_balance: T <= 2^27 - 1, 1 <= E <= 1024, 1 <= k <= 64,
+ *                 and T k and R below 2^31.
+ *   align         1 .. 1024: each expert's rows are padded to a multiple of it, for
+ *                 products that go by tiles of rows.
+ *
+ * A slot outside [-1, E) raises GBCE_ERR_BAD_TARGET and counts as empty.  Stable:
+ * an expert's rows keep the order of their slots.
+ */
+GBCE_API int moe_sort(const int64_t *experts, int64_t experts_stride, int32_t *position, int32_t *source,
+                      int32_t *offsets, int32_t *counts, int64_t T, int64_t E, int64_t k, int64_t align,
+                      gbce_stream_t stream);
+
+/*
+ * moe_dispatch -- tokens' rows in the plan's order, out[position[t, j]] = x[t].
+ *
+ *   x             [T, x_stride] of dtype, rows of H values, read only.
+ *   position      [T, k] int32 and
+ *   source        [rows] int32: the plan, read only.  Positions outside [0, rows) are
+ *                 empty slots.
+ *   out           [rows, out_stride] of dtype: bits are copied; rows whose source is
+ *                 negative are zeroed.  Overlaps no input.
+ *   T, H, k, rows sizes: 1 <= H <= 2^24, 1 <= k <= 64, T k and rows below 2^31.
+ *
+ * Its gradient is moe_combine without weights.
+ */
+GBCE_API int moe_dispatch(const void *x, int64_t x_stride, const int32_t *position, const int32_t *source,
+                          void *out, int64_t out_stride, int64_t T, int64_t H, int64_t k, int64_t rows,
+                          int dtype, gbce_stream_t stream);
+
+/*
+ * moe_combine -- rows of the plan's order back by token,
+ *   out[t] = sum_j w[t, j] y[position[t, j]]  over the slots in use.
+ *
+ *   y             [rows, y_stride] of dtype, rows of H values, read only; rows that
+ *                 are no slot's are not read.
+ *   position, T, H, k, rows: as for moe_dispatch.
+ *   weights       [T, weights_stride] of weights_dtype (GBCE_F32, or dtype), rows of k
+ *                 values, or NULL (1; weights_stride and weights_dtype are not looked at).
+ *   out           [T, out_stride] of dtype, zeros for tokens without a slot.
+ *                 Overlaps no input.
+ *
+ * Sums are fp32, j ascending, rounded once.  The weight of an empty slot is not used.
+ */
+GBCE_API int moe_combine(const void *y, int64_t y_stride, const int32_t *position, const void *weights,
+                         int64_t weights_stride, int weights_dtype, void *out, int64_t out_stride, int64_t T,
+                         int64_t H, int64_t k, int64_t rows, int dtype, gbce_stream_t stream);
+
+/*
+ * moe_combine_bwd -- gradients of moe_combine with weights.  (Without, the rows'
+ * gradient is moe_dispatch of d_out.)
+ *
+ *   d_out         [T, d_out_stride] of dtype, read only.
+ *   y, position, source, weights, T, H, k, rows: as for moe_combine and moe_dispatch;
+ *                 weights is given, y is read for d_weights only (else it may be NULL).
+ *   d_y           [rows, d_y_stride] of dtype or NULL: w[t, j] d_out[t] in row
+ *                 position[t, j], zeros in rows whose source is negative.
+ *   d_weights     [T, d_weights_stride] of weights_dtype or NULL: the product of d_out[t]
+ *                 and y[position[t, j]] summed in fp32 in an order that the sizes fix, 0 for
+ *                 empty slots.  At least one of the two; neither overlaps an input.
+ */
+GBCE_API int moe_combine_bwd(const void *d_out, int64_t d_out_stride, const void *y, int64_t y_stride,
+                             const int32_t *position, const int32_t *source, const void *weights,
+                             int64_t weights_stride, int weights_dtype, void *d_y, int64_t d_y_stride,
+                             void *d_weights, int64_t d_weights_stride, int64_t T, int64_t H, int64_t k,
+                             int64_t rows, int dtype, gbce_stream_t stream);
+
+/*
+ * grad_norm -- the norm of n tensors taken as one vector.
+ *
+ *   tensors       n device pointers, values[i] contiguous elements of dtypes[i] each
+ *                 (GBCE_F32, GBCE_BF16 or GBCE_F16, in any mixture; 0 elements are
+ *                 fine).  The three arrays are HOST memory, read before the call returns.
+ *   kind          a gbce_norm.
+ *   norm          one float: 0 for no values, infinite past fp32's range, NaN where a
+ *                 value is NaN.
+ *   n, values     n <= 2^20; values[i] <= 2^46.
+ *
+ * Squares and magnitudes are added in fp32 over 32 to 64 values, scaled by a power of
+ * two where they would leave fp32's range, then with their rounding errors carried, at last
+ * in fp64, in an order that the sizes and the device fix.  Values below 2^-126 count as 0.
+ */
+GBCE_API int grad_norm(const void *const *tensors, const int64_t *values, const int *dtypes, int64_t n, int kind,
+                       float *norm, gbce_stream_t stream);
+
+/*
+ * clip_grad_norm -- n tensors scaled so that their norm keeps a limit:
+ *   outs[i] = f tensors[i],  f = min(1, max_norm / (norm + eps)).
+ *
+ *   tensors, values, dtypes, n, kind, norm: as for grad_norm (norm is that of the
+ *                 tensors as they came).
+ *   outs          n device pointers (the array in HOST memory): tensors[i] itself, or
+ *                 memory that no other tensor shares, of the same type.  Any other
+ *                 sharing is refused: GBCE_ERR_OVERLAP.
+ *   max_norm, eps the limit and what is added to the norm, both >= 0 (else GBCE_ERR_SIZE).
+ *
+ * f is formed in fp64, products in fp32, rounded once.  f = 1 copies the bits, and in
+ * place writes nothing.  An infinite norm makes f 0 (and infinite values NaN), a NaN makes
+ * every result NaN.  Nothing is synchronised.
+ */
+GBCE_API int clip_grad_norm(const void *const *tensors, void *const *outs, const int64_t *values,
+                            const int *dtypes, int64_t n, int kind, double max_norm, double eps, float *norm,
+                            gbce_stream_t stream);
 
 /*
  * gbce_test_failure_path -- a test of the bounded waits (no counterpart on the
