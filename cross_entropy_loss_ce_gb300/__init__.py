@@ -13,6 +13,7 @@ A call with ``stream=`` works as one under ``torch.cuda.stream(stream)``: it rea
 operands, and makes its outputs, on that stream.  Operands from another stream have to
 be ready on it, and kept until it is done; outputs are used elsewhere after it.
 """
+import array
 import ctypes
 import os
 
@@ -895,46 +896,44 @@ class MoePlan:
 
     @classmethod
     def _packed(cls, T, k, rows, E, align, device, stream):
-        """A plan whose four parts are one buffer, each from a 16-byte boundary; a part is made
-        a tensor when it is asked for."""
+        """A plan whose four parts lie in one buffer; tensors are made of them when one is asked for."""
         self = cls.__new__(cls)
-        source = (T * k + 3) // 4 * 4
-        offsets = source + (rows + 3) // 4 * 4
-        counts = offsets + (E + 4) // 4 * 4
-        self._buffer = _empty((counts + E,), torch.int32, device, stream)
-        self._position = self._source = self._offsets = self._counts = None
+        self._buffer = _empty((T * k + rows + 2 * E + 1,), torch.int32, device, stream)
         p = self._buffer.data_ptr()
-        self._places = p, p + 4 * source, p + 4 * offsets, p + 4 * counts
+        self._places = p, p + 4 * T * k, p + 4 * (T * k + rows), p + 4 * (T * k + rows + E + 1)
         self.tokens, self.slots, self.rows, self.experts = T, k, rows, E
         self.align, self.device = align, self._buffer.device
         return self
 
-    def _part(self, i, *shape):
-        return self._buffer.as_strided(shape, (shape[1], 1) if len(shape) == 2 else (1,),
-                                       (self._places[i] - self._places[0]) // 4)
+    def _parts(self):
+        slots, rows, E = self.tokens * self.slots, self.rows, self.experts
+        flat, self._source, self._offsets, self._counts = \
+            self._buffer.split_with_sizes((slots, rows, E + 1, E))
+        self._position = flat.view(self.tokens, self.slots)
+        self._buffer = None
 
     @property
     def position(self):
-        if self._position is None:
-            self._position = self._part(0, self.tokens, self.slots)
+        if self._buffer is not None:
+            self._parts()
         return self._position
 
     @property
     def source(self):
-        if self._source is None:
-            self._source = self._part(1, self.rows)
+        if self._buffer is not None:
+            self._parts()
         return self._source
 
     @property
     def offsets(self):
-        if self._offsets is None:
-            self._offsets = self._part(2, self.experts + 1)
+        if self._buffer is not None:
+            self._parts()
         return self._offsets
 
     @property
     def counts(self):
-        if self._counts is None:
-            self._counts = self._part(3, self.experts)
+        if self._buffer is not None:
+            self._parts()
         return self._counts
 
 
@@ -1122,56 +1121,55 @@ def _dense(t):
 
 
 def _tensor_list(tensors, name):
-    """(tensors that are not None, device, pointers, sizes, types) of a call on many tensors."""
-    if torch.is_tensor(tensors):
-        tensors = [tensors]
-    tensors = [t for t in tensors if t is not None]
-    pointers, sizes, types, dev = [], [], [], None
-    for t in tensors:
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be CUDA tensors")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{name} are on {dev} and {t.device}")
-        kind = DTYPES.get(t.dtype)
-        if kind is None:
-            raise TypeError(f"{name} must be float32, bfloat16 or float16, not {t.dtype}")
-        if not _dense(t):
-            raise ValueError(f"{name} must each fill one stretch of memory, not strides {t.stride()} "
-                             f"of shape {tuple(t.shape)}")
-        pointers.append(t.data_ptr())
-        sizes.append(t.numel())
-        types.append(kind)
-    return tensors, dev, pointers, sizes, types
+    """(device index or None, pointers, sizes, types, whether all are contiguous) of the tensors of
+    a call on many; a list at a time, as a model has hundreds."""
+    devices = set(map(torch.Tensor.get_device, tensors))
+    if -1 in devices:
+        raise ValueError(f"{name} must be CUDA tensors")
+    if len(devices) > 1:
+        raise ValueError(f"{name} are on several devices: {sorted(devices)}")
+    try:
+        types = [DTYPES[t.dtype] for t in tensors]
+    except KeyError as e:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, not {e.args[0]}") from None
+    contiguous = all(map(torch.Tensor.is_contiguous, tensors))
+    if not contiguous:
+        for t in tensors:
+            if not _dense(t):
+                raise ValueError(f"{name} must each fill one stretch of memory, not strides {t.stride()} "
+                                 f"of shape {tuple(t.shape)}")
+    pointers = array.array("Q", map(torch.Tensor.data_ptr, tensors))
+    sizes = array.array("q", map(torch.Tensor.numel, tensors))
+    return next(iter(devices), None), pointers, sizes, array.array("i", types), contiguous
 
 
 def _norm_call(where, tensors, norm_type, norm, stream, max_norm=None, eps=0.0, outs=None):
     kind = NORMS.get(float(norm_type))
     if kind is None:
         raise ValueError(f"norm_type must be 1, 2 or inf, not {norm_type}")
-    given = [t is not None for t in tensors] if outs is not None and not torch.is_tensor(tensors) else None
-    tensors, dev, pointers, sizes, types = _tensor_list(tensors, "tensors")
+    tensors = [tensors] if torch.is_tensor(tensors) else list(tensors)
+    if outs is not None:
+        outs = [outs] if torch.is_tensor(outs) else list(outs)
+        if len(outs) != len(tensors):
+            raise ValueError(f"{len(outs)} outs for {len(tensors)} tensors")
+        outs = [o for o, t in zip(outs, tensors) if t is not None]
+    tensors = [t for t in tensors if t is not None]
+    index, pointers, sizes, types, contiguous = _tensor_list(tensors, "tensors")
     if norm is None:
-        norm = _empty((), torch.float32, dev if dev is not None else "cuda", stream)
+        norm = _empty((), torch.float32, "cuda" if index is None else tensors[0].device, stream)
     elif norm.dtype != torch.float32 or norm.numel() != 1:
         raise ValueError("norm must be a one-element float32 CUDA tensor")
     dev = _call_device(("norm", norm), ("tensors", tensors[0] if tensors else None))
-    n = len(tensors)
-    args = [(ctypes.c_void_p * n)(*pointers), (ctypes.c_int64 * n)(*sizes), (ctypes.c_int * n)(*types), n, kind]
+    args = [pointers.buffer_info()[0], sizes.buffer_info()[0], types.buffer_info()[0], len(tensors), kind]
     if max_norm is not None:
-        if outs is None:
-            args.insert(1, args[0])
-        else:
-            outs = [outs] if torch.is_tensor(outs) else list(outs)
-            if given is not None and len(outs) == len(given):
-                outs = [o for o, there in zip(outs, given) if there]
-            if len(outs) != n:
-                raise ValueError(f"{len(outs)} outs for {n} tensors")
-            for o, t in zip(outs, tensors):
-                if o.shape != t.shape or o.dtype != t.dtype or o.device != dev or o.stride() != t.stride():
-                    raise ValueError("outs must match the tensors in shape, strides, dtype and device")
-            args.insert(1, (ctypes.c_void_p * n)(*[o.data_ptr() for o in outs]))
+        results = pointers
+        if outs is not None:
+            out_index, results, out_sizes, out_types, out_contiguous = _tensor_list(outs, "outs")
+            if out_index != index or out_types != types or out_sizes != sizes or \
+                    not (contiguous and out_contiguous) and \
+                    [(o.shape, o.stride()) for o in outs] != [(t.shape, t.stride()) for t in tensors]:
+                raise ValueError("outs must match the tensors in size, order of values, dtype and device")
+        args.insert(1, results.buffer_info()[0])
         args += [float(max_norm), float(eps)]
     with _OnDevice(dev):
         rc = getattr(load_library(), where)(*args, norm.data_ptr(), _stream_handle(stream, dev))
@@ -1188,7 +1186,8 @@ def grad_norm(tensors, norm_type: float = 2.0, norm: torch.Tensor = None, stream
 
 def clip_grad_norm(tensors, max_norm: float, norm_type: float = 2.0, eps: float = 1e-6, outs=None,
                    norm: torch.Tensor = None, stream=None) -> torch.Tensor:
-    """Scales ``tensors`` by min(1, max_norm / (norm + eps)), in place or into ``outs`` (one for
-    each tensor, of the same shape, strides and type), and returns the norm they had, as
-    grad_norm does.  Where the norm keeps the limit, tensors in place are not written."""
+    """Scales ``tensors`` by min(1, max_norm / (norm + eps)), in place or into ``outs``, and returns
+    the norm they had, as grad_norm does.  There is one out for each tensor, of the same type and,
+    where they are not contiguous, the same shape and strides; it shares no memory with any other
+    tensor.  Where the norm keeps the limit, tensors in place are not written."""
     return _norm_call("clip_grad_norm", tensors, norm_type, norm, stream, max_norm, eps, outs)

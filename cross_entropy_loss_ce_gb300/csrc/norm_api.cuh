@@ -10,7 +10,7 @@ namespace gbce {
 namespace {
 
 constexpr int64_t kNormMaxTensors = int64_t{1} << 20;
-constexpr int64_t kNormMaxValues = int64_t{1} << 46;  // of a tensor
+constexpr int64_t kNormMaxValues = int64_t{1} << 40;  // of a tensor: 2^27 tiles
 constexpr int64_t kNormMaxTiles = INT32_MAX / 2;      // of a launch, its grid's step included
 
 struct TensorList {
@@ -41,15 +41,16 @@ int check_tensors(const TensorList &l)
     return GBCE_OK;
 }
 
-// Does an output share memory with another tensor (or with its own and starts elsewhere)?
-bool outputs_overlap(const TensorList &l)
+// Does an output (the norm among them) share memory with another tensor, or with its own and starts elsewhere?
+bool outputs_overlap(const TensorList &l, const float *norm)
 {
     struct Span {
         uintptr_t first, last;
         bool out;
     };
     std::vector<Span> spans;
-    spans.reserve(static_cast<size_t>(2 * l.n));
+    spans.reserve(static_cast<size_t>(2 * l.n + 1));
+    spans.push_back({reinterpret_cast<uintptr_t>(norm), reinterpret_cast<uintptr_t>(norm) + sizeof(float), true});
     for (int64_t i = 0; i < l.n; ++i) {
         const size_t bytes = static_cast<size_t>(l.values[i]) * elem_size(l.dtypes[i]);
         const auto add = [&](const void *p, bool out) {
@@ -115,9 +116,10 @@ template <int KIND, int N>
 cudaError_t launch_norm(const Call &call, const TensorList &l, float *norm, double max_norm, double eps, bool in_place)
 {
     NormTable<N> t;
-    int64_t parts = 0;
-    for (int64_t i = 0; i < l.n;) {
-        i = fill_table<N>(l, i, &t);
+    int64_t next = fill_table<N>(l, 0, &t), parts = norm_grid(call, t.first[t.tensors]);
+    const bool one = next == l.n;  // the only table is filled once
+    while (next < l.n) {
+        next = fill_table<N>(l, next, &t);
         parts += norm_grid(call, t.first[t.tensors]);
     }
     PoolScratch scratch(call.stream);
@@ -125,27 +127,30 @@ cudaError_t launch_norm(const Call &call, const TensorList &l, float *norm, doub
     if (e != cudaSuccess)
         return e;
     double *part = static_cast<double *>(scratch.p);
-    int64_t at = 0;
-    for (int64_t i = 0; i < l.n && e == cudaSuccess;) {
-        i = fill_table<N>(l, i, &t);
-        const int64_t grid = norm_grid(call, t.first[t.tensors]);
-        if (grid == 0)
-            continue;
-        e = launch_kernel(call, at > 0, norm_parts_kernel<KIND, N>, grid, kNormThreads, 0, t, part + at);
-        at += grid;
-    }
-    bool written = false;
-    for (int64_t i = 0; l.out && i < l.n && e == cudaSuccess;) {
-        i = fill_table<N>(l, i, &t);
-        const int64_t grid = norm_grid(call, t.first[t.tensors]);
-        if (grid == 0)
-            continue;
-        e = launch_kernel(call, true, norm_scale_kernel<KIND, N>, grid, kNormThreads, 0, t, part,
-                          static_cast<int>(at), written ? nullptr : norm, max_norm, eps, in_place);
-        written = true;
-    }
-    if (e == cudaSuccess && !written)
-        e = launch_kernel(call, at > 0, norm_finish_kernel<KIND>, 1, kNormThreads, 0, part, static_cast<int>(at), norm);
+    int at = 0;
+    const auto each = [&](auto launch) {  // launch(grid) for each table that holds a value
+        for (int64_t i = 0; i < l.n && e == cudaSuccess;) {
+            i = one ? l.n : fill_table<N>(l, i, &t);
+            if (t.tensors > 0)
+                e = launch(norm_grid(call, t.first[t.tensors]));
+        }
+    };
+    each([&](int64_t grid) {
+        double *here = part + at;
+        const bool early = at > 0;
+        at += static_cast<int>(grid);
+        return launch_kernel(call, early, norm_parts_kernel<KIND, N>, grid, kNormThreads, 0, t, here);
+    });
+    float *result = norm;  // written by the first of the scaling kernels
+    if (l.out)
+        each([&](int64_t grid) {
+            float *here = result;
+            result = nullptr;
+            return launch_kernel(call, true, norm_scale_kernel<KIND, N>, grid, kNormThreads, 0, t, part, at, here,
+                                 max_norm, eps, in_place);
+        });
+    if (e == cudaSuccess && result)
+        e = launch_kernel(call, at > 0, norm_finish_kernel<KIND>, 1, kNormThreads, 0, part, at, result);
     return scratch.release(e);
 }
 
@@ -175,7 +180,7 @@ int norm_call(const TensorList &l, int kind, float *norm, double max_norm, doubl
     for (int64_t i = 0; l.out && i < l.n; ++i)
         in_place &= l.in[i] == l.out[i] || l.values[i] == 0;
     try {
-        if (l.out && outputs_overlap(l))
+        if (l.out && outputs_overlap(l, norm))
             return GBCE_ERR_OVERLAP;
     } catch (...) {  // no memory on the host
         return GBCE_ERR_CUDA;

@@ -185,9 +185,11 @@ __device__ __forceinline__ double norm_reduce(double v)
     if ((threadIdx.x & 31) == 0)
         part[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = part[0];
-    for (int w = 1; w < kNormThreads / 32; ++w)
-        v = join(v, part[w]);
+    if (threadIdx.x == 0) {
+        v = part[0];
+        for (int w = 1; w < kNormThreads / 32; ++w)
+            v = join(v, part[w]);
+    }
     return v;
 }
 
@@ -215,7 +217,7 @@ __global__ void __launch_bounds__(kNormThreads, kNormCtasPerSm) norm_parts_kerne
         part[blockIdx.x] = v;
 }
 
-// The norm from the CTAs' numbers, the same in every thread.
+// The sum or maximum of the CTAs' numbers, in thread 0.
 template <int KIND>
 __device__ __forceinline__ double norm_total(const double *part, int parts)
 {
@@ -224,7 +226,12 @@ __device__ __forceinline__ double norm_total(const double *part, int parts)
         const double p = __ldcg(part + i);
         v = KIND == kNormMax ? (v >= p || v != v ? v : p) : v + p;
     }
-    v = norm_reduce<KIND>(v);
+    return norm_reduce<KIND>(v);
+}
+
+template <int KIND>
+__device__ __forceinline__ double norm_root(double v)
+{
     return KIND == kNormTwo ? sqrt(v) : v;
 }
 
@@ -234,7 +241,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_finish_kernel(const double 
     wait_prerequisite_grid();
     const double n = norm_total<KIND>(part, parts);
     if (threadIdx.x == 0)
-        *norm = static_cast<float>(n);
+        *norm = static_cast<float>(norm_root<KIND>(n));
 }
 
 // f as two fp32 factors, the second a power of two: 1, or 2^-100 where f is
@@ -244,12 +251,20 @@ struct NormFactor {
     bool copy;
 };
 
+template <typename T>
+__device__ __forceinline__ T scaled(T x, const NormFactor &by)
+{
+    if (!by.copy)
+        Elem<T>::store(&x, Elem<T>::load(&x) * by.f * by.power);
+    return x;
+}
+
 // n values of memory that starts at another place within 16 bytes than its
 // result: one value at a time, kNormValues of a thread in flight.
 constexpr int kNormValues = 16;
 
 template <typename T>
-__device__ __noinline__ void scale_apart(const T *x, T *y, int n, const NormFactor by)
+__device__ __forceinline__ void scale_apart(const T *x, T *y, int n, const NormFactor &by)
 {
     using E = Elem<T>;
 #pragma unroll 1
@@ -257,16 +272,11 @@ __device__ __noinline__ void scale_apart(const T *x, T *y, int n, const NormFact
         T raw[kNormValues];
 #pragma unroll
         for (int i = 0; i < kNormValues; ++i)
-            if (i0 + i * kNormThreads < n)
-                raw[i] = x[i0 + i * kNormThreads];
+            raw[i] = i0 + i * kNormThreads < n ? x[i0 + i * kNormThreads] : T{};
 #pragma unroll
         for (int i = 0; i < kNormValues; ++i) {
-            if (i0 + i * kNormThreads >= n)
-                continue;
-            if (by.copy)
-                y[i0 + i * kNormThreads] = raw[i];
-            else
-                E::store(y + i0 + i * kNormThreads, E::load(&raw[i]) * by.f * by.power);
+            if (i0 + i * kNormThreads < n)
+                y[i0 + i * kNormThreads] = scaled(raw[i], by);
         }
     }
 }
@@ -279,19 +289,12 @@ __device__ __forceinline__ void scale_tile(const void *p, void *q, int64_t value
     const NormGeom<T> g = norm_geom<T>(p, values);
     const T *x = static_cast<const T *>(p);
     T *y = static_cast<T *>(q);
-    const auto one = [&](int64_t i) {
-        if (by.copy)
-            y[i] = x[i];
-        else
-            E::store(y + i, E::load(x + i) * by.f * by.power);
-    };
     if (tile == 0) {
         const int tail = static_cast<int>(g.values - g.tail_start);
         const int i = static_cast<int>(threadIdx.x);
-        if (i < g.head)
-            one(i);
-        else if (i - g.head < tail)
-            one(g.tail_start + (i - g.head));
+        const int64_t at = i < g.head ? i : g.tail_start + (i - g.head);
+        if (i < g.head + tail)
+            y[at] = scaled(x[at], by);
     }
     if (((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(q)) & 15u) == 0) {
         const int64_t at = tile * kNormTileVecs + threadIdx.x;
@@ -301,21 +304,17 @@ __device__ __forceinline__ void scale_tile(const void *p, void *q, int64_t value
         uint4 raw[kNormVecs];
 #pragma unroll
         for (int i = 0; i < kNormVecs; ++i)
-            if (i * kNormThreads < here)
-                raw[i] = __ldcs(v + i * kNormThreads);
+            raw[i] = i * kNormThreads < here ? __ldcs(v + i * kNormThreads) : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int i = 0; i < kNormVecs; ++i) {
-            if (i * kNormThreads >= here)
-                continue;
-            if (!by.copy) {
-                float w[V];
-                E::unpack(raw[i], w);
+            float w[V];
+            E::unpack(raw[i], w);
 #pragma unroll
-                for (int e = 0; e < V; ++e)
-                    w[e] = w[e] * by.f * by.power;
-                raw[i] = E::pack(w);
-            }
-            __stcs(o + i * kNormThreads, raw[i]);
+            for (int e = 0; e < V; ++e)
+                w[e] = w[e] * by.f * by.power;
+            const uint4 r = by.copy ? raw[i] : E::pack(w);
+            if (i * kNormThreads < here)
+                __stcs(o + i * kNormThreads, r);
         }
         return;
     }
@@ -331,16 +330,24 @@ __global__ void __launch_bounds__(kNormThreads, kNormCtasPerSm) norm_scale_kerne
 {
     wait_prerequisite_grid();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // one thread forms the factor: fp64 is slow here, and nothing of it is left to the loop
+    __shared__ NormFactor shared;
     const double n = norm_total<KIND>(part, parts);
-    if (norm && blockIdx.x == 0 && threadIdx.x == 0)
-        *norm = static_cast<float>(n);
-    double f = max_norm / (n + eps);
-    f = f >= 1.0 ? 1.0 : f;  // a NaN stays one
-    if (in_place && f == 1.0)
+    if (threadIdx.x == 0) {
+        const double root = norm_root<KIND>(n);
+        if (norm && blockIdx.x == 0)
+            *norm = static_cast<float>(root);
+        double f = max_norm / (root + eps);
+        f = f >= 1.0 ? 1.0 : f;  // a NaN stays one
+        const bool low = f > 0.0 && f < 0x1p-126;
+        shared = {static_cast<float>(low ? f * 0x1p100 : f), low ? 0x1p-100f : 1.f, f == 1.0};
+    }
+    __syncthreads();
+    const NormFactor by = shared;
+    if (in_place && by.copy)
         return;
-    const bool low = f > 0.0 && f < 0x1p-126;
-    const NormFactor by{static_cast<float>(low ? f * 0x1p100 : f), low ? 0x1p-100f : 1.f, f == 1.0};
     const int tiles = a.first[a.tensors];
+#pragma unroll 1
     for (int tile = tiles - 1 - static_cast<int>(blockIdx.x); tile >= 0; tile -= static_cast<int>(gridDim.x)) {
         const int i = norm_tensor(a, tile);
         const int64_t at = tile - a.first[i];

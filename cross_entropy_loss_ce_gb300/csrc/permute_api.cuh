@@ -35,11 +35,13 @@ int sort_rank_smem(int E, int threads, bool all)
     return (all ? 2 * E + 1 : E) * 4 + sort_hist_stride(E) * 2 * (threads / 32 + 1);
 }
 
+int sort_place_smem(int E) { return (6 * E + 2 + static_cast<int>(kSortRound)) * 4; }
+
 cudaError_t launch_sort(const Call &call, SortArgs a)
 {
     cudaError_t e;
     if (a.n <= kSortRound) {
-        const int threads = a.n <= 32 * kSortItems ? 32 : (a.n <= 256 * kSortItems ? 256 : 1024);
+        const int threads = a.n <= 256 * kSortItems ? 256 : 1024;
         const int smem = sort_rank_smem(a.E, threads, true);
         a.per_cta = threads * kSortItems;
         if ((e = configure_smem(reinterpret_cast<const void *>(sort_rank_kernel<true>), call.device,
@@ -61,7 +63,9 @@ cudaError_t launch_sort(const Call &call, SortArgs a)
     if (e == cudaSuccess)
         e = launch_kernel(call, false, sort_rank_kernel<false>, ctas, 1024, sort_rank_smem(a.E, 1024, false), a);
     if (e == cudaSuccess)
-        e = launch_kernel(call, true, sort_place_kernel, ctas, 1024, (3 * a.E + 1) * 4, a);
+        e = configure_smem(reinterpret_cast<const void *>(sort_place_kernel), call.device, sort_place_smem(kSortMaxExperts));
+    if (e == cudaSuccess)
+        e = launch_kernel(call, true, sort_place_kernel, ctas, 1024, sort_place_smem(a.E), a);
     return scratch.release(e);
 }
 
@@ -102,8 +106,9 @@ cudaError_t launch_dispatch_as(const Call &call, PermuteArgs a, size_t es)
     a.units = static_cast<int>(a.H / v);
     a.segs = (a.units + 32 * U - 1) / (32 * U);
     a.token_ctas = token_ctas(a.T * a.segs);
-    return launch_kernel(call, false, dispatch_kernel<Raw, U>, a.token_ctas + zero_ctas(call, a.rows),
-                         kPermuteThreads, 0, a, a.is / v, a.os / v);
+    a.zero_ctas = zero_ctas(call, a.rows);
+    return launch_kernel(call, false, dispatch_kernel<Raw, U>, a.zero_ctas + a.token_ctas, kPermuteThreads, 0, a,
+                         a.is / v, a.os / v);
 }
 
 cudaError_t launch_dispatch(const Call &call, const PermuteArgs &a)
@@ -146,13 +151,15 @@ cudaError_t launch_combine_bwd(const Call &call, PermuteArgs a)
     constexpr int kWarps = kPermuteThreads / 32;
     a.segs = a.T >= kPermuteWarpsPerSm * call.sms || a.units <= 32 ? 1 : kWarps;
     a.token_ctas = token_ctas(a.T * a.segs);
-    const int64_t grid = a.token_ctas + (a.out ? zero_ctas(call, a.rows) : 0);
+    a.zero_ctas = a.out ? zero_ctas(call, a.rows) : 0;
     void (*fn)(const PermuteArgs) = nullptr;
     if (wide)
-        fn = a.k <= 4 ? combine_bwd_kernel<T, V, 4> : combine_bwd_kernel<T, V, 8>;
+        fn = a.k <= 2 ? combine_bwd_kernel<T, V, 2, 4>
+                      : (a.k <= 4 ? combine_bwd_kernel<T, V, 4, 2> : combine_bwd_kernel<T, V, 8, 1>);
     else
-        fn = a.k <= 4 ? combine_bwd_kernel<T, 1, 4> : combine_bwd_kernel<T, 1, 8>;
-    return launch_kernel(call, false, fn, grid, kPermuteThreads, 0, a);
+        fn = a.k <= 2 ? combine_bwd_kernel<T, 1, 2, 8>
+                      : (a.k <= 4 ? combine_bwd_kernel<T, 1, 4, 4> : combine_bwd_kernel<T, 1, 8, 4>);
+    return launch_kernel(call, false, fn, a.zero_ctas + a.token_ctas, kPermuteThreads, 0, a);
 }
 
 int check_weights(const void *w, int64_t stride, int wdtype, int64_t k, int dtype)

@@ -23,7 +23,8 @@ namespace gbce {
 
 constexpr int kSortItems = 8;           // slots a thread holds
 constexpr int kSortMaxExperts = 1024;
-constexpr int kSortRankBits = 21;       // a rank within a CTA's slots, beside 10 bits of expert
+constexpr int kSortRoundBits = 13;      // a slot within a round of 1024 threads, beside 10 bits of expert
+constexpr int kSortRankBits = 21;        // a rank within a CTA's slots, beside 10 bits of expert
 constexpr int kPermuteThreads = 256;
 
 struct SortArgs {
@@ -36,6 +37,8 @@ struct SortArgs {
     int *table;      // [gridDim.x, E] slots of each CTA and expert
     int *position, *source, *offsets, *counts;
 };
+
+static_assert((1 << kSortRoundBits) == 1024 * kSortItems, "a round's slots");
 
 __host__ __device__ __forceinline__ int sort_hist_stride(int E) { return (E + 1) / 2 * 2; }
 
@@ -56,11 +59,9 @@ __device__ __forceinline__ void sort_offsets(const int *v, int *off, int E, int 
         if (lane == 31)
             sums[warp] = sum;
         __syncthreads();
-        int before = carry, all = 0;
-        for (int w = 0; w < warps; ++w) {
-            before += w < warp ? sums[w] : 0;
-            all += sums[w];
-        }
+        const int of_warp = lane < warps ? sums[lane] : 0;
+        const int before = carry + __reduce_add_sync(0xffffffffu, lane < warp ? of_warp : 0);
+        const int all = __reduce_add_sync(0xffffffffu, of_warp);
         if (e < E)
             off[e] = before + sum - own;
         carry += all;
@@ -74,8 +75,10 @@ __device__ __forceinline__ void sort_offsets(const int *v, int *off, int E, int 
 // Rows that are no slot's: behind an expert's slots, and behind the last expert.
 __device__ __forceinline__ void sort_fill(const SortArgs &a, const int *off, const int *total)
 {
-    for (int e = blockIdx.x; e < a.E; e += static_cast<int>(gridDim.x))
-        for (int r = off[e] + total[e] + static_cast<int>(threadIdx.x); r < off[e + 1]; r += static_cast<int>(blockDim.x))
+    const int lane = threadIdx.x & 31, warps = static_cast<int>(blockDim.x) >> 5;
+    for (int e = static_cast<int>(blockIdx.x) * warps + static_cast<int>(threadIdx.x >> 5); a.align > 1 && e < a.E;
+         e += static_cast<int>(gridDim.x) * warps)
+        for (int r = off[e] + total[e] + lane; r < off[e + 1]; r += 32)
             a.source[r] = -1;
     for (int64_t r = off[a.E] + blockIdx.x * int64_t{blockDim.x} + threadIdx.x; r < a.rows;
          r += int64_t{gridDim.x} * blockDim.x)
@@ -88,10 +91,22 @@ __device__ __forceinline__ void sort_fill(const SortArgs &a, const int *off, con
     }
 }
 
+// The lanes whose expert is this lane's, from a vote on each of its `bits` bits.
+__device__ __forceinline__ unsigned sort_peers(int e, int bits)
+{
+    unsigned peers = __ballot_sync(0xffffffffu, e >= 0);
+    for (int b = 0; b < bits; ++b) {
+        const bool set = (e >> b) & 1;
+        const unsigned with = __ballot_sync(0xffffffffu, set);
+        peers &= set ? with : ~with;
+    }
+    return peers;
+}
+
 // Ranks the slots of a CTA by expert, in their order: a warp takes 32
-// consecutive slots at a time, lanes of the same expert find each other with a
-// match and count on from the warp's own histogram; the warps' histograms are
-// then added up in order.  ALL: this CTA holds every slot and writes the plan;
+// consecutive slots at a time, lanes of the same expert find each other and
+// count on from the warp's own histogram; the warps' histograms are then added
+// up in order.  ALL: this CTA holds every slot and writes the plan;
 // else expert and rank go to `position` (packed) and the CTA's counts to `table`.
 template <bool ALL>
 __global__ void __launch_bounds__(1024) sort_rank_kernel(const SortArgs a)
@@ -99,7 +114,7 @@ __global__ void __launch_bounds__(1024) sort_rank_kernel(const SortArgs a)
     extern __shared__ int sort_smem[];
     __shared__ int scan_sums[32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const int hs = sort_hist_stride(a.E);
+    const int hs = sort_hist_stride(a.E), bits = 32 - __clz(a.E - 1);
     int *base = sort_smem;                  // [E] slots of earlier rounds; ALL: of all
     int *off = base + a.E;                  // [E + 1], ALL
     unsigned short *chunk = reinterpret_cast<unsigned short *>(off + (ALL ? a.E + 1 : 0));  // [E]
@@ -110,6 +125,12 @@ __global__ void __launch_bounds__(1024) sort_rank_kernel(const SortArgs a)
     const int64_t first = blockIdx.x * a.per_cta;
     const int64_t last = first + a.per_cta < a.n ? first + a.per_cta : a.n;
     bool bad = false;
+    if constexpr (ALL) {
+        if (a.n == 0) {
+            __syncthreads();
+            sort_offsets(base, off, a.E, a.align, scan_sums);
+        }
+    }
     for (int64_t s0 = first; s0 < last; s0 += int64_t{blockDim.x} * kSortItems) {
         int expert[kSortItems], rank[kSortItems];
         const int64_t w0 = s0 + warp * (32 * kSortItems) + lane;
@@ -135,9 +156,11 @@ __global__ void __launch_bounds__(1024) sort_rank_kernel(const SortArgs a)
 #pragma unroll
         for (int i = 0; i < kSortItems; ++i) {
             const int e = expert[i];
-            const unsigned peers = __match_any_sync(0xffffffffu, e);
-            const unsigned before = peers & ((1u << lane) - 1u);
             rank[i] = 0;
+            if (s0 + warp * (32 * kSortItems) + i * 32 >= last)
+                continue;  // nor has a later round
+            const unsigned peers = sort_peers(e, bits);
+            const unsigned before = peers & ((1u << lane) - 1u);
             if (e >= 0)
                 rank[i] = mine[e] + __popc(before);
             __syncwarp();
@@ -199,50 +222,91 @@ __global__ void __launch_bounds__(1024) sort_rank_kernel(const SortArgs a)
 }
 
 // The plan from the CTAs' counts: each CTA adds up what stands before it and
-// places the slots of the CTA of its number.
+// places the slots of the CTA of its number, a round of them at a time, sorted
+// in shared memory first: an expert's slots go to consecutive rows, so their
+// stores go out together (one by one: 4 us more for 131072 x 8 slots).
 __global__ void __launch_bounds__(1024) sort_place_kernel(const SortArgs a)
 {
     extern __shared__ int sort_smem[];
     __shared__ int scan_sums[32];
-    int *total = sort_smem, *before = total + a.E, *off = before + a.E;  // [E], [E], [E + 1]
-    for (int e = threadIdx.x; e < 2 * a.E; e += static_cast<int>(blockDim.x))
+    const int threads = static_cast<int>(blockDim.x), cta = static_cast<int>(blockIdx.x);
+    int *total = sort_smem;          // [E] slots of each expert
+    int *before = total + a.E;       // [E] ... in earlier CTAs and rounds
+    int *done = before + a.E;        // [E] ... in earlier rounds of this CTA
+    int *mine = done + a.E;          // [E] ... in this round
+    int *off = mine + a.E;           // [E + 1] the plan's offsets
+    int *start = off + a.E + 1;      // [E + 1] the round's
+    int *list = start + a.E + 1;     // [slots of a round] by expert: expert and place in the round
+    for (int e = threadIdx.x; e < 4 * a.E; e += threads)
         total[e] = 0;
     wait_prerequisite_grid();
     __syncthreads();
-    const int groups = static_cast<int>(blockDim.x) / a.E, ctas = static_cast<int>(gridDim.x);
-    const int group = static_cast<int>(threadIdx.x) / a.E, e = static_cast<int>(threadIdx.x) % a.E;
-    if (group < groups) {
-        int all = 0, mine = 0;
-#pragma unroll 8
-        for (int b = group; b < ctas; b += groups) {
-            const int c = __ldcg(a.table + int64_t{b} * a.E + e);
-            all += c;
-            mine += b < static_cast<int>(blockIdx.x) ? c : 0;
-        }
-        atomicAdd(total + e, all);  // integers: any order, the same sum
-        atomicAdd(before + e, mine);
-    }
-    __syncthreads();
-    sort_offsets(total, off, a.E, a.align, scan_sums);
-    const int64_t first = blockIdx.x * a.per_cta;
+    // the first round's slots and the CTAs' counts are on their way together
+    const int64_t first = cta * a.per_cta, round = int64_t{threads} * kSortItems;
     const int64_t last = first + a.per_cta < a.n ? first + a.per_cta : a.n;
-    for (int64_t s0 = first + threadIdx.x; s0 < last; s0 += int64_t{blockDim.x} * kSortItems) {
-        int packed[kSortItems];
+    int packed[kSortItems];
+    const auto load = [&](int64_t s0) {
 #pragma unroll
         for (int i = 0; i < kSortItems; ++i) {
-            const int64_t s = s0 + i * int64_t{blockDim.x};
+            const int64_t s = s0 + i * threads + threadIdx.x;
             packed[i] = s < last ? __ldcg(a.position + s) : -1;
         }
+    };
+    load(first);
+    const int groups = threads / a.E, ctas = static_cast<int>(gridDim.x);
+    const int group = static_cast<int>(threadIdx.x) / a.E, own = static_cast<int>(threadIdx.x) % a.E;
+    if (group < groups) {
+        int all = 0, lower = 0;
+        for (int b0 = group; b0 < ctas; b0 += 16 * groups) {
+            int c[16];
 #pragma unroll
-        for (int i = 0; i < kSortItems; ++i) {
-            const int64_t s = s0 + i * int64_t{blockDim.x};
-            if (s < last && packed[i] >= 0) {
-                const int x = packed[i] >> kSortRankBits;
-                const int row = off[x] + before[x] + (packed[i] & ((1 << kSortRankBits) - 1));
-                a.position[s] = row;
-                a.source[row] = static_cast<int>(s);
+            for (int i = 0; i < 16; ++i)
+                c[i] = b0 + i * groups < ctas ? __ldcg(a.table + int64_t{b0 + i * groups} * a.E + own) : 0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                all += c[i];
+                lower += b0 + i * groups < cta ? c[i] : 0;
             }
         }
+        atomicAdd(total + own, all);  // integers: any order, the same sum
+        atomicAdd(before + own, lower);
+    }
+    for (int64_t s0 = first; s0 < last; s0 += round) {
+        if (last - first > round) {
+#pragma unroll
+            for (int i = 0; i < kSortItems; ++i)
+                if (packed[i] >= 0)
+                    atomicAdd(mine + (packed[i] >> kSortRankBits), 1);
+        } else {
+            for (int e = threadIdx.x; e < a.E; e += threads)
+                mine[e] = __ldcg(a.table + int64_t{cta} * a.E + e);
+        }
+        __syncthreads();
+        if (s0 == first)
+            sort_offsets(total, off, a.E, a.align, scan_sums);
+        sort_offsets(mine, start, a.E, 1, scan_sums);
+#pragma unroll
+        for (int i = 0; i < kSortItems; ++i) {
+            if (packed[i] < 0)
+                continue;
+            const int e = packed[i] >> kSortRankBits, at = i * threads + static_cast<int>(threadIdx.x);
+            const int rank = (packed[i] & ((1 << kSortRankBits) - 1)) - done[e];
+            a.position[s0 + at] = off[e] + before[e] + rank;
+            list[start[e] + rank] = e << kSortRoundBits | at;
+        }
+        load(s0 + round);
+        __syncthreads();
+        for (int i = threadIdx.x; i < start[a.E]; i += threads) {
+            const int e = list[i] >> kSortRoundBits, at = list[i] & ((1 << kSortRoundBits) - 1);
+            a.source[off[e] + before[e] + (i - start[e])] = static_cast<int>(s0) + at;
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < a.E; e += threads) {
+            before[e] += mine[e];
+            done[e] += mine[e];
+            mine[e] = 0;
+        }
+        __syncthreads();
     }
     sort_fill(a, off, total);
 }
@@ -265,23 +329,25 @@ struct PermuteArgs {
     int k, rows;
     int units;          // of a row: H in what a lane moves at a time
     int segs;           // warps that share a token's row
-    int64_t token_ctas; // CTAs for tokens; those behind them zero the rows that are no slot's
+    int64_t zero_ctas;  // CTAs that zero the rows that are no slot's; those behind them take tokens
+    int64_t token_ctas;
     bool weights_f32;   // else of the rows' type
 };
 
-// Zeroes the rows of `out` that are no slot's, a warp 32 rows at a time.
+// Zeroes the rows of `out` that are no slot's.  They lie in runs (behind an
+// expert's slots, behind the last expert), so a warp looks at rows far apart.
 template <typename Raw>
-__device__ __forceinline__ void zero_rows(const PermuteArgs &a, int64_t os_units, int64_t cta, int64_t ctas)
+__device__ __forceinline__ void zero_rows(const PermuteArgs &a, int64_t os_units)
 {
     const int lane = threadIdx.x & 31;
-    const int64_t warps = ctas * (blockDim.x >> 5);
-    for (int64_t r0 = (cta * (blockDim.x >> 5) + (threadIdx.x >> 5)) * 32; r0 < a.rows; r0 += warps * 32) {
-        const bool mine = r0 + lane < a.rows && __ldg(a.source + r0 + lane) < 0;
-        unsigned todo = __ballot_sync(0xffffffffu, mine);
+    const int64_t warps = a.zero_ctas * (blockDim.x >> 5);
+    for (int64_t r0 = blockIdx.x * int64_t{blockDim.x >> 5} + (threadIdx.x >> 5); r0 < a.rows; r0 += warps * 32) {
+        const int64_t r = r0 + lane * warps;
+        unsigned todo = __ballot_sync(0xffffffffu, r < a.rows && __ldg(a.source + (r < a.rows ? r : 0)) < 0);
         while (todo) {
             const int i = __ffs(todo) - 1;
             todo &= todo - 1;
-            Raw *row = static_cast<Raw *>(a.out) + (r0 + i) * os_units;
+            Raw *row = static_cast<Raw *>(a.out) + (r0 + i * warps) * os_units;
             for (int u = lane; u < a.units; u += 32)
                 row[u] = Raw{};
         }
@@ -292,22 +358,21 @@ __device__ __forceinline__ void zero_rows(const PermuteArgs &a, int64_t os_units
 template <typename Raw, int U>
 __global__ void __launch_bounds__(kPermuteThreads) dispatch_kernel(const PermuteArgs a, int64_t is_units, int64_t os_units)
 {
-    if (static_cast<int64_t>(blockIdx.x) >= a.token_ctas) {
-        zero_rows<Raw>(a, os_units, blockIdx.x - a.token_ctas, gridDim.x - a.token_ctas);
+    if (blockIdx.x < a.zero_ctas) {
+        zero_rows<Raw>(a, os_units);
         return;
     }
     const int lane = threadIdx.x & 31;
     constexpr int kWarps = kPermuteThreads / 32;
     const int64_t all = a.T * a.segs;
-    for (int64_t w = blockIdx.x * int64_t{kWarps} + (threadIdx.x >> 5); w < all; w += a.token_ctas * kWarps) {
+    for (int64_t w = (blockIdx.x - a.zero_ctas) * int64_t{kWarps} + (threadIdx.x >> 5); w < all; w += a.token_ctas * kWarps) {
         const int64_t t = w / a.segs;
         const int u0 = static_cast<int>(w - t * a.segs) * (32 * U) + lane;
         const Raw *x = static_cast<const Raw *>(a.in) + t * is_units;
         Raw v[U];
 #pragma unroll
         for (int i = 0; i < U; ++i)
-            if (u0 + i * 32 < a.units)
-                v[i] = __ldcs(x + u0 + i * 32);
+            v[i] = u0 + i * 32 < a.units ? __ldcs(x + u0 + i * 32) : Raw{};
         const int *pos = a.position + t * a.k;
         for (int j0 = 0; j0 < a.k; j0 += 8) {
             int p[8];
@@ -420,23 +485,24 @@ __global__ void __launch_bounds__(kPermuteThreads) combine_kernel(const PermuteA
 }
 
 // combine's gradients: a token belongs to `segs` warps (1, or all of a CTA),
-// which read its row of d_out once for up to KC slots, write that row times
-// the weight to each slot's place and add up the products with each slot's y.
-template <typename T, int VEC, int KC>
+// which read its row of d_out once for up to KC slots, U units of a lane at a
+// time, write that row times the weight to each slot's place and add up the
+// products with each slot's y.
+template <typename T, int VEC, int KC, int U>
 __global__ void __launch_bounds__(kPermuteThreads) combine_bwd_kernel(const PermuteArgs a)
 {
     using Unit = RowUnit<T, VEC>;
+    using Raw = typename Unit::Raw;
     constexpr int kWarps = kPermuteThreads / 32;
     __shared__ float part[kWarps][KC];
-    if (static_cast<int64_t>(blockIdx.x) >= a.token_ctas) {
-        if (a.out)
-            zero_rows<typename Unit::Raw>(a, a.os / VEC, blockIdx.x - a.token_ctas, gridDim.x - a.token_ctas);
+    if (blockIdx.x < a.zero_ctas) {
+        zero_rows<Raw>(a, a.os / VEC);
         return;
     }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int sub = a.segs == 1 ? 0 : warp, step = 32 * a.segs;
+    const int first = a.segs == 1 ? lane : warp * (32 * U) + lane;
     const int64_t tokens = kWarps / a.segs;  // of a CTA at a time
-    for (int64_t t0 = blockIdx.x * tokens; t0 < a.T; t0 += a.token_ctas * tokens) {
+    for (int64_t t0 = (blockIdx.x - a.zero_ctas) * tokens; t0 < a.T; t0 += a.token_ctas * tokens) {
         const int64_t t = t0 + (a.segs == 1 ? warp : 0);
         if (t >= a.T)
             continue;  // segs == 1: nothing below waits for other warps
@@ -452,33 +518,37 @@ __global__ void __launch_bounds__(kPermuteThreads) combine_bwd_kernel(const Perm
                 if (p[j] >= a.rows)
                     p[j] = -1;
             }
-            for (int u = sub * 32 + lane; u < a.units; u += step) {
-                typename Unit::Raw gr = Unit::load(g_row + int64_t{u} * VEC), v[KC];
-                if (a.d_weights) {
+            for (int u = first; u < a.units; u += 32 * U * a.segs) {
+                Raw gr[U], v[KC][U];
 #pragma unroll
-                    for (int j = 0; j < KC; ++j)
-                        if (p[j] >= 0)
-                            v[j] = Unit::load(static_cast<const T *>(a.in) + p[j] * a.is + int64_t{u} * VEC);
-                }
-                float g[VEC];
-                Unit::unpack(gr, g);
+                for (int i = 0; i < U; ++i)
+                    gr[i] = u + i * 32 < a.units ? Unit::load(g_row + int64_t{u + i * 32} * VEC) : Raw{};
 #pragma unroll
                 for (int j = 0; j < KC; ++j) {
-                    if (p[j] < 0)
-                        continue;
-                    if (a.out) {
-                        float o[VEC];
+                    const T *y = static_cast<const T *>(a.in) + p[j] * a.is;
 #pragma unroll
-                        for (int e = 0; e < VEC; ++e)
-                            o[e] = wt[j] * g[e];
-                        Unit::store(static_cast<T *>(a.out) + p[j] * a.os + int64_t{u} * VEC, o);
-                    }
-                    if (a.d_weights) {
+                    for (int i = 0; i < U; ++i)
+                        v[j][i] = a.d_weights && p[j] >= 0 && u + i * 32 < a.units
+                                      ? Unit::load(y + int64_t{u + i * 32} * VEC)
+                                      : Raw{};
+                }
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    float g[VEC];
+                    Unit::unpack(gr[i], g);
+#pragma unroll
+                    for (int j = 0; j < KC; ++j) {
                         float f[VEC];
-                        Unit::unpack(v[j], f);
+                        Unit::unpack(v[j][i], f);
 #pragma unroll
                         for (int e = 0; e < VEC; ++e)
                             dot[j] = fmaf(g[e], f[e], dot[j]);
+                        if (a.out && p[j] >= 0 && u + i * 32 < a.units) {
+#pragma unroll
+                            for (int e = 0; e < VEC; ++e)
+                                f[e] = wt[j] * g[e];
+                            Unit::store(static_cast<T *>(a.out) + p[j] * a.os + int64_t{u + i * 32} * VEC, f);
+                        }
                     }
                 }
             }
@@ -508,10 +578,11 @@ __global__ void __launch_bounds__(kPermuteThreads) combine_bwd_kernel(const Perm
                 if (lane != j || j0 + j >= a.k)
                     continue;
                 const int64_t at = t * a.dws + j0 + j;
+                const float d = p[j] < 0 ? 0.f : dot[j];  // not 0 times an infinity
                 if (a.weights_f32)
-                    static_cast<float *>(a.d_weights)[at] = dot[j];
+                    static_cast<float *>(a.d_weights)[at] = d;
                 else
-                    Elem<T>::store(static_cast<T *>(a.d_weights) + at, dot[j]);
+                    Elem<T>::store(static_cast<T *>(a.d_weights) + at, d);
             }
         }
     }

@@ -651,7 +651,7 @@ GBCE_API int moe_combine_bwd(const void *d_out, int64_t d_out_stride, const void
  *   kind          a gbce_norm.
  *   norm          one float: 0 for no values, infinite past fp32's range, NaN where a
  *                 value is NaN.
- *   n, values     n <= 2^20; values[i] <= 2^46.
+ *   n, values     n <= 2^20; values[i] <= 2^40.
  *
  * Squares and magnitudes are added in fp32 over 32 to 64 values, scaled by a power of
  * two where they would leave fp32's range, then with their rounding errors carried, at last
@@ -667,8 +667,8 @@ GBCE_API int grad_norm(const void *const *tensors, const int64_t *values, const 
  *   tensors, values, dtypes, n, kind, norm: as for grad_norm (norm is that of the
  *                 tensors as they came).
  *   outs          n device pointers (the array in HOST memory): tensors[i] itself, or
- *                 memory that no other tensor shares, of the same type.  Any other
- *                 sharing is refused: GBCE_ERR_OVERLAP.
+ *                 memory that no tensor of the call, nor norm, shares, of the same type.
+ *                 Any other sharing is refused: GBCE_ERR_OVERLAP.
  *   max_norm, eps the limit and what is added to the norm, both >= 0 (else GBCE_ERR_SIZE).
  *
  * f is formed in fp64, products in fp32, rounded once.  f = 1 copies the bits, and in
