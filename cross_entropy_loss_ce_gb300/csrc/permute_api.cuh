@@ -35,7 +35,7 @@ int sort_rank_smem(int E, int threads, bool all)
     return (all ? 2 * E + 1 : E) * 4 + sort_hist_stride(E) * 2 * (threads / 32 + 1);
 }
 
-int sort_place_smem(int E) { return (6 * E + 2 + static_cast<int>(kSortRound)) * 4; }
+int sort_place_smem(int E) { return (8 * E + 2 + static_cast<int>(kSortRound)) * 4; }
 
 cudaError_t launch_sort(const Call &call, SortArgs a)
 {
@@ -49,8 +49,13 @@ cudaError_t launch_sort(const Call &call, SortArgs a)
             return e;
         return launch_kernel(call, false, sort_rank_kernel<true>, 1, threads, smem, a);
     }
-    const int64_t rounds = (a.n + kSortRound - 1) / kSortRound;
-    a.per_cta = (rounds + call.sms - 1) / call.sms * kSortRound;
+    // a CTA's time is one slot after another of its warps: small ones, while there are few (131072 slots: 22 us
+    // with 16 CTAs of 1024 threads, 15 with 64 of 256); many CTAs make the sums before each one long
+    int threads = 256;
+    while (threads < 1024 && a.n > call.sms / 2 * threads * kSortItems)
+        threads *= 2;
+    const int64_t round = int64_t{threads} * kSortItems, rounds = (a.n + round - 1) / round;
+    a.per_cta = (rounds + call.sms - 1) / call.sms * round;
     if (a.per_cta > kSortMaxPerCta)
         a.per_cta = kSortMaxPerCta;
     const int64_t ctas = (a.n + a.per_cta - 1) / a.per_cta;
@@ -61,11 +66,11 @@ cudaError_t launch_sort(const Call &call, SortArgs a)
     e = configure_smem(reinterpret_cast<const void *>(sort_rank_kernel<false>), call.device,
                        sort_rank_smem(kSortMaxExperts, 1024, false));
     if (e == cudaSuccess)
-        e = launch_kernel(call, false, sort_rank_kernel<false>, ctas, 1024, sort_rank_smem(a.E, 1024, false), a);
+        e = launch_kernel(call, false, sort_rank_kernel<false>, ctas, threads, sort_rank_smem(a.E, threads, false), a);
     if (e == cudaSuccess)
         e = configure_smem(reinterpret_cast<const void *>(sort_place_kernel), call.device, sort_place_smem(kSortMaxExperts));
     if (e == cudaSuccess)
-        e = launch_kernel(call, true, sort_place_kernel, ctas, 1024, sort_place_smem(a.E), a);
+        e = launch_kernel(call, true, sort_place_kernel, ctas, threads, sort_place_smem(a.E), a);
     return scratch.release(e);
 }
 
@@ -133,8 +138,12 @@ cudaError_t launch_combine(const Call &call, PermuteArgs a)
         a.segs = (a.units + 32 * u - 1) / (32 * u);
         return launch_kernel(call, false, fn, token_ctas(a.T * a.segs), kPermuteThreads, 0, a);
     };
-    if (!in_units(16, sizeof(T), a.H, a.in, a.is, a.out, a.os))
+    if (!in_units(16, sizeof(T), a.H, a.in, a.is, a.out, a.os)) {
+        if constexpr (sizeof(T) == 2)
+            if (in_units(4, sizeof(T), a.H, a.in, a.is, a.out, a.os))
+                return go(combine_kernel<T, 2, 4>, 2, 4);
         return go(combine_kernel<T, 1, 4>, 1, 4);
+    }
     return a.T * ((a.H / V + 63) / 64) < kPermuteWarpsPerSm * call.sms ? go(combine_kernel<T, V, 1>, V, 1)
                                                                        : go(combine_kernel<T, V, 2>, V, 2);
 }
@@ -143,22 +152,33 @@ template <typename T>
 cudaError_t launch_combine_bwd(const Call &call, PermuteArgs a)
 {
     constexpr int V = Elem<T>::kPerVec;
-    const void *other = a.d_weights ? a.in : a.d_out;
-    const int64_t other_stride = a.d_weights ? a.is : a.ds;
-    const bool wide = in_units(16, sizeof(T), a.H, a.d_out, a.ds, other, other_stride) &&
-                      (!a.out || in_units(16, sizeof(T), a.H, a.out, a.os, a.out, a.os));
-    a.units = static_cast<int>(wide ? a.H / V : a.H);
+    const void *y = a.d_weights ? a.in : a.d_out;
+    const int64_t y_stride = a.d_weights ? a.is : a.ds;
+    const auto whole = [&](size_t bytes) {
+        return in_units(bytes, sizeof(T), a.H, a.d_out, a.ds, y, y_stride) &&
+               (!a.out || in_units(bytes, sizeof(T), a.H, a.out, a.os, a.out, a.os));
+    };
+    void (*fn)(const PermuteArgs) = nullptr;
+    int vec = 1;
+    if (whole(16)) {
+        vec = V;
+        fn = a.k <= 2 ? combine_bwd_kernel<T, V, 2, 4>
+                      : (a.k <= 4 ? combine_bwd_kernel<T, V, 4, 2> : combine_bwd_kernel<T, V, 8, 1>);
+    } else {
+        fn = a.k <= 2 ? combine_bwd_kernel<T, 1, 2, 8>
+                      : (a.k <= 4 ? combine_bwd_kernel<T, 1, 4, 4> : combine_bwd_kernel<T, 1, 8, 2>);
+        if constexpr (sizeof(T) == 2)
+            if (whole(4)) {
+                vec = 2;
+                fn = a.k <= 2 ? combine_bwd_kernel<T, 2, 2, 8>
+                              : (a.k <= 4 ? combine_bwd_kernel<T, 2, 4, 4> : combine_bwd_kernel<T, 2, 8, 2>);
+            }
+    }
+    a.units = static_cast<int>(a.H / vec);
     constexpr int kWarps = kPermuteThreads / 32;
     a.segs = a.T >= kPermuteWarpsPerSm * call.sms || a.units <= 32 ? 1 : kWarps;
     a.token_ctas = token_ctas(a.T * a.segs);
     a.zero_ctas = a.out ? zero_ctas(call, a.rows) : 0;
-    void (*fn)(const PermuteArgs) = nullptr;
-    if (wide)
-        fn = a.k <= 2 ? combine_bwd_kernel<T, V, 2, 4>
-                      : (a.k <= 4 ? combine_bwd_kernel<T, V, 4, 2> : combine_bwd_kernel<T, V, 8, 1>);
-    else
-        fn = a.k <= 2 ? combine_bwd_kernel<T, 1, 2, 8>
-                      : (a.k <= 4 ? combine_bwd_kernel<T, 1, 4, 4> : combine_bwd_kernel<T, 1, 8, 4>);
     return launch_kernel(call, false, fn, a.zero_ctas + a.token_ctas, kPermuteThreads, 0, a);
 }
 

@@ -91,14 +91,18 @@ __device__ __forceinline__ void sort_fill(const SortArgs &a, const int *off, con
     }
 }
 
-// The lanes whose expert is this lane's, from a vote on each of its `bits` bits.
+// The lanes whose expert is this lane's, from votes on its `bits` bits, four at a time (a match
+// instruction instead: 4 us more for 131072 x 8 slots).
 __device__ __forceinline__ unsigned sort_peers(int e, int bits)
 {
     unsigned peers = __ballot_sync(0xffffffffu, e >= 0);
-    for (int b = 0; b < bits; ++b) {
-        const bool set = (e >> b) & 1;
-        const unsigned with = __ballot_sync(0xffffffffu, set);
-        peers &= set ? with : ~with;
+    for (int b0 = 0; b0 < bits; b0 += 4) {
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const bool set = (e >> (b0 + b)) & 1;
+            const unsigned with = __ballot_sync(0xffffffffu, set);
+            peers &= set ? with : ~with;
+        }
     }
     return peers;
 }
@@ -134,20 +138,21 @@ __global__ void __launch_bounds__(1024) sort_rank_kernel(const SortArgs a)
     for (int64_t s0 = first; s0 < last; s0 += int64_t{blockDim.x} * kSortItems) {
         int expert[kSortItems], rank[kSortItems];
         const int64_t w0 = s0 + warp * (32 * kSortItems) + lane;
+        int64_t id[kSortItems];  // all on their way before the first is looked at
 #pragma unroll
         for (int i = 0; i < kSortItems; ++i) {
             const int64_t s = w0 + i * 32;
-            int64_t e = -1;
-            if (s < last) {
-                if (a.es == a.k) {
-                    e = __ldg(a.experts + s);
-                } else {
-                    const unsigned t = static_cast<unsigned>(s) / static_cast<unsigned>(a.k);
-                    e = __ldg(a.experts + t * a.es + (s - int64_t{t} * a.k));
-                }
-                bad |= e < -1 || e >= a.E;
+            int64_t at = s;
+            if (a.es != a.k) {
+                const unsigned t = static_cast<unsigned>(s) / static_cast<unsigned>(a.k);
+                at += t * (a.es - a.k);
             }
-            expert[i] = e >= 0 && e < a.E ? static_cast<int>(e) : -1;
+            id[i] = s < last ? __ldg(a.experts + at) : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < kSortItems; ++i) {
+            bad |= id[i] < -1 || id[i] >= a.E;
+            expert[i] = id[i] >= 0 && id[i] < a.E ? static_cast<int>(id[i]) : -1;
         }
         for (int i = threadIdx.x; i < warps * hs / 2; i += static_cast<int>(blockDim.x))
             reinterpret_cast<unsigned *>(hist)[i] = 0;
@@ -231,12 +236,14 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(const SortArgs a)
     __shared__ int scan_sums[32];
     const int threads = static_cast<int>(blockDim.x), cta = static_cast<int>(blockIdx.x);
     int *total = sort_smem;          // [E] slots of each expert
-    int *before = total + a.E;       // [E] ... in earlier CTAs and rounds
+    int *before = total + a.E;       // [E] ... in earlier CTAs
     int *done = before + a.E;        // [E] ... in earlier rounds of this CTA
     int *mine = done + a.E;          // [E] ... in this round
     int *off = mine + a.E;           // [E + 1] the plan's offsets
     int *start = off + a.E + 1;      // [E + 1] the round's
-    int *list = start + a.E + 1;     // [slots of a round] by expert: expert and place in the round
+    // [E] from a slot's rank among the CTA's of its expert to its row and to its place in the list
+    int2 *to = reinterpret_cast<int2 *>(start + a.E + 1);
+    int *list = reinterpret_cast<int *>(to + a.E);  // [slots of a round] by expert: expert and place in the round
     for (int e = threadIdx.x; e < 4 * a.E; e += threads)
         total[e] = 0;
     wait_prerequisite_grid();
@@ -253,19 +260,22 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(const SortArgs a)
         }
     };
     load(first);
-    const int groups = threads / a.E, ctas = static_cast<int>(gridDim.x);
-    const int group = static_cast<int>(threadIdx.x) / a.E, own = static_cast<int>(threadIdx.x) % a.E;
-    if (group < groups) {
+    const int width = a.E < threads ? a.E : threads, groups = threads / width, ctas = static_cast<int>(gridDim.x);
+    const int group = static_cast<int>(threadIdx.x) / width;
+    for (int own = static_cast<int>(threadIdx.x) % width; group < groups && own < a.E; own += width) {
+        constexpr int kRows = 32;
         int all = 0, lower = 0;
-        for (int b0 = group; b0 < ctas; b0 += 16 * groups) {
-            int c[16];
+        for (int b0 = group; b0 < ctas; b0 += kRows * groups) {
+            int c[kRows];
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
+            for (int i = 0; i < kRows; ++i)
                 c[i] = b0 + i * groups < ctas ? __ldcg(a.table + int64_t{b0 + i * groups} * a.E + own) : 0;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < kRows; ++i) {
                 all += c[i];
                 lower += b0 + i * groups < cta ? c[i] : 0;
+                if (b0 + i * groups == cta && last - first <= round)
+                    mine[own] = c[i];  // its only round
             }
         }
         atomicAdd(total + own, all);  // integers: any order, the same sum
@@ -277,36 +287,38 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(const SortArgs a)
             for (int i = 0; i < kSortItems; ++i)
                 if (packed[i] >= 0)
                     atomicAdd(mine + (packed[i] >> kSortRankBits), 1);
-        } else {
-            for (int e = threadIdx.x; e < a.E; e += threads)
-                mine[e] = __ldcg(a.table + int64_t{cta} * a.E + e);
         }
         __syncthreads();
         if (s0 == first)
             sort_offsets(total, off, a.E, a.align, scan_sums);
         sort_offsets(mine, start, a.E, 1, scan_sums);
+        for (int e = threadIdx.x; e < a.E; e += threads)
+            to[e] = make_int2(off[e] + before[e], start[e] - done[e]);
+        __syncthreads();
 #pragma unroll
         for (int i = 0; i < kSortItems; ++i) {
             if (packed[i] < 0)
                 continue;
             const int e = packed[i] >> kSortRankBits, at = i * threads + static_cast<int>(threadIdx.x);
-            const int rank = (packed[i] & ((1 << kSortRankBits) - 1)) - done[e];
-            a.position[s0 + at] = off[e] + before[e] + rank;
-            list[start[e] + rank] = e << kSortRoundBits | at;
+            const int rank = packed[i] & ((1 << kSortRankBits) - 1);
+            const int2 by = to[e];
+            a.position[s0 + at] = by.x + rank;
+            list[by.y + rank] = e << kSortRoundBits | at;
         }
         load(s0 + round);
         __syncthreads();
         for (int i = threadIdx.x; i < start[a.E]; i += threads) {
-            const int e = list[i] >> kSortRoundBits, at = list[i] & ((1 << kSortRoundBits) - 1);
-            a.source[off[e] + before[e] + (i - start[e])] = static_cast<int>(s0) + at;
+            const int2 by = to[list[i] >> kSortRoundBits];
+            a.source[by.x - by.y + i] = static_cast<int>(s0) + (list[i] & ((1 << kSortRoundBits) - 1));
         }
         __syncthreads();
-        for (int e = threadIdx.x; e < a.E; e += threads) {
-            before[e] += mine[e];
-            done[e] += mine[e];
-            mine[e] = 0;
+        if (s0 + round < last) {
+            for (int e = threadIdx.x; e < a.E; e += threads) {
+                done[e] += mine[e];
+                mine[e] = 0;
+            }
+            __syncthreads();
         }
-        __syncthreads();
     }
     sort_fill(a, off, total);
 }
@@ -393,30 +405,39 @@ __global__ void __launch_bounds__(kPermuteThreads) dispatch_kernel(const Permute
     }
 }
 
-// VEC values of a row: 16 bytes, or one value.
+// VEC values of a row: 16 bytes, two 16-bit values, or one value.
 template <typename T, int VEC>
 struct RowUnit {
-    using Raw = std::conditional_t<VEC == 1, T, uint4>;
+    static constexpr bool kPair = VEC == 2;
+    using Raw = std::conditional_t<VEC == 1, T, std::conditional_t<kPair, unsigned, uint4>>;
     __device__ static __forceinline__ Raw load(const T *p)
     {
         if constexpr (VEC == 1)
             return *p;
         else
-            return __ldcs(reinterpret_cast<const uint4 *>(p));
+            return __ldcs(reinterpret_cast<const Raw *>(p));
     }
     __device__ static __forceinline__ void unpack(const Raw &r, float (&f)[VEC])
     {
-        if constexpr (VEC == 1)
+        if constexpr (VEC == 1) {
             f[0] = Elem<T>::load(&r);
-        else
+        } else if constexpr (kPair) {
+            float v[8];
+            Elem<T>::unpack(make_uint4(r, 0, 0, 0), v);
+            f[0] = v[0];
+            f[1] = v[1];
+        } else {
             Elem<T>::unpack(r, f);
+        }
     }
     __device__ static __forceinline__ void store(T *p, const float (&f)[VEC])
     {
         if constexpr (VEC == 1)
             Elem<T>::store(p, f[0]);
+        else if constexpr (kPair)
+            __stcs(reinterpret_cast<unsigned *>(p), Elem<T>::pack2(f[0], f[1]));
         else
-            *reinterpret_cast<uint4 *>(p) = Elem<T>::pack(f);
+            __stcs(reinterpret_cast<uint4 *>(p), Elem<T>::pack(f));
     }
 };
 
@@ -489,7 +510,7 @@ __global__ void __launch_bounds__(kPermuteThreads) combine_kernel(const PermuteA
 // time, write that row times the weight to each slot's place and add up the
 // products with each slot's y.
 template <typename T, int VEC, int KC, int U>
-__global__ void __launch_bounds__(kPermuteThreads) combine_bwd_kernel(const PermuteArgs a)
+__global__ void __launch_bounds__(kPermuteThreads, 3) combine_bwd_kernel(const PermuteArgs a)
 {
     using Unit = RowUnit<T, VEC>;
     using Raw = typename Unit::Raw;
