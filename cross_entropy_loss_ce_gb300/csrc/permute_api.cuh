@@ -12,7 +12,9 @@ constexpr int64_t kSortRound = 1024 * kSortItems;   // slots that one CTA ranks 
 constexpr int64_t kSortMaxPerCta = int64_t{1} << kSortRankBits;
 constexpr int kMaxAlign = 1024;
 constexpr int64_t kPermuteMaxCols = int64_t{1} << 24;
-constexpr int64_t kPermuteWarpsPerSm = 16;  // fewer warps than that: a lane takes one unit, not several
+// with fewer warps a lane takes one unit, not several (304 tokens, 4 x 2048 bf16: combine 2.26 us with one and two
+// units; 152: 1.96 and 2.26; 608: 2.98 and 2.78)
+constexpr int64_t kPermuteWarpsPerSm = 16;
 
 // Rows of a plan, or -1 where they pass 2^31 - 1.
 int64_t plan_rows(int64_t T, int64_t E, int64_t k, int64_t align)
@@ -120,9 +122,12 @@ cudaError_t launch_dispatch(const Call &call, const PermuteArgs &a)
 {
     const size_t es = elem_size(call.dtype);
     if (in_units(16, es, a.H, a.in, a.is, a.out, a.os)) {
-        const int64_t warps = a.T * ((a.H * static_cast<int64_t>(es) / 16 + 127) / 128);
-        return warps < kPermuteWarpsPerSm * call.sms ? launch_dispatch_as<uint4, 1>(call, a, es)
-                                                     : launch_dispatch_as<uint4, 4>(call, a, es);
+        // with stores enough behind each load one unit a lane is best (608 x 8 x 2048 bf16: 4.7 us, with four units
+        // 6.3); a token's one or two copies need more loads in flight (1216 x 2 x 4096: 4.9 us with four, 5.6)
+        const int64_t units = a.H * static_cast<int64_t>(es) / 16;
+        return a.k > 2 || units <= 32 || a.T * ((units + 127) / 128) < kPermuteWarpsPerSm * call.sms
+                   ? launch_dispatch_as<uint4, 1>(call, a, es)
+                   : launch_dispatch_as<uint4, 4>(call, a, es);
     }
     if (in_units(4, es, a.H, a.in, a.is, a.out, a.os))
         return launch_dispatch_as<unsigned, 8>(call, a, es);
@@ -141,11 +146,15 @@ cudaError_t launch_combine(const Call &call, PermuteArgs a)
     if (!in_units(16, sizeof(T), a.H, a.in, a.is, a.out, a.os)) {
         if constexpr (sizeof(T) == 2)
             if (in_units(4, sizeof(T), a.H, a.in, a.is, a.out, a.os))
-                return go(combine_kernel<T, 2, 4>, 2, 4);
-        return go(combine_kernel<T, 1, 4>, 1, 4);
+                return go(combine_kernel<T, 2, 4, 4>, 2, 4);
+        return go(combine_kernel<T, 1, 4, 4>, 1, 4);
     }
-    return a.T * ((a.H / V + 63) / 64) < kPermuteWarpsPerSm * call.sms ? go(combine_kernel<T, V, 1>, V, 1)
-                                                                       : go(combine_kernel<T, V, 2>, V, 2);
+    // as many units of a lane as the row has, or as few as leave every SM its warps; twice as many where a
+    // token has one or two rows (65536 x 2 x 2048 bf16: 148 us with two units, 134 with four)
+    const int64_t units = a.H / V;
+    if (units <= 32 || a.T * ((units + 63) / 64) < kPermuteWarpsPerSm * call.sms)
+        return go(combine_kernel<T, V, 4, 1>, V, 1);
+    return a.k <= 2 && units > 64 ? go(combine_kernel<T, V, 2, 4>, V, 4) : go(combine_kernel<T, V, 4, 2>, V, 2);
 }
 
 template <typename T>
@@ -159,9 +168,10 @@ cudaError_t launch_combine_bwd(const Call &call, PermuteArgs a)
                (!a.out || in_units(bytes, sizeof(T), a.H, a.out, a.os, a.out, a.os));
     };
     void (*fn)(const PermuteArgs) = nullptr;
-    int vec = 1;
+    int vec = 1, u = a.k <= 2 ? 8 : (a.k <= 4 ? 4 : 2);  // units of a lane
     if (whole(16)) {
         vec = V;
+        u /= 2;
         fn = a.k <= 2 ? combine_bwd_kernel<T, V, 2, 4>
                       : (a.k <= 4 ? combine_bwd_kernel<T, V, 4, 2> : combine_bwd_kernel<T, V, 8, 1>);
     } else {
@@ -174,9 +184,15 @@ cudaError_t launch_combine_bwd(const Call &call, PermuteArgs a)
                               : (a.k <= 4 ? combine_bwd_kernel<T, 2, 4, 4> : combine_bwd_kernel<T, 2, 8, 2>);
             }
     }
+    // Warps of a token: each takes two trips or more over its part of the row (16384 x 8 x 2048 bf16: 172 us
+    // with 4 warps, 193 with 8, 173 with one), one where tokens are too few to fill the SMs (152 x 8 x 4096: 5.5
+    // us with 8 warps, 19 with one)
     a.units = static_cast<int>(a.H / vec);
     constexpr int kWarps = kPermuteThreads / 32;
-    a.segs = a.T >= kPermuteWarpsPerSm * call.sms || a.units <= 32 ? 1 : kWarps;
+    const int64_t trips = a.T < 2 * call.sms ? 1 : 2, spans = (a.H / vec + 32 * u - 1) / (32 * u);
+    a.segs = 1;
+    while (a.segs < kWarps && (trips == 1 ? a.segs < spans : 2 * a.segs * trips <= spans))
+        a.segs *= 2;
     a.token_ctas = token_ctas(a.T * a.segs);
     a.zero_ctas = a.out ? zero_ctas(call, a.rows) : 0;
     return launch_kernel(call, false, fn, a.zero_ctas + a.token_ctas, kPermuteThreads, 0, a);

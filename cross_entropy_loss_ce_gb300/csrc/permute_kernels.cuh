@@ -14,7 +14,14 @@
 // All of it is memory traffic.  Both directions go by tokens: dispatch reads a
 // token's row once and writes it to its k places, combine reads the k rows
 // and writes one, so every row crosses HBM once whatever the order, and sums
-// have a fixed order (j ascending) without atomics.
+// have a fixed order (j ascending) without atomics.  Measured (bf16, H 2048
+// unless said, with 6.7 TB/s the rate of a plain copy):
+//   dispatch  8192 x 4 tokens, 23% more rows by padding   29 us, 6.8 TB/s
+//   combine   16384 x 8, H 4096                          177 us, 6.8 TB/s
+//   its gradients  16384 x 8                             172 us, 6.6 TB/s
+//   the plan  131072 x 8 slots of 256 experts             20 us in two kernels: the
+//             time of a CTA's slots one after another, not of their 17 MB; 131072
+//             slots 11 us, a single token 3 us
 #pragma once
 
 #include "row_kernels.cuh"
@@ -366,7 +373,9 @@ __device__ __forceinline__ void zero_rows(const PermuteArgs &a, int64_t os_units
     }
 }
 
-// x's rows to their places: bits are copied, so the type is that of a unit.
+// x's rows to their places: bits are copied, so the type is that of a unit.  A
+// warp takes 32 U units of a row; its stores need no waiting.  Bound by HBM.  Rows that are no slot's come first in the grid: 8192 x
+// 4 x 2048 took 41 to 54 us with them as its tail on few SMs, and takes 29.
 template <typename Raw, int U>
 __global__ void __launch_bounds__(kPermuteThreads) dispatch_kernel(const PermuteArgs a, int64_t is_units, int64_t os_units)
 {
@@ -451,9 +460,11 @@ __device__ __forceinline__ float slot_weight(const PermuteArgs &a, int64_t t, in
     return Elem<T>::load(static_cast<const T *>(a.weights) + t * a.ws + j);
 }
 
-constexpr int kCombineSlots = 4;  // rows of a token whose loads are in flight together
-
-template <typename T, int VEC, int U>
+// KC rows of a token, U units of a lane each, are in flight together: 8 loads of
+// 16 bytes a lane keep HBM busy with the 24 warps that 78 registers leave an SM.
+// (The loads are predicated; as selects they went out two by two: 240 us for
+// 177.)  A weight is applied in fp32 and the sum rounded once.
+template <typename T, int VEC, int KC, int U>
 __global__ void __launch_bounds__(kPermuteThreads) combine_kernel(const PermuteArgs a)
 {
     using Unit = RowUnit<T, VEC>;
@@ -464,19 +475,19 @@ __global__ void __launch_bounds__(kPermuteThreads) combine_kernel(const PermuteA
         const int64_t t = w / a.segs;
         const int u0 = static_cast<int>(w - t * a.segs) * (32 * U) + lane;
         float acc[U][VEC] = {};
-        for (int j0 = 0; j0 < a.k; j0 += kCombineSlots) {
-            int p[kCombineSlots];
-            float wt[kCombineSlots];
-            typename Unit::Raw v[kCombineSlots][U];
+        for (int j0 = 0; j0 < a.k; j0 += KC) {
+            int p[KC];
+            float wt[KC];
+            typename Unit::Raw v[KC][U];
 #pragma unroll
-            for (int j = 0; j < kCombineSlots; ++j) {
+            for (int j = 0; j < KC; ++j) {
                 p[j] = j0 + j < a.k ? __ldg(a.position + t * a.k + j0 + j) : -1;
                 wt[j] = j0 + j < a.k ? slot_weight<T>(a, t, j0 + j) : 0.f;
                 if (p[j] >= a.rows)
                     p[j] = -1;
             }
 #pragma unroll
-            for (int j = 0; j < kCombineSlots; ++j) {
+            for (int j = 0; j < KC; ++j) {
                 const T *y = static_cast<const T *>(a.in) + p[j] * a.is;
 #pragma unroll
                 for (int i = 0; i < U; ++i)
@@ -484,7 +495,7 @@ __global__ void __launch_bounds__(kPermuteThreads) combine_kernel(const PermuteA
                         v[j][i] = Unit::load(y + int64_t{u0 + i * 32} * VEC);
             }
 #pragma unroll
-            for (int j = 0; j < kCombineSlots; ++j) {
+            for (int j = 0; j < KC; ++j) {
                 if (p[j] < 0)
                     continue;
 #pragma unroll
@@ -505,10 +516,11 @@ __global__ void __launch_bounds__(kPermuteThreads) combine_kernel(const PermuteA
     }
 }
 
-// combine's gradients: a token belongs to `segs` warps (1, or all of a CTA),
+// combine's gradients: a token belongs to `segs` warps (1, 2, 4 or 8 of a CTA),
 // which read its row of d_out once for up to KC slots, U units of a lane at a
 // time, write that row times the weight to each slot's place and add up the
-// products with each slot's y.
+// products with each slot's y.  Three CTAs an SM and streaming stores: 185 -> 178
+// us for 16384 x 8 x 2048 bf16, four warps a token 172.
 template <typename T, int VEC, int KC, int U>
 __global__ void __launch_bounds__(kPermuteThreads, 3) combine_bwd_kernel(const PermuteArgs a)
 {
@@ -521,12 +533,14 @@ __global__ void __launch_bounds__(kPermuteThreads, 3) combine_bwd_kernel(const P
         return;
     }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int first = a.segs == 1 ? lane : warp * (32 * U) + lane;
+    const int mine = warp / a.segs, first = (warp - mine * a.segs) * (32 * U) + lane;
     const int64_t tokens = kWarps / a.segs;  // of a CTA at a time
     for (int64_t t0 = (blockIdx.x - a.zero_ctas) * tokens; t0 < a.T; t0 += a.token_ctas * tokens) {
-        const int64_t t = t0 + (a.segs == 1 ? warp : 0);
-        if (t >= a.T)
-            continue;  // segs == 1: nothing below waits for other warps
+        const bool live = t0 + mine < a.T;  // else only there for the barriers
+        if (!live && a.segs == 1)
+            continue;
+        const int64_t t = live ? t0 + mine : t0;
+        const int units = live ? a.units : 0;
         const T *g_row = static_cast<const T *>(a.d_out) + t * a.ds;
         for (int j0 = 0; j0 < a.k; j0 += KC) {
             int p[KC];
@@ -539,17 +553,17 @@ __global__ void __launch_bounds__(kPermuteThreads, 3) combine_bwd_kernel(const P
                 if (p[j] >= a.rows)
                     p[j] = -1;
             }
-            for (int u = first; u < a.units; u += 32 * U * a.segs) {
+            for (int u = first; u < units; u += 32 * U * a.segs) {
                 Raw gr[U], v[KC][U];
 #pragma unroll
                 for (int i = 0; i < U; ++i)
-                    gr[i] = u + i * 32 < a.units ? Unit::load(g_row + int64_t{u + i * 32} * VEC) : Raw{};
+                    gr[i] = u + i * 32 < units ? Unit::load(g_row + int64_t{u + i * 32} * VEC) : Raw{};
 #pragma unroll
                 for (int j = 0; j < KC; ++j) {
                     const T *y = static_cast<const T *>(a.in) + p[j] * a.is;
 #pragma unroll
                     for (int i = 0; i < U; ++i)
-                        v[j][i] = a.d_weights && p[j] >= 0 && u + i * 32 < a.units
+                        v[j][i] = a.d_weights && p[j] >= 0 && u + i * 32 < units
                                       ? Unit::load(y + int64_t{u + i * 32} * VEC)
                                       : Raw{};
                 }
@@ -564,7 +578,7 @@ __global__ void __launch_bounds__(kPermuteThreads, 3) combine_bwd_kernel(const P
 #pragma unroll
                         for (int e = 0; e < VEC; ++e)
                             dot[j] = fmaf(g[e], f[e], dot[j]);
-                        if (a.out && p[j] >= 0 && u + i * 32 < a.units) {
+                        if (a.out && p[j] >= 0 && u + i * 32 < units) {
 #pragma unroll
                             for (int e = 0; e < VEC; ++e)
                                 f[e] = wt[j] * g[e];
@@ -585,13 +599,13 @@ __global__ void __launch_bounds__(kPermuteThreads, 3) combine_bwd_kernel(const P
                     if (lane == 0)
                         part[warp][j] = dot[j];
                 __syncthreads();
-                if (warp > 0)
+                if (warp != mine * a.segs || !live)
                     continue;
 #pragma unroll
                 for (int j = 0; j < KC; ++j) {
                     dot[j] = 0.f;
-                    for (int i = 0; i < kWarps; ++i)
-                        dot[j] += part[i][j];
+                    for (int i = 0; i < a.segs; ++i)
+                        dot[j] += part[warp + i][j];
                 }
             }
 #pragma unroll

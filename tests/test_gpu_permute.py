@@ -114,8 +114,15 @@ def test_shapes(T, k, E, H, dtype):
 @pytest.mark.parametrize("T,k,H", [(2600, 2, 512), (2600, 4, 264), (2600, 8, 100), (2600, 7, 1003), (2433, 1, 33),
                                    (1300, 3, 2056)])
 def test_many_tokens(T, k, H):
-    # from 16 warps a SM on a lane takes several units, and a token's gradients one warp
+    # from 16 warps a SM on a lane takes several units
     check_all(T, k, 40, H, torch.bfloat16, align=16)
+
+
+@pytest.mark.parametrize("T,k,H", [(401, 8, 2056), (401, 4, 2048), (403, 2, 4104), (309, 8, 8200), (307, 1, 8192),
+                                   (150, 2, 1024), (151, 4, 2050), (149, 3, 3001), (7, 8, 16384)])
+def test_tokens_that_several_warps_share(T, k, H):
+    # 2, 4 and 8 warps a token, the last CTA not full; k 8 at H 2056 is one unit more than whole trips
+    check_all(T, k, 12, H, torch.bfloat16, align=4)
 
 
 @pytest.mark.parametrize("wtype", ["f32", "bf16"])
