@@ -872,6 +872,23 @@ def moe_balance_loss(logits: torch.Tensor, experts: torch.Tensor, balance_coef: 
 # a router's tokens sorted by expert and back
 
 
+def _launch(where, device, stream, *args):
+    """The library's call `where` on `device` and a stream; raises on an error.  (Small calls are
+    host time: no objects are made on the common way.)"""
+    fn = getattr(load_library(), where)
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(device.index)
+    else:
+        handle = _stream_handle(stream, device)
+    if torch._C._cuda_getDevice() == device.index:
+        rc = fn(*args, handle)
+    else:
+        with _OnDevice(device):
+            rc = fn(*args, handle)
+    if rc != OK:
+        raise GbceError(rc, where)
+
+
 class MoePlan:
     """Where a router's tokens go: ``position`` [T, k], ``source`` [R], ``offsets`` [E + 1] and
     ``counts`` [E], all int32 on one device, as moe_sort makes them (expert e's rows are
@@ -880,17 +897,16 @@ class MoePlan:
                  "slots", "rows", "experts", "align", "device")
 
     def __init__(self, position, source, offsets, counts, align: int = 1):
-        for name, t, dim in (("position", position, 2), ("source", source, 1), ("offsets", offsets, 1),
-                             ("counts", counts, 1)):
-            if t.dtype != torch.int32 or t.dim() != dim or not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous int32, {dim}-D")
-        if offsets.shape[0] != counts.shape[0] + 1:
+        for t, dim in ((position, 2), (source, 1), (offsets, 1), (counts, 1)):
+            if t.dtype is not torch.int32 or t.dim() != dim or not t.is_contiguous():
+                raise ValueError("position must be contiguous int32 and 2-D, source, offsets and counts 1-D")
+        if offsets.numel() != counts.numel() + 1:
             raise ValueError("offsets must hold one value more than counts")
         self._position, self._source, self._offsets, self._counts = position, source, offsets, counts
         self._buffer = None
         self._places = position.data_ptr(), source.data_ptr()
         self.tokens, self.slots = position.shape
-        self.rows, self.experts, self.align = source.shape[0], counts.shape[0], align
+        self.rows, self.experts, self.align = source.numel(), counts.numel(), align
         self.device = _call_device(("position", position), ("source", source), ("offsets", offsets),
                                    ("counts", counts))
 
@@ -948,15 +964,11 @@ def moe_sort(experts: torch.Tensor, n_experts: int, align: int = 1, stream=None)
     if (k > 1 and unit != 1) or (T > 1 and es < k):
         raise ValueError("experts needs unit column stride and rows that do not overlap")
     dev = _call_device(("experts", experts))
-    lib = load_library()
-    rows = lib.moe_plan_rows(T, n_experts, k, align)
+    rows = load_library().moe_plan_rows(T, n_experts, k, align)
     if rows < 0:
         raise GbceError(ERR_SIZE, "moe_sort")
     plan = MoePlan._packed(T, k, rows, n_experts, align, dev, stream)
-    with _OnDevice(dev):
-        rc = lib.moe_sort(experts.data_ptr(), max(es, k), *plan._places, T, n_experts, k, align,
-                          _stream_handle(stream, dev))
-    _check(rc, "moe_sort")
+    _launch("moe_sort", dev, stream, experts.data_ptr(), max(es, k), *plan._places, T, n_experts, k, align)
     return plan
 
 
@@ -973,7 +985,8 @@ def _plan_matrix(t, rows, plan, name):
 def _plan_output(out, name, rows, H, like, plan, stream, *inputs):
     """(out, pointer, row stride): allocated when None, else checked against the inputs."""
     if out is None:
-        out = _empty((rows, H), like.dtype, plan.device, stream)
+        out = torch.empty((rows, H), dtype=like.dtype, device=plan.device) if stream is None else \
+            _empty((rows, H), like.dtype, plan.device, stream)
         return out, out.data_ptr(), H
     p, step = _plan_matrix(out, rows, plan, name)
     if out.shape[1] != H or out.dtype != like.dtype:
@@ -998,11 +1011,8 @@ def moe_dispatch(x: torch.Tensor, plan: MoePlan, out: torch.Tensor = None, strea
     xp, xs = _plan_matrix(x, plan.tokens, plan, "x")
     H = x.shape[1]
     out, op, os_ = _plan_output(out, "out", plan.rows, H, x, plan, stream, ("x", x))
-    with _OnDevice(plan.device):
-        rc = load_library().moe_dispatch(xp, xs, plan._places[0], plan._places[1], op, os_, plan.tokens, H,
-                                         plan.slots, plan.rows, DTYPES[x.dtype],
-                                         _stream_handle(stream, plan.device))
-    _check(rc, "moe_dispatch")
+    _launch("moe_dispatch", plan.device, stream, xp, xs, plan._places[0], plan._places[1], op, os_,
+            plan.tokens, H, plan.slots, plan.rows, DTYPES[x.dtype])
     return out
 
 
@@ -1014,11 +1024,8 @@ def moe_combine(y: torch.Tensor, plan: MoePlan, weights: torch.Tensor = None, ou
     H = y.shape[1]
     wp, ws, wt = (None, 0, 0) if weights is None else _plan_weights(weights, plan, y, "weights")
     out, op, os_ = _plan_output(out, "out", plan.tokens, H, y, plan, stream, ("y", y), ("weights", weights))
-    with _OnDevice(plan.device):
-        rc = load_library().moe_combine(yp, ys, plan._places[0], wp, ws, wt, op, os_, plan.tokens, H,
-                                        plan.slots, plan.rows, DTYPES[y.dtype],
-                                        _stream_handle(stream, plan.device))
-    _check(rc, "moe_combine")
+    _launch("moe_combine", plan.device, stream, yp, ys, plan._places[0], wp, ws, wt, op, os_, plan.tokens, H,
+            plan.slots, plan.rows, DTYPES[y.dtype])
     return out
 
 
@@ -1047,11 +1054,8 @@ def moe_combine_bwd(d_out: torch.Tensor, y: torch.Tensor, plan: MoePlan, weights
         d_weights = None
     if d_y is None and d_weights is None:
         return None, None
-    with _OnDevice(plan.device):
-        rc = load_library().moe_combine_bwd(dp, ds, yp, ys, plan._places[0], plan._places[1], wp, ws, wt, dyp,
-                                            dys, dwp, dws, plan.tokens, H, plan.slots, plan.rows,
-                                            DTYPES[y.dtype], _stream_handle(stream, plan.device))
-    _check(rc, "moe_combine_bwd")
+    _launch("moe_combine_bwd", plan.device, stream, dp, ds, yp, ys, plan._places[0], plan._places[1], wp, ws, wt,
+            dyp, dys, dwp, dws, plan.tokens, H, plan.slots, plan.rows, DTYPES[y.dtype])
     return d_y, d_weights
 
 
@@ -1129,7 +1133,7 @@ def _tensor_list(tensors, name):
     if len(devices) > 1:
         raise ValueError(f"{name} are on several devices: {sorted(devices)}")
     try:
-        types = [DTYPES[t.dtype] for t in tensors]
+        types = array.array("i", [DTYPES[t.dtype] for t in tensors])
     except KeyError as e:
         raise TypeError(f"{name} must be float32, bfloat16 or float16, not {e.args[0]}") from None
     contiguous = all(map(torch.Tensor.is_contiguous, tensors))
@@ -1140,7 +1144,7 @@ def _tensor_list(tensors, name):
                                  f"of shape {tuple(t.shape)}")
     pointers = array.array("Q", map(torch.Tensor.data_ptr, tensors))
     sizes = array.array("q", map(torch.Tensor.numel, tensors))
-    return next(iter(devices), None), pointers, sizes, array.array("i", types), contiguous
+    return next(iter(devices), None), pointers, sizes, types, contiguous
 
 
 def _norm_call(where, tensors, norm_type, norm, stream, max_norm=None, eps=0.0, outs=None):
@@ -1171,9 +1175,7 @@ def _norm_call(where, tensors, norm_type, norm, stream, max_norm=None, eps=0.0, 
                 raise ValueError("outs must match the tensors in size, order of values, dtype and device")
         args.insert(1, results.buffer_info()[0])
         args += [float(max_norm), float(eps)]
-    with _OnDevice(dev):
-        rc = getattr(load_library(), where)(*args, norm.data_ptr(), _stream_handle(stream, dev))
-    _check(rc, where)
+    _launch(where, dev, stream, *args, norm.data_ptr())
     return norm
 
 
