@@ -922,9 +922,10 @@ class MoePlan:
         return self
 
     def _parts(self):
-        slots, rows, E = self.tokens * self.slots, self.rows, self.experts
-        flat, self._source, self._offsets, self._counts = \
-            self._buffer.split_with_sizes((slots, rows, E + 1, E))
+        buffer, slots, rows, E = self._buffer, self.tokens * self.slots, self.rows, self.experts
+        if buffer is None:  # another thread has been here
+            return
+        flat, self._source, self._offsets, self._counts = buffer.split_with_sizes((slots, rows, E + 1, E))
         self._position = flat.view(self.tokens, self.slots)
         self._buffer = None
 
@@ -1098,7 +1099,8 @@ class CombineTokens(torch.autograd.Function):
 
 
 def dispatch_tokens(x: torch.Tensor, plan: MoePlan) -> torch.Tensor:
-    """moe_dispatch of ``x`` [..., H], differentiable (the leading sizes hold the plan's tokens)."""
+    """moe_dispatch of ``x`` [..., H], differentiable (the leading sizes hold the plan's tokens).
+    (Captured into a CUDA graph with its backward: as for linear_cross_entropy.)"""
     return DispatchTokens.apply(x.reshape(-1, x.shape[-1]), plan)
 
 
@@ -1188,8 +1190,8 @@ def grad_norm(tensors, norm_type: float = 2.0, norm: torch.Tensor = None, stream
 
 def clip_grad_norm(tensors, max_norm: float, norm_type: float = 2.0, eps: float = 1e-6, outs=None,
                    norm: torch.Tensor = None, stream=None) -> torch.Tensor:
-    """Scales ``tensors`` by min(1, max_norm / (norm + eps)), in place or into ``outs``, and returns
-    the norm they had, as grad_norm does.  There is one out for each tensor, of the same type and,
+    """Scales ``tensors`` (gradients, not their parameters) by min(1, max_norm / (norm + eps)), in
+    place or into ``outs``, and returns the norm they had, as grad_norm does.  There is one out for each tensor, of the same type and,
     where they are not contiguous, the same shape and strides; it shares no memory with any other
     tensor.  Where the norm keeps the limit, tensors in place are not written."""
     return _norm_call("clip_grad_norm", tensors, norm_type, norm, stream, max_norm, eps, outs)

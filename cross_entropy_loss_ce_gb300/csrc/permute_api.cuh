@@ -150,11 +150,13 @@ cudaError_t launch_combine(const Call &call, PermuteArgs a)
         return go(combine_kernel<T, 1, 4, 4>, 1, 4);
     }
     // as many units of a lane as the row has, or as few as leave every SM its warps; twice as many where a
-    // token has one or two rows (65536 x 2 x 2048 bf16: 148 us with two units, 134 with four)
+    // token has one or two rows (65536 x 2 x 2048 bf16: 148 us with two units, 133 with four)
     const int64_t units = a.H / V;
     if (units <= 32 || a.T * ((units + 63) / 64) < kPermuteWarpsPerSm * call.sms)
         return go(combine_kernel<T, V, 4, 1>, V, 1);
-    return a.k <= 2 && units > 64 ? go(combine_kernel<T, V, 2, 4>, V, 4) : go(combine_kernel<T, V, 4, 2>, V, 2);
+    if (a.k > 2 || units <= 64)
+        return go(combine_kernel<T, V, 4, 2>, V, 2);
+    return a.k == 1 ? go(combine_kernel<T, V, 1, 4>, V, 4) : go(combine_kernel<T, V, 2, 4>, V, 4);
 }
 
 template <typename T>

@@ -31,7 +31,7 @@ namespace gbce {
 constexpr int kSortItems = 8;           // slots a thread holds
 constexpr int kSortMaxExperts = 1024;
 constexpr int kSortRoundBits = 13;      // a slot within a round of 1024 threads, beside 10 bits of expert
-constexpr int kSortRankBits = 21;        // a rank within a CTA's slots, beside 10 bits of expert
+constexpr int kSortRankBits = 21;       // a rank within a CTA's slots, beside 10 bits of expert
 constexpr int kPermuteThreads = 256;
 
 struct SortArgs {
@@ -374,8 +374,9 @@ __device__ __forceinline__ void zero_rows(const PermuteArgs &a, int64_t os_units
 }
 
 // x's rows to their places: bits are copied, so the type is that of a unit.  A
-// warp takes 32 U units of a row; its stores need no waiting.  Bound by HBM.  Rows that are no slot's come first in the grid: 8192 x
-// 4 x 2048 took 41 to 54 us with them as its tail on few SMs, and takes 29.
+// warp takes 32 U units of a row; its stores need no waiting.  Bound by HBM.  Rows
+// that are no slot's come first in the grid: 8192 x 4 x 2048 took 41 to 54 us with
+// them as its tail on few SMs, and takes 29.
 template <typename Raw, int U>
 __global__ void __launch_bounds__(kPermuteThreads) dispatch_kernel(const PermuteArgs a, int64_t is_units, int64_t os_units)
 {
