@@ -16,10 +16,11 @@
 //
 // Sums: a thread adds the values of a tile that it holds (32 or 64) in fp32,
 // and the tiles' sums in fp32 with the rounding errors carried (two words); the
-// threads' sums are added in fp64 in an order that the sizes and the device
-// fix.  A tile's sum below 2^-92 may have lost terms to fp32's range (64 squares
-// below 2^-126), one above 2^100 nearly so: it is taken again from values times
-// a power of two.  (fp32 numbers below 2^-126 count as 0.)
+// threads' sums are added in fp64 in an order that the sizes, the tensors' starts
+// within 16 bytes and the device fix.  A tile's sum below 2^-92 may have lost
+// terms to fp32's range (64 squares below 2^-126), one above 2^100 nearly so: it
+// is taken again from values times a power of two.  (fp32 numbers below 2^-126
+// count as 0.)
 #pragma once
 
 #include "row_kernels.cuh"

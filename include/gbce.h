@@ -655,7 +655,8 @@ GBCE_API int moe_combine_bwd(const void *d_out, int64_t d_out_stride, const void
  *
  * Squares and magnitudes are added in fp32 over 32 to 64 values, scaled by a power of
  * two where they would leave fp32's range, then with their rounding errors carried, at last
- * in fp64, in an order that the sizes and the device fix.  Values below 2^-126 count as 0.
+ * in fp64, in an order that the sizes, the tensors' starts within 16 bytes and the device
+ * fix.  Values below 2^-126 count as 0.
  */
 GBCE_API int grad_norm(const void *const *tensors, const int64_t *values, const int *dtypes, int64_t n, int kind,
                        float *norm, gbce_stream_t stream);
