@@ -34,7 +34,8 @@ int check_plan(int64_t T, int64_t E, int64_t k, int64_t align)
 
 int sort_rank_smem(int E, int threads, bool all)
 {
-    return (all ? 2 * E + 1 : E) * 4 + sort_hist_stride(E) * 2 * (threads / 32 + 1);
+    const int warps = threads / 32;
+    return (all ? 2 * E + 1 : E) * 4 + sort_hist_stride(E) * 2 * (warps + 1) + warps * E * 4;
 }
 
 int sort_place_smem(int E) { return (8 * E + 2 + static_cast<int>(kSortRound)) * 4; }
@@ -51,8 +52,9 @@ cudaError_t launch_sort(const Call &call, SortArgs a)
             return e;
         return launch_kernel(call, false, sort_rank_kernel<true>, 1, threads, smem, a);
     }
-    // a CTA's time is one slot after another of its warps: small ones, while there are few (131072 slots: 22 us
-    // with 16 CTAs of 1024 threads, 15 with 64 of 256); many CTAs make the sums before each one long
+    // a CTA's time is one slot after another of its warps: small ones, while there are few (131072 slots of 256
+    // experts, with peers still found by votes: 15 us with 64 CTAs of 256 threads, 22 with 16 of 1024); many CTAs
+    // make the sums before each one long (131072 x 8: 29 us with 256 of 512 threads, 23 with 128 of 1024)
     int threads = 256;
     while (threads < 1024 && a.n > call.sms / 2 * threads * kSortItems)
         threads *= 2;
@@ -61,18 +63,21 @@ cudaError_t launch_sort(const Call &call, SortArgs a)
     if (a.per_cta > kSortMaxPerCta)
         a.per_cta = kSortMaxPerCta;
     const int64_t ctas = (a.n + a.per_cta - 1) / a.per_cta;
+    a.one_round = a.per_cta == round;
+    const size_t row = a.one_round ? sort_hist_stride(a.E) * 2 : a.E * 4;
     PoolScratch scratch(call.stream);
-    if ((e = scratch.get(call.device, static_cast<size_t>(ctas) * a.E * sizeof(int))) != cudaSuccess)
+    if ((e = scratch.get(call.device, static_cast<size_t>(ctas) * row)) != cudaSuccess)
         return e;
-    a.table = static_cast<int *>(scratch.p);
+    a.table = scratch.p;
     e = configure_smem(reinterpret_cast<const void *>(sort_rank_kernel<false>), call.device,
                        sort_rank_smem(kSortMaxExperts, 1024, false));
     if (e == cudaSuccess)
         e = launch_kernel(call, false, sort_rank_kernel<false>, ctas, threads, sort_rank_smem(a.E, threads, false), a);
+    void (*const place)(const SortArgs) = a.one_round ? sort_place_kernel<true> : sort_place_kernel<false>;
     if (e == cudaSuccess)
-        e = configure_smem(reinterpret_cast<const void *>(sort_place_kernel), call.device, sort_place_smem(kSortMaxExperts));
+        e = configure_smem(reinterpret_cast<const void *>(place), call.device, sort_place_smem(kSortMaxExperts));
     if (e == cudaSuccess)
-        e = launch_kernel(call, true, sort_place_kernel, ctas, threads, sort_place_smem(a.E), a);
+        e = launch_kernel(call, true, place, ctas, threads, sort_place_smem(a.E), a);
     return scratch.release(e);
 }
 

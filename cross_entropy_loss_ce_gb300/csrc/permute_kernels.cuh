@@ -19,9 +19,9 @@
 //   dispatch  8192 x 4 tokens, 23% more rows by padding   29 us, 6.8 TB/s
 //   combine   16384 x 8, H 4096                          177 us, 6.8 TB/s
 //   its gradients  16384 x 8                             172 us, 6.6 TB/s
-//   the plan  131072 x 8 slots of 256 experts             20 us in two kernels: the
+//   the plan  131072 x 8 slots of 256 experts             15 us in two kernels: the
 //             time of a CTA's slots one after another, not of their 17 MB; 131072
-//             slots 11 us, a single token 3 us
+//             slots 9 us, a single token 3 us
 #pragma once
 
 #include "row_kernels.cuh"
@@ -41,7 +41,8 @@ struct SortArgs {
     int E, k, align;
     int64_t per_cta; // slots of a CTA, a multiple of its threads' kSortItems
     int rows;        // R
-    int *table;      // [gridDim.x, E] slots of each CTA and expert
+    void *table;     // slots of each CTA and expert: 16 bits, rows of sort_hist_stride(E), or 32 bits, rows of E
+    bool one_round;  // a CTA ranks its slots at once
     int *position, *source, *offsets, *counts;
 };
 
@@ -98,41 +99,30 @@ __device__ __forceinline__ void sort_fill(const SortArgs &a, const int *off, con
     }
 }
 
-// The lanes whose expert is this lane's, from votes on its `bits` bits, four at a time (a match
-// instruction instead: 4 us more for 131072 x 8 slots).
-__device__ __forceinline__ unsigned sort_peers(int e, int bits)
-{
-    unsigned peers = __ballot_sync(0xffffffffu, e >= 0);
-    for (int b0 = 0; b0 < bits; b0 += 4) {
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const bool set = (e >> (b0 + b)) & 1;
-            const unsigned with = __ballot_sync(0xffffffffu, set);
-            peers &= set ? with : ~with;
-        }
-    }
-    return peers;
-}
-
 // Ranks the slots of a CTA by expert, in their order: a warp takes 32
-// consecutive slots at a time, lanes of the same expert find each other and
-// count on from the warp's own histogram; the warps' histograms are then added
-// up in order.  ALL: this CTA holds every slot and writes the plan;
-// else expert and rank go to `position` (packed) and the CTA's counts to `table`.
+// consecutive slots at a time, lanes of the same expert find each other (each
+// sets its bit in the warp's word of that expert; with a vote on each bit of the
+// expert 131072 x 8 slots of 256 took 3 us more, with a match instruction 7) and
+// count on from the warp's own histogram; the warps' histograms are then added up
+// in order.  ALL: this CTA holds every slot and writes the plan; else expert and
+// rank go to `position` (packed) and the CTA's counts to `table`.
 template <bool ALL>
 __global__ void __launch_bounds__(1024) sort_rank_kernel(const SortArgs a)
 {
     extern __shared__ int sort_smem[];
     __shared__ int scan_sums[32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const int hs = sort_hist_stride(a.E), bits = 32 - __clz(a.E - 1);
+    const int hs = sort_hist_stride(a.E);
     int *base = sort_smem;                  // [E] slots of earlier rounds; ALL: of all
     int *off = base + a.E;                  // [E + 1], ALL
     unsigned short *chunk = reinterpret_cast<unsigned short *>(off + (ALL ? a.E + 1 : 0));  // [E]
-    unsigned short *hist = chunk + sort_hist_stride(a.E);                                  // [warps][hs]
+    unsigned short *hist = chunk + hs;                                                     // [warps][hs]
+    unsigned *bits = reinterpret_cast<unsigned *>(hist + warps * hs) + warp * a.E;         // [E] of each warp
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     for (int e = threadIdx.x; e < a.E; e += static_cast<int>(blockDim.x))
         base[e] = 0;
+    for (int e = lane; e < a.E; e += 32)
+        bits[e] = 0;
     const int64_t first = blockIdx.x * a.per_cta;
     const int64_t last = first + a.per_cta < a.n ? first + a.per_cta : a.n;
     bool bad = false;
@@ -146,15 +136,19 @@ __global__ void __launch_bounds__(1024) sort_rank_kernel(const SortArgs a)
         int expert[kSortItems], rank[kSortItems];
         const int64_t w0 = s0 + warp * (32 * kSortItems) + lane;
         int64_t id[kSortItems];  // all on their way before the first is looked at
+        if (a.es == a.k) {
+            const int64_t *p = a.experts + w0;
+            const int left = static_cast<int>(last - w0 < 32 * kSortItems ? last - w0 : 32 * kSortItems);
 #pragma unroll
-        for (int i = 0; i < kSortItems; ++i) {
-            const int64_t s = w0 + i * 32;
-            int64_t at = s;
-            if (a.es != a.k) {
+            for (int i = 0; i < kSortItems; ++i)
+                id[i] = i * 32 < left ? __ldg(p + i * 32) : -1;
+        } else {
+#pragma unroll
+            for (int i = 0; i < kSortItems; ++i) {
+                const int64_t s = w0 + i * 32;
                 const unsigned t = static_cast<unsigned>(s) / static_cast<unsigned>(a.k);
-                at += t * (a.es - a.k);
+                id[i] = s < last ? __ldg(a.experts + s + t * (a.es - a.k)) : -1;
             }
-            id[i] = s < last ? __ldg(a.experts + at) : -1;
         }
 #pragma unroll
         for (int i = 0; i < kSortItems; ++i) {
@@ -171,13 +165,17 @@ __global__ void __launch_bounds__(1024) sort_rank_kernel(const SortArgs a)
             rank[i] = 0;
             if (s0 + warp * (32 * kSortItems) + i * 32 >= last)
                 continue;  // nor has a later round
-            const unsigned peers = sort_peers(e, bits);
-            const unsigned before = peers & ((1u << lane) - 1u);
             if (e >= 0)
-                rank[i] = mine[e] + __popc(before);
+                atomicOr(bits + e, 1u << lane);
             __syncwarp();
-            if (e >= 0 && !before)
-                mine[e] = static_cast<unsigned short>(mine[e] + __popc(peers));
+            const unsigned peers = e >= 0 ? bits[e] : 0u, before = peers & ((1u << lane) - 1u);
+            const int had = e >= 0 ? mine[e] : 0;
+            rank[i] = had + __popc(before);
+            __syncwarp();
+            if (e >= 0 && !before) {  // the first of them counts them and clears the word
+                mine[e] = static_cast<unsigned short>(had + __popc(peers));
+                bits[e] = 0;
+            }
             __syncwarp();
         }
         __syncthreads();
@@ -227,9 +225,14 @@ __global__ void __launch_bounds__(1024) sort_rank_kernel(const SortArgs a)
         atomicOr(&g_flags, kFlagBadTarget);
     if constexpr (ALL) {
         sort_fill(a, off, base);
+    } else if (a.one_round) {  // counts of up to 8192, read two at a time
+        unsigned short *counts = static_cast<unsigned short *>(a.table) + int64_t{blockIdx.x} * hs;
+        for (int e = threadIdx.x; e < hs; e += static_cast<int>(blockDim.x))
+            counts[e] = e < a.E ? static_cast<unsigned short>(base[e]) : 0;
     } else {
+        int *counts = static_cast<int *>(a.table) + int64_t{blockIdx.x} * a.E;
         for (int e = threadIdx.x; e < a.E; e += static_cast<int>(blockDim.x))
-            a.table[int64_t{blockIdx.x} * a.E + e] = base[e];
+            counts[e] = base[e];
     }
 }
 
@@ -237,6 +240,8 @@ __global__ void __launch_bounds__(1024) sort_rank_kernel(const SortArgs a)
 // places the slots of the CTA of its number, a round of them at a time, sorted
 // in shared memory first: an expert's slots go to consecutive rows, so their
 // stores go out together (one by one: 4 us more for 131072 x 8 slots).
+// ONE: a.one_round.
+template <bool ONE>
 __global__ void __launch_bounds__(1024) sort_place_kernel(const SortArgs a)
 {
     extern __shared__ int sort_smem[];
@@ -267,29 +272,43 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(const SortArgs a)
         }
     };
     load(first);
-    const int width = a.E < threads ? a.E : threads, groups = threads / width, ctas = static_cast<int>(gridDim.x);
-    const int group = static_cast<int>(threadIdx.x) / width;
-    for (int own = static_cast<int>(threadIdx.x) % width; group < groups && own < a.E; own += width) {
-        constexpr int kRows = 32;
-        int all = 0, lower = 0;
+    // counts of a row: pairs of 16 bits, or single ones
+    const int entries = ONE ? sort_hist_stride(a.E) / 2 : a.E;
+    const int width = entries < threads ? entries : threads, groups = threads / width;
+    const int group = static_cast<int>(threadIdx.x) / width, ctas = static_cast<int>(gridDim.x);
+    for (int own = static_cast<int>(threadIdx.x) % width; group < groups && own < entries; own += width) {
+        constexpr int kRows = ONE ? 16 : 32;
+        int all[2] = {}, lower[2] = {};
         for (int b0 = group; b0 < ctas; b0 += kRows * groups) {
-            int c[kRows];
+            unsigned c[kRows];
 #pragma unroll
             for (int i = 0; i < kRows; ++i)
-                c[i] = b0 + i * groups < ctas ? __ldcg(a.table + int64_t{b0 + i * groups} * a.E + own) : 0;
+                c[i] = b0 + i * groups < ctas
+                           ? __ldcg(static_cast<const unsigned *>(a.table) + int64_t{b0 + i * groups} * entries + own)
+                           : 0u;
 #pragma unroll
             for (int i = 0; i < kRows; ++i) {
-                all += c[i];
-                lower += b0 + i * groups < cta ? c[i] : 0;
-                if (b0 + i * groups == cta && last - first <= round)
-                    mine[own] = c[i];  // its only round
+                const int n[2] = {static_cast<int>(ONE ? c[i] & 0xffffu : c[i]), static_cast<int>(ONE ? c[i] >> 16 : 0u)};
+#pragma unroll
+                for (int h = 0; h < (ONE ? 2 : 1); ++h) {
+                    all[h] += n[h];
+                    lower[h] += b0 + i * groups < cta ? n[h] : 0;
+                    if (ONE && b0 + i * groups == cta && 2 * own + h < a.E)
+                        mine[2 * own + h] = n[h];  // the round's
+                }
             }
         }
-        atomicAdd(total + own, all);  // integers: any order, the same sum
-        atomicAdd(before + own, lower);
+#pragma unroll
+        for (int h = 0; h < (ONE ? 2 : 1); ++h) {
+            const int e = ONE ? 2 * own + h : own;
+            if (e < a.E) {
+                atomicAdd(total + e, all[h]);  // integers: any order, the same sum
+                atomicAdd(before + e, lower[h]);
+            }
+        }
     }
     for (int64_t s0 = first; s0 < last; s0 += round) {
-        if (last - first > round) {
+        if constexpr (!ONE) {
 #pragma unroll
             for (int i = 0; i < kSortItems; ++i)
                 if (packed[i] >= 0)
@@ -312,14 +331,15 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(const SortArgs a)
             a.position[s0 + at] = by.x + rank;
             list[by.y + rank] = e << kSortRoundBits | at;
         }
-        load(s0 + round);
+        if constexpr (!ONE)
+            load(s0 + round);
         __syncthreads();
         for (int i = threadIdx.x; i < start[a.E]; i += threads) {
             const int2 by = to[list[i] >> kSortRoundBits];
             a.source[by.x - by.y + i] = static_cast<int>(s0) + (list[i] & ((1 << kSortRoundBits) - 1));
         }
-        __syncthreads();
-        if (s0 + round < last) {
+        if (!ONE && s0 + round < last) {
+            __syncthreads();
             for (int e = threadIdx.x; e < a.E; e += threads) {
                 done[e] += mine[e];
                 mine[e] = 0;

@@ -617,7 +617,8 @@ GBCE_API int moe_dispatch(const void *x, int64_t x_stride, const int32_t *positi
  *   out           [T, out_stride] of dtype, zeros for tokens without a slot.
  *                 Overlaps no input.
  *
- * Sums are fp32, j ascending, rounded once.  The weight of an empty slot is not used.
+ * Sums are fp32, j ascending, rounded once (terms and results below 2^-126 may be
+ * flushed to 0).  The weight of an empty slot is not used.
  */
 GBCE_API int moe_combine(const void *y, int64_t y_stride, const int32_t *position, const void *weights,
                          int64_t weights_stride, int weights_dtype, void *out, int64_t out_stride, int64_t T,
@@ -672,8 +673,8 @@ GBCE_API int grad_norm(const void *const *tensors, const int64_t *values, const 
  *                 Any other sharing is refused: GBCE_ERR_OVERLAP.
  *   max_norm, eps the limit and what is added to the norm, both >= 0 (else GBCE_ERR_SIZE).
  *
- * f is formed in fp64, products in fp32, rounded once.  f = 1 copies the bits, and in
- * place writes nothing.  An infinite norm makes f 0 (and infinite values NaN), a NaN makes
+ * f is formed in fp64, products in fp32, rounded once (values and results below 2^-126
+ * may be flushed to 0).  f = 1 copies the bits, and in place writes nothing.  An infinite norm makes f 0 (and infinite values NaN), a NaN makes
  * every result NaN.  Nothing is synchronised.
  */
 GBCE_API int clip_grad_norm(const void *const *tensors, void *const *outs, const int64_t *values,
