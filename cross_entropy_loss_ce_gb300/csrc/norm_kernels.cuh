@@ -12,7 +12,7 @@
 // Both passes are bound by HBM: 1.3e9 values of bf16 (2.7 GB) take 370 us to read
 // (7.2 TB/s) and 840 to scale into other memory (6.4 TB/s); a tensor and its
 // result that start at different places within 16 bytes go value by value
-// (22% slower for 0.6 GB clipped).
+// (13 to 19% slower for 0.6 and 1.2 GB clipped).
 //
 // Sums: a thread adds the values of a tile that it holds (32 or 64) in fp32,
 // and the tiles' sums in fp32 with the rounding errors carried (two words); the
@@ -27,6 +27,8 @@
 
 namespace gbce {
 
+// 8 vectors a thread and 4 CTAs an SM: 1.3e9 values read in 379 us, clipped in 1257 (4 vectors: 402 and 1279
+// with 6 CTAs, 390 and 1318 with 8; 3 CTAs of 8 vectors: 383 and 1270)
 constexpr int kNormThreads = 256;
 constexpr int kNormCtasPerSm = 4;
 constexpr int kNormVecs = 8;                             // 16-byte vectors of a tile that a thread holds
@@ -265,24 +267,27 @@ __device__ __forceinline__ T scaled(T x, const NormFactor &by)
 }
 
 // n values of memory that starts at another place within 16 bytes than its
-// result: one value at a time, kNormValues of a thread in flight.
+// result: one value at a time, kNormValues of a thread in flight, from a whole
+// line of the result on, so that a warp's store fills its sectors.
 constexpr int kNormValues = 16;
 
 template <typename T>
 __device__ __forceinline__ void scale_apart(const T *x, T *y, int n, const NormFactor &by)
 {
-    using E = Elem<T>;
+    const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(y) & 127u) / static_cast<int>(sizeof(T));
+    const int whole = mis ? 128 / static_cast<int>(sizeof(T)) - mis : 0, lead = whole < n ? whole : n;
+    if (static_cast<int>(threadIdx.x) < lead)
+        y[threadIdx.x] = scaled(x[threadIdx.x], by);
 #pragma unroll 1
-    for (int i0 = threadIdx.x; i0 < n; i0 += kNormValues * kNormThreads) {
+    for (int i0 = lead + static_cast<int>(threadIdx.x); i0 < n; i0 += kNormValues * kNormThreads) {
         T raw[kNormValues];
 #pragma unroll
         for (int i = 0; i < kNormValues; ++i)
             raw[i] = i0 + i * kNormThreads < n ? x[i0 + i * kNormThreads] : T{};
 #pragma unroll
-        for (int i = 0; i < kNormValues; ++i) {
+        for (int i = 0; i < kNormValues; ++i)
             if (i0 + i * kNormThreads < n)
                 y[i0 + i * kNormThreads] = scaled(raw[i], by);
-        }
     }
 }
 
