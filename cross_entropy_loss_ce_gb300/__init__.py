@@ -897,9 +897,13 @@ class MoePlan:
                  "slots", "rows", "experts", "align", "device")
 
     def __init__(self, position, source, offsets, counts, align: int = 1):
+        index = position.get_device()
         for t, dim in ((position, 2), (source, 1), (offsets, 1), (counts, 1)):
             if t.dtype is not torch.int32 or t.dim() != dim or not t.is_contiguous():
                 raise ValueError("position must be contiguous int32 and 2-D, source, offsets and counts 1-D")
+            if t.get_device() != index or index < 0:
+                _call_device(("position", position), ("source", source), ("offsets", offsets),
+                             ("counts", counts))  # says which is where
         if offsets.numel() != counts.numel() + 1:
             raise ValueError("offsets must hold one value more than counts")
         self._position, self._source, self._offsets, self._counts = position, source, offsets, counts
@@ -907,8 +911,7 @@ class MoePlan:
         self._places = position.data_ptr(), source.data_ptr()
         self.tokens, self.slots = position.shape
         self.rows, self.experts, self.align = source.numel(), counts.numel(), align
-        self.device = _call_device(("position", position), ("source", source), ("offsets", offsets),
-                                   ("counts", counts))
+        self.device = position.device
 
     @classmethod
     def _packed(cls, T, k, rows, E, align, device, stream):
@@ -975,7 +978,11 @@ def moe_sort(experts: torch.Tensor, n_experts: int, align: int = 1, stream=None)
 
 def _plan_matrix(t, rows, plan, name):
     """Pointer and row stride of a matrix with `rows` rows on the plan's device."""
-    p, step, n, _ = _rows(t, name)
+    if t.dim() == 2 and t.dtype in DTYPES and t.get_device() == plan.device.index:
+        (n, cols), (step, unit) = t.shape, t.stride()
+        if n == rows and unit == 1 and step >= cols:
+            return t.data_ptr(), step
+    p, step, n, _ = _rows(t, name)  # other strides that will do, or what is wrong
     if n != rows:
         raise ValueError(f"{name} has {n} rows, the plan asks for {rows}")
     if t.device != plan.device:
