@@ -326,3 +326,22 @@ def test_refusals_on_the_device():
         with pytest.raises(gbce.GbceError):
             gbce.moe_sort(ex, E, align)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("T,k,E,align", [(1, 8, 128, 1), (700, 3, 5, 16), (9000, 1, 1000, 1), (20000, 8, 61, 128)])
+def test_a_plan_in_memory_of_the_caller_and_its_neighbours(T, k, E, align):
+    ex = choose(T, k, E, 0.2)
+    ref = PlanRef(ex, E, align)
+    sizes, gap = [T * k, ref.rows, E + 1, E], 9
+    buf = torch.full((sum(sizes) + gap * 5,), 77, device="cuda", dtype=torch.int32)
+    at, parts = gap, []
+    for n in sizes:
+        parts.append(buf[at:at + n])
+        at += n + gap
+    rc = gbce.load_library().moe_sort(ex.data_ptr(), k, *[p.data_ptr() for p in parts], T, E, k, align,
+                                      torch.cuda.current_stream().cuda_stream)
+    assert rc == gbce.OK
+    ref.check(gbce.MoePlan(parts[0].view(T, k), *parts[1:], align))
+    for p in parts:
+        p.fill_(77)
+    assert bool((buf == 77).all())
