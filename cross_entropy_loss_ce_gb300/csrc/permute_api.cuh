@@ -149,10 +149,18 @@ cudaError_t launch_combine(const Call &call, PermuteArgs a)
         return launch_kernel(call, false, fn, token_ctas(a.T * a.segs), kPermuteThreads, 0, a);
     };
     if (!in_units(16, sizeof(T), a.H, a.in, a.is, a.out, a.os)) {
+        // small units: many of a lane, or its loads are too few bytes (65536 x 2 x 2046 bf16: 201 us with 4 pairs, 144
+        // with 16; 65536 x 2 x 2045: 391 with 4 values, 236 with 16; 32768 x 4 x 2045: 240 with 4, 172 with 8, 179
+        // with 16); few where that leaves warps enough (33 x 4 x 2045: 2.1 us with 4 values, 2.9 with 16)
+        const auto few = [&](int64_t units) {
+            return a.T * ((units + 511) / 512) < kPermuteWarpsPerSm * call.sms;
+        };
         if constexpr (sizeof(T) == 2)
             if (in_units(4, sizeof(T), a.H, a.in, a.is, a.out, a.os))
-                return go(combine_kernel<T, 2, 4, 4>, 2, 4);
-        return go(combine_kernel<T, 1, 4, 4>, 1, 4);
+                return few(a.H / 2) ? go(combine_kernel<T, 2, 4, 4>, 2, 4) : go(combine_kernel<T, 2, 2, 16>, 2, 16);
+        if (few(a.H))
+            return go(combine_kernel<T, 1, 4, 4>, 1, 4);
+        return a.k <= 2 ? go(combine_kernel<T, 1, 2, 16>, 1, 16) : go(combine_kernel<T, 1, 4, 8>, 1, 8);
     }
     // as many units of a lane as the row has, or as few as leave every SM its warps; twice as many where a
     // token has one or two rows (65536 x 2 x 2048 bf16: 148 us with two units, 133 with four)
@@ -175,20 +183,20 @@ cudaError_t launch_combine_bwd(const Call &call, PermuteArgs a)
                (!a.out || in_units(bytes, sizeof(T), a.H, a.out, a.os, a.out, a.os));
     };
     void (*fn)(const PermuteArgs) = nullptr;
-    int vec = 1, u = a.k <= 2 ? 8 : (a.k <= 4 ? 4 : 2);  // units of a lane
+    int vec = 1, u = a.k <= 4 ? 8 : 4;  // units of a lane
     if (whole(16)) {
         vec = V;
-        u /= 2;
+        u = a.k <= 2 ? 4 : (a.k <= 4 ? 2 : 1);
         fn = a.k <= 2 ? combine_bwd_kernel<T, V, 2, 4>
                       : (a.k <= 4 ? combine_bwd_kernel<T, V, 4, 2> : combine_bwd_kernel<T, V, 8, 1>);
     } else {
         fn = a.k <= 2 ? combine_bwd_kernel<T, 1, 2, 8>
-                      : (a.k <= 4 ? combine_bwd_kernel<T, 1, 4, 4> : combine_bwd_kernel<T, 1, 8, 2>);
+                      : (a.k <= 4 ? combine_bwd_kernel<T, 1, 4, 8> : combine_bwd_kernel<T, 1, 8, 4>);
         if constexpr (sizeof(T) == 2)
             if (whole(4)) {
                 vec = 2;
                 fn = a.k <= 2 ? combine_bwd_kernel<T, 2, 2, 8>
-                              : (a.k <= 4 ? combine_bwd_kernel<T, 2, 4, 4> : combine_bwd_kernel<T, 2, 8, 2>);
+                              : (a.k <= 4 ? combine_bwd_kernel<T, 2, 4, 8> : combine_bwd_kernel<T, 2, 8, 4>);
             }
     }
     // Warps of a token: each takes two trips or more over its part of the row (16384 x 8 x 2048 bf16: 172 us

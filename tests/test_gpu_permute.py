@@ -51,7 +51,7 @@ def check_all(T, k, E, H, dtype, align=1, empty=0.2, wtype=torch.float32, pad=0,
 
 @pytest.mark.parametrize("T,k,E", [(1, 1, 1), (1, 8, 128), (3, 2, 5), (33, 4, 64), (256, 8, 8), (257, 8, 60),
                                    (1024, 8, 17), (1025, 8, 256), (8193, 1, 1), (4097, 2, 1024), (3000, 64, 9),
-                                   (40000, 2, 512), (20000, 6, 1023)])
+                                   (40000, 2, 512), (20000, 6, 1023), (4000, 2, 1024), (8192, 1, 1000)])
 @pytest.mark.parametrize("align", [1, 128])
 def test_plans(T, k, E, align):
     for empty in (0.0, 0.4):
@@ -112,7 +112,7 @@ def test_shapes(T, k, E, H, dtype):
 
 
 @pytest.mark.parametrize("T,k,H", [(2600, 2, 512), (2600, 4, 264), (2600, 8, 100), (2600, 7, 1003), (2433, 1, 33),
-                                   (1300, 3, 2056)])
+                                   (1300, 3, 2056), (1300, 2, 1030), (1300, 5, 1030), (1300, 1, 1001), (1300, 6, 2061)])
 def test_many_tokens(T, k, H):
     # from 16 warps a SM on a lane takes several units
     check_all(T, k, 40, H, torch.bfloat16, align=16)
