@@ -80,14 +80,29 @@ __device__ __forceinline__ void sort_offsets(const int *v, int *off, int E, int 
     __syncthreads();
 }
 
+// Hands to visit(row) the rows of one expert that are no slot's, every 32nd from its `lane`-th on: its slots
+// take `total` rows from `off` on, the next expert's begin at `next`.  Plans have up to 2^31 - 1 rows, so what is
+// counted is the distance (below `align`): the row a step past the last may not be an int.
+template <typename Visit>
+__host__ __device__ __forceinline__ void sort_pad_rows(int off, int total, int next, int lane, const Visit &visit)
+{
+    const int first = off + total, pad = next - first;
+    for (int i = lane; i < pad; i += 32)
+        visit(first + i);
+}
+
+struct SortNoSlot {
+    int *source;
+    __host__ __device__ __forceinline__ void operator()(int row) const { source[row] = -1; }
+};
+
 // Rows that are no slot's: behind an expert's slots, and behind the last expert.
 __device__ __forceinline__ void sort_fill(const SortArgs &a, const int *off, const int *total)
 {
     const int lane = threadIdx.x & 31, warps = static_cast<int>(blockDim.x) >> 5;
     for (int e = static_cast<int>(blockIdx.x) * warps + static_cast<int>(threadIdx.x >> 5); a.align > 1 && e < a.E;
          e += static_cast<int>(gridDim.x) * warps)
-        for (int r = off[e] + total[e] + lane; r < off[e + 1]; r += 32)
-            a.source[r] = -1;
+        sort_pad_rows(off[e], total[e], off[e + 1], lane, SortNoSlot{a.source});
     for (int64_t r = off[a.E] + blockIdx.x * int64_t{blockDim.x} + threadIdx.x; r < a.rows;
          r += int64_t{gridDim.x} * blockDim.x)
         a.source[r] = -1;
