@@ -9,18 +9,18 @@
 // them in turn, whatever tensor they are of: many small tensors cost what one
 // of their size costs.  The table of tensors travels in the kernel's
 // parameters, so a call copies nothing to the device and can be captured.
-// Both passes are bound by HBM: 1.3e9 values of bf16 (2.7 GB) take 370 us to read
+// Both passes are bound by HBM: 1.3e9 values of bf16 (2.7 GB) take 373 us to read
 // (7.2 TB/s) and 840 to scale into other memory (6.4 TB/s); a tensor and its
 // result that start at different places within 16 bytes go value by value
 // (13 to 19% slower for 0.6 and 1.2 GB clipped).
 //
-// Sums: a thread adds the values of a tile that it holds (32 or 64) in fp32,
-// and the tiles' sums in fp32 with the rounding errors carried (two words); the
-// threads' sums are added in fp64 in an order that the sizes, the tensors' starts
+// Sums: a thread adds the values of a 16-byte vector in fp32, and those sums and
+// the tiles' in fp32 with the rounding errors carried (two words); the threads'
+// sums are added in fp64 in an order that the sizes, the tensors' starts
 // within 16 bytes and the device fix.  A tile's sum below 2^-92 may have lost
 // terms to fp32's range (64 squares below 2^-126), one above 2^100 nearly so: it
-// is taken again from values times a power of two.  (fp32 numbers below 2^-126
-// count as 0.)
+// is taken again from values times a power of two (618 us where all are).  (fp32
+// numbers below 2^-126 count as 0.)
 #pragma once
 
 #include "row_kernels.cuh"
@@ -104,17 +104,42 @@ __device__ __forceinline__ void norm_value(float x, float &s, unsigned &top)
         top = max(top, __float_as_uint(x) & 0x7fffffffu);
 }
 
+// sum += s, its rounding error to carry (exact where both are finite).
+__device__ __forceinline__ void norm_carry(float &sum, float &carry, float s)
+{
+    const float t = sum + s;
+    carry += sum >= s ? (sum - t) + s : (s - t) + sum;
+    sum = t;
+}
+
+// Adds the values of a vector, times `by` if SCALED: in fp32 within it, vector after vector with the errors
+// carried.  A chain of a tile's 64 values was 4 to 6e-8 of the sum too low for 16-bit types, whatever their
+// number: the last bits of their short squares are not spread evenly and round down more often than up.  Chains
+// of 8 leave 0.7e-8 (bf16) and 1.5e-8 (fp16).
+template <int KIND, typename T, bool SCALED>
+__device__ __forceinline__ void norm_vector(const uint4 &raw, float by, float &s, float &carry, unsigned &top)
+{
+    using E = Elem<T>;
+    constexpr int V = E::kPerVec;
+    float f[V], of_vec = 0.f;
+    E::unpack(raw, f);
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+        norm_value<KIND>(SCALED ? f[e] * by : f[e], of_vec, top);
+    if constexpr (KIND != kNormMax)
+        norm_carry(s, carry, of_vec);
+}
+
 // Adds one tile's sum, or tells that it is out of range.
 template <int KIND>
-__device__ __forceinline__ bool norm_add(NormSum &a, float s)
+__device__ __forceinline__ bool norm_add(NormSum &a, float s, float carry)
 {
     if constexpr (KIND == kNormMax)
         return true;
     if (!(s < kNormHigh) || (KIND == kNormTwo && s < kNormLow))
         return false;
-    const float t = a.sum + s;
-    a.carry += a.sum >= s ? (a.sum - t) + s : (s - t) + a.sum;
-    a.sum = t;
+    norm_carry(a.sum, a.carry, s);
+    a.carry += carry;
     return true;
 }
 
@@ -122,7 +147,6 @@ template <int KIND, typename T>
 __device__ __forceinline__ void norm_tile(const void *p, int64_t values, int64_t tile, NormSum &sum)
 {
     using E = Elem<T>;
-    constexpr int V = E::kPerVec;
     const NormGeom<T> g = norm_geom<T>(p, values);
     const T *x = static_cast<const T *>(p);
     const uint4 *v = reinterpret_cast<const uint4 *>(x + g.head);
@@ -136,7 +160,7 @@ __device__ __forceinline__ void norm_tile(const void *p, int64_t values, int64_t
 #pragma unroll
     for (int i = 0; i < kNormVecs; ++i)
         raw[i] = load(i);
-    float s = 0.f, edge = 0.f;
+    float s = 0.f, carry = 0.f, edge = 0.f;
     if (tile == 0) {  // up to 14 values before and behind the vectors
         const int tail = static_cast<int>(g.values - g.tail_start);
         const int i = static_cast<int>(threadIdx.x);
@@ -147,32 +171,25 @@ __device__ __forceinline__ void norm_tile(const void *p, int64_t values, int64_t
         norm_value<KIND>(edge, s, sum.top);
     }
 #pragma unroll
-    for (int i = 0; i < kNormVecs; ++i) {
-        float f[V];
-        E::unpack(raw[i], f);
-#pragma unroll
-        for (int e = 0; e < V; ++e)
-            norm_value<KIND>(f[e], s, sum.top);
-    }
-    if (!norm_add<KIND>(sum, s)) {
+    for (int i = 0; i < kNormVecs; ++i)
+        norm_vector<KIND, T, false>(raw[i], 1.f, s, carry, sum.top);
+    if (!norm_add<KIND>(sum, s, carry)) {
         unsigned any = __float_as_uint(edge);
 #pragma unroll
         for (int i = 0; i < kNormVecs; ++i)
             any |= raw[i].x | raw[i].y | raw[i].z | raw[i].w;
         if (any) {  // not the zeros of rows that no token used
             const float by = s < kNormLow ? kNormUp : kNormDown;
-            s = 0.f;
+            s = carry = 0.f;
             norm_value<KIND>(edge * by, s, sum.top);
+            // read again, one by one: kept, the vectors spilled 416 bytes, and two at a time cost the common path 5 us
+            // of 373 (this one 580 us for 618 with 1.3e9 values of 1e-16)
 #pragma unroll 1
-            for (int i = 0; i < kNormVecs; ++i) {
-                float f[V];
-                E::unpack(load(i), f);
-#pragma unroll
-                for (int e = 0; e < V; ++e)
-                    norm_value<KIND>(f[e] * by, s, sum.top);
-            }
+            for (int i = 0; i < kNormVecs; ++i)
+                norm_vector<KIND, T, true>(load(i), by, s, carry, sum.top);
             const double back = 1.0 / static_cast<double>(by);
-            sum.more += static_cast<double>(s) * (KIND == kNormTwo ? back * back : back);
+            const double all = static_cast<double>(s) + static_cast<double>(s < INFINITY ? carry : 0.f);
+            sum.more += all * (KIND == kNormTwo ? back * back : back);
         }
     }
 }

@@ -654,9 +654,9 @@ GBCE_API int moe_combine_bwd(const void *d_out, int64_t d_out_stride, const void
  *                 value is NaN.
  *   n, values     n <= 2^20; values[i] <= 2^40.
  *
- * Squares and magnitudes are added in fp32 over 32 to 64 values, scaled by a power of
- * two where they would leave fp32's range, then with their rounding errors carried, at last
- * in fp64, in an order that the sizes, the tensors' starts within 16 bytes and the device
+ * Squares and magnitudes are added in fp32 over the 4 or 8 values of 16 bytes, then with
+ * their rounding errors carried, scaled by a power of two where they would leave fp32's
+ * range, at last in fp64, in an order that the sizes, the tensors' starts within 16 bytes and the device
  * fix.  Values below 2^-126 count as 0.
  */
 GBCE_API int grad_norm(const void *const *tensors, const int64_t *values, const int *dtypes, int64_t n, int kind,
