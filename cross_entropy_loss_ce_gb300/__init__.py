@@ -1097,9 +1097,10 @@ class CombineTokens(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad_output):
         g = _unit_rows(grad_output.detach())
-        if not ctx.saved_tensors:
+        saved = ctx.saved_tensors  # once: a recomputed forward's can be unpacked no second time
+        if not saved:
             return moe_dispatch(g, ctx.plan), None, None
-        y, w = ctx.saved_tensors
+        y, w = saved
         dy, dw = moe_combine_bwd(g, y, ctx.plan, w, want_y=ctx.needs_input_grad[0],
                                  want_weights=ctx.needs_input_grad[2])
         return dy, None, dw
