@@ -893,7 +893,7 @@ class MoePlan:
     """Where a router's tokens go: ``position`` [T, k], ``source`` [R], ``offsets`` [E + 1] and
     ``counts`` [E], all int32 on one device, as moe_sort makes them (expert e's rows are
     offsets[e] .. offsets[e] + counts[e], offsets[e + 1] being a multiple of ``align``)."""
-    __slots__ = ("_position", "_source", "_offsets", "_counts", "_buffer", "_places", "tokens",
+    __slots__ = ("_position", "_source", "_offsets", "_counts", "_buffer", "_kept", "_places", "tokens",
                  "slots", "rows", "experts", "align", "device")
 
     def __init__(self, position, source, offsets, counts, align: int = 1):
@@ -907,7 +907,7 @@ class MoePlan:
         if offsets.numel() != counts.numel() + 1:
             raise ValueError("offsets must hold one value more than counts")
         self._position, self._source, self._offsets, self._counts = position, source, offsets, counts
-        self._buffer = None
+        self._buffer, self._kept = None, (position, source)
         self._places = position.data_ptr(), source.data_ptr()
         self.tokens, self.slots = position.shape
         self.rows, self.experts, self.align = source.numel(), counts.numel(), align
@@ -915,14 +915,28 @@ class MoePlan:
 
     @classmethod
     def _packed(cls, T, k, rows, E, align, device, stream):
+        """A plan whose four parts lie in one buffer, made here."""
+        return cls._in_buffer(_empty((T * k + rows + 2 * E + 1,), torch.int32, device, stream), T, k, rows, E, align)
+
+    @classmethod
+    def _in_buffer(cls, buffer, T, k, rows, E, align):
         """A plan whose four parts lie in one buffer; tensors are made of them when one is asked for."""
         self = cls.__new__(cls)
-        self._buffer = _empty((T * k + rows + 2 * E + 1,), torch.int32, device, stream)
-        p = self._buffer.data_ptr()
+        self._buffer, self._kept = buffer, (buffer,)
+        p = buffer.data_ptr()
         self._places = p, p + 4 * T * k, p + 4 * (T * k + rows), p + 4 * (T * k + rows + E + 1)
         self.tokens, self.slots, self.rows, self.experts = T, k, rows, E
-        self.align, self.device = align, self._buffer.device
+        self.align, self.device = align, buffer.device
         return self
+
+    def _of(self, kept):
+        """The plan of what autograd saved of it (its ``_kept``): itself, or one of the copies that hooks
+        on saved tensors gave back."""
+        if all(a.data_ptr() == b.data_ptr() for a, b in zip(kept, self._kept)):
+            return self
+        if len(kept) == 1:
+            return MoePlan._in_buffer(*kept, self.tokens, self.slots, self.rows, self.experts, self.align)
+        return MoePlan(*kept, self._offsets, self._counts, self.align)
 
     def _parts(self):
         buffer, slots, rows, E = self._buffer, self.tokens * self.slots, self.rows, self.experts
@@ -1068,29 +1082,31 @@ def moe_combine_bwd(d_out: torch.Tensor, y: torch.Tensor, plan: MoePlan, weights
 
 
 class DispatchTokens(torch.autograd.Function):
-    """Autograd form of moe_dispatch."""
+    """Autograd form of moe_dispatch; saves the plan's memory, so one that is written to before
+    the backward is refused there."""
 
     @staticmethod
     def forward(ctx, x, plan):
         ctx.plan = plan
+        ctx.save_for_backward(*plan._kept)
         return moe_dispatch(_unit_rows(x.detach()), plan)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad_output):
-        return moe_combine(_unit_rows(grad_output.detach()), ctx.plan), None
+        return moe_combine(_unit_rows(grad_output.detach()), ctx.plan._of(ctx.saved_tensors)), None
 
 
 class CombineTokens(torch.autograd.Function):
-    """Autograd form of moe_combine; saves the rows and the weights, so backward may run more
-    than once."""
+    """Autograd form of moe_combine; saves the rows, the weights and the plan's memory, so backward
+    may run more than once and refuses what was written to before it."""
 
     @staticmethod
     def forward(ctx, y, plan, weights=None):
         y = _unit_rows(y.detach())
         w = None if weights is None else _unit_rows(weights.detach())
         ctx.plan = plan
-        ctx.save_for_backward(*(() if w is None else (y, w)))
+        ctx.save_for_backward(*plan._kept, *(() if w is None else (y, w)))
         return moe_combine(y, plan, w)
 
     @staticmethod
@@ -1098,10 +1114,12 @@ class CombineTokens(torch.autograd.Function):
     def backward(ctx, grad_output):
         g = _unit_rows(grad_output.detach())
         saved = ctx.saved_tensors  # once: a recomputed forward's can be unpacked no second time
+        n = len(ctx.plan._kept)
+        plan, saved = ctx.plan._of(saved[:n]), saved[n:]
         if not saved:
-            return moe_dispatch(g, ctx.plan), None, None
+            return moe_dispatch(g, plan), None, None
         y, w = saved
-        dy, dw = moe_combine_bwd(g, y, ctx.plan, w, want_y=ctx.needs_input_grad[0],
+        dy, dw = moe_combine_bwd(g, y, plan, w, want_y=ctx.needs_input_grad[0],
                                  want_weights=ctx.needs_input_grad[2])
         return dy, None, dw
 

@@ -30,3 +30,44 @@ def test_recomputed_forward():
     want = combine_bwd_ref(x, y.detach(), ref.position, w.detach())
     near(d_y, *want[0], "d_y")
     near(d_w, *want[1], "d_weights")
+
+
+def of_parts(plan):
+    return gbce.MoePlan(plan.position.clone(), plan.source.clone(), plan.offsets.clone(), plan.counts.clone(),
+                        plan.align)
+
+
+@pytest.mark.parametrize("own", [True, False])  # a plan of moe_sort, and one of the caller's tensors
+@pytest.mark.parametrize("part", ["position", "source"])
+def test_a_plan_that_changed_before_the_backward_is_refused(own, part):
+    plan, _, x, y, w = operands()
+    if not own:
+        plan = of_parts(plan)
+    x, y, w = x.requires_grad_(), y.requires_grad_(), w.requires_grad_()
+    outs = [gbce.dispatch_tokens(x, plan), gbce.combine_tokens(y, plan, w), gbce.combine_tokens(y, plan)]
+    torch.autograd.grad(outs[0].sum(), x, retain_graph=True)
+    getattr(plan, part).fill_(0)
+    for out, leaf in zip(outs, (x, y, y)):
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            torch.autograd.grad(out.sum(), leaf)
+
+
+@pytest.mark.parametrize("own", [True, False])
+def test_backward_from_what_hooks_kept(own):
+    # hooks that move saved tensors away: the plan may then change, the gradients are of the one that was saved
+    plan, ref, x, y, w = operands()
+    if not own:
+        plan = of_parts(plan)
+    x, y, w = x.requires_grad_(), y.requires_grad_(), w.requires_grad_()
+    with torch.autograd.graph.save_on_cpu():
+        rows, out, bare = gbce.dispatch_tokens(x, plan), gbce.combine_tokens(y, plan, w), gbce.combine_tokens(y, plan)
+    plan.position.fill_(-1)
+    plan.source.fill_(-1)
+    near(torch.autograd.grad(rows, x, y.detach())[0], *combine_ref(y.detach(), ref.position, None), "d_x")
+    d_y, d_w = torch.autograd.grad(out, (y, w), x.detach())
+    want = combine_bwd_ref(x.detach(), y.detach(), ref.position, w.detach())
+    near(d_y, *want[0], "d_y")
+    near(d_w, *want[1], "d_weights")
+    (d_bare,) = torch.autograd.grad(bare, y, x.detach())
+    token = ref.source.long().clamp_min(0) // k
+    assert torch.equal(d_bare, torch.where((ref.source >= 0)[:, None], x.detach()[token], 0.0))
