@@ -1056,17 +1056,22 @@ def moe_combine_bwd(d_out: torch.Tensor, y: torch.Tensor, plan: MoePlan, weights
                     d_weights: torch.Tensor = None, stream=None):
     """(d_y, d_weights) of moe_combine with weights, for the incoming ``d_out`` [T, H]; rows of
     d_y that are no slot's are zeros, and so are the gradients of empty slots' weights.  A
-    gradient that is not wanted is None."""
+    gradient that is not wanted is None; ``y`` is read for the weights' only, and may be None
+    without."""
     dp, ds = _plan_matrix(d_out, plan.tokens, plan, "d_out")
-    yp, ys = _plan_matrix(y, plan.rows, plan, "y")
-    H = y.shape[1]
-    if d_out.shape[1] != H or d_out.dtype != y.dtype:
-        raise ValueError(f"d_out must be {y.dtype} of {H} columns, as y")
-    wp, ws, wt = _plan_weights(weights, plan, y, "weights")
+    H = d_out.shape[1]
+    yp, ys = None, 0
+    if y is not None:
+        yp, ys = _plan_matrix(y, plan.rows, plan, "y")
+        if y.shape[1] != H or d_out.dtype != y.dtype:
+            raise ValueError(f"d_out must be {y.dtype} of {y.shape[1]} columns, as y")
+    elif want_weights:
+        raise ValueError("y is needed for the weights' gradient")
+    wp, ws, wt = _plan_weights(weights, plan, d_out, "weights")
     inputs = ("d_out", d_out), ("y", y), ("weights", weights)
     dyp, dys, dwp, dws = None, 0, None, 0
     if want_y:
-        d_y, dyp, dys = _plan_output(d_y, "d_y", plan.rows, H, y, plan, stream, *inputs)
+        d_y, dyp, dys = _plan_output(d_y, "d_y", plan.rows, H, d_out, plan, stream, *inputs)
     else:
         d_y = None
     if want_weights:
@@ -1077,7 +1082,7 @@ def moe_combine_bwd(d_out: torch.Tensor, y: torch.Tensor, plan: MoePlan, weights
     if d_y is None and d_weights is None:
         return None, None
     _launch("moe_combine_bwd", plan.device, stream, dp, ds, yp, ys, plan._places[0], plan._places[1], wp, ws, wt,
-            dyp, dys, dwp, dws, plan.tokens, H, plan.slots, plan.rows, DTYPES[y.dtype])
+            dyp, dys, dwp, dws, plan.tokens, H, plan.slots, plan.rows, DTYPES[d_out.dtype])
     return d_y, d_weights
 
 
@@ -1098,15 +1103,17 @@ class DispatchTokens(torch.autograd.Function):
 
 
 class CombineTokens(torch.autograd.Function):
-    """Autograd form of moe_combine; saves the rows, the weights and the plan's memory, so backward
-    may run more than once and refuses what was written to before it."""
+    """Autograd form of moe_combine; saves the weights, the plan's memory and, where the weights
+    need a gradient, the rows, so backward may run more than once and refuses what was written to
+    before it."""
 
     @staticmethod
     def forward(ctx, y, plan, weights=None):
         y = _unit_rows(y.detach())
         w = None if weights is None else _unit_rows(weights.detach())
         ctx.plan = plan
-        ctx.save_for_backward(*plan._kept, *(() if w is None else (y, w)))
+        rows = (y,) if w is not None and ctx.needs_input_grad[2] else ()
+        ctx.save_for_backward(*plan._kept, *(() if w is None else (w,)), *rows)
         return moe_combine(y, plan, w)
 
     @staticmethod
@@ -1118,7 +1125,7 @@ class CombineTokens(torch.autograd.Function):
         plan, saved = ctx.plan._of(saved[:n]), saved[n:]
         if not saved:
             return moe_dispatch(g, plan), None, None
-        y, w = saved
+        w, y = saved if len(saved) == 2 else (*saved, None)
         dy, dw = moe_combine_bwd(g, y, plan, w, want_y=ctx.needs_input_grad[0],
                                  want_weights=ctx.needs_input_grad[2])
         return dy, None, dw

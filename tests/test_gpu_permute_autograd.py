@@ -1,4 +1,6 @@
 """What the autograd forms of the expert permutation keep between forward and backward (GPU)."""
+import gc
+
 import pytest
 import torch
 from torch.utils.checkpoint import checkpoint
@@ -71,3 +73,43 @@ def test_backward_from_what_hooks_kept(own):
     (d_bare,) = torch.autograd.grad(bare, y, x.detach())
     token = ref.source.long().clamp_min(0) // k
     assert torch.equal(d_bare, torch.where((ref.source >= 0)[:, None], x.detach()[token], 0.0))
+
+
+@pytest.mark.parametrize("weighted", [True, False])
+def test_rows_are_kept_for_the_weights_gradient_only(weighted):
+    plan, ref, x, y, w = operands(torch.bfloat16)
+    gc.collect()
+    leaf = y.requires_grad_()
+    rows = leaf * 1  # an activation that nothing else keeps
+    size = rows.untyped_storage().nbytes()
+    out = gbce.combine_tokens(rows, plan, w if weighted else None)
+    after = torch.cuda.memory_allocated()
+    del rows
+    gc.collect()
+    assert torch.cuda.memory_allocated() <= after - size
+    (d_y,) = torch.autograd.grad(out, leaf, x)
+    (want, tol), _ = combine_bwd_ref(x, y.detach(), ref.position, w if weighted else torch.ones_like(w))
+    near(d_y, want, tol, "d_y")
+
+
+def test_rows_may_change_where_no_gradient_needs_them():
+    plan, ref, x, y, w = operands()
+    leaf = y.requires_grad_()
+    rows = leaf * 1
+    out = gbce.combine_tokens(rows, plan, w)
+    rows.detach().zero_()
+    (d_y,) = torch.autograd.grad(out, leaf, x)
+    near(d_y, *combine_bwd_ref(x, y.detach(), ref.position, w)[0], "d_y")
+
+
+def test_gradient_of_the_rows_without_the_rows():
+    plan, ref, x, y, w = operands(torch.float16)
+    d_y, d_w = gbce.moe_combine_bwd(x, None, plan, w, want_weights=False)
+    assert d_w is None and torch.equal(d_y, gbce.moe_combine_bwd(x, y, plan, w)[0])
+    with pytest.raises(ValueError, match="y is needed"):
+        gbce.moe_combine_bwd(x, None, plan, w)
+    with pytest.raises(ValueError, match="y is needed"):
+        gbce.moe_combine_bwd(x, None, plan, w, want_y=False)
+    buf = torch.zeros(plan.rows, H, device="cuda")
+    with pytest.raises(ValueError, match="shares memory with d_out"):
+        gbce.moe_combine_bwd(buf[:T], None, plan, w, want_weights=False, d_y=buf)
