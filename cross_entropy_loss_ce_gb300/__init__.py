@@ -1182,6 +1182,15 @@ def _tensor_list(tensors, name):
     return next(iter(devices), None), pointers, sizes, types, contiguous
 
 
+def _writable(tensors, name):
+    """Raises ValueError where parameters would be written to: torch.nn.utils.clip_grad_norm_ takes
+    parameters and scales their gradients, clip_grad_norm takes the gradients."""
+    for t in tensors:
+        if t.requires_grad and t.is_leaf:
+            raise ValueError(f"{name} hold leaves that require gradients: clip_grad_norm takes gradients, "
+                             "not their parameters")
+
+
 def _norm_call(where, tensors, norm_type, norm, stream, max_norm=None, eps=0.0, outs=None):
     kind = NORMS.get(float(norm_type))
     if kind is None:
@@ -1201,6 +1210,7 @@ def _norm_call(where, tensors, norm_type, norm, stream, max_norm=None, eps=0.0, 
     dev = _call_device(("norm", norm), ("tensors", tensors[0] if tensors else None))
     args = [pointers.buffer_info()[0], sizes.buffer_info()[0], types.buffer_info()[0], len(tensors), kind]
     if max_norm is not None:
+        _writable(tensors if outs is None else outs, "tensors" if outs is None else "outs")
         results = pointers
         if outs is not None:
             out_index, results, out_sizes, out_types, out_contiguous = _tensor_list(outs, "outs")
@@ -1223,8 +1233,9 @@ def grad_norm(tensors, norm_type: float = 2.0, norm: torch.Tensor = None, stream
 
 def clip_grad_norm(tensors, max_norm: float, norm_type: float = 2.0, eps: float = 1e-6, outs=None,
                    norm: torch.Tensor = None, stream=None) -> torch.Tensor:
-    """Scales ``tensors`` (gradients, not their parameters) by min(1, max_norm / (norm + eps)), in
-    place or into ``outs``, and returns the norm they had, as grad_norm does.  There is one out for each tensor, of the same type and,
-    where they are not contiguous, the same shape and strides; it shares no memory with any other
-    tensor.  Where the norm keeps the limit, tensors in place are not written."""
+    """Scales ``tensors`` (gradients, not their parameters: leaves that require gradients are not
+    written to) by min(1, max_norm / (norm + eps)), in place or into ``outs``, and returns the norm
+    they had, as grad_norm does.  There is one out for each tensor, of the same type and, where they
+    are not contiguous, the same shape and strides; it shares no memory with any other tensor.
+    Where the norm keeps the limit, tensors in place are not written."""
     return _norm_call("clip_grad_norm", tensors, norm_type, norm, stream, max_norm, eps, outs)

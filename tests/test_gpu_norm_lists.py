@@ -1,0 +1,33 @@
+"""Lists that clip_grad_norm takes and refuses (GPU)."""
+import pytest
+import torch
+
+import cross_entropy_loss_ce_gb300 as gbce
+from permute_ref import near, norm_ref
+
+pytestmark = pytest.mark.gpu
+
+
+def test_parameters_are_refused_where_their_gradients_are_meant():
+    layer = torch.nn.Linear(64, 32, device="cuda")
+    layer(torch.ones(4, 64, device="cuda")).sum().backward()
+    before = [p.detach().clone() for p in layer.parameters()]
+    for call in (lambda: gbce.clip_grad_norm(layer.parameters(), 1e-3),
+                 lambda: gbce.clip_grad_norm(list(layer.parameters()), 1e-3),
+                 lambda: gbce.clip_grad_norm(layer.weight, 1e-3),
+                 lambda: gbce.clip_grad_norm([layer.weight.grad], 1e-3, outs=[layer.weight]),
+                 lambda: gbce.clip_grad_norm([layer.weight.grad, layer.bias], 1e-3,
+                                             outs=[layer.weight.grad, layer.bias])):
+        with pytest.raises(ValueError, match="require gradients"):
+            call()
+    with torch.no_grad(), pytest.raises(ValueError, match="require gradients"):
+        gbce.clip_grad_norm(layer.parameters(), 1e-3)
+    assert all(torch.equal(p, b) for p, b in zip(layer.parameters(), before))
+    # what is only read may be a parameter, and what a caller has detached is its own affair
+    near(gbce.grad_norm(layer.parameters()), norm_ref(before, 2.0)[0].cuda(), 1e-5, "norm")
+    gbce.clip_grad_norm(layer.parameters(), 1e-3, outs=[torch.empty_like(p) for p in layer.parameters()])
+    assert all(torch.equal(p, b) for p, b in zip(layer.parameters(), before))
+    gbce.clip_grad_norm([p.grad for p in layer.parameters()], 1e-3)
+    near(gbce.grad_norm([p.grad for p in layer.parameters()]), torch.tensor(1e-3, dtype=torch.float64).cuda(), 1e-6, "norm")
+    gbce.clip_grad_norm([p.detach() for p in layer.parameters()], 1e-3)
+    assert not torch.equal(layer.weight, before[0])
