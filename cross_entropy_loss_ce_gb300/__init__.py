@@ -1159,6 +1159,13 @@ def _dense(t):
     return True
 
 
+def _same_order(t, o):
+    """Do the values of two tensors that each fill one stretch of memory lie there in the same order?
+    (The stride of an axis of one says nothing.)"""
+    return t.is_contiguous() and o.is_contiguous() or t.shape == o.shape and \
+        all(a == b for n, a, b in zip(t.shape, t.stride(), o.stride()) if n != 1)
+
+
 def _tensor_list(tensors, name):
     """(device index or None, pointers, sizes, types, whether all are contiguous) of the tensors of
     a call on many; a list at a time, as a model has hundreds."""
@@ -1215,8 +1222,7 @@ def _norm_call(where, tensors, norm_type, norm, stream, max_norm=None, eps=0.0, 
         if outs is not None:
             out_index, results, out_sizes, out_types, out_contiguous = _tensor_list(outs, "outs")
             if out_index != index or out_types != types or out_sizes != sizes or \
-                    not (contiguous and out_contiguous) and \
-                    [(o.shape, o.stride()) for o in outs] != [(t.shape, t.stride()) for t in tensors]:
+                    not (contiguous and out_contiguous or all(map(_same_order, tensors, outs))):
                 raise ValueError("outs must match the tensors in size, order of values, dtype and device")
         args.insert(1, results.buffer_info()[0])
         args += [float(max_norm), float(eps)]

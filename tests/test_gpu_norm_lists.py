@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import cross_entropy_loss_ce_gb300 as gbce
-from permute_ref import near, norm_ref
+from permute_ref import clip_ref, near, norm_ref
 
 pytestmark = pytest.mark.gpu
 
@@ -31,3 +31,21 @@ def test_parameters_are_refused_where_their_gradients_are_meant():
     near(gbce.grad_norm([p.grad for p in layer.parameters()]), torch.tensor(1e-3, dtype=torch.float64).cuda(), 1e-6, "norm")
     gbce.clip_grad_norm([p.detach() for p in layer.parameters()], 1e-3)
     assert not torch.equal(layer.weight, before[0])
+
+
+def test_each_out_is_compared_with_its_own_tensor():
+    g = torch.Generator("cuda").manual_seed(3)
+    w = torch.randn(64, 32, device="cuda", generator=g).t()  # not contiguous
+    v = torch.randn(6, 10, device="cuda", generator=g)
+    one = torch.randn(1, 8, 5, device="cuda", generator=g).transpose(1, 2)
+    outs = [torch.empty(64, 32, device="cuda").t(), torch.empty(60, device="cuda"),
+            torch.empty(8, 5, device="cuda").t()[None]]  # the same order, another stride of the axis of one
+    assert one.stride() != outs[2].stride()
+    want, rel = norm_ref([w, v, one], 2.0)
+    gbce.clip_grad_norm([w, v, one], 1.0, outs=outs)
+    for t, o in zip((w, v, one), outs):
+        ref, tol = clip_ref(t.reshape(-1), want, rel, 1.0, 1e-6)
+        near(o.reshape(-1), ref, tol, "clipped")
+    for bad in (torch.empty(32, 64, device="cuda"), torch.empty(2048, device="cuda"), torch.empty(64, 32, device="cuda")):
+        with pytest.raises(ValueError, match="outs must match"):
+            gbce.clip_grad_norm([w, v], 1.0, outs=[bad, outs[1]])
