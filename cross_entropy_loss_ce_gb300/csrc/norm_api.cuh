@@ -142,15 +142,26 @@ cudaError_t launch_norm(const Call &call, const TensorList &l, float *norm, doub
         return launch_kernel(call, early, norm_parts_kernel<KIND, N>, grid, kNormThreads, 0, t, here);
     });
     float *result = norm;  // written by the first of the scaling kernels
+    const double *total = part;
+    int totals = at;
+    const auto finish = [&](double *sum) {
+        e = launch_kernel(call, at > 0, norm_finish_kernel<KIND>, 1, kNormThreads, 0, part, at, result, sum);
+        result = nullptr;
+    };
+    if (e == cudaSuccess && l.out && !one && at > 0) {  // not by every CTA of every table's kernel
+        finish(part + at);
+        total = part + at;
+        totals = 1;
+    }
     if (l.out)
         each([&](int64_t grid) {
             float *here = result;
             result = nullptr;
-            return launch_kernel(call, true, norm_scale_kernel<KIND, N>, grid, kNormThreads, 0, t, part, at, here,
+            return launch_kernel(call, true, norm_scale_kernel<KIND, N>, grid, kNormThreads, 0, t, total, totals, here,
                                  max_norm, eps, in_place);
         });
     if (e == cudaSuccess && result)
-        e = launch_kernel(call, at > 0, norm_finish_kernel<KIND>, 1, kNormThreads, 0, part, at, result);
+        finish(nullptr);
     return scratch.release(e);
 }
 

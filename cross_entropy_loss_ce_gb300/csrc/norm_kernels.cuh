@@ -6,9 +6,10 @@
 // The factor needs every value before the first result, so the clipped form
 // reads twice and writes once; tensors that fit in L2 come from HBM once.  The
 // tensors are cut into tiles of 32 KB and a grid of the device's size takes
-// them in turn, whatever tensor they are of: many small tensors cost what one
-// of their size costs.  The table of tensors travels in the kernel's
-// parameters, so a call copies nothing to the device and can be captured.
+// them in turn, whatever tensor they are of; a tensor below that costs a tile.
+// The table of up to 1024 tensors travels in the kernel's parameters, so a call
+// copies nothing to the device and can be captured; a longer list takes a launch
+// for each 1024, twice when it is clipped.
 // Both passes are bound by HBM: 1.3e9 values of bf16 (2.7 GB) take 373 us to read
 // (7.2 TB/s) and 840 to scale into other memory (6.4 TB/s); a tensor and its
 // result that start at different places within 16 bytes go value by value
@@ -260,12 +261,16 @@ __device__ __forceinline__ double norm_root(double v)
 }
 
 template <int KIND>
-__global__ void __launch_bounds__(kNormThreads) norm_finish_kernel(const double *part, int parts, float *norm)
+__global__ void __launch_bounds__(kNormThreads) norm_finish_kernel(const double *part, int parts, float *norm,
+                                                                   double *total)
 {
     wait_prerequisite_grid();
     const double n = norm_total<KIND>(part, parts);
-    if (threadIdx.x == 0)
+    if (threadIdx.x == 0) {
         *norm = static_cast<float>(norm_root<KIND>(n));
+        if (total)
+            *total = n;
+    }
 }
 
 // f as two fp32 factors, the second a power of two: 1, or 2^-100 where f is

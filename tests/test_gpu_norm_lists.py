@@ -1,4 +1,6 @@
-"""Lists that clip_grad_norm takes and refuses (GPU)."""
+"""Lists that clip_grad_norm takes and refuses, and what long ones cost (GPU)."""
+import ctypes
+
 import pytest
 import torch
 
@@ -49,3 +51,39 @@ def test_each_out_is_compared_with_its_own_tensor():
     for bad in (torch.empty(32, 64, device="cuda"), torch.empty(2048, device="cuda"), torch.empty(64, 32, device="cuda")):
         with pytest.raises(ValueError, match="outs must match"):
             gbce.clip_grad_norm([w, v], 1.0, outs=[bad, outs[1]])
+
+
+def test_long_lists_cost_what_their_tables_cost():
+    # 2^18 tensors of a few values: 256 launches of each kernel.  Clipping launches twice what the norm does, and each
+    # of its launches may add up what that one launch's kernels left, not what all did.
+    n, lib = 2 ** 18, gbce.load_library()
+    src = torch.randn(n, 4, device="cuda", generator=torch.Generator("cuda").manual_seed(7))
+    dst, norm = torch.zeros_like(src), torch.zeros((), device="cuda")
+    ins = (ctypes.c_uint64 * n)(*range(src.data_ptr(), src.data_ptr() + 16 * n, 16))
+    outs = (ctypes.c_uint64 * n)(*range(dst.data_ptr(), dst.data_ptr() + 16 * n, 16))
+    sizes, types = (ctypes.c_int64 * n)(*[4] * n), (ctypes.c_int * n)()
+    s = torch.cuda.current_stream().cuda_stream
+
+    def read():
+        assert lib.grad_norm(ins, sizes, types, n, 0, norm.data_ptr(), s) == gbce.OK
+
+    def clip():
+        assert lib.clip_grad_norm(ins, outs, sizes, types, n, 0, 1.0, 1e-6, norm.data_ptr(), s) == gbce.OK
+
+    def ms(call):
+        times = []
+        for _ in range(4):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            torch.cuda.synchronize()
+            torch.cuda._sleep(100_000_000)  # the host is ahead: its time is not counted
+            a.record()
+            call()
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b))
+        return min(times)
+    of_read, of_clip = ms(read), ms(clip)
+    want, rel = norm_ref([src], 2.0)
+    near(norm, want.cuda(), (rel + 2.0 ** -24) * float(want), "norm")
+    near(dst, *clip_ref(src, want, rel, 1.0, 1e-6), "clipped")
+    assert of_clip < 6 * of_read, (of_read, of_clip)
