@@ -81,6 +81,29 @@ cudaError_t launch_sort(const Call &call, SortArgs a)
     return scratch.release(e);
 }
 
+// Do two of a plan's arrays, each from its first value to its last, share memory?  The second kernel follows what the
+// first left in `position`, into shared memory too.
+bool plan_arrays_overlap(const SortArgs &a)
+{
+    constexpr int64_t kMost = INT64_MAX / 16;  // of values: past any address
+    const int64_t tokens = a.n / a.k, before = tokens > 0 && tokens - 1 <= kMost / a.es ? (tokens - 1) * a.es : kMost;
+    const struct {
+        const void *p;
+        int64_t bytes;
+    } arrays[] = {{a.experts, tokens > 0 ? (before + a.k) * 8 : 0},
+                  {a.position, a.n * 4},
+                  {a.source, int64_t{a.rows} * 4},
+                  {a.offsets, (a.E + 1) * 4},
+                  {a.counts, a.E * 4}};
+    for (const auto &x : arrays)
+        for (const auto &y : arrays) {
+            const uintptr_t p = reinterpret_cast<uintptr_t>(x.p), q = reinterpret_cast<uintptr_t>(y.p);
+            if (&x != &y && x.bytes > 0 && y.bytes > 0 && p <= q && q - p < static_cast<uintptr_t>(x.bytes))
+                return true;
+        }
+    return false;
+}
+
 int check_permute(int64_t T, int64_t H, int64_t k, int64_t rows, int dtype)
 {
     const int st = check_common(T, H, dtype);
@@ -246,10 +269,6 @@ extern "C" int moe_sort(const int64_t *experts, int64_t experts_stride, int32_t 
     if (!aligned_to(experts, 8) || !aligned_to(position, 4) || !aligned_to(source, 4) || !aligned_to(offsets, 4) ||
         !aligned_to(counts, 4))
         return GBCE_ERR_ALIGN;
-    Call call;
-    const cudaError_t e = begin_call(&call, GBCE_F32, stream);
-    if (e != cudaSuccess)
-        return map_error(e);
     SortArgs a{};
     a.experts = experts;
     a.es = experts_stride;
@@ -262,6 +281,12 @@ extern "C" int moe_sort(const int64_t *experts, int64_t experts_stride, int32_t 
     a.source = source;
     a.offsets = offsets;
     a.counts = counts;
+    if (plan_arrays_overlap(a))
+        return GBCE_ERR_OVERLAP;
+    Call call;
+    const cudaError_t e = begin_call(&call, GBCE_F32, stream);
+    if (e != cudaSuccess)
+        return map_error(e);
     return map_error(launch_sort(call, a));
 }
 

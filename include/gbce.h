@@ -81,7 +81,7 @@ enum gbce_status {
     GBCE_ERR_NO_DEVICE = 8,   /* no usable CUDA device */
     GBCE_ERR_REDUCTION = 9,   /* reduction is not a gbce_reduction, or kind not a gbce_norm */
     GBCE_ERR_BAD_TABLE = 10,  /* device flag: a block-sparse look-up table entry is malformed */
-    GBCE_ERR_OVERLAP = 11     /* an output shares memory with another tensor (clip_grad_norm) */
+    GBCE_ERR_OVERLAP = 11     /* an output shares memory with another tensor (clip_grad_norm, moe_sort) */
 };
 
 /* Norms of grad_norm and clip_grad_norm. */
@@ -582,7 +582,8 @@ GBCE_API int64_t moe_plan_rows(int64_t T, int64_t E, int64_t k, int64_t align);
  *                 products that go by tiles of rows.
  *
  * A slot outside [-1, E) raises GBCE_ERR_BAD_TARGET and counts as empty.  Stable:
- * an expert's rows keep the order of their slots.
+ * an expert's rows keep the order of their slots.  Arrays that share memory, each
+ * from its first value to its last, are refused: GBCE_ERR_OVERLAP.
  */
 GBCE_API int moe_sort(const int64_t *experts, int64_t experts_stride, int32_t *position, int32_t *source,
                       int32_t *offsets, int32_t *counts, int64_t T, int64_t E, int64_t k, int64_t align,
