@@ -113,3 +113,23 @@ def test_gradient_of_the_rows_without_the_rows():
     buf = torch.zeros(plan.rows, H, device="cuda")
     with pytest.raises(ValueError, match="shares memory with d_out"):
         gbce.moe_combine_bwd(buf[:T], None, plan, w, want_weights=False, d_y=buf)
+
+
+def test_recomputed_plan():
+    # a whole block under checkpointing: its plan is made again, in other memory
+    _, ref, x, y, w = operands()
+    experts = torch.randint(-1, E, (T, k), device="cuda", generator=torch.Generator("cuda").manual_seed(5))
+    x, w = x.requires_grad_(), w.requires_grad_()
+
+    def block(a, b):
+        plan = gbce.moe_sort(experts, E, 4)
+        return gbce.combine_tokens(gbce.dispatch_tokens(a, plan), plan, b)
+    d_out = x.detach().flip(0)
+    want = torch.autograd.grad(block(x, w), (x, w), d_out)
+    out = checkpoint(block, x, w, use_reentrant=False)
+    filler = [torch.full((ref.rows * 4,), 7, device="cuda", dtype=torch.int32) for _ in range(8)]
+    got = torch.autograd.grad(out, (x, w), d_out)
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and len(filler) == 8
+    # each token's own row comes back, times the sum of its weights in use
+    used = torch.where(ref.position >= 0, w.detach(), 0.0).double().sum(1, keepdim=True)
+    near(out, used * x.detach().double(), 2.0 ** -21 * used * x.detach().double().abs() + 2.0 ** -120, "out")
