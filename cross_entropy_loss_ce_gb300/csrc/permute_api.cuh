@@ -53,8 +53,10 @@ cudaError_t launch_sort(const Call &call, SortArgs a)
         return launch_kernel(call, false, sort_rank_kernel<true>, 1, threads, smem, a);
     }
     // a CTA's time is one slot after another of its warps: small ones, while there are few (131072 slots of 256
-    // experts, with peers still found by votes: 15 us with 64 CTAs of 256 threads, 22 with 16 of 1024); many CTAs
-    // make the sums before each one long (131072 x 8: 29 us with 256 of 512 threads, 23 with 128 of 1024)
+    // experts: 9.2 us with 64 CTAs of 256 threads, 9.9 with 32 of 512, 14.9 with 16 of 1024); many CTAs make the sums
+    // before each one long (262144: 9.9 us with 64 of 512, 18.2 with 128 of 256; 131072 x 8: 15.2 with 128 of 1024,
+    // 17.9 with 512 threads, 39 with 256).  Between these sizes not always the best: 524288 take 14.9 with 64 of
+    // 1024, 11.1 with 128 of 512
     int threads = 256;
     while (threads < 1024 && a.n > call.sms / 2 * threads * kSortItems)
         threads *= 2;

@@ -18,7 +18,7 @@
 // unless said, with 6.7 TB/s the rate of a plain copy):
 //   dispatch  8192 x 4 tokens, 23% more rows by padding   29 us, 6.8 TB/s
 //   combine   16384 x 8, H 4096                          177 us, 6.8 TB/s
-//   its gradients  16384 x 8                             172 us, 6.6 TB/s
+//   its gradients  16384 x 8                             170 us, 6.7 TB/s
 //   the plan  131072 x 8 slots of 256 experts             15 us in two kernels: the
 //             time of a CTA's slots one after another, not of their 17 MB; 131072
 //             slots 9 us, a single token 3 us
@@ -555,8 +555,10 @@ __global__ void __launch_bounds__(kPermuteThreads) combine_kernel(const PermuteA
 // combine's gradients: a token belongs to `segs` warps (1, 2, 4 or 8 of a CTA),
 // which read its row of d_out once for up to KC slots, U units of a lane at a
 // time, write that row times the weight to each slot's place and add up the
-// products with each slot's y.  Three CTAs an SM and streaming stores: 185 -> 178
-// us for 16384 x 8 x 2048 bf16, four warps a token 172.
+// products with each slot's y.  Three CTAs an SM, though with 8 slots of 16-bit
+// values that spills 12 to 108 bytes a thread (16384 x 8 x 2048 bf16: 170 us, with
+// two and no spill 187; pairs, 2046: 224 and 216), streaming stores, and four warps
+// a token (with one 178).
 template <typename T, int VEC, int KC, int U>
 __global__ void __launch_bounds__(kPermuteThreads, 3) combine_bwd_kernel(const PermuteArgs a)
 {
