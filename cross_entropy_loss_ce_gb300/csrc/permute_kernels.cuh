@@ -555,10 +555,9 @@ __global__ void __launch_bounds__(kPermuteThreads) combine_kernel(const PermuteA
 // combine's gradients: a token belongs to `segs` warps (1, 2, 4 or 8 of a CTA),
 // which read its row of d_out once for up to KC slots, U units of a lane at a
 // time, write that row times the weight to each slot's place and add up the
-// products with each slot's y.  Three CTAs an SM, though with 8 slots of 16-bit
-// values that spills 12 to 108 bytes a thread (16384 x 8 x 2048 bf16: 170 us, with
-// two and no spill 187; pairs, 2046: 224 and 216), streaming stores, and four warps
-// a token (with one 178).
+// products with each slot's y.  Stores are streaming ones; three CTAs an SM, though
+// with 8 slots of 16-bit values that spills 4 to 108 bytes a thread (16384 x 8 x
+// 2048 bf16: 170 us, with two and no spill 187; pairs, 2046: 224 and 216).
 template <typename T, int VEC, int KC, int U>
 __global__ void __launch_bounds__(kPermuteThreads, 3) combine_bwd_kernel(const PermuteArgs a)
 {
